@@ -371,6 +371,152 @@ size_t santa_attend_vs_workspace_bytes(int batch, int num_q_heads, int num_kv_he
 int santa_attend_vs(const santa_decode_args* a, int value_rows, int32_t* value_ids,
                     void* stream);
 
+/*
+ * ---- The prompt side of the cache and the deterministic sparse step ----
+ *
+ * A "chunk" is the run of new tokens of every sequence in one call, as many as each has (a
+ * prompt, a slice of a prompt, drafted tokens, or the single token of a decode step).  The
+ * chunks of a batch lie one behind the other in the token dimension of q, k_new and v_new:
+ *   cu_q [B + 1] int32 (device): sequence b's tokens are rows cu_q[b] .. cu_q[b+1] - 1, with
+ *   0 <= cu_q[0] and cu_q non-decreasing up to at most num_tokens.  Rows outside
+ *   [cu_q[0], cu_q[B]) belong to no sequence (padding): they are neither read for a result
+ *   nor written.  A sequence may have no new token.
+ * A cu_q that is not so sets SANTA_DEV_BAD_SEQLEN; nothing outside the given buffers is then
+ * touched, but the results are not meaningful.
+ */
+
+/*
+ * santa_rope_table — cosines and sines of a rotary position embedding:
+ *   table[p][j] = cos(p theta^(-2j / rope_dim)), table[p][rope_dim / 2 + j] = sin(same),
+ *   0 <= j < rope_dim / 2, each computed in 64 bits and rounded once to fp32 (an angle of a
+ *   far position has no accurate fp32 value).
+ * table [positions][rope_dim] fp32 (device, 16-byte aligned); rope_dim a multiple of 16 up to
+ * 128; theta > 1.  Made once; santa_append_chunk also takes tables that the caller computes in
+ * another way (scaled frequencies).
+ */
+int santa_rope_table(float* table, int64_t positions, int rope_dim, double theta, void* stream);
+
+/* One chunk append (layouts as above; see santa_append_chunk). */
+typedef struct santa_append_chunk_args {
+  const void* q;               /* [num_tokens][Hq][d] or NULL */
+  const void* k_new;           /* [num_tokens][Hkv][d] */
+  const void* v_new;           /* [num_tokens][Hkv][d] */
+  int64_t q_stride;            /* elements from one token's row to the next (>= Hq * d) */
+  int64_t k_stride;            /* (>= Hkv * d) */
+  int64_t v_stride;
+  const int32_t* cu_q;         /* [B + 1] */
+  const int32_t* page_table;   /* [B][max_teams] */
+  const int32_t* seq_lens;     /* [B] cached tokens before the call */
+  const float* rope;           /* [rope_positions][rope_dim], or NULL with rope_dim = 0 */
+  int64_t rope_positions;
+  int64_t num_tokens;
+  int64_t num_pages;
+  int dtype;                   /* santa_dtype of q, k_new, v_new, the pools and q_out */
+  int batch;
+  int num_q_heads;             /* Hq (ignored when q is NULL) */
+  int num_kv_heads;
+  int head_dim;
+  int team_size;
+  int max_teams;
+  int rope_dim;                /* R: 0 (no rotation) or a multiple of 16 up to head_dim */
+  int interleaved;             /* 0: pairs (j, j + R/2); 1: pairs (2j, 2j + 1) */
+  void* q_out;                 /* [num_tokens][Hq][d] contiguous, rotated queries; may be q
+                                  itself when q_stride = Hq * d; NULL with q */
+  void* k_pool;                /* [P][Hkv][T][d] */
+  void* v_pool;
+  float* reps;                 /* [P][Hkv][d] */
+  int32_t* seq_lens_next;      /* [B] receives the new lengths (may be NULL; not seq_lens) */
+  int32_t* device_status;      /* may be NULL */
+} santa_append_chunk_args;
+
+/*
+ * santa_append_chunk — a chunk's keys and values into the paged cache, keys (and queries)
+ * rotated by position on the way, and the representatives of the touched pages brought up to
+ * date.  Token i of sequence b gets position p = seq_lens[b] + i: slot p % T of page
+ * page_table[b][p / T].  With (c, s) = (rope[p][j], rope[p][R/2 + j]), pair j becomes
+ *   x' = x c - y s,   y' = y c + x s      (products and sum each rounded to fp32),
+ * elements from R on pass unchanged, and the result is rounded once to the cache's type.
+ * The representative of every touched page becomes the mean of its valid keys, bit-identical
+ * to santa_build_reps on the grown cache.  One launch; reads the earlier keys of a page that
+ * was already begun, and nothing else of the cache.
+ *
+ *   - A sequence whose length is out of range (seq_lens[b] < 0, or seq_lens[b] plus its new
+ *     tokens above max_teams * T or, with rotation, above rope_positions) sets
+ *     SANTA_DEV_BAD_SEQLEN and is skipped: no token, query or length of it is written.
+ *   - A page id out of range sets SANTA_DEV_BAD_PAGE; the tokens of that page are not stored.
+ *   - Every page that receives a token must belong to that sequence alone.
+ *   - num_tokens may be 0 (seq_lens_next is then a copy of the lengths).
+ *   - Pointers are 16-byte aligned (int32 arrays 4), strides multiples of 16 bytes.
+ */
+int santa_append_chunk(const santa_append_chunk_args* a, void* stream);
+
+/* One chunk attention (see santa_chunk_attend). */
+typedef struct santa_chunk_args {
+  const void* q;               /* [num_tokens][Hq][d] contiguous, dtype */
+  const void* k_pool;          /* [P][Hkv][T][d] */
+  const void* v_pool;
+  const int32_t* page_table;   /* [B][max_teams] */
+  const int32_t* seq_lens;     /* [B] cached tokens, the chunk's included */
+  const int32_t* cu_q;         /* [B + 1] */
+  int64_t num_tokens;
+  int64_t num_pages;
+  int dtype;
+  int batch;
+  int num_q_heads;
+  int num_kv_heads;
+  int head_dim;
+  int team_size;
+  int max_teams;
+  void* out;                   /* [num_tokens][Hq][d] dtype */
+  void* workspace;             /* santa_chunk_workspace_bytes; contents need not be set */
+  size_t workspace_bytes;
+  int32_t* device_status;      /* may be NULL */
+} santa_chunk_args;
+
+/*
+ * santa_chunk_attend — exact causal attention of a chunk over the paged cache that already
+ * holds it (santa_append_chunk).  Sequence b's new tokens, n_b = cu_q[b+1] - cu_q[b], are the
+ * last n_b of its seq_lens[b]: token i sees the cached tokens 0 .. seq_lens[b] - n_b + i, and
+ *   out_i = sum_j softmax_j(q_i . k_j / sqrt(d)) v_j  over them.
+ * bf16 runs on the tensor cores with fp32 accumulation (the weights are rounded to bf16 before
+ * their product with V, the sum of the weights is not); fp32 is fp32 throughout.  A row whose
+ * every score is -inf gets zeros.  What a row does not see (later tokens, slots behind the
+ * sequence's end, other sequences' pages) has no influence on it, whatever it holds.
+ *
+ *   - A sequence with new tokens and a length outside [n_b, max_teams * T] sets
+ *     SANTA_DEV_BAD_SEQLEN and is skipped: its rows of out are not written.
+ *   - A page id out of range sets SANTA_DEV_BAD_PAGE; page 0 is read in its place, and the
+ *     rows of that sequence are not meaningful.
+ *   - The workspace holds partial results of tiles that several blocks share; it needs no
+ *     initialisation and serves one call at a time.  Results do not depend on its contents
+ *     or on timing: equal calls give equal bits.
+ *   - num_tokens may be 0 (nothing is launched).
+ */
+size_t santa_chunk_workspace_bytes(int dtype, int batch, int64_t num_tokens, int num_q_heads,
+                                   int num_kv_heads, int head_dim, int team_size,
+                                   int max_teams);
+int santa_chunk_attend(const santa_chunk_args* a, void* stream);
+
+/*
+ * santa_select_topk — the deterministic counterpart of santa_sample: the score of team i for
+ * unit (b, h) is s_i = max over the group's heads g of q_g . rep_i, and S is the min(M, n)
+ * teams of largest s_i (ties to the lower index; a NaN score ranks last).  M = num_draws.
+ * Scores are fp32; teams whose scores lie too close to the border of S for fp32 to order are
+ * compared in 64 bits, so S is the set that 64-bit scores give.  Writes sel_ids (ascending,
+ * padded with -1), sel_count and pi (1 for each selected team, padded with 0).  Reads q, reps,
+ * page_table, seq_lens; k_pool, v_pool, seed, sampler, draw_ids, team_probs and workspace are
+ * not used.  A team with a page id out of range ranks last and sets SANTA_DEV_BAD_PAGE.
+ */
+int santa_select_topk(const santa_decode_args* a, void* stream);
+
+/*
+ * santa_topk_decode — santa_select_topk followed by santa_attend on `stream`: exact attention
+ * inside the M teams of best representative score.  A chunk of several query tokens of one
+ * sequence is served as that many rows of the batch, with the same page-table row and
+ * growing lengths.  Workspace as for santa_decode.
+ */
+int santa_topk_decode(const santa_decode_args* a, void* stream);
+
 /* Size in bytes of the scratch array santa_decode_noalloc uses. */
 size_t santa_noalloc_scratch_bytes(void);
 

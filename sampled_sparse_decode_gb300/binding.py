@@ -10,6 +10,7 @@ bfloat16); reps [P][Hkv][d] float32; page_table [B][max_teams] int32; seq_lens [
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -41,6 +42,34 @@ class _DecodeArgs(ctypes.Structure):
         ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
         ("device_status", ctypes.c_void_p),
         ("sampler", ctypes.c_int32), ("mix_alpha", ctypes.c_float),
+    ]
+
+
+class _AppendChunkArgs(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k_new", ctypes.c_void_p), ("v_new", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+        ("cu_q", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+        ("seq_lens", ctypes.c_void_p), ("rope", ctypes.c_void_p),
+        ("rope_positions", ctypes.c_int64), ("num_tokens", ctypes.c_int64),
+        ("num_pages", ctypes.c_int64), ("dtype", ctypes.c_int), ("batch", ctypes.c_int),
+        ("num_q_heads", ctypes.c_int), ("num_kv_heads", ctypes.c_int),
+        ("head_dim", ctypes.c_int), ("team_size", ctypes.c_int), ("max_teams", ctypes.c_int),
+        ("rope_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("q_out", ctypes.c_void_p),
+        ("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p), ("reps", ctypes.c_void_p),
+        ("seq_lens_next", ctypes.c_void_p), ("device_status", ctypes.c_void_p),
+    ]
+
+
+class _ChunkArgs(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+        ("cu_q", ctypes.c_void_p), ("num_tokens", ctypes.c_int64), ("num_pages", ctypes.c_int64),
+        ("dtype", ctypes.c_int), ("batch", ctypes.c_int), ("num_q_heads", ctypes.c_int),
+        ("num_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("team_size", ctypes.c_int),
+        ("max_teams", ctypes.c_int), ("out", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t), ("device_status", ctypes.c_void_p),
     ]
 
 
@@ -82,6 +111,12 @@ def lib():
             "santa_decode_plan": (i32, [A, i32, vp]),
             "santa_decode_path": (i32, [A]),
             "santa_noalloc_scratch_bytes": (sz, []),
+            "santa_rope_table": (i32, [vp, i64, i32, ctypes.c_double, vp]),
+            "santa_append_chunk": (i32, [ctypes.POINTER(_AppendChunkArgs), vp]),
+            "santa_chunk_workspace_bytes": (sz, [i32, i32, i64] + [i32] * 5),
+            "santa_chunk_attend": (i32, [ctypes.POINTER(_ChunkArgs), vp]),
+            "santa_select_topk": (i32, [A, vp]),
+            "santa_topk_decode": (i32, [A, vp]),
         }
         for name, (res, args) in sigs.items():
             f = getattr(L, name)
@@ -604,3 +639,307 @@ def santa_dense_decode(q, k_pool, v_pool, page_table, seq_lens,
     a = _args(q, k_pool, v_pool, None, page_table, seq_lens, 1, 0, bufs)
     _check(lib().santa_dense_decode(ctypes.byref(a), _stream(stream)), "santa_dense_decode")
     return bufs
+
+
+# ---------------------------------------------------------------- chunks and top-k
+
+def _same_device(**tensors):
+    """Every given tensor lives on the current CUDA device (the one a call runs on)."""
+    cur = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.device.index != cur:
+            raise SantaError(f"{name} is on {t.device}, the current device is cuda:{cur}")
+
+
+def _allocating(stream):
+    """Context in which torch allocates for `stream` (None: the current stream), so that a
+    buffer's memory is reused only after the stream's work on it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def _status_word(t):
+    if t is not None:
+        _req(t, "device_status", torch.int32)
+        if t.numel() < 1:
+            raise SantaError("device_status must hold one int32")
+
+
+def _pools(k_pool, v_pool, dtype):
+    _req(k_pool, "k_pool", dtype, 4)
+    _req(v_pool, "v_pool", dtype, 4)
+    if k_pool.shape != v_pool.shape:
+        raise SantaError("k_pool and v_pool must have the same shape")
+    return k_pool.shape
+
+
+def _ragged(cu_q, page_table, seq_lens):
+    """Checks the batch's int32 tensors; returns B."""
+    _req(cu_q, "cu_q", torch.int32, 1)
+    _req(page_table, "page_table", torch.int32, 2)
+    _req(seq_lens, "seq_lens", torch.int32, 1)
+    B = seq_lens.shape[0]
+    if cu_q.shape[0] != B + 1 or page_table.shape[0] != B:
+        raise SantaError("cu_q must be [B + 1], page_table [B][max_teams] and seq_lens [B]")
+    return B
+
+
+def _token_rows(t, name, dtype, heads, d):
+    """[tokens][heads][d] whose rows are contiguous; returns the row stride in elements."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise SantaError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise SantaError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != d:
+        raise SantaError(f"{name} must be [tokens][heads][{d}], got {tuple(t.shape)}")
+    if t.shape[0] == 0:
+        return t.shape[1] * d
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d):
+        raise SantaError(f"the heads of one token of {name} must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * d)
+
+
+class _Prepared:
+    """A call whose arguments are checked and marshalled once, for steps that reuse the same
+    tensors: their contents may change between runs, their storage may not."""
+
+    def __init__(self, name, args, keep, result):
+        self._name, self._fn = name, getattr(lib(), name)
+        self._a, self._aref = args, ctypes.byref(args)
+        self._keep, self._result = keep, result
+        self._device = torch.cuda.current_device()
+
+    def run(self, stream=None):
+        """Enqueues the call on `stream` (the current stream by default); returns its result
+        buffers."""
+        if torch.cuda.current_device() != self._device:
+            raise SantaError(f"{self._name} was prepared on cuda:{self._device}")
+        rc = self._fn(self._aref, _stream(stream))
+        if rc:
+            _check(rc, self._name)
+        return self._result
+
+
+def santa_rope_table(positions: int, rope_dim: int, theta: float = 10000.0, device="cuda",
+                     stream=None) -> torch.Tensor:
+    """[positions][rope_dim] float32: cos(p theta^(-2j / rope_dim)), j < rope_dim / 2, then the
+    sines; angles in 64 bits."""
+    if torch.device(device).type != "cuda":
+        raise SantaError("santa_rope_table makes a table on a CUDA device")
+    if positions < 1 or rope_dim < 1:
+        raise SantaError("positions and rope_dim must be positive")
+    with _allocating(stream):
+        table = torch.empty((positions, rope_dim), dtype=torch.float32, device=device)
+    _same_device(table=table)
+    _check(lib().santa_rope_table(_ptr(table), positions, rope_dim, float(theta),
+                                  _stream(stream)), "santa_rope_table")
+    return table
+
+
+def _append_chunk(q, k_new, v_new, cu_q, k_pool, v_pool, reps, page_table, seq_lens, rope,
+                  seq_lens_next, q_out, interleaved, device_status, stream):
+    if not isinstance(k_pool, torch.Tensor) or k_pool.dtype not in _DTYPES:
+        raise SantaError("k_pool must be a float32 or bfloat16 tensor")
+    dt = k_pool.dtype
+    P, Hkv, T, d = _pools(k_pool, v_pool, dt)
+    B = _ragged(cu_q, page_table, seq_lens)
+    _req(reps, "reps", torch.float32, 3)
+    if tuple(reps.shape) != (P, Hkv, d):
+        raise SantaError("reps must be [P][Hkv][d] of the pools")
+    a = _AppendChunkArgs()
+    a.k_stride = _token_rows(k_new, "k_new", dt, Hkv, d)
+    a.v_stride = _token_rows(v_new, "v_new", dt, Hkv, d)
+    n = k_new.shape[0]
+    if v_new.shape[0] != n:
+        raise SantaError("k_new and v_new must hold the same tokens")
+    if q is not None:
+        a.q_stride = _token_rows(q, "q", dt, None, d)
+        if q.shape[0] != n:
+            raise SantaError("q and k_new must hold the same tokens")
+        if q.shape[1] < 1:
+            raise SantaError("q must have a head")
+        if q_out is None:
+            with _allocating(stream):
+                # rows that belong to no sequence are not written
+                q_out = torch.zeros((n, q.shape[1], d), dtype=dt, device=q.device)
+        _req(q_out, "q_out", dt, 3)
+        if q_out.shape != q.shape:
+            raise SantaError("q_out must have q's shape")
+        a.num_q_heads = q.shape[1]
+    elif q_out is not None:
+        raise SantaError("q_out without q")
+    if rope is not None:
+        _req(rope, "rope", torch.float32, 2)
+        a.rope_positions, a.rope_dim = rope.shape
+    if seq_lens_next is not None:
+        _req(seq_lens_next, "seq_lens_next", torch.int32, 1)
+        if seq_lens_next.shape[0] != B:
+            raise SantaError("seq_lens_next must be [B]")
+    _status_word(device_status)
+    _same_device(q=q, k_new=k_new, v_new=v_new, cu_q=cu_q, k_pool=k_pool, v_pool=v_pool,
+                 reps=reps, page_table=page_table, seq_lens=seq_lens, rope=rope, q_out=q_out,
+                 seq_lens_next=seq_lens_next, device_status=device_status)
+    # an empty chunk has tensors without storage
+    a.q, a.q_out = (_ptr(q), _ptr(q_out)) if n else (None, None)
+    a.k_new, a.v_new = _ptr(k_new), _ptr(v_new)
+    a.cu_q, a.page_table, a.seq_lens, a.rope = (_ptr(cu_q), _ptr(page_table), _ptr(seq_lens),
+                                                _ptr(rope))
+    a.num_tokens, a.num_pages, a.dtype, a.batch = n, P, _DTYPES[dt], B
+    a.num_kv_heads, a.head_dim, a.team_size, a.max_teams = Hkv, d, T, page_table.shape[1]
+    a.interleaved = int(bool(interleaved))
+    a.k_pool, a.v_pool, a.reps = _ptr(k_pool), _ptr(v_pool), _ptr(reps)
+    a.seq_lens_next, a.device_status = _ptr(seq_lens_next), _ptr(device_status)
+    keep = (q, k_new, v_new, cu_q, k_pool, v_pool, reps, page_table, seq_lens, rope,
+            seq_lens_next, device_status)
+    return _Prepared("santa_append_chunk", a, keep, q_out)
+
+
+def santa_append_chunk(q, k_new, v_new, cu_q, k_pool, v_pool, reps, page_table, seq_lens,
+                       rope: torch.Tensor | None = None,
+                       seq_lens_next: torch.Tensor | None = None,
+                       q_out: torch.Tensor | None = None, interleaved: bool = False,
+                       device_status: torch.Tensor | None = None, stream=None):
+    """A ragged chunk of new tokens (k_new, v_new [tokens][Hkv][d]; cu_q [B + 1]) into the paged
+    cache behind seq_lens, keys and queries (q [tokens][Hq][d] or None) rotated by position with
+    the table `rope` (None: not rotated), representatives of the touched pages refreshed;
+    seq_lens_next (if given) receives the new lengths.  q, k_new and v_new may be strided from
+    token to token (views of a fused projection).  Returns the rotated queries: q_out, or a new
+    tensor whose rows outside every sequence are zero; q_out may be q itself if q is
+    contiguous."""
+    return _append_chunk(q, k_new, v_new, cu_q, k_pool, v_pool, reps, page_table, seq_lens,
+                         rope, seq_lens_next, q_out, interleaved, device_status,
+                         stream).run(stream)
+
+
+def santa_append_chunk_prepared(q, k_new, v_new, cu_q, k_pool, v_pool, reps, page_table,
+                                seq_lens, rope: torch.Tensor | None = None,
+                                seq_lens_next: torch.Tensor | None = None,
+                                q_out: torch.Tensor | None = None, interleaved: bool = False,
+                                device_status: torch.Tensor | None = None) -> _Prepared:
+    """santa_append_chunk's checks and argument structure done once; .run(stream=None)."""
+    return _append_chunk(q, k_new, v_new, cu_q, k_pool, v_pool, reps, page_table, seq_lens,
+                         rope, seq_lens_next, q_out, interleaved, device_status, None)
+
+
+def santa_chunk_workspace_bytes(dtype, batch, num_tokens, num_q_heads, num_kv_heads, head_dim,
+                                team_size, max_teams) -> int:
+    """dtype: torch.float32 / torch.bfloat16 (or 0 / 1); 0 for an unsupported shape."""
+    return lib().santa_chunk_workspace_bytes(_dtype_code(dtype), batch, num_tokens, num_q_heads,
+                                             num_kv_heads, head_dim, team_size, max_teams)
+
+
+def _chunk_attend(q, k_pool, v_pool, page_table, seq_lens, cu_q, out, workspace, device_status,
+                  stream):
+    _req(q, "q", ndim=3)
+    if q.dtype not in _DTYPES:
+        raise SantaError("q must be float32 or bfloat16")
+    P, Hkv, T, d = _pools(k_pool, v_pool, q.dtype)
+    B = _ragged(cu_q, page_table, seq_lens)
+    n, Hq, d2 = q.shape
+    if d2 != d:
+        raise SantaError("q and the pools must have the same head size")
+    if out is not None:
+        _req(out, "out", q.dtype, 3)
+        if out.shape != q.shape:
+            raise SantaError("out must have q's shape")
+    _status_word(device_status)
+    if workspace is not None:
+        _req(workspace, "workspace", torch.uint8, 1)
+    _same_device(q=q, k_pool=k_pool, v_pool=v_pool, page_table=page_table, seq_lens=seq_lens,
+                 cu_q=cu_q, out=out, workspace=workspace, device_status=device_status)
+    with _allocating(stream):
+        if out is None:
+            # rows that belong to no sequence are not written
+            out = torch.zeros_like(q)
+        if workspace is None:
+            need = santa_chunk_workspace_bytes(q.dtype, B, n, Hq, Hkv, d, T,
+                                               page_table.shape[1])
+            if need == 0:
+                raise SantaError("unsupported shape for santa_chunk_attend")
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    a = _ChunkArgs()
+    a.q, a.k_pool, a.v_pool = _ptr(q), _ptr(k_pool), _ptr(v_pool)
+    a.page_table, a.seq_lens, a.cu_q = _ptr(page_table), _ptr(seq_lens), _ptr(cu_q)
+    a.num_tokens, a.num_pages, a.dtype, a.batch = n, P, _DTYPES[q.dtype], B
+    a.num_q_heads, a.num_kv_heads, a.head_dim = Hq, Hkv, d
+    a.team_size, a.max_teams = T, page_table.shape[1]
+    a.out, a.workspace, a.workspace_bytes = _ptr(out), _ptr(workspace), workspace.numel()
+    a.device_status = _ptr(device_status)
+    keep = (q, k_pool, v_pool, page_table, seq_lens, cu_q, workspace, device_status)
+    return _Prepared("santa_chunk_attend", a, keep, out)
+
+
+def santa_chunk_attend(q, k_pool, v_pool, page_table, seq_lens, cu_q,
+                       out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                       device_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Exact causal attention of a ragged chunk (q [tokens][Hq][d], cu_q [B + 1]; the last
+    cu_q[b + 1] - cu_q[b] of sequence b's seq_lens[b] cached tokens) over the paged cache.
+    Returns out [tokens][Hq][d] in q's dtype (a new tensor: zero outside every sequence)."""
+    return _chunk_attend(q, k_pool, v_pool, page_table, seq_lens, cu_q, out, workspace,
+                         device_status, stream).run(stream)
+
+
+def santa_chunk_attend_prepared(q, k_pool, v_pool, page_table, seq_lens, cu_q,
+                                out: torch.Tensor | None = None,
+                                workspace: torch.Tensor | None = None,
+                                device_status: torch.Tensor | None = None) -> _Prepared:
+    """santa_chunk_attend's checks, buffers and argument structure done once;
+    .run(stream=None)."""
+    return _chunk_attend(q, k_pool, v_pool, page_table, seq_lens, cu_q, out, workspace,
+                         device_status, None)
+
+
+def _topk(name, q, k_pool, v_pool, reps, page_table, seq_lens, num_teams, bufs, stream):
+    if reps is None:
+        raise SantaError("reps must be a CUDA tensor")
+    _req(k_pool, "k_pool", ndim=4)
+    _req(q, "q", ndim=3)
+    _req(page_table, "page_table", torch.int32, 2)
+    if tuple(reps.shape) != (k_pool.shape[0], k_pool.shape[1], k_pool.shape[3]):
+        raise SantaError("reps must be [P][Hkv][d] of the pools")
+    if bufs is None:
+        if q.dtype not in _DTYPES:
+            raise SantaError("q must be float32 or bfloat16")
+        _same_device(q=q)
+        with _allocating(stream):
+            bufs = _bufs_for(q, k_pool, page_table, num_teams, None)
+    B, Hq, d = q.shape
+    Hkv = k_pool.shape[1]
+    for field, shape, dt in (("out", (B, Hq, d), torch.float32),
+                             ("sel_ids", (B, Hkv, num_teams), torch.int32),
+                             ("sel_count", (B, Hkv), torch.int32),
+                             ("pi", (B, Hkv, num_teams), torch.float32)):
+        _req(getattr(bufs, field), f"bufs.{field}", dt)
+        if tuple(getattr(bufs, field).shape) != shape:
+            raise SantaError(f"bufs.{field} must be {shape}")
+    a = _args(q, k_pool, v_pool, reps, page_table, seq_lens, num_teams, 0, bufs)
+    _same_device(q=q, k_pool=k_pool, v_pool=v_pool, reps=reps, page_table=page_table,
+                 seq_lens=seq_lens, out=bufs.out, workspace=bufs.workspace)
+    keep = (q, k_pool, v_pool, reps, page_table, seq_lens)
+    return _Prepared(name, a, keep, bufs)
+
+
+def santa_select_topk(q, k_pool, v_pool, reps, page_table, seq_lens, num_teams: int,
+                      bufs: DecodeBuffers | None = None, stream=None) -> DecodeBuffers:
+    """The num_teams teams of best representative score of every unit into bufs.sel_ids,
+    bufs.sel_count and bufs.pi (1): the deterministic counterpart of santa_sample."""
+    return _topk("santa_select_topk", q, k_pool, v_pool, reps, page_table, seq_lens, num_teams,
+                 bufs, stream).run(stream)
+
+
+def santa_topk_decode(q, k_pool, v_pool, reps, page_table, seq_lens, num_teams: int,
+                      bufs: DecodeBuffers | None = None, stream=None) -> DecodeBuffers:
+    """One sparse decode step: santa_select_topk, then exact attention inside those teams."""
+    return _topk("santa_topk_decode", q, k_pool, v_pool, reps, page_table, seq_lens, num_teams,
+                 bufs, stream).run(stream)
+
+
+def santa_topk_decode_prepared(q, k_pool, v_pool, reps, page_table, seq_lens, num_teams: int,
+                               bufs: DecodeBuffers | None = None) -> _Prepared:
+    """santa_topk_decode's checks, buffers and argument structure done once;
+    .run(stream=None)."""
+    return _topk("santa_topk_decode", q, k_pool, v_pool, reps, page_table, seq_lens, num_teams,
+                 bufs, None)

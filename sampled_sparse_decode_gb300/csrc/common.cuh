@@ -267,6 +267,41 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// ---------------------------------------------------------------- ragged chunks
+
+// The sequence that owns work slot `slot` of a ragged batch: the last b < batch with
+// s(b) <= slot, s(b) = floor(cu[b] / per) + extra * b (0 if there is none).  cu[b] is clamped to
+// [0, num_tokens], and any cu at all gives some b in [0, batch).  The whole warp calls it with
+// the same arguments; 32 candidates per round.
+__device__ __forceinline__ int find_sequence(const int32_t* cu, int batch, int64_t num_tokens,
+                                             int per, int extra, int64_t slot) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = batch;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + lane * step;
+    bool below = lane == 0;
+    if (lane > 0 && at < hi) {
+      int64_t c = cu[at];
+      c = c < 0 ? 0 : c > num_tokens ? num_tokens : c;
+      below = c / per + static_cast<int64_t>(extra) * at <= slot;
+    }
+    const unsigned m = __ballot_sync(0xffffffffu, below);
+    lo += (31 - __clz(m)) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+// Sets SANTA_DEV_BAD_SEQLEN if cu is not non-decreasing within [0, num_tokens] (a search over
+// such a cu may miss the sequence it concerns); by all threads of one block.
+__device__ __forceinline__ void check_bounds(const int32_t* cu, int batch, int64_t num_tokens,
+                                             int32_t* status) {
+  for (int b = threadIdx.x; b < batch; b += blockDim.x)
+    if (cu[b] < 0 || cu[b + 1] < cu[b] || cu[b + 1] > num_tokens)
+      set_status(status, SANTA_DEV_BAD_SEQLEN);
+}
+
 // ---------------------------------------------------------------- Philox4x32-10
 
 // Counter-based generator of Salmon, Moraes, Dror and Shaw, "Parallel Random Numbers: As

@@ -75,6 +75,72 @@ struct AppendParams {
 };
 cudaError_t launch_append(const AppendParams& p, int head_dim, cudaStream_t stream);
 
+// ---------------------------------------------------------------- chunk append
+struct AppendChunkParams {
+  const void* q;              // [num_tokens] rows of q_stride elements, or nullptr
+  const void* k_new;
+  const void* v_new;
+  int64_t q_stride, k_stride, v_stride;   // elements
+  const int32_t* cu_q;        // [B + 1]
+  const int32_t* page_table;  // [B][max_teams]
+  const int32_t* seq_lens;    // [B] lengths before
+  const float* rope;          // [rope_positions][rope_dim]
+  int64_t rope_positions, num_tokens, num_pages;
+  int batch, num_q_heads, num_kv_heads, team_size, max_teams, rope_dim;
+  bool interleaved;
+  void* q_out;                // [num_tokens][Hq][d]
+  void* k_pool;
+  void* v_pool;
+  float* reps;
+  int32_t* seq_lens_next;     // [B] or nullptr
+  int32_t* status;
+  uint32_t page_items;        // blocks of page items (set by the launcher)
+};
+// Blocks of the launch (the launcher refuses more than a grid dimension holds).
+int64_t append_chunk_blocks(int64_t num_tokens, int batch, int num_q_heads, int num_kv_heads,
+                            int head_dim, int team_size, bool bf16);
+cudaError_t launch_append_chunk(const AppendChunkParams& p, int head_dim, bool bf16,
+                                cudaStream_t stream);
+cudaError_t launch_rope_table(float* table, int64_t positions, int rope_dim, double theta,
+                              cudaStream_t stream);
+
+// ---------------------------------------------------------------- top-k selection
+struct SelectParams {
+  const void* q;
+  const float* reps;
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  bool bf16;
+  int batch, num_q_heads, num_kv_heads, team_size, max_teams, keep;
+  int64_t num_pages;
+  int32_t* sel_ids;
+  int32_t* sel_count;
+  float* pi;
+  int32_t* status;
+};
+cudaError_t launch_select_topk(const SelectParams& p, int head_dim, int sms, cudaStream_t stream);
+
+// ---------------------------------------------------------------- chunk attention
+struct ChunkParams {
+  const void* q;              // [num_tokens][Hq][d]
+  const void* k_pool;
+  const void* v_pool;
+  const int32_t* page_table;  // [B][max_teams]
+  const int32_t* seq_lens;    // [B] lengths, the chunk included
+  const int32_t* cu_q;        // [B + 1]
+  int64_t num_tokens, num_pages;
+  int batch, num_q_heads, num_kv_heads, team_size, max_teams;
+  float scale_log2;           // log2(e) / sqrt(d)
+  void* out;                  // [num_tokens][Hq][d]
+  int32_t* status;
+};
+// The plain-arithmetic form: 64-row tiles, `splits` blocks share a tile's keys; partials
+// [tiles][splits][64][d] and (m, l) [tiles][splits][64][2] fp32 when splits > 1.
+int64_t chunk_simt_tiles(int64_t num_tokens, int batch, int group, int num_kv_heads);
+int chunk_simt_splits(int64_t tiles, int64_t max_len, int sms);
+cudaError_t launch_chunk_simt(const ChunkParams& p, int head_dim, bool bf16, int splits,
+                              float* part_acc, float* part_ml, cudaStream_t stream);
+
 // ---------------------------------------------------------------- host slabs of santa_decode_host
 // bytes / 16 words from src to dst (both 16-byte aligned; one of them host memory mapped into
 // the device's address space).  stage-in lets the next launch be scheduled early; stage-out
@@ -157,9 +223,22 @@ cudaError_t decode_launch_bf16_wide_fast_var(const DecodeParams& p, int head_dim
 int decode_resident_bf16_fast_var(int head_dim, int group);
 int decode_resident_bf16_wide_fast_var(int head_dim, int group);
 
+// Helpers of the host side that both ABI files use (defined in santa_abi.cu): streaming
+// multiprocessors of the current device (0 on failure), the driver's tensor-map encoder
+// (nullptr if it is not there), and the tensor map of a bf16 pool.
+int device_sms();
+typedef CUresult (*TensorMapEncode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                    const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+TensorMapEncode tensor_map_encode();
+int pool_tensor_map(CUtensorMap* map, const void* pool, int64_t rows, int d);
+
 // Every host-side check santa_decode makes on `a`, then its launch plan; launches nothing
 // and touches no device memory.  On SANTA_OK *clusters_per_unit receives the plan's NC (> 1:
 // the partials and arrival counters go through a->workspace).
 int check_and_plan_decode(const santa_decode_args* a, int* clusters_per_unit);
+// The same for santa_attend.
+int check_attend(const santa_decode_args* a);
 
 }  // namespace santa

@@ -541,11 +541,25 @@ int do_reps(const void* k_pool, int dtype, int64_t num_pages, int hkv, int T, in
 }  // namespace
 
 namespace santa {
+int device_sms() { return current_sms(); }
+TensorMapEncode tensor_map_encode() { return tensor_map_encoder(); }
+int pool_tensor_map(CUtensorMap* map, const void* pool, int64_t rows, int d) {
+  return encode_pool_map(map, pool, rows, d);
+}
+
 int check_and_plan_decode(const santa_decode_args* a, int* clusters_per_unit) {
   Plan pl;
   const int rc = check_and_plan(a, kModeDecode, &pl);
   if (rc == SANTA_OK && clusters_per_unit) *clusters_per_unit = pl.clusters;
   return rc;
+}
+
+int check_attend(const santa_decode_args* a) {
+  Plan pl;
+  const int rc = check_and_plan(a, kModeAttend, &pl);
+  if (rc) return rc;
+  const int64_t rows = a->num_pages * a->num_kv_heads * static_cast<int64_t>(a->team_size);
+  return a->dtype == SANTA_BF16 && rows > 0x7fffffffll ? SANTA_ERR_UNSUPPORTED : SANTA_OK;
 }
 }  // namespace santa
 

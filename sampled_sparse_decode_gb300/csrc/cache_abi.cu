@@ -35,15 +35,24 @@ int check_tokens(int64_t num_tokens) {
   return num_tokens > kMaxTokens ? SANTA_ERR_UNSUPPORTED : SANTA_OK;
 }
 
-// Partial results of the split tiles of a chunk attention in fp32: accumulators, then (m, l).
+// Workspace of a chunk attention: bf16 has one of its own; fp32 keeps the partial results of
+// its split tiles, accumulators, then (m, l).
 struct ChunkLayout {
-  int splits;
+  int splits, sms;
   size_t acc_bytes, bytes;
 };
 int chunk_layout(int dtype, int batch, int64_t num_tokens, int hq, int hkv, int d, int T,
                  int max_teams, ChunkLayout* l) {
   const int sms = santa::device_sms();
   if (sms <= 0) return SANTA_ERR_CUDA;
+  l->sms = sms;
+  if (dtype == SANTA_BF16) {
+    l->splits = 1;
+    l->acc_bytes = 0;
+    l->bytes = kAlign + santa::chunk_tc_workspace(num_tokens, batch, hq / hkv, hkv, d,
+                                                  static_cast<int64_t>(max_teams) * T, sms);
+    return SANTA_OK;
+  }
   const int64_t tiles = santa::chunk_simt_tiles(num_tokens, batch, hq / hkv, hkv);
   l->splits = santa::chunk_simt_splits(tiles, static_cast<int64_t>(max_teams) * T, sms);
   const size_t rows = l->splits > 1 ? static_cast<size_t>(tiles) * l->splits * 64 : 0;
@@ -191,7 +200,9 @@ int santa_chunk_attend(const santa_chunk_args* a, void* stream) {
       static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(a->head_dim)));
   p.out = a->out;
   p.status = a->device_status;
-  return map_cuda(santa::launch_chunk_simt(p, a->head_dim, a->dtype == SANTA_BF16, l.splits,
+  if (a->dtype == SANTA_BF16)
+    return santa::launch_chunk_tc(p, a->head_dim, base, l.sms, static_cast<cudaStream_t>(stream));
+  return map_cuda(santa::launch_chunk_simt(p, a->head_dim, l.splits,
                                            reinterpret_cast<float*>(base),
                                            reinterpret_cast<float*>(base + l.acc_bytes),
                                            static_cast<cudaStream_t>(stream)));

@@ -30,24 +30,11 @@ struct SimtSmem {
   float p[kRows][kKeys + 4];
 };
 
-// One row piece of 4 fp32 values, from fp32 or bf16.
-template <bool BF16>
 __device__ __forceinline__ float4 load4(const void* base, int64_t elem) {
-  if constexpr (BF16) {
-    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + elem);
-    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
-  } else {
-    return *reinterpret_cast<const float4*>(static_cast<const float*>(base) + elem);
-  }
+  return *reinterpret_cast<const float4*>(static_cast<const float*>(base) + elem);
 }
-
-template <bool BF16>
 __device__ __forceinline__ void store4(void* base, int64_t elem, float4 v) {
-  if constexpr (BF16)
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + elem) =
-        make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-  else
-    *reinterpret_cast<float4*>(static_cast<float*>(base) + elem) = v;
+  *reinterpret_cast<float4*>(static_cast<float*>(base) + elem) = v;
 }
 
 struct Tile {
@@ -93,7 +80,7 @@ __device__ __forceinline__ bool find_tile(const ChunkParams& p, int64_t slot, in
   return true;
 }
 
-template <bool BF16, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(ChunkParams p, int splits,
                                                                  float* part_acc,
                                                                  float* part_ml) {
@@ -116,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(ChunkParams p, 
     const int64_t row = t.row0 + r;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (row < t.n * G)
-      x = load4<BF16>(p.q, ((t.first + row / G) * p.num_q_heads + h * G + row % G) * D + c);
+      x = load4(p.q, ((t.first + row / G) * p.num_q_heads + h * G + row % G) * D + c);
     *reinterpret_cast<float4*>(&s.q[r][c]) = x;
   }
   // keys that row ty * 4 + i sees
@@ -154,8 +141,8 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(ChunkParams p, 
       const int r = i / (D / 4), c = i % (D / 4) * 4;
       float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
       if (r < valid) {
-        kx = load4<BF16>(p.k_pool, base + r * D + c);
-        vx = load4<BF16>(p.v_pool, base + r * D + c);
+        kx = load4(p.k_pool, base + r * D + c);
+        vx = load4(p.v_pool, base + r * D + c);
       }
       *reinterpret_cast<float4*>(&s.k[r][c]) = kx;
       *reinterpret_cast<float4*>(&s.v[r][c]) = vx;
@@ -263,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(ChunkParams p, 
       const int64_t out = ((t.first + row / G) * p.num_q_heads + h * G + row % G) * D;
 #pragma unroll
       for (int c = 0; c < kCols; ++c)
-        store4<BF16>(p.out, out + tx * 4 + 64 * c,
+        store4(p.out, out + tx * 4 + 64 * c,
                      make_float4(o[i][c][0] * inv, o[i][c][1] * inv, o[i][c][2] * inv,
                                  o[i][c][3] * inv));
     } else {
@@ -281,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(ChunkParams p, 
 }
 
 // Joins a tile's partial results in split order: one warp per row.
-template <bool BF16, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) chunk_join_kernel(ChunkParams p, int splits,
                                                               const float* part_acc,
                                                               const float* part_ml) {
@@ -316,23 +303,18 @@ __global__ void __launch_bounds__(kThreads) chunk_join_kernel(ChunkParams p, int
     const int64_t out = ((t.first + row / G) * p.num_q_heads + h * G + row % G) * D;
 #pragma unroll
     for (int e = 0; e < kVals; ++e) {
-      const float x = acc[e] * inv;
-      if constexpr (BF16)
-        static_cast<uint16_t*>(p.out)[out + e * 32 + lane] =
-            static_cast<uint16_t>(pack_bf16(x, 0.f) & 0xffffu);
-      else
-        static_cast<float*>(p.out)[out + e * 32 + lane] = x;
+      static_cast<float*>(p.out)[out + e * 32 + lane] = acc[e] * inv;
     }
   }
 }
 
-template <bool BF16, int D>
+template <int D>
 cudaError_t launch(const ChunkParams& p, int splits, float* part_acc, float* part_ml,
                    cudaStream_t stream) {
   const int G = p.num_q_heads / p.num_kv_heads;
   const int64_t slots = chunk_simt_tiles(p.num_tokens, p.batch, G, 1);
   static std::atomic<unsigned long long> done{0};
-  cudaError_t e = ensure_dynamic_smem(chunk_simt_kernel<BF16, D>, sizeof(SimtSmem<D>), done);
+  cudaError_t e = ensure_dynamic_smem(chunk_simt_kernel<D>, sizeof(SimtSmem<D>), done);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -344,11 +326,11 @@ cudaError_t launch(const ChunkParams& p, int splits, float* part_acc, float* par
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, chunk_simt_kernel<BF16, D>, p, splits, part_acc, part_ml);
+  e = cudaLaunchKernelEx(&cfg, chunk_simt_kernel<D>, p, splits, part_acc, part_ml);
   if (e != cudaSuccess || splits == 1) return e;
   cfg.gridDim = dim3(static_cast<unsigned>(slots), p.num_kv_heads, 2);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, chunk_join_kernel<BF16, D>, p, splits,
+  return cudaLaunchKernelEx(&cfg, chunk_join_kernel<D>, p, splits,
                             static_cast<const float*>(part_acc),
                             static_cast<const float*>(part_ml));
 }
@@ -368,13 +350,10 @@ int chunk_simt_splits(int64_t tiles, int64_t max_len, int sms) {
   return static_cast<int>(s < 1 ? 1 : s > 64 ? 64 : s);
 }
 
-cudaError_t launch_chunk_simt(const ChunkParams& p, int head_dim, bool bf16, int splits,
-                              float* part_acc, float* part_ml, cudaStream_t stream) {
-  if (bf16)
-    return head_dim == 128 ? launch<true, 128>(p, splits, part_acc, part_ml, stream)
-                           : launch<true, 64>(p, splits, part_acc, part_ml, stream);
-  return head_dim == 128 ? launch<false, 128>(p, splits, part_acc, part_ml, stream)
-                         : launch<false, 64>(p, splits, part_acc, part_ml, stream);
+cudaError_t launch_chunk_simt(const ChunkParams& p, int head_dim, int splits, float* part_acc,
+                              float* part_ml, cudaStream_t stream) {
+  return head_dim == 128 ? launch<128>(p, splits, part_acc, part_ml, stream)
+                         : launch<64>(p, splits, part_acc, part_ml, stream);
 }
 
 }  // namespace santa

@@ -1,0 +1,966 @@
+// chunk_tc.cu — causal attention of a chunk of new tokens over a paged bf16 cache on the tensor
+// cores (tcgen05, accumulators in TMEM).
+//
+// A KV head's G query heads share its keys, so the rows of a tile are (token, head) pairs,
+// token-major: 128 / G tokens make one 128-row tile, and two tiles (A, B) one work item, which
+// walks the keys that its last token sees in steps of 128.  Per step and tile:
+//   S = Q K^T   (128 x 128 x d, both operands in shared memory)      -> TMEM
+//   P = 2^(S scale - m), running maximum m and sum l per row; bf16   -> TMEM, over S
+//   O += P V    (128 x d x 128, P from TMEM, V in shared memory)     -> TMEM
+// Roles of a block (one per SM, persistent): warps 0-3 softmax of tile A and warps 4-7 of tile B
+// (a thread owns a row, so maxima and sums need no exchange), warp 8 issues the products, warp 9
+// feeds K and V through a ring of tensor copies (warps 10 and 11 only give up registers).  While one tile's softmax runs, the tensor
+// pipe works on the other tile.  O is rescaled only when a row's maximum has grown by more than
+// 2^8 since the last time (the stored m is then any upper reference, not the maximum; weights
+// stay below 2^8), so most steps touch O by the product alone.
+//
+// Work split.  The steps of all items, in the order (sequence, KV head, item, step), are one line
+// of W steps; block c of N takes the steps [W c / N, W (c + 1) / N).  An item that crosses a
+// border leaves partial (m, l, O) rows in the workspace, at most two per block, and a second
+// launch joins them in order: every block has the same work to within a step, for one long
+// sequence as for many short ones, and nothing depends on timing.
+//
+// Unseen values.  P is 0 for a masked pair, but 0 * V is not 0 for an infinite or NaN V.  Steps
+// that hold masked pairs (the causal border and the sequence's end) therefore pass through the
+// copying warp after they land: rows of V that no row of the item sees are cleared, and in rows
+// that only some see, non-finite elements are cleared and noted; the rows that do see them add
+// their product in the epilogue.
+#include <algorithm>
+
+#include "kernels.h"
+
+namespace santa {
+
+namespace {
+
+constexpr int kTcThreads = 384;          // three warpgroups: softmax A, softmax B, the rest
+constexpr int kSoftmaxRegs = 208;         // registers per thread: 2 * 208 + 88 = 3 * 168, what
+constexpr int kIssueRegs = 88;            // 384 threads are launched with
+constexpr int kStep = 128;                 // keys per step
+constexpr int kMinSteps = 4;               // steps a block takes at least
+constexpr float kSlack = 8.f;              // growth of a row's maximum that triggers a rescale
+
+template <int D>
+struct TcCfg {
+  static constexpr int kHalves = D / 64;                 // 128-byte wide column blocks
+  static constexpr int kTileBytes = 128 * D * 2;         // one Q tile, one K or V step
+  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr size_t kSmem = 1024 + (2 + kStages) * static_cast<size_t>(kTileBytes);
+  static constexpr int kColS = 0, kColO = 256;           // TMEM columns: S_A S_B | O_A O_B
+};
+
+struct TcParams {
+  ChunkParams c;
+  int tpt;                   // tokens per 128-row tile
+  float* part_acc;           // [N][2][256][D]
+  float* part_ml;            // [N][2][256][2]
+  int32_t* join;             // [N][8]
+  CUtensorMap tmap_q, tmap_k, tmap_v;
+};
+
+struct TcShared {
+  uint64_t q_full, q_empty, land, drain;
+  uint64_t kv_full[10], kv_empty[10];
+  uint64_t s_full[2], p_ready[2], o_full[2];
+  uint32_t tmem;
+  volatile int abort;
+  int start[4];              // b, h, tile, step of the block's first step
+  int64_t left, total;       // the block's steps, all steps
+  int64_t begin;
+  int blocks;                // blocks with work
+  uint32_t noted[3][4][4];   // [item ring][step of the last four][token bits]
+};
+
+// ---------------------------------------------------------------- tcgen05
+
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                          bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+// 32 consecutive columns of this warp's 32 TMEM lanes: one row piece per thread.
+__device__ __forceinline__ void tc_ld32(uint32_t (&r)[32], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// Ties later uses of loaded registers to the wait before it.
+__device__ __forceinline__ void tc_loaded(uint32_t (&r)[32]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+  asm volatile(""
+               : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
+                 "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+__device__ __forceinline__ void tc_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Shared-memory operand with the 128-byte swizzle: rows of 128 bytes, 8-row groups of 1 KiB.
+// `lead` is the distance of the 64-element blocks of an operand whose rows run along K (V); it
+// is not used by operands whose rows hold K (Q, K).
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lead) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3fff) |
+         static_cast<uint64_t>((lead >> 4) & 0x3fff) << 16 |
+         static_cast<uint64_t>(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// bf16 x bf16 -> fp32, 128 x n; `b_rows_k`: B's rows run along K.
+constexpr uint32_t tc_idesc(int n, bool b_rows_k) {
+  return 1u << 4 | 1u << 7 | 1u << 10 | (b_rows_k ? 1u << 16 : 0u) |
+         static_cast<uint32_t>(n >> 3) << 17 | 8u << 24;
+}
+
+// Waits for a phase; gives up after the limit or once any warp has (the block then drains).
+__device__ __forceinline__ bool wait_or_abort(TcShared& s, uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t start = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (s.abort) return false;
+    if (global_timer_ns() - start > kWaitLimitNs) {
+      s.abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+// ---------------------------------------------------------------- work line
+
+// sum over i < n of floor((a i + b) / m)
+__device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+  int64_t sum = 0;
+  while (n > 0) {
+    sum += static_cast<int64_t>(n) * (n - 1) / 2 * (a / m) + static_cast<int64_t>(n) * (b / m);
+    a %= m;
+    b %= m;
+    const uint32_t top = a * n + b;
+    if (top < m) break;
+    n = top / m;
+    b = top % m;
+    const uint32_t t = m;
+    m = a;
+    a = t;
+  }
+  return sum;
+}
+
+struct Seq {
+  int first, n, ctx;         // first token row, new tokens, cached tokens before them
+};
+// Sequence b's chunk; n = 0 if it has none or must be skipped (*bad).
+__device__ __forceinline__ Seq load_seq(const ChunkParams& p, int b, bool* bad) {
+  const int64_t c0 = p.cu_q[b], c1 = p.cu_q[b + 1], len = p.seq_lens[b];
+  Seq s = {0, 0, 0};
+  *bad = c0 < 0 || c1 < c0 || c1 > p.num_tokens ||
+         (c1 > c0 && (len < c1 - c0 || len > static_cast<int64_t>(p.max_teams) * p.team_size));
+  if (!*bad) {
+    s.first = static_cast<int>(c0);
+    s.n = static_cast<int>(c1 - c0);
+    s.ctx = static_cast<int>(len) - s.n;
+  }
+  return s;
+}
+// Steps of the items 0 .. i - 1 (all of them with full token counts) of a sequence.
+__device__ __forceinline__ int64_t steps_before(const Seq& s, int tpi, int i) {
+  return floor_sum(i, kStep, tpi, s.ctx + tpi + kStep - 1);
+}
+__device__ __forceinline__ int item_steps(const Seq& s, int tpi, int i) {
+  return (s.ctx + min(s.n, (i + 1) * tpi) + kStep - 1) / kStep;
+}
+__device__ __forceinline__ int64_t seq_steps(const Seq& s, int tpi) {
+  if (s.n == 0) return 0;
+  const int items = (s.n + tpi - 1) / tpi;
+  return steps_before(s, tpi, items - 1) + (s.ctx + s.n + kStep - 1) / kStep;
+}
+
+// Where the line's step `pos` lies, by one warp: sequence, head, item, step.
+__device__ void find_step(const ChunkParams& p, int tpi, int64_t pos, int* out) {
+  const int lane = threadIdx.x & 31;
+  int64_t before = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += 32) {
+    bool bad;
+    const Seq s = b0 + lane < p.batch ? load_seq(p, b0 + lane, &bad) : Seq{0, 0, 0};
+    const int64_t mine = seq_steps(s, tpi) * p.num_kv_heads;
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const unsigned over = __ballot_sync(0xffffffffu, before + incl > pos);
+    if (over) {
+      const int at = __ffs(over) - 1;
+      const int64_t start = before + __shfl_sync(0xffffffffu, incl - mine, at);
+      const int64_t per_head = __shfl_sync(0xffffffffu, mine, at) / p.num_kv_heads;
+      Seq q;
+      q.first = 0;
+      q.n = __shfl_sync(0xffffffffu, s.n, at);
+      q.ctx = __shfl_sync(0xffffffffu, s.ctx, at);
+      const int h = static_cast<int>((pos - start) / per_head);
+      const int64_t rem = (pos - start) - h * per_head;
+      // the last item i with steps_before(i) <= rem
+      int lo = 0, hi = (q.n + tpi - 1) / tpi;
+      while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32;
+        const int i = lo + lane * step;
+        const bool below = lane == 0 || (i < hi && steps_before(q, tpi, i) <= rem);
+        const unsigned m = __ballot_sync(0xffffffffu, below);
+        lo += (31 - __clz(m)) * step;
+        hi = min(hi, lo + step);
+      }
+      out[0] = b0 + at;
+      out[1] = h;
+      out[2] = lo;
+      out[3] = static_cast<int>(rem - steps_before(q, tpi, lo));
+      return;
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  out[0] = p.batch;
+  out[1] = out[2] = out[3] = 0;
+}
+
+// One run of steps of one item, and the walk from run to run.
+struct Run {
+  int b, h, item, s0, s1, steps;
+  Seq seq;
+  int64_t left;
+  bool got;
+  __device__ __forceinline__ void begin(const TcShared& s, const ChunkParams& p) {
+    b = s.start[0];
+    h = s.start[1];
+    item = s.start[2];
+    s0 = s.start[3];
+    left = s.left;
+    got = left > 0;
+    bool bad;
+    if (got) seq = load_seq(p, b, &bad);
+  }
+  // Sets s1 and steps; false at the end of the block's range.
+  __device__ __forceinline__ bool open(int tpi) {
+    if (!got) return false;
+    steps = item_steps(seq, tpi, item);
+    s1 = static_cast<int>(min(static_cast<int64_t>(steps), s0 + left));
+    return true;
+  }
+  __device__ __forceinline__ void next(const ChunkParams& p, int tpi) {
+    left -= s1 - s0;
+    got = left > 0;
+    if (!got) return;
+    s0 = 0;                                     // more is left: the item was finished
+    if (static_cast<int64_t>(++item) * tpi < seq.n) return;
+    item = 0;
+    if (++h < p.num_kv_heads) return;
+    h = 0;
+    bool bad;
+    do seq = load_seq(p, ++b, &bad);            // left > 0: a later sequence has steps
+    while (seq.n == 0);
+  }
+};
+
+// ---------------------------------------------------------------- roles
+
+template <int D>
+__device__ void copy_role(const TcParams& t, TcShared& s, unsigned char* q_smem,
+                          unsigned char* ring) {
+  using C = TcCfg<D>;
+  const ChunkParams& p = t.c;
+  const int lane = threadIdx.x & 31, tpi = 2 * t.tpt, G = p.num_q_heads / p.num_kv_heads;
+  const int T = p.team_size;
+  uint32_t stage = 0, empty_parity = 1, q_parity = 1, land_parity = 0;
+  uint32_t issued = 0, runs = 0;                 // stages and Q ever filled (for the drain)
+  Run r;
+  r.begin(s, p);
+  bool ok = true;
+  for (int turn = 0; ok && r.open(tpi); r.next(p, tpi), turn = turn == 2 ? 0 : turn + 1) {
+    const int tok = r.item * tpi;
+    const bool two = tok + t.tpt < r.seq.n;
+    ok = wait_or_abort(s, &s.q_empty, q_parity);
+    q_parity ^= 1;
+    if (!ok) break;
+    if (lane < 16) s.noted[turn][lane / 4][lane % 4] = 0u;
+    if (lane == 0) {
+      const uint32_t box = t.tpt * G * 128;      // bytes of one 64-element wide box
+      mbar_arrive_expect_tx(&s.q_full, box * C::kHalves * (two ? 2 : 1));
+      for (int x = 0; x < (two ? 2 : 1); ++x)
+        for (int i = 0; i < C::kHalves; ++i)
+          asm volatile(
+              "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+              " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+                  smem_u32(q_smem + x * C::kTileBytes + i * 16384)),
+              "l"(reinterpret_cast<uint64_t>(&t.tmap_q)), "r"(i * 64), "r"(0), "r"(r.h),
+              "r"(r.seq.first + tok + x * t.tpt), "r"(smem_u32(&s.q_full))
+              : "memory");
+    }
+    ++runs;
+    const int len = r.seq.ctx + r.seq.n;
+    const int seen = r.seq.ctx + min(r.seq.n, tok + tpi);   // keys that some row sees
+    const int all_see = r.seq.ctx + tok + 1;                // keys that every row sees
+    const int teams = (len + T - 1) / T;
+    int window = -1, ids = 0;
+    for (int j = r.s0; ok && j < r.s1; ++j) {
+      // page ids of 32 teams at a time, one per lane
+      int row[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int at = j * kStep + c * 64;
+        row[c] = -1;
+        if (at >= len) continue;
+        const int team = at / T;
+        if (window < 0 || team >= window + 32) {
+          window = team;
+          ids = 0;
+          if (team + lane < teams) {
+            ids = p.page_table[static_cast<int64_t>(r.b) * p.max_teams + team + lane];
+            if (ids < 0 || ids >= p.num_pages) {
+              set_status(p.status, SANTA_DEV_BAD_PAGE);
+              ids = 0;
+            }
+          }
+        }
+        const int page = __shfl_sync(0xffffffffu, ids, team - window);
+        row[c] = (page * p.num_kv_heads + r.h) * T + at % T;
+      }
+      const uint32_t bytes = (row[1] >= 0 ? 2 : 1) * 64 * D * 2;
+      for (int kv = 0; ok && kv < 2; ++kv) {     // K, then V
+        unsigned char* dst = ring + stage * C::kTileBytes;
+        const bool check = kv == 1 && (j + 1) * kStep > all_see;
+        ok = wait_or_abort(s, &s.kv_empty[stage], empty_parity);
+        if (!ok) break;
+        uint64_t* bar = check ? &s.land : &s.kv_full[stage];
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, bytes);
+          for (int c = 0; c < 2; ++c)
+            if (row[c] >= 0)
+              for (int i = 0; i < C::kHalves; ++i)
+                tma_load_2d(dst + i * 16384 + c * 8192, kv ? &t.tmap_v : &t.tmap_k, i * 64,
+                            row[c], bar);
+        }
+        if (check) {
+          ok = wait_or_abort(s, &s.land, land_parity);
+          land_parity ^= 1;
+          if (!ok) break;
+          // rows [lo, hi) are seen by some rows of the item only, rows from hi on by none;
+          // a row is 128 bytes in each half, in some order of its 16-byte pieces
+          const int lo = max(0, all_see - j * kStep), hi = min(kStep, seen - j * kStep);
+          for (int i = lane; i < (kStep - lo) * 8 * C::kHalves; i += 32) {
+            const int row_at = lo + i / (8 * C::kHalves), piece = i % (8 * C::kHalves);
+            uint4* w = reinterpret_cast<uint4*>(dst + (piece / 8) * 16384 + row_at * 128 +
+                                                (piece % 8) * 16);
+            if (row_at >= hi) {
+              *w = make_uint4(0u, 0u, 0u, 0u);
+              continue;
+            }
+            uint4 v = *w;
+            const uint32_t e = 0x7f807f80u;      // all exponent bits: infinite or NaN
+            const uint32_t bx = __vcmpeq2(v.x & e, e), by = __vcmpeq2(v.y & e, e);
+            const uint32_t bz = __vcmpeq2(v.z & e, e), bw = __vcmpeq2(v.w & e, e);
+            if (bx | by | bz | bw) {
+              *w = make_uint4(v.x & ~bx, v.y & ~by, v.z & ~bz, v.w & ~bw);
+              atomicOr(&s.noted[turn][j - r.steps + 4][row_at / 32], 1u << (row_at % 32));
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.kv_full[stage]);
+        }
+        if (++issued, ++stage == C::kStages) {
+          stage = 0;
+          empty_parity ^= 1;
+        }
+      }
+    }
+  }
+  if (!ok) {
+    // drain: every copy that was issued lands before the block may end (bounded)
+    if (lane == 0) {
+      const uint64_t start = global_timer_ns();
+      while (runs && !mbar_try_wait(&s.q_full, (runs - 1) & 1) &&
+             global_timer_ns() - start < kWaitLimitNs) {
+      }
+      for (uint32_t i = 0; i < C::kStages && i < issued; ++i) {
+        const uint32_t k = (issued - 1 - i) / C::kStages, st = (issued - 1 - i) % C::kStages;
+        while (!mbar_try_wait(&s.kv_full[st], k & 1) &&
+               global_timer_ns() - start < kWaitLimitNs) {
+        }
+      }
+    }
+  }
+}
+
+template <int D>
+__device__ void mma_role(const TcParams& t, TcShared& s, uint32_t q_smem, uint32_t ring) {
+  using C = TcCfg<D>;
+  const ChunkParams& p = t.c;
+  const int tpi = 2 * t.tpt;
+  constexpr uint32_t kIdS = tc_idesc(kStep, false), kIdO = tc_idesc(D, true);
+  const uint32_t tmem = s.tmem;
+  uint32_t stage = 0, full_parity = 0, q_parity = 0, p_parity[2] = {0, 0};
+  Run r;
+  r.begin(s, p);
+  auto advance = [&] {
+    if (++stage == C::kStages) {
+      stage = 0;
+      full_parity ^= 1;
+    }
+  };
+  auto scores = [&](int x, uint32_t k_addr) {       // S_x = Q_x K^T
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
+      tc_mma_ss(tmem + C::kColS + 128 * x, tc_desc(q_smem + x * C::kTileBytes + off, 16),
+                tc_desc(k_addr + off, 16), kIdS, k > 0);
+    }
+    tc_commit(&s.s_full[x]);
+  };
+  for (; r.open(tpi); r.next(p, tpi)) {
+    const bool two = r.item * tpi + t.tpt < r.seq.n;
+    if (!wait_or_abort(s, &s.q_full, q_parity)) return;
+    q_parity ^= 1;
+    if (!wait_or_abort(s, &s.kv_full[stage], full_parity)) return;
+    tc_fence_after();
+    uint32_t k_addr = ring + stage * C::kTileBytes;
+    scores(0, k_addr);
+    if (two) scores(1, k_addr);
+    tc_commit(&s.kv_empty[stage]);
+    advance();
+    if (r.s1 - r.s0 == 1) tc_commit(&s.q_empty);
+    for (int j = r.s0; j < r.s1; ++j) {
+      const bool last = j + 1 == r.s1;
+      const uint32_t v_stage = stage;
+      if (!wait_or_abort(s, &s.kv_full[stage], full_parity)) return;
+      advance();
+      const uint32_t k_stage = stage;
+      if (!last) {
+        if (!wait_or_abort(s, &s.kv_full[stage], full_parity)) return;
+        advance();
+      }
+      const uint32_t v_addr = ring + v_stage * C::kTileBytes;
+      k_addr = ring + k_stage * C::kTileBytes;
+      for (int x = 0; x < (two ? 2 : 1); ++x) {
+        if (!wait_or_abort(s, &s.p_ready[x], p_parity[x])) return;
+        p_parity[x] ^= 1;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < kStep / 16; ++k)          // O_x += P_x V
+          tc_mma_ts(tmem + C::kColO + D * x, tmem + C::kColS + 128 * x + 8 * k,
+                    tc_desc(v_addr + 2048 * k, 16384), kIdO, j > r.s0 || k > 0);
+        if (last)
+          tc_commit(&s.o_full[x]);
+        else
+          scores(x, k_addr);
+      }
+      tc_commit(&s.kv_empty[v_stage]);
+      if (!last) {
+        tc_commit(&s.kv_empty[k_stage]);
+        if (j + 2 == r.s1) tc_commit(&s.q_empty);
+      }
+    }
+  }
+}
+
+// Products of noted V elements (see the top of the file) that this row sees, added to 32 of
+// its accumulators.
+template <int D>
+__device__ __noinline__ void add_noted(const TcParams& t, const Run& r, const uint32_t (*noted)[4],
+                                       int sees, int64_t q_row, float m, int col0, float* o) {
+  const ChunkParams& p = t.c;
+  const uint16_t* q = static_cast<const uint16_t*>(p.q) + q_row;
+  for (int e = 0; e < 4; ++e)
+    for (int w = 0; w < 4; ++w)
+      for (uint32_t bits = noted[e][w]; bits; bits &= bits - 1) {
+        const int tok = (r.steps - 4 + e) * kStep + w * 32 + __ffs(bits) - 1;
+        if (tok >= sees) continue;
+        int64_t page = p.page_table[static_cast<int64_t>(r.b) * p.max_teams + tok / p.team_size];
+        if (page < 0 || page >= p.num_pages) page = 0;
+        const int64_t row =
+            ((page * p.num_kv_heads + r.h) * p.team_size + tok % p.team_size) * D;
+        const uint16_t* k = static_cast<const uint16_t*>(p.k_pool) + row;
+        const uint16_t* v = static_cast<const uint16_t*>(p.v_pool) + row;
+        float dot = 0.f;
+        for (int i = 0; i < D; ++i) dot = fmaf(bf16_to_f32(q[i]), bf16_to_f32(k[i]), dot);
+        const float w32 = ex2_approx(fmaf(dot, p.scale_log2, -m));
+        const float weight = bf16_lo_f(pack_bf16(w32, 0.f));
+        for (int i = 0; i < 32; ++i)
+          if ((v[col0 + i] & 0x7f80) == 0x7f80) o[i] = fmaf(weight, bf16_to_f32(v[col0 + i]), o[i]);
+      }
+}
+
+template <int D>
+__device__ void softmax_role(const TcParams& t, TcShared& s) {
+  using C = TcCfg<D>;
+  const ChunkParams& p = t.c;
+  const int x = threadIdx.x / 128, row = threadIdx.x % 128, warp = (threadIdx.x / 32) % 4;
+  const int tpi = 2 * t.tpt, G = p.num_q_heads / p.num_kv_heads;
+  const int g = row % G, token_in_tile = row / G;
+  const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+  const uint32_t tm_s = s.tmem + C::kColS + 128 * x + lanes;
+  const uint32_t tm_o = s.tmem + C::kColO + D * x + lanes;
+  const float scale = p.scale_log2;
+  uint32_t s_parity = 0, o_parity = 0;
+  Run r;
+  r.begin(s, p);
+  for (int turn = 0; r.open(tpi); r.next(p, tpi), turn = turn == 2 ? 0 : turn + 1) {
+    const int tok0 = r.item * tpi + x * t.tpt;           // first token of this tile
+    if (tok0 >= r.seq.n) continue;
+    const int tok = tok0 + token_in_tile;
+    const bool mine = token_in_tile < t.tpt && tok < r.seq.n;
+    const int sees = mine ? r.seq.ctx + tok + 1 : 0;
+    const int all_see = r.seq.ctx + tok0 + 1;
+    const bool warp_idle = __ballot_sync(0xffffffffu, mine) == 0u;
+    float m = -INFINITY, l = 0.f;
+    for (int j = r.s0; j < r.s1; ++j) {
+      if (!wait_or_abort(s, &s.s_full[x], s_parity)) return;
+      s_parity ^= 1;
+      if (!warp_idle) {
+        tc_fence_after();
+        uint32_t sc[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc_ld32(sc[c], tm_s + 32 * c);
+        tc_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc_loaded(sc[c]);
+        if ((j + 1) * kStep > all_see) {
+          const int cut = sees - j * kStep;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c * 32 + e >= cut) sc[c][e] = 0xff800000u;   // -inf
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mx[c] = __uint_as_float(sc[c][0]);
+#pragma unroll
+          for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(sc[c][e]));
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+        // grown past the slack (or the first finite score): a new reference
+        const bool grow = top > m + kSlack || (m == -INFINITY && top > -INFINITY);
+        if (__any_sync(0xffffffffu, grow)) {
+          const float old = m;
+          if (grow) m = top;
+          if (j > r.s0) {
+            const float keep = grow ? ex2_approx(old - m) : 1.f;
+            l *= keep;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tc_ld32(o, tm_o + 32 * c);
+              tc_wait_ld();
+              tc_loaded(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+              tc_st32(tm_o + 32 * c, o);
+            }
+          }
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float a = ex2_approx(
+                fmaf(__uint_as_float(sc[half * 2 + e / 16][(2 * e) % 32]), scale, -ref));
+            const float b = ex2_approx(
+                fmaf(__uint_as_float(sc[half * 2 + e / 16][(2 * e) % 32 + 1]), scale, -ref));
+            sum[0] += a;
+            sum[1] += b;
+            pk[e] = pack_bf16(a, b);
+          }
+          tc_st32(tm_s + 32 * half, pk);
+        }
+        l += sum[0] + sum[1];
+        tc_wait_st();
+        tc_fence_before();
+      }
+      mbar_arrive(&s.p_ready[x]);
+    }
+    // ---- epilogue: the row, or its partial result
+    if (!wait_or_abort(s, &s.o_full[x], o_parity)) return;
+    o_parity ^= 1;
+    if (warp_idle) continue;
+    tc_fence_after();
+    const bool whole = r.s0 == 0 && r.s1 == r.steps;
+    const int64_t out_row =
+        (static_cast<int64_t>(r.seq.first + tok) * p.num_q_heads + r.h * G + g) * D;
+    bool noted = false;
+    if ((r.s1) * kStep > all_see)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) noted |= s.noted[turn][e / 4][e % 4] != 0u;
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (r.s0 > 0 ? 0 : 1)) * 256 +
+                         x * 128 + row;
+    if (!whole && mine) {
+      t.part_ml[2 * part] = m;
+      t.part_ml[2 * part + 1] = l;
+    }
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t o[32];
+      __syncwarp();
+      tc_ld32(o, tm_o + 32 * c);
+      tc_wait_ld();
+      tc_loaded(o);
+      if (mine) {
+        float f[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]);
+        if (noted)
+          add_noted<D>(t, r, s.noted[turn], sees, out_row, m == -INFINITY ? 0.f : m, 32 * c, f);
+        if (whole) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + out_row + 32 * c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            dst[e] = make_uint4(pack_bf16(f[8 * e] * inv, f[8 * e + 1] * inv),
+                                pack_bf16(f[8 * e + 2] * inv, f[8 * e + 3] * inv),
+                                pack_bf16(f[8 * e + 4] * inv, f[8 * e + 5] * inv),
+                                pack_bf16(f[8 * e + 6] * inv, f[8 * e + 7] * inv));
+        } else {
+          float4* dst = reinterpret_cast<float4*>(t.part_acc + part * D + 32 * c);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            dst[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+        }
+      }
+    }
+    __syncwarp();
+    tc_fence_before();
+  }
+}
+
+// The copying warp's work, then what the join needs to know of an item that starts in this
+// block and ends in a later one.
+template <int D>
+__device__ void run_copies(const TcParams& t, TcShared& s, unsigned char* q_smem,
+                           unsigned char* ring) {
+  const ChunkParams& p = t.c;
+  const int tpi = 2 * t.tpt;
+  copy_role<D>(t, s, q_smem, ring);
+  Run r;
+  r.begin(s, p);
+  int64_t pos = s.begin;
+  int parts = 0, first = 0, n = 0, item = 0, h = 0;
+  if (!s.abort)
+    for (; r.open(tpi); r.next(p, tpi)) {
+      if (r.s0 == 0 && r.s1 < r.steps) {
+        const int64_t stop = pos + r.steps;      // the item's end on the line
+        parts = 1;
+        for (int64_t c = blockIdx.x + 1; c < s.blocks && s.total * c / s.blocks < stop; ++c)
+          ++parts;
+        first = r.seq.first;
+        n = r.seq.n;
+        item = r.item;
+        h = r.h;
+      }
+      pos += r.s1 - r.s0;
+    }
+  if ((threadIdx.x & 31) == 0) {
+    int32_t* j = t.join + blockIdx.x * 8;
+    j[0] = parts;
+    j[1] = first;
+    j[2] = n;
+    j[3] = item;
+    j[4] = h;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    chunk_tc_kernel(const __grid_constant__ TcParams t) {
+  using C = TcCfg<D>;
+  extern __shared__ unsigned char raw[];
+  __shared__ TcShared s;
+  const ChunkParams& p = t.c;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  unsigned char* base =
+      raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);    // operand tiles: 1 KiB aligned
+  unsigned char* q_smem = base;
+  unsigned char* ring = base + 2 * C::kTileBytes;
+  if (threadIdx.x == 0) {
+    mbar_init(&s.q_full, 1);
+    mbar_init(&s.q_empty, 1);
+    mbar_init(&s.land, 1);
+    mbar_init(&s.drain, 1);
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&s.kv_full[i], 1);
+      mbar_init(&s.kv_empty[i], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&s.s_full[x], 1);
+      mbar_init(&s.p_ready[x], 128);
+      mbar_init(&s.o_full[x], 1);
+    }
+    s.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_u32(&s.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (warp == 9 && lane == 0) {
+    prefetch_tensormap(&t.tmap_q);
+    prefetch_tensormap(&t.tmap_k);
+    prefetch_tensormap(&t.tmap_v);
+  }
+  grid_dependency_wait();
+  const int tpi = 2 * t.tpt;
+  if (warp == 0) {
+    // the length of the line, then this block's part of it
+    int64_t total = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      bool bad = false;
+      const Seq q = b0 + lane < p.batch ? load_seq(p, b0 + lane, &bad) : Seq{0, 0, 0};
+      if (bad && blockIdx.x == 0) set_status(p.status, SANTA_DEV_BAD_SEQLEN);
+      int64_t v = seq_steps(q, tpi) * p.num_kv_heads;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      total += v;
+    }
+    const int64_t blocks =
+        max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), total / kMinSteps));
+    const int64_t c = blockIdx.x;
+    const int64_t begin = c < blocks ? total * c / blocks : total;
+    const int64_t end = c < blocks ? total * (c + 1) / blocks : total;
+    int start[4] = {p.batch, 0, 0, 0};
+    if (begin < end) find_step(p, tpi, begin, start);
+    if (lane == 0) {
+      for (int i = 0; i < 4; ++i) s.start[i] = start[i];
+      s.left = end - begin;
+      s.begin = begin;
+      s.total = total;
+      s.blocks = static_cast<int>(blocks);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_launch_dependents();
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    softmax_role<D>(t, s);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    if (warp == 8) {
+      if (lane == 0) {
+        mma_role<D>(t, s, smem_u32(q_smem), smem_u32(ring));
+        if (s.abort) {                           // no product is in flight when TMEM is freed
+          tc_commit(&s.drain);
+          const uint64_t begin = global_timer_ns();
+          while (!mbar_try_wait(&s.drain, 0) && global_timer_ns() - begin < kWaitLimitNs) {
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == 9) {
+      run_copies<D>(t, s, q_smem, ring);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && s.abort) set_status(p.status, SANTA_DEV_TIMEOUT);
+  if (warp == 8) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(s.tmem));
+  }
+}
+
+// Joins the partial results of the items that several blocks shared: block (c, i) takes some
+// rows of the item that starts in block c, one warp per row, its parts in the line's order.
+template <int D>
+__global__ void __launch_bounds__(256) chunk_tc_join_kernel(ChunkParams p, int tpt,
+                                                            const float* part_acc,
+                                                            const float* part_ml,
+                                                            const int32_t* join, int num_blocks) {
+  grid_dependency_wait();
+  const int c0 = blockIdx.x;
+  const int32_t* j = join + c0 * 8;
+  const int parts = j[0];
+  if (parts < 2 || c0 + parts > num_blocks) return;
+  const int first = j[1], n = j[2], item = j[3], h = j[4];
+  const int G = p.num_q_heads / p.num_kv_heads, lane = threadIdx.x & 31;
+  constexpr int kVals = D / 32;
+  for (int row = blockIdx.y * 8 + threadIdx.x / 32; row < 256; row += gridDim.y * 8) {
+    const int x = row / 128, in_tile = (row % 128) / G;
+    const int tok = item * 2 * tpt + x * tpt + in_tile;
+    if (in_tile >= tpt || tok >= n) continue;
+    // part 0 is the second partial of block c0, part i the first one of block c0 + i
+    auto at = [&](int i) {
+      return (static_cast<int64_t>(c0 + i) * 2 + (i == 0 ? 1 : 0)) * 256 + row;
+    };
+    float m = -INFINITY;
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldg(part_ml + 2 * at(i)));
+    m = warp_max(m);
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f, acc[kVals];
+#pragma unroll
+    for (int e = 0; e < kVals; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+      const int64_t a = at(i);
+      const float2 ml = __ldg(reinterpret_cast<const float2*>(part_ml) + a);
+      const float w = ex2_approx(ml.x - ref);
+      l = fmaf(w, ml.y, l);
+      const float* src = part_acc + a * D + lane * kVals;
+#pragma unroll
+      for (int e = 0; e < kVals; e += 2) {
+        const float2 v = __ldg(reinterpret_cast<const float2*>(src + e));
+        acc[e] = fmaf(w, v.x, acc[e]);
+        acc[e + 1] = fmaf(w, v.y, acc[e + 1]);
+      }
+    }
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(
+        static_cast<uint16_t*>(p.out) +
+        (static_cast<int64_t>(first + tok) * p.num_q_heads + h * G + (row % 128) % G) * D +
+        lane * kVals);
+#pragma unroll
+    for (int e = 0; e < kVals; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+  }
+}
+
+// Blocks that the line is shared out to: one per SM, and no more than the longest possible line
+// (known from the shape alone) has pieces of kMinSteps.
+int tc_blocks(int64_t num_tokens, int batch, int group, int hkv, int64_t max_len, int sms) {
+  const int64_t tpi = 2 * (128 / group);
+  const int64_t items = (num_tokens + tpi - 1) / tpi + batch;
+  const int64_t steps = (max_len + kStep - 1) / kStep;
+  const int64_t most = std::max<int64_t>(1, items * hkv * steps / kMinSteps);
+  return static_cast<int>(std::min<int64_t>(sms, most));
+}
+
+struct TcLayout {
+  size_t acc, ml, join, bytes;
+};
+TcLayout tc_layout(int blocks, int d) {
+  TcLayout l;
+  l.acc = 0;
+  l.ml = static_cast<size_t>(blocks) * 512 * d * sizeof(float);
+  l.join = l.ml + static_cast<size_t>(blocks) * 512 * 2 * sizeof(float);
+  l.bytes = l.join + static_cast<size_t>(blocks) * 8 * sizeof(int32_t);
+  return l;
+}
+
+template <int D>
+cudaError_t launch(const TcParams& t, int blocks, cudaStream_t stream) {
+  using C = TcCfg<D>;
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = ensure_dynamic_smem(chunk_tc_kernel<D>, C::kSmem, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, chunk_tc_kernel<D>, t);
+  if (e != cudaSuccess || blocks == 1) return e;
+  cfg.gridDim = dim3(blocks, 16);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, chunk_tc_join_kernel<D>, t.c, t.tpt,
+                            static_cast<const float*>(t.part_acc),
+                            static_cast<const float*>(t.part_ml),
+                            static_cast<const int32_t*>(t.join), blocks);
+}
+
+}  // namespace
+
+size_t chunk_tc_workspace(int64_t num_tokens, int batch, int group, int hkv, int d,
+                          int64_t max_len, int sms) {
+  return tc_layout(tc_blocks(num_tokens, batch, group, hkv, max_len, sms), d).bytes;
+}
+
+int launch_chunk_tc(const ChunkParams& p, int d, void* workspace, int sms, cudaStream_t stream) {
+  const int G = p.num_q_heads / p.num_kv_heads;
+  const int64_t rows = p.num_pages * p.num_kv_heads * static_cast<int64_t>(p.team_size);
+  if (rows > 0x7fffffffll) return SANTA_ERR_UNSUPPORTED;       // 32-bit row coordinates
+  TcParams t = {};
+  t.c = p;
+  t.tpt = 128 / G;
+  int rc = pool_tensor_map(&t.tmap_k, p.k_pool, rows, d);
+  if (rc || (rc = pool_tensor_map(&t.tmap_v, p.v_pool, rows, d))) return rc;
+  // queries [token][KV head][head of the group][d]: a box is one tile's rows, 64 elements wide
+  TensorMapEncode encode = tensor_map_encode();
+  if (!encode) return SANTA_ERR_CUDA;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(G),
+                              static_cast<cuuint64_t>(p.num_kv_heads),
+                              static_cast<cuuint64_t>(p.num_tokens)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 2,
+                                 static_cast<cuuint64_t>(G) * d * 2,
+                                 static_cast<cuuint64_t>(p.num_q_heads) * d * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(G), 1, static_cast<cuuint32_t>(t.tpt)};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  if (encode(&t.tmap_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p.q), dims,
+             strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return SANTA_ERR_CUDA;
+  const int blocks = tc_blocks(p.num_tokens, p.batch, G, p.num_kv_heads,
+                               static_cast<int64_t>(p.max_teams) * p.team_size, sms);
+  const TcLayout l = tc_layout(blocks, d);
+  unsigned char* base = static_cast<unsigned char*>(workspace);
+  t.part_acc = reinterpret_cast<float*>(base + l.acc);
+  t.part_ml = reinterpret_cast<float*>(base + l.ml);
+  t.join = reinterpret_cast<int32_t*>(base + l.join);
+  const cudaError_t e = d == 128 ? launch<128>(t, blocks, stream) : launch<64>(t, blocks, stream);
+  return e == cudaSuccess ? SANTA_OK : SANTA_ERR_CUDA;
+}
+
+}  // namespace santa

@@ -134,12 +134,18 @@ struct ChunkParams {
   void* out;                  // [num_tokens][Hq][d]
   int32_t* status;
 };
-// The plain-arithmetic form: 64-row tiles, `splits` blocks share a tile's keys; partials
+// The fp32 form: 64-row tiles, `splits` blocks share a tile's keys; partials
 // [tiles][splits][64][d] and (m, l) [tiles][splits][64][2] fp32 when splits > 1.
 int64_t chunk_simt_tiles(int64_t num_tokens, int batch, int group, int num_kv_heads);
 int chunk_simt_splits(int64_t tiles, int64_t max_len, int sms);
-cudaError_t launch_chunk_simt(const ChunkParams& p, int head_dim, bool bf16, int splits,
-                              float* part_acc, float* part_ml, cudaStream_t stream);
+cudaError_t launch_chunk_simt(const ChunkParams& p, int head_dim, int splits, float* part_acc,
+                              float* part_ml, cudaStream_t stream);
+
+// The tensor-core form (bf16): bytes of its workspace (256-byte aligned base), and the launch,
+// which returns a santa_status.
+size_t chunk_tc_workspace(int64_t num_tokens, int batch, int group, int hkv, int d,
+                          int64_t max_len, int sms);
+int launch_chunk_tc(const ChunkParams& p, int d, void* workspace, int sms, cudaStream_t stream);
 
 // ---------------------------------------------------------------- host slabs of santa_decode_host
 // bytes / 16 words from src to dst (both 16-byte aligned; one of them host memory mapped into

@@ -37,7 +37,7 @@ constexpr int kTcThreads = 384;          // three warpgroups: softmax A, softmax
 constexpr int kSoftmaxRegs = 208;         // registers per thread: 2 * 208 + 88 = 3 * 168, what
 constexpr int kIssueRegs = 88;            // 384 threads are launched with
 constexpr int kStep = 128;                 // keys per step
-constexpr int kMinSteps = 4;               // steps a block takes at least
+constexpr int kSnap = 6;                   // steps a border may move to an item's end
 constexpr float kSlack = 8.f;              // growth of a row's maximum that triggers a rescale
 
 template <int D>
@@ -52,7 +52,7 @@ struct TcCfg {
 struct TcParams {
   ChunkParams c;
   int tpt;                   // tokens per 128-row tile
-  float* part_acc;           // [N][2][256][D]
+  float* part_acc;           // [N][2][D / 4][256][4]
   float* part_ml;            // [N][2][256][2]
   int32_t* join;             // [N][8]
   CUtensorMap tmap_q, tmap_k, tmap_v;
@@ -64,10 +64,9 @@ struct TcShared {
   uint64_t s_full[2], p_ready[2], o_full[2];
   uint32_t tmem;
   volatile int abort;
-  int start[4];              // b, h, tile, step of the block's first step
-  int64_t left, total;       // the block's steps, all steps
-  int64_t begin;
-  int blocks;                // blocks with work
+  int start[4];              // b, h, item, step of the block's first step
+  int64_t total, begin, end; // all steps; the block's first step and the one behind its last
+  int blocks, snap;          // blocks with work; see line_border
   uint32_t noted[3][4][4];   // [item ring][step of the last four][token bits]
 };
 
@@ -144,12 +143,16 @@ __device__ __forceinline__ void tc_wait_st() {
 }
 
 // Shared-memory operand with the 128-byte swizzle: rows of 128 bytes, 8-row groups of 1 KiB.
-// `lead` is the distance of the 64-element blocks of an operand whose rows run along K (V); it
-// is not used by operands whose rows hold K (Q, K).
-__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lead) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3fff) |
-         static_cast<uint64_t>((lead >> 4) & 0x3fff) << 16 |
-         static_cast<uint64_t>(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+// The low word holds the address and `lead`, the distance of the 64-element blocks of an operand
+// whose rows run along K (V; not used by operands whose rows hold K: Q, K).  The high word is a
+// constant, and an address step is one 32-bit addition (16-byte units; no carry: addresses stay
+// below 2^18).
+__device__ __forceinline__ uint32_t tc_desc_lo(uint32_t addr, uint32_t lead) {
+  return ((addr >> 4) & 0x3fff) | ((lead >> 4) & 0x3fff) << 16;
+}
+__device__ __forceinline__ uint64_t tc_desc(uint32_t lo) {
+  constexpr uint64_t hi = (1024 >> 4) | 1u << 14 | 2u << 29;
+  return hi << 32 | lo;
 }
 // bf16 x bf16 -> fp32, 128 x n; `b_rows_k`: B's rows run along K.
 constexpr uint32_t tc_idesc(int n, bool b_rows_k) {
@@ -169,6 +172,31 @@ __device__ __forceinline__ bool wait_or_abort(TcShared& s, uint64_t* bar, uint32
     }
   }
   return true;
+}
+
+// Two fp32 values in a register pair, and the instructions that work on both.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float* a, float* b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 // ---------------------------------------------------------------- work line
@@ -267,6 +295,27 @@ __device__ void find_step(const ChunkParams& p, int tpi, int64_t pos, int* out) 
   out[1] = out[2] = out[3] = 0;
 }
 
+// Border c of the line (the first step of block c): total * c / blocks, moved to the next item's
+// border if that is at most `snap` steps away, which saves a join for a little unevenness.  The
+// moves keep the borders in order.  By one warp; `out` as in find_step.
+__device__ int64_t line_border(const ChunkParams& p, int tpi, int64_t total, int blocks, int snap,
+                               int c, int* out) {
+  const int64_t pos = total * c / blocks;
+  if (pos >= total) return total;
+  find_step(p, tpi, pos, out);
+  bool bad;
+  const Seq q = load_seq(p, out[0], &bad);
+  const int step = out[3], steps = item_steps(q, tpi, out[2]);
+  if (step <= snap) {
+    out[3] = 0;
+    return pos - step;
+  }
+  if (steps - step > snap) return pos;
+  const int64_t next = pos + steps - step;         // the next item's first step
+  if (next < total) find_step(p, tpi, next, out);
+  return next;
+}
+
 // One run of steps of one item, and the walk from run to run.
 struct Run {
   int b, h, item, s0, s1, steps;
@@ -278,7 +327,7 @@ struct Run {
     h = s.start[1];
     item = s.start[2];
     s0 = s.start[3];
-    left = s.left;
+    left = s.end - s.begin;
     got = left > 0;
     bool bad;
     if (got) seq = load_seq(p, b, &bad);
@@ -306,6 +355,43 @@ struct Run {
 };
 
 // ---------------------------------------------------------------- roles
+
+// V rows [hi, 128) of a landed step are cleared; in rows [lo, hi) non-finite elements are
+// cleared and their rows noted.  By one warp, so the common path is kept short: x * 0 is NaN
+// exactly if x is not finite, so one packed product-and-sum per two elements carries the answer
+// for many of them, and the exact search runs only where it says so.
+template <int D>
+__device__ __forceinline__ void clean_rows(unsigned char* v, int lo, int hi, uint32_t* noted) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kPieces = D / 8;                   // 16-byte pieces per row
+  constexpr int kRowsAt = 32 / kPieces;            // rows the warp covers at once
+  const int piece = lane % kPieces;
+  unsigned char* at = v + (piece / 8) * 16384 + (piece % 8) * 16;
+#pragma unroll 8
+  for (int r = hi + lane / kPieces; r < kStep; r += kRowsAt)
+    *reinterpret_cast<uint4*>(at + r * 128) = make_uint4(0u, 0u, 0u, 0u);
+  uint32_t acc[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 8
+  for (int r = lo + lane / kPieces; r < hi; r += kRowsAt) {
+    const uint4 w = *reinterpret_cast<const uint4*>(at + r * 128);
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[0]) : "r"(w.x), "r"(0u));
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[1]) : "r"(w.y), "r"(0u));
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[2]) : "r"(w.z), "r"(0u));
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[3]) : "r"(w.w), "r"(0u));
+  }
+  if (!__any_sync(0xffffffffu, ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu) != 0u)) return;
+  const uint32_t e = 0x7f807f80u;                  // all exponent bits: infinite or NaN
+  for (int r = lo + lane / kPieces; r < hi; r += kRowsAt) {
+    uint4* w = reinterpret_cast<uint4*>(at + r * 128);
+    const uint4 x = *w;
+    const uint32_t bx = __vcmpeq2(x.x & e, e), by = __vcmpeq2(x.y & e, e);
+    const uint32_t bz = __vcmpeq2(x.z & e, e), bw = __vcmpeq2(x.w & e, e);
+    if (bx | by | bz | bw) {
+      *w = make_uint4(x.x & ~bx, x.y & ~by, x.z & ~bz, x.w & ~bw);
+      atomicOr(&noted[r / 32], 1u << (r % 32));
+    }
+  }
+}
 
 template <int D>
 __device__ void copy_role(const TcParams& t, TcShared& s, unsigned char* q_smem,
@@ -387,26 +473,9 @@ __device__ void copy_role(const TcParams& t, TcShared& s, unsigned char* q_smem,
           ok = wait_or_abort(s, &s.land, land_parity);
           land_parity ^= 1;
           if (!ok) break;
-          // rows [lo, hi) are seen by some rows of the item only, rows from hi on by none;
-          // a row is 128 bytes in each half, in some order of its 16-byte pieces
+          // rows [lo, hi) are seen by some rows of the item only, rows from hi on by none
           const int lo = max(0, all_see - j * kStep), hi = min(kStep, seen - j * kStep);
-          for (int i = lane; i < (kStep - lo) * 8 * C::kHalves; i += 32) {
-            const int row_at = lo + i / (8 * C::kHalves), piece = i % (8 * C::kHalves);
-            uint4* w = reinterpret_cast<uint4*>(dst + (piece / 8) * 16384 + row_at * 128 +
-                                                (piece % 8) * 16);
-            if (row_at >= hi) {
-              *w = make_uint4(0u, 0u, 0u, 0u);
-              continue;
-            }
-            uint4 v = *w;
-            const uint32_t e = 0x7f807f80u;      // all exponent bits: infinite or NaN
-            const uint32_t bx = __vcmpeq2(v.x & e, e), by = __vcmpeq2(v.y & e, e);
-            const uint32_t bz = __vcmpeq2(v.z & e, e), bw = __vcmpeq2(v.w & e, e);
-            if (bx | by | bz | bw) {
-              *w = make_uint4(v.x & ~bx, v.y & ~by, v.z & ~bz, v.w & ~bw);
-              atomicOr(&s.noted[turn][j - r.steps + 4][row_at / 32], 1u << (row_at % 32));
-            }
-          }
+          clean_rows<D>(dst, lo, hi, s.noted[turn][j - r.steps + 4]);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&s.kv_full[stage]);
@@ -451,12 +520,16 @@ __device__ void mma_role(const TcParams& t, TcShared& s, uint32_t q_smem, uint32
       full_parity ^= 1;
     }
   };
-  auto scores = [&](int x, uint32_t k_addr) {       // S_x = Q_x K^T
+  const uint32_t q_lo = tc_desc_lo(q_smem, 16), k_lo = tc_desc_lo(ring, 16),
+                 v_lo = tc_desc_lo(ring, 16384);
+  constexpr uint32_t kTile = C::kTileBytes >> 4;
+  auto scores = [&](int x, uint32_t k_at) {         // S_x = Q_x K^T
+    const uint32_t q_at = q_lo + x * kTile;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
-      const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
-      tc_mma_ss(tmem + C::kColS + 128 * x, tc_desc(q_smem + x * C::kTileBytes + off, 16),
-                tc_desc(k_addr + off, 16), kIdS, k > 0);
+      constexpr uint32_t kHalf = 16384 >> 4;
+      const uint32_t off = (k / 4) * kHalf + (k % 4) * 2;
+      tc_mma_ss(tmem + C::kColS + 128 * x, tc_desc(q_at + off), tc_desc(k_at + off), kIdS, k > 0);
     }
     tc_commit(&s.s_full[x]);
   };
@@ -466,9 +539,9 @@ __device__ void mma_role(const TcParams& t, TcShared& s, uint32_t q_smem, uint32
     q_parity ^= 1;
     if (!wait_or_abort(s, &s.kv_full[stage], full_parity)) return;
     tc_fence_after();
-    uint32_t k_addr = ring + stage * C::kTileBytes;
-    scores(0, k_addr);
-    if (two) scores(1, k_addr);
+    uint32_t k_at = k_lo + stage * kTile;
+    scores(0, k_at);
+    if (two) scores(1, k_at);
     tc_commit(&s.kv_empty[stage]);
     advance();
     if (r.s1 - r.s0 == 1) tc_commit(&s.q_empty);
@@ -482,8 +555,8 @@ __device__ void mma_role(const TcParams& t, TcShared& s, uint32_t q_smem, uint32
         if (!wait_or_abort(s, &s.kv_full[stage], full_parity)) return;
         advance();
       }
-      const uint32_t v_addr = ring + v_stage * C::kTileBytes;
-      k_addr = ring + k_stage * C::kTileBytes;
+      const uint32_t v_at = v_lo + v_stage * kTile;
+      k_at = k_lo + k_stage * kTile;
       for (int x = 0; x < (two ? 2 : 1); ++x) {
         if (!wait_or_abort(s, &s.p_ready[x], p_parity[x])) return;
         p_parity[x] ^= 1;
@@ -491,11 +564,11 @@ __device__ void mma_role(const TcParams& t, TcShared& s, uint32_t q_smem, uint32
 #pragma unroll
         for (int k = 0; k < kStep / 16; ++k)          // O_x += P_x V
           tc_mma_ts(tmem + C::kColO + D * x, tmem + C::kColS + 128 * x + 8 * k,
-                    tc_desc(v_addr + 2048 * k, 16384), kIdO, j > r.s0 || k > 0);
+                    tc_desc(v_at + (2048 >> 4) * k), kIdO, j > r.s0 || k > 0);
         if (last)
           tc_commit(&s.o_full[x]);
         else
-          scores(x, k_addr);
+          scores(x, k_at);
       }
       tc_commit(&s.kv_empty[v_stage]);
       if (!last) {
@@ -577,12 +650,14 @@ __device__ void softmax_role(const TcParams& t, TcShared& s) {
         }
         float mx[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          mx[c] = __uint_as_float(sc[c][0]);
+        for (int c = 0; c < 4; ++c)
+          mx[c] = fmaxf(__uint_as_float(sc[c][0]), __uint_as_float(sc[c][1]));
 #pragma unroll
-          for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(sc[c][e]));
-        }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+        for (int e = 2; e < 32; e += 2)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            mx[c] = max3(mx[c], __uint_as_float(sc[c][e]), __uint_as_float(sc[c][e + 1]));
+        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
         // grown past the slack (or the first finite score): a new reference
         const bool grow = top > m + kSlack || (m == -INFINITY && top > -INFINITY);
         if (__any_sync(0xffffffffu, grow)) {
@@ -605,23 +680,29 @@ __device__ void softmax_role(const TcParams& t, TcShared& s) {
           }
         }
         const float ref = m == -INFINITY ? 0.f : m;
-        float sum[2] = {0.f, 0.f};
+        const uint64_t scale2 = pair(scale, scale), ref2 = pair(-ref, -ref);
+        uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t pk[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const float a = ex2_approx(
-                fmaf(__uint_as_float(sc[half * 2 + e / 16][(2 * e) % 32]), scale, -ref));
-            const float b = ex2_approx(
-                fmaf(__uint_as_float(sc[half * 2 + e / 16][(2 * e) % 32 + 1]), scale, -ref));
-            sum[0] += a;
-            sum[1] += b;
+            const uint32_t(&row_sc)[32] = sc[half * 2 + e / 16];
+            float a, b;
+            unpair(fma2(pair(__uint_as_float(row_sc[(2 * e) % 32]),
+                             __uint_as_float(row_sc[(2 * e) % 32 + 1])),
+                        scale2, ref2),
+                   &a, &b);
+            a = ex2_approx(a);
+            b = ex2_approx(b);
+            sum[e & 1] = add2(sum[e & 1], pair(a, b));
             pk[e] = pack_bf16(a, b);
           }
           tc_st32(tm_s + 32 * half, pk);
         }
-        l += sum[0] + sum[1];
+        float la, lb;
+        unpair(add2(sum[0], sum[1]), &la, &lb);
+        l += la + lb;
         tc_wait_st();
         tc_fence_before();
       }
@@ -640,8 +721,8 @@ __device__ void softmax_role(const TcParams& t, TcShared& s) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) noted |= s.noted[turn][e / 4][e % 4] != 0u;
     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-    const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (r.s0 > 0 ? 0 : 1)) * 256 +
-                         x * 128 + row;
+    const int64_t part_block = static_cast<int64_t>(blockIdx.x) * 2 + (r.s0 > 0 ? 0 : 1);
+    const int64_t part = part_block * 256 + x * 128 + row;
     if (!whole && mine) {
       t.part_ml[2 * part] = m;
       t.part_ml[2 * part + 1] = l;
@@ -668,10 +749,12 @@ __device__ void softmax_role(const TcParams& t, TcShared& s) {
                                 pack_bf16(f[8 * e + 4] * inv, f[8 * e + 5] * inv),
                                 pack_bf16(f[8 * e + 6] * inv, f[8 * e + 7] * inv));
         } else {
-          float4* dst = reinterpret_cast<float4*>(t.part_acc + part * D + 32 * c);
+          // column quads outermost: a warp's 32 rows make one 512-byte piece
+          float4* dst = reinterpret_cast<float4*>(t.part_acc) + (part_block * (D / 4) + 8 * c) * 256 +
+                        x * 128 + row;
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            dst[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+            dst[e * 256] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
         }
       }
     }
@@ -695,10 +778,13 @@ __device__ void run_copies(const TcParams& t, TcShared& s, unsigned char* q_smem
   if (!s.abort)
     for (; r.open(tpi); r.next(p, tpi)) {
       if (r.s0 == 0 && r.s1 < r.steps) {
-        const int64_t stop = pos + r.steps;      // the item's end on the line
+        // borders inside the item that were not moved to its ends
         parts = 1;
-        for (int64_t c = blockIdx.x + 1; c < s.blocks && s.total * c / s.blocks < stop; ++c)
+        for (int64_t c = blockIdx.x + 1; c < s.blocks; ++c) {
+          const int64_t off = s.total * c / s.blocks - pos;
+          if (r.steps - off <= s.snap) break;
           ++parts;
+        }
         first = r.seq.first;
         n = r.seq.n;
         item = r.item;
@@ -758,8 +844,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   grid_dependency_wait();
   const int tpi = 2 * t.tpt;
-  if (warp == 0) {
-    // the length of the line, then this block's part of it
+  if (warp < 2) {
+    // the length of the line, then the border before this block (warp 0) and after it (warp 1)
     int64_t total = 0;
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
       bool bad = false;
@@ -770,20 +856,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
       total += v;
     }
-    const int64_t blocks =
-        max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), total / kMinSteps));
-    const int64_t c = blockIdx.x;
-    const int64_t begin = c < blocks ? total * c / blocks : total;
-    const int64_t end = c < blocks ? total * (c + 1) / blocks : total;
+    const int blocks =
+        static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), total)));
+    const int snap = static_cast<int>(min(static_cast<int64_t>(kSnap), total / (2 * blocks)));
     int start[4] = {p.batch, 0, 0, 0};
-    if (begin < end) find_step(p, tpi, begin, start);
-    if (lane == 0) {
+    const int64_t at =
+        line_border(p, tpi, total, blocks, snap, min(static_cast<int>(blockIdx.x) + warp, blocks), start);
+    if (lane == 0 && warp == 0) {
       for (int i = 0; i < 4; ++i) s.start[i] = start[i];
-      s.left = end - begin;
-      s.begin = begin;
+      s.begin = at;
       s.total = total;
-      s.blocks = static_cast<int>(blocks);
+      s.blocks = blocks;
+      s.snap = snap;
     }
+    if (lane == 0 && warp == 1) s.end = at;
   }
   tc_fence_before();
   __syncthreads();
@@ -818,67 +904,66 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
-// Joins the partial results of the items that several blocks shared: block (c, i) takes some
-// rows of the item that starts in block c, one warp per row, its parts in the line's order.
+// Joins the partial results of the items that several blocks shared: block (c, y) takes 32 rows
+// (a lane each) of the item that starts in block c, its parts in the line's order.
 template <int D>
-__global__ void __launch_bounds__(256) chunk_tc_join_kernel(ChunkParams p, int tpt,
-                                                            const float* part_acc,
-                                                            const float* part_ml,
-                                                            const int32_t* join, int num_blocks) {
+__global__ void __launch_bounds__(D * 4) chunk_tc_join_kernel(ChunkParams p, int tpt,
+                                                                     const float* part_acc,
+                                                                     const float* part_ml,
+                                                                     const int32_t* join,
+                                                                     int num_blocks) {
   grid_dependency_wait();
   const int c0 = blockIdx.x;
   const int32_t* j = join + c0 * 8;
   const int parts = j[0];
   if (parts < 2 || c0 + parts > num_blocks) return;
   const int first = j[1], n = j[2], item = j[3], h = j[4];
-  const int G = p.num_q_heads / p.num_kv_heads, lane = threadIdx.x & 31;
-  constexpr int kVals = D / 32;
-  for (int row = blockIdx.y * 8 + threadIdx.x / 32; row < 256; row += gridDim.y * 8) {
-    const int x = row / 128, in_tile = (row % 128) / G;
-    const int tok = item * 2 * tpt + x * tpt + in_tile;
-    if (in_tile >= tpt || tok >= n) continue;
-    // part 0 is the second partial of block c0, part i the first one of block c0 + i
-    auto at = [&](int i) {
-      return (static_cast<int64_t>(c0 + i) * 2 + (i == 0 ? 1 : 0)) * 256 + row;
-    };
-    float m = -INFINITY;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldg(part_ml + 2 * at(i)));
-    m = warp_max(m);
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f, acc[kVals];
-#pragma unroll
-    for (int e = 0; e < kVals; ++e) acc[e] = 0.f;
+  const int G = p.num_q_heads / p.num_kv_heads;
+  const int row = blockIdx.y * 32 + (threadIdx.x & 31), in_tile = (row % 128) / G;
+  const int tok = item * 2 * tpt + (row / 128) * tpt + in_tile;
+  if (in_tile >= tpt || tok >= n) return;
+  // part 0 is the second partial of block c0, part i the first one of block c0 + i
+  auto at = [&](int i) { return static_cast<int64_t>(c0 + i) * 2 + (i == 0 ? 1 : 0); };
+  const float2* ml = reinterpret_cast<const float2*>(part_ml);
+  float m = -INFINITY;
 #pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-      const int64_t a = at(i);
-      const float2 ml = __ldg(reinterpret_cast<const float2*>(part_ml) + a);
-      const float w = ex2_approx(ml.x - ref);
-      l = fmaf(w, ml.y, l);
-      const float* src = part_acc + a * D + lane * kVals;
-#pragma unroll
-      for (int e = 0; e < kVals; e += 2) {
-        const float2 v = __ldg(reinterpret_cast<const float2*>(src + e));
-        acc[e] = fmaf(w, v.x, acc[e]);
-        acc[e + 1] = fmaf(w, v.y, acc[e + 1]);
-      }
-    }
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(
-        static_cast<uint16_t*>(p.out) +
-        (static_cast<int64_t>(first + tok) * p.num_q_heads + h * G + (row % 128) % G) * D +
-        lane * kVals);
-#pragma unroll
-    for (int e = 0; e < kVals; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+  for (int i = 0; i < parts; ++i) m = fmaxf(m, __ldg(ml + at(i) * 256 + row).x);
+  const float ref = m == -INFINITY ? 0.f : m;
+  // this warp's 8 columns
+  const int q0 = (threadIdx.x / 32) * 2;
+  const float4* acc = reinterpret_cast<const float4*>(part_acc);
+  float l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) {
+    const float2 e = __ldg(ml + at(i) * 256 + row);
+    const float4 a = __ldg(acc + (at(i) * (D / 4) + q0) * 256 + row);
+    const float4 b = __ldg(acc + (at(i) * (D / 4) + q0 + 1) * 256 + row);
+    const float w = ex2_approx(e.x - ref);
+    l = fmaf(w, e.y, l);
+    o[0] = fmaf(w, a.x, o[0]);
+    o[1] = fmaf(w, a.y, o[1]);
+    o[2] = fmaf(w, a.z, o[2]);
+    o[3] = fmaf(w, a.w, o[3]);
+    o[4] = fmaf(w, b.x, o[4]);
+    o[5] = fmaf(w, b.y, o[5]);
+    o[6] = fmaf(w, b.z, o[6]);
+    o[7] = fmaf(w, b.w, o[7]);
   }
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  uint4* dst = reinterpret_cast<uint4*>(
+      static_cast<uint16_t*>(p.out) +
+      (static_cast<int64_t>(first + tok) * p.num_q_heads + h * G + (row % 128) % G) * D + q0 * 4);
+  *dst = make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv),
+                    pack_bf16(o[4] * inv, o[5] * inv), pack_bf16(o[6] * inv, o[7] * inv));
 }
 
 // Blocks that the line is shared out to: one per SM, and no more than the longest possible line
-// (known from the shape alone) has pieces of kMinSteps.
+// (known from the shape alone) has steps.
 int tc_blocks(int64_t num_tokens, int batch, int group, int hkv, int64_t max_len, int sms) {
   const int64_t tpi = 2 * (128 / group);
   const int64_t items = (num_tokens + tpi - 1) / tpi + batch;
   const int64_t steps = (max_len + kStep - 1) / kStep;
-  const int64_t most = std::max<int64_t>(1, items * hkv * steps / kMinSteps);
+  const int64_t most = std::max<int64_t>(1, items * hkv * steps);
   return static_cast<int>(std::min<int64_t>(sms, most));
 }
 
@@ -912,8 +997,8 @@ cudaError_t launch(const TcParams& t, int blocks, cudaStream_t stream) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, chunk_tc_kernel<D>, t);
   if (e != cudaSuccess || blocks == 1) return e;
-  cfg.gridDim = dim3(blocks, 16);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(blocks, 8);
+  cfg.blockDim = dim3(D * 4);                     // a warp for every 8 columns
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, chunk_tc_join_kernel<D>, t.c, t.tpt,
                             static_cast<const float*>(t.part_acc),

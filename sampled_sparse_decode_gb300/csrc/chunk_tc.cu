@@ -15,7 +15,8 @@
 // stay below 2^8), so most steps touch O by the product alone.
 //
 // Work split.  The steps of all items, in the order (sequence, KV head, item, step), are one line
-// of W steps; block c of N takes the steps [W c / N, W (c + 1) / N).  An item that crosses a
+// of W units, a few more for each item's opening; block c of N takes the units [W c / N,
+// W (c + 1) / N).  An item that crosses a
 // border leaves partial (m, l, O) rows in the workspace, at most two per block, and a second
 // launch joins them in order: every block has the same work to within a step, for one long
 // sequence as for many short ones, and nothing depends on timing.
@@ -38,6 +39,7 @@ constexpr int kSoftmaxRegs = 208;         // registers per thread: 2 * 208 + 88 
 constexpr int kIssueRegs = 88;            // 384 threads are launched with
 constexpr int kStep = 128;                 // keys per step
 constexpr int kSnap = 6;                   // steps a border may move to an item's end
+constexpr int kOpen = 4;                   // what opening and closing an item costs, in steps
 constexpr float kSlack = 8.f;              // growth of a row's maximum that triggers a rescale
 
 template <int D>
@@ -61,11 +63,11 @@ struct TcParams {
 struct TcShared {
   uint64_t q_full, q_empty, land, drain;
   uint64_t kv_full[10], kv_empty[10];
-  uint64_t s_full[2], p_ready[2], o_full[2];
+  uint64_t s_full[2], p_ready[2][2], o_full[2];   // p_ready: the halves of P
   uint32_t tmem;
   volatile int abort;
   int start[4];              // b, h, item, step of the block's first step
-  int64_t total, begin, end; // all steps; the block's first step and the one behind its last
+  int64_t total, begin, end; // the line's length; the block's part of it
   int blocks, snap;          // blocks with work; see line_border
   uint32_t noted[3][4][4];   // [item ring][step of the last four][token bits]
 };
@@ -235,27 +237,28 @@ __device__ __forceinline__ Seq load_seq(const ChunkParams& p, int b, bool* bad) 
   }
   return s;
 }
-// Steps of the items 0 .. i - 1 (all of them with full token counts) of a sequence.
-__device__ __forceinline__ int64_t steps_before(const Seq& s, int tpi, int i) {
-  return floor_sum(i, kStep, tpi, s.ctx + tpi + kStep - 1);
+// Line length of the items 0 .. i - 1 (all of them with full token counts) of a sequence: the
+// steps, and kOpen for each item.
+__device__ __forceinline__ int64_t line_before(const Seq& s, int tpi, int i) {
+  return floor_sum(i, kStep, tpi, s.ctx + tpi + kStep - 1) + static_cast<int64_t>(i) * kOpen;
 }
 __device__ __forceinline__ int item_steps(const Seq& s, int tpi, int i) {
   return (s.ctx + min(s.n, (i + 1) * tpi) + kStep - 1) / kStep;
 }
-__device__ __forceinline__ int64_t seq_steps(const Seq& s, int tpi) {
+__device__ __forceinline__ int64_t seq_line(const Seq& s, int tpi) {
   if (s.n == 0) return 0;
   const int items = (s.n + tpi - 1) / tpi;
-  return steps_before(s, tpi, items - 1) + (s.ctx + s.n + kStep - 1) / kStep;
+  return line_before(s, tpi, items - 1) + kOpen + (s.ctx + s.n + kStep - 1) / kStep;
 }
 
-// Where the line's step `pos` lies, by one warp: sequence, head, item, step.
+// Where the line's unit `pos` lies, by one warp: sequence, head, item, offset in the item.
 __device__ void find_step(const ChunkParams& p, int tpi, int64_t pos, int* out) {
   const int lane = threadIdx.x & 31;
   int64_t before = 0;
   for (int b0 = 0; b0 < p.batch; b0 += 32) {
     bool bad;
     const Seq s = b0 + lane < p.batch ? load_seq(p, b0 + lane, &bad) : Seq{0, 0, 0};
-    const int64_t mine = seq_steps(s, tpi) * p.num_kv_heads;
+    const int64_t mine = seq_line(s, tpi) * p.num_kv_heads;
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -273,12 +276,12 @@ __device__ void find_step(const ChunkParams& p, int tpi, int64_t pos, int* out) 
       q.ctx = __shfl_sync(0xffffffffu, s.ctx, at);
       const int h = static_cast<int>((pos - start) / per_head);
       const int64_t rem = (pos - start) - h * per_head;
-      // the last item i with steps_before(i) <= rem
+      // the last item i with line_before(i) <= rem
       int lo = 0, hi = (q.n + tpi - 1) / tpi;
       while (hi - lo > 1) {
         const int step = (hi - lo + 31) / 32;
         const int i = lo + lane * step;
-        const bool below = lane == 0 || (i < hi && steps_before(q, tpi, i) <= rem);
+        const bool below = lane == 0 || (i < hi && line_before(q, tpi, i) <= rem);
         const unsigned m = __ballot_sync(0xffffffffu, below);
         lo += (31 - __clz(m)) * step;
         hi = min(hi, lo + step);
@@ -286,7 +289,7 @@ __device__ void find_step(const ChunkParams& p, int tpi, int64_t pos, int* out) 
       out[0] = b0 + at;
       out[1] = h;
       out[2] = lo;
-      out[3] = static_cast<int>(rem - steps_before(q, tpi, lo));
+      out[3] = static_cast<int>(rem - line_before(q, tpi, lo));
       return;
     }
     before += __shfl_sync(0xffffffffu, incl, 31);
@@ -295,9 +298,9 @@ __device__ void find_step(const ChunkParams& p, int tpi, int64_t pos, int* out) 
   out[1] = out[2] = out[3] = 0;
 }
 
-// Border c of the line (the first step of block c): total * c / blocks, moved to the next item's
-// border if that is at most `snap` steps away, which saves a join for a little unevenness.  The
-// moves keep the borders in order.  By one warp; `out` as in find_step.
+// Border c of the line (where block c starts): total * c / blocks, moved to the item's start or
+// end if that is at most `snap` steps away, which saves a join for a little unevenness.  The
+// moves keep the borders in order.  By one warp; out = sequence, head, item, step.
 __device__ int64_t line_border(const ChunkParams& p, int tpi, int64_t total, int blocks, int snap,
                                int c, int* out) {
   const int64_t pos = total * c / blocks;
@@ -305,13 +308,14 @@ __device__ int64_t line_border(const ChunkParams& p, int tpi, int64_t total, int
   find_step(p, tpi, pos, out);
   bool bad;
   const Seq q = load_seq(p, out[0], &bad);
-  const int step = out[3], steps = item_steps(q, tpi, out[2]);
+  const int off = out[3], step = max(0, off - kOpen), steps = item_steps(q, tpi, out[2]);
+  out[3] = step;
   if (step <= snap) {
     out[3] = 0;
-    return pos - step;
+    return pos - off;
   }
   if (steps - step > snap) return pos;
-  const int64_t next = pos + steps - step;         // the next item's first step
+  const int64_t next = pos + kOpen + steps - off;  // the next item's start
   if (next < total) find_step(p, tpi, next, out);
   return next;
 }
@@ -336,11 +340,11 @@ struct Run {
   __device__ __forceinline__ bool open(int tpi) {
     if (!got) return false;
     steps = item_steps(seq, tpi, item);
-    s1 = static_cast<int>(min(static_cast<int64_t>(steps), s0 + left));
+    s1 = static_cast<int>(min(static_cast<int64_t>(steps), s0 + left - (s0 ? 0 : kOpen)));
     return true;
   }
   __device__ __forceinline__ void next(const ChunkParams& p, int tpi) {
-    left -= s1 - s0;
+    left -= s1 - s0 + (s0 ? 0 : kOpen);
     got = left > 0;
     if (!got) return;
     s0 = 0;                                     // more is left: the item was finished
@@ -558,13 +562,17 @@ __device__ void mma_role(const TcParams& t, TcShared& s, uint32_t q_smem, uint32
       const uint32_t v_at = v_lo + v_stage * kTile;
       k_at = k_lo + k_stage * kTile;
       for (int x = 0; x < (two ? 2 : 1); ++x) {
-        if (!wait_or_abort(s, &s.p_ready[x], p_parity[x])) return;
-        p_parity[x] ^= 1;
-        tc_fence_after();
+        for (int half = 0; half < 2; ++half) {        // O_x += P_x V, as P_x comes in
+          if (!wait_or_abort(s, &s.p_ready[x][half], p_parity[x])) return;
+          tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < kStep / 16; ++k)          // O_x += P_x V
-          tc_mma_ts(tmem + C::kColO + D * x, tmem + C::kColS + 128 * x + 8 * k,
-                    tc_desc(v_at + (2048 >> 4) * k), kIdO, j > r.s0 || k > 0);
+          for (int k = 0; k < kStep / 32; ++k)
+            tc_mma_ts(tmem + C::kColO + D * x,
+                      tmem + C::kColS + 128 * x + 8 * (half * (kStep / 32) + k),
+                      tc_desc(v_at + (2048 >> 4) * (half * (kStep / 32) + k)), kIdO,
+                      j > r.s0 || half > 0 || k > 0);
+        }
+        p_parity[x] ^= 1;
         if (last)
           tc_commit(&s.o_full[x]);
         else
@@ -579,11 +587,13 @@ __device__ void mma_role(const TcParams& t, TcShared& s, uint32_t q_smem, uint32
   }
 }
 
-// Products of noted V elements (see the top of the file) that this row sees, added to 32 of
-// its accumulators.
+// Products of noted V elements (see the top of the file) that this row sees, added to the row
+// where it was just written: the output (bf16, step 2 bytes) or the partial result.  Such an
+// element is infinite or NaN, and so is the sum, whatever the order and the divisor.
 template <int D>
 __device__ __noinline__ void add_noted(const TcParams& t, const Run& r, const uint32_t (*noted)[4],
-                                       int sees, int64_t q_row, float m, int col0, float* o) {
+                                       int sees, int64_t q_row, float m, uint16_t* out,
+                                       float* part) {
   const ChunkParams& p = t.c;
   const uint16_t* q = static_cast<const uint16_t*>(p.q) + q_row;
   for (int e = 0; e < 4; ++e)
@@ -601,9 +611,32 @@ __device__ __noinline__ void add_noted(const TcParams& t, const Run& r, const ui
         for (int i = 0; i < D; ++i) dot = fmaf(bf16_to_f32(q[i]), bf16_to_f32(k[i]), dot);
         const float w32 = ex2_approx(fmaf(dot, p.scale_log2, -m));
         const float weight = bf16_lo_f(pack_bf16(w32, 0.f));
-        for (int i = 0; i < 32; ++i)
-          if ((v[col0 + i] & 0x7f80) == 0x7f80) o[i] = fmaf(weight, bf16_to_f32(v[col0 + i]), o[i]);
+        for (int i = 0; i < D; ++i)
+          if ((v[i] & 0x7f80) == 0x7f80) {
+            const float x = weight * bf16_to_f32(v[i]);
+            if (out)
+              out[i] = static_cast<uint16_t>(pack_bf16(bf16_to_f32(out[i]) + x, 0.f));
+            else
+              part[(i / 4) * 1024 + i % 4] += x;
+          }
       }
+}
+
+// 16 consecutive fp32 values (32 bytes of bf16) of a row, scaled; `wide`: dst is 32-byte aligned.
+__device__ __forceinline__ void store_row16(uint16_t* dst, const uint32_t* o, float inv,
+                                            bool wide) {
+  uint32_t w[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    w[e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 
 template <int D>
@@ -617,6 +650,7 @@ __device__ void softmax_role(const TcParams& t, TcShared& s) {
   const uint32_t tm_s = s.tmem + C::kColS + 128 * x + lanes;
   const uint32_t tm_o = s.tmem + C::kColO + D * x + lanes;
   const float scale = p.scale_log2;
+  const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
   uint32_t s_parity = 0, o_parity = 0;
   Run r;
   r.begin(s, p);
@@ -681,32 +715,42 @@ __device__ void softmax_role(const TcParams& t, TcShared& s) {
         }
         const float ref = m == -INFINITY ? 0.f : m;
         const uint64_t scale2 = pair(scale, scale), ref2 = pair(-ref, -ref);
-        uint64_t sum[2] = {0ull, 0ull};
+        // each half is handed over as soon as it is stored; the sum waits until then
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t pk[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const uint32_t(&row_sc)[32] = sc[half * 2 + e / 16];
+            uint32_t(&src)[32] = sc[half * 2 + e / 16];
+            const int at = (2 * e) % 32;
             float a, b;
-            unpair(fma2(pair(__uint_as_float(row_sc[(2 * e) % 32]),
-                             __uint_as_float(row_sc[(2 * e) % 32 + 1])),
-                        scale2, ref2),
+            unpair(fma2(pair(__uint_as_float(src[at]), __uint_as_float(src[at + 1])), scale2, ref2),
                    &a, &b);
             a = ex2_approx(a);
             b = ex2_approx(b);
-            sum[e & 1] = add2(sum[e & 1], pair(a, b));
             pk[e] = pack_bf16(a, b);
+            src[at] = __float_as_uint(a);
+            src[at + 1] = __float_as_uint(b);
           }
           tc_st32(tm_s + 32 * half, pk);
+          tc_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if ((threadIdx.x & 31) == 0) mbar_arrive(&s.p_ready[x][half]);
         }
+        uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int e = 0; e < 32; e += 2)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            sum[c] = add2(sum[c], pair(__uint_as_float(sc[c][e]), __uint_as_float(sc[c][e + 1])));
         float la, lb;
-        unpair(add2(sum[0], sum[1]), &la, &lb);
+        unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), &la, &lb);
         l += la + lb;
-        tc_wait_st();
-        tc_fence_before();
+      } else if ((threadIdx.x & 31) == 0) {
+        mbar_arrive(&s.p_ready[x][0]);
+        mbar_arrive(&s.p_ready[x][1]);
       }
-      mbar_arrive(&s.p_ready[x]);
     }
     // ---- epilogue: the row, or its partial result
     if (!wait_or_abort(s, &s.o_full[x], o_parity)) return;
@@ -723,6 +767,8 @@ __device__ void softmax_role(const TcParams& t, TcShared& s) {
     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
     const int64_t part_block = static_cast<int64_t>(blockIdx.x) * 2 + (r.s0 > 0 ? 0 : 1);
     const int64_t part = part_block * 256 + x * 128 + row;
+    float* part_row = t.part_acc + (part_block * (D / 4) * 256 + x * 128 + row) * 4;
+    uint16_t* out = static_cast<uint16_t*>(p.out) + out_row;
     if (!whole && mine) {
       t.part_ml[2 * part] = m;
       t.part_ml[2 * part + 1] = l;
@@ -734,30 +780,20 @@ __device__ void softmax_role(const TcParams& t, TcShared& s) {
       tc_ld32(o, tm_o + 32 * c);
       tc_wait_ld();
       tc_loaded(o);
-      if (mine) {
-        float f[32];
+      if (mine && whole) {
+        store_row16(out + 32 * c, o, inv, wide);
+        store_row16(out + 32 * c + 16, o + 16, inv, wide);
+      } else if (mine) {
+        // column quads outermost: a warp's 32 rows make one 512-byte piece
+        uint4* dst = reinterpret_cast<uint4*>(part_row) + 8 * c * 256;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]);
-        if (noted)
-          add_noted<D>(t, r, s.noted[turn], sees, out_row, m == -INFINITY ? 0.f : m, 32 * c, f);
-        if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + out_row + 32 * c);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            dst[e] = make_uint4(pack_bf16(f[8 * e] * inv, f[8 * e + 1] * inv),
-                                pack_bf16(f[8 * e + 2] * inv, f[8 * e + 3] * inv),
-                                pack_bf16(f[8 * e + 4] * inv, f[8 * e + 5] * inv),
-                                pack_bf16(f[8 * e + 6] * inv, f[8 * e + 7] * inv));
-        } else {
-          // column quads outermost: a warp's 32 rows make one 512-byte piece
-          float4* dst = reinterpret_cast<float4*>(t.part_acc) + (part_block * (D / 4) + 8 * c) * 256 +
-                        x * 128 + row;
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            dst[e * 256] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
-        }
+        for (int e = 0; e < 8; ++e)
+          dst[e * 256] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
       }
     }
+    if (noted && mine)
+      add_noted<D>(t, r, s.noted[turn], sees, out_row, m == -INFINITY ? 0.f : m,
+                   whole ? out : nullptr, part_row);
     __syncwarp();
     tc_fence_before();
   }
@@ -781,7 +817,7 @@ __device__ void run_copies(const TcParams& t, TcShared& s, unsigned char* q_smem
         // borders inside the item that were not moved to its ends
         parts = 1;
         for (int64_t c = blockIdx.x + 1; c < s.blocks; ++c) {
-          const int64_t off = s.total * c / s.blocks - pos;
+          const int64_t off = s.total * c / s.blocks - pos - kOpen;
           if (r.steps - off <= s.snap) break;
           ++parts;
         }
@@ -790,7 +826,7 @@ __device__ void run_copies(const TcParams& t, TcShared& s, unsigned char* q_smem
         item = r.item;
         h = r.h;
       }
-      pos += r.s1 - r.s0;
+      pos += r.s1 - r.s0 + (r.s0 ? 0 : kOpen);
     }
   if ((threadIdx.x & 31) == 0) {
     int32_t* j = t.join + blockIdx.x * 8;
@@ -825,7 +861,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s.s_full[x], 1);
-      mbar_init(&s.p_ready[x], 128);
+      mbar_init(&s.p_ready[x][0], 4);
+      mbar_init(&s.p_ready[x][1], 4);
       mbar_init(&s.o_full[x], 1);
     }
     s.abort = 0;
@@ -851,14 +888,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       bool bad = false;
       const Seq q = b0 + lane < p.batch ? load_seq(p, b0 + lane, &bad) : Seq{0, 0, 0};
       if (bad && blockIdx.x == 0) set_status(p.status, SANTA_DEV_BAD_SEQLEN);
-      int64_t v = seq_steps(q, tpi) * p.num_kv_heads;
+      int64_t v = seq_line(q, tpi) * p.num_kv_heads;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
       total += v;
     }
     const int blocks =
         static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), total)));
-    const int snap = static_cast<int>(min(static_cast<int64_t>(kSnap), total / (2 * blocks)));
+    const int snap = static_cast<int>(
+        max(static_cast<int64_t>(1), min(static_cast<int64_t>(kSnap), total / (2 * blocks))));
     int start[4] = {p.batch, 0, 0, 0};
     const int64_t at =
         line_border(p, tpi, total, blocks, snap, min(static_cast<int>(blockIdx.x) + warp, blocks), start);
@@ -958,12 +996,12 @@ __global__ void __launch_bounds__(D * 4) chunk_tc_join_kernel(ChunkParams p, int
 }
 
 // Blocks that the line is shared out to: one per SM, and no more than the longest possible line
-// (known from the shape alone) has steps.
+// (known from the shape alone) has units.
 int tc_blocks(int64_t num_tokens, int batch, int group, int hkv, int64_t max_len, int sms) {
   const int64_t tpi = 2 * (128 / group);
   const int64_t items = (num_tokens + tpi - 1) / tpi + batch;
   const int64_t steps = (max_len + kStep - 1) / kStep;
-  const int64_t most = std::max<int64_t>(1, items * hkv * steps);
+  const int64_t most = std::max<int64_t>(1, items * hkv * (steps + kOpen));
   return static_cast<int>(std::min<int64_t>(sms, most));
 }
 

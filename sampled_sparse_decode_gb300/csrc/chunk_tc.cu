@@ -35,11 +35,13 @@ namespace santa {
 namespace {
 
 constexpr int kTcThreads = 384;          // three warpgroups: softmax A, softmax B, the rest
-constexpr int kSoftmaxRegs = 208;         // registers per thread: 2 * 208 + 88 = 3 * 168, what
-constexpr int kIssueRegs = 88;            // 384 threads are launched with
+constexpr int kSoftmaxRegs = 200;         // registers per thread: 2 * 200 + 104 = 3 * 168, what
+constexpr int kIssueRegs = 104;           // 384 threads are launched with
 constexpr int kStep = 128;                 // keys per step
+constexpr int kGroups = 16;                // barriers of the copy groups (more than ring stages)
 constexpr int kSnap = 6;                   // steps a border may move to an item's end
 constexpr int kOpen = 4;                   // what opening and closing an item costs, in steps
+constexpr uint64_t kDrainNs = 1000000;      // longer than any copy in flight takes
 constexpr float kSlack = 8.f;              // growth of a row's maximum that triggers a rescale
 
 template <int D>
@@ -62,8 +64,9 @@ struct TcParams {
 
 struct TcShared {
   uint64_t q_full, q_empty, land, drain;
-  uint64_t kv_full[10], kv_empty[10];
-  uint64_t s_full[2], p_ready[2][2], o_full[2];   // p_ready: the halves of P
+  uint64_t kv_full[kGroups], kv_empty[kGroups];
+  uint64_t s_full[2], p_ready[2], o_full[2];
+  int group_of[10];          // by ring stage: the group of the tile in it (copying warp only)
   uint32_t tmem;
   volatile int abort;
   int start[4];              // b, h, item, step of the block's first step
@@ -199,6 +202,27 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+
+// 2^(s scale - ref) of 64 scores, as packed bf16 and, returned, their sum by even and odd ones.
+__device__ __forceinline__ uint64_t half_weights(uint32_t (&pk)[32], const uint32_t (&s0)[32],
+                                                 const uint32_t (&s1)[32], float scale,
+                                                 float ref) {
+  const uint64_t scale2 = pair(scale, scale), ref2 = pair(-ref, -ref);
+  uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+  for (int e = 0; e < 32; ++e) {
+    const uint32_t(&src)[32] = e < 16 ? s0 : s1;
+    const int at = (2 * e) % 32;
+    float a, b;
+    unpair(fma2(pair(__uint_as_float(src[at]), __uint_as_float(src[at + 1])), scale2, ref2), &a,
+           &b);
+    a = ex2_approx(a);
+    b = ex2_approx(b);
+    pk[e] = pack_bf16(a, b);
+    sum[e & 1] = add2(sum[e & 1], pair(a, b));
+  }
+  return add2(sum[0], sum[1]);
 }
 
 // ---------------------------------------------------------------- work line
@@ -397,6 +421,17 @@ __device__ __forceinline__ void clean_rows(unsigned char* v, int lo, int hi, uin
   }
 }
 
+// Adds to the bytes that a barrier's phase waits for (no arrival).
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+               "r"(bytes)
+               : "memory");
+}
+
+// K and V of a run arrive in groups, {K(s0)}, {V(s0), K(s0 + 1)}, {V(s0 + 1), K(s0 + 2)}, ...,
+// {V(s1 - 1)}: what the products between two hand-overs of P use.  A group has one full and one
+// empty barrier, so the issuing warp waits and commits once per step; its tiles take the next
+// stages of the ring.
 template <int D>
 __device__ void copy_role(const TcParams& t, TcShared& s, unsigned char* q_smem,
                           unsigned char* ring) {
@@ -404,11 +439,25 @@ __device__ void copy_role(const TcParams& t, TcShared& s, unsigned char* q_smem,
   const ChunkParams& p = t.c;
   const int lane = threadIdx.x & 31, tpi = 2 * t.tpt, G = p.num_q_heads / p.num_kv_heads;
   const int T = p.team_size;
-  uint32_t stage = 0, empty_parity = 1, q_parity = 1, land_parity = 0;
-  uint32_t issued = 0, runs = 0;                 // stages and Q ever filled (for the drain)
+  uint32_t q_parity = 1, land_parity = 0, runs = 0;
+  int group = 0, tiles = 0, stage = 0;
   Run r;
   r.begin(s, p);
   bool ok = true;
+  // the next ring stage, once the tile in it has been used
+  auto claim = [&] {
+    if (tiles >= C::kStages) {
+      const int g = s.group_of[stage];
+      ok = wait_or_abort(s, &s.kv_empty[g % kGroups], (g / kGroups) & 1);
+      __syncwarp();
+    }
+    if (lane == 0) s.group_of[stage] = group;
+    __syncwarp();
+    unsigned char* dst = ring + stage * C::kTileBytes;
+    ++tiles;
+    if (++stage == C::kStages) stage = 0;
+    return dst;
+  };
   for (int turn = 0; ok && r.open(tpi); r.next(p, tpi), turn = turn == 2 ? 0 : turn + 1) {
     const int tok = r.item * tpi;
     const bool two = tok + t.tpt < r.seq.n;
@@ -435,75 +484,79 @@ __device__ void copy_role(const TcParams& t, TcShared& s, unsigned char* q_smem,
     const int all_see = r.seq.ctx + tok + 1;                // keys that every row sees
     const int teams = (len + T - 1) / T;
     int window = -1, ids = 0;
-    for (int j = r.s0; ok && j < r.s1; ++j) {
-      // page ids of 32 teams at a time, one per lane
-      int row[2];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int at = j * kStep + c * 64;
-        row[c] = -1;
-        if (at >= len) continue;
-        const int team = at / T;
-        if (window < 0 || team >= window + 32) {
-          window = team;
-          ids = 0;
-          if (team + lane < teams) {
-            ids = p.page_table[static_cast<int64_t>(r.b) * p.max_teams + team + lane];
-            if (ids < 0 || ids >= p.num_pages) {
-              set_status(p.status, SANTA_DEV_BAD_PAGE);
-              ids = 0;
-            }
-          }
-        }
-        const int page = __shfl_sync(0xffffffffu, ids, team - window);
-        row[c] = (page * p.num_kv_heads + r.h) * T + at % T;
-      }
-      const uint32_t bytes = (row[1] >= 0 ? 2 : 1) * 64 * D * 2;
-      for (int kv = 0; ok && kv < 2; ++kv) {     // K, then V
-        unsigned char* dst = ring + stage * C::kTileBytes;
-        const bool check = kv == 1 && (j + 1) * kStep > all_see;
-        ok = wait_or_abort(s, &s.kv_empty[stage], empty_parity);
-        if (!ok) break;
-        uint64_t* bar = check ? &s.land : &s.kv_full[stage];
+    int row[2] = {-1, -1};                       // pool rows of the step's 64-key halves
+    for (int j = r.s0; ok && j <= r.s1; ++j, ++group) {     // group {V(j - 1), K(j)}
+      uint64_t* bar = &s.kv_full[group % kGroups];
+      bool check = false;
+      unsigned char* v_dst = nullptr;
+      auto load = [&](unsigned char* dst, const CUtensorMap* map, uint64_t* on) {
         if (lane == 0) {
-          mbar_arrive_expect_tx(bar, bytes);
+          mbar_expect_tx(on, (row[1] >= 0 ? 2 : 1) * 64 * D * 2);
           for (int c = 0; c < 2; ++c)
             if (row[c] >= 0)
               for (int i = 0; i < C::kHalves; ++i)
-                tma_load_2d(dst + i * 16384 + c * 8192, kv ? &t.tmap_v : &t.tmap_k, i * 64,
-                            row[c], bar);
+                tma_load_2d(dst + i * 16384 + c * 8192, map, i * 64, row[c], on);
         }
-        if (check) {
-          ok = wait_or_abort(s, &s.land, land_parity);
-          land_parity ^= 1;
-          if (!ok) break;
-          // rows [lo, hi) are seen by some rows of the item only, rows from hi on by none
-          const int lo = max(0, all_see - j * kStep), hi = min(kStep, seen - j * kStep);
-          clean_rows<D>(dst, lo, hi, s.noted[turn][j - r.steps + 4]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s.kv_full[stage]);
-        }
-        if (++issued, ++stage == C::kStages) {
-          stage = 0;
-          empty_parity ^= 1;
-        }
+      };
+      if (j > r.s0) {
+        v_dst = claim();
+        if (!ok) break;
+        check = j * kStep > all_see;             // step j - 1 holds masked pairs
+        load(v_dst, &t.tmap_v, check ? &s.land : bar);
+        if (check && lane == 0) mbar_arrive(&s.land);
       }
+      if (j < r.s1) {
+        // page ids of 32 teams at a time, one per lane
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int at = j * kStep + c * 64;
+          row[c] = -1;
+          if (at >= len) continue;
+          const int team = at / T;
+          if (window < 0 || team >= window + 32) {
+            window = team;
+            ids = 0;
+            if (team + lane < teams) {
+              ids = p.page_table[static_cast<int64_t>(r.b) * p.max_teams + team + lane];
+              if (ids < 0 || ids >= p.num_pages) {
+                set_status(p.status, SANTA_DEV_BAD_PAGE);
+                ids = 0;
+              }
+            }
+          }
+          const int page = __shfl_sync(0xffffffffu, ids, team - window);
+          row[c] = (page * p.num_kv_heads + r.h) * T + at % T;
+        }
+        unsigned char* k_dst = claim();
+        if (!ok) break;
+        load(k_dst, &t.tmap_k, bar);
+      }
+      if (check) {
+        ok = wait_or_abort(s, &s.land, land_parity);
+        land_parity ^= 1;
+        if (!ok) break;
+        // rows [lo, hi) are seen by some rows of the item only, rows from hi on by none
+        const int at = (j - 1) * kStep;
+        clean_rows<D>(v_dst, max(0, all_see - at), min(kStep, seen - at),
+                      s.noted[turn][j - 1 - r.steps + 4]);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (lane == 0) mbar_arrive(bar);
     }
   }
-  if (!ok) {
-    // drain: every copy that was issued lands before the block may end (bounded)
-    if (lane == 0) {
-      const uint64_t start = global_timer_ns();
-      while (runs && !mbar_try_wait(&s.q_full, (runs - 1) & 1) &&
+  if (!ok && lane == 0) {
+    // drain: what was issued lands before the block may end (bounded)
+    const uint64_t start = global_timer_ns();
+    while (runs && !mbar_try_wait(&s.q_full, (runs - 1) & 1) &&
+           global_timer_ns() - start < kWaitLimitNs) {
+    }
+    for (int g = max(0, group - C::kStages); g < group; ++g)
+      while (!mbar_try_wait(&s.kv_full[g % kGroups], (g / kGroups) & 1) &&
              global_timer_ns() - start < kWaitLimitNs) {
       }
-      for (uint32_t i = 0; i < C::kStages && i < issued; ++i) {
-        const uint32_t k = (issued - 1 - i) / C::kStages, st = (issued - 1 - i) % C::kStages;
-        while (!mbar_try_wait(&s.kv_full[st], k & 1) &&
-               global_timer_ns() - start < kWaitLimitNs) {
-        }
-      }
+    // copies of a group that was not completed: nothing signals them, so the time is waited out
+    while (global_timer_ns() - start < kDrainNs) {
     }
   }
 }
@@ -515,18 +568,18 @@ __device__ void mma_role(const TcParams& t, TcShared& s, uint32_t q_smem, uint32
   const int tpi = 2 * t.tpt;
   constexpr uint32_t kIdS = tc_idesc(kStep, false), kIdO = tc_idesc(D, true);
   const uint32_t tmem = s.tmem;
-  uint32_t stage = 0, full_parity = 0, q_parity = 0, p_parity[2] = {0, 0};
+  uint32_t q_parity = 0, p_parity[2] = {0, 0};
+  int group = 0, stage = 0;
   Run r;
   r.begin(s, p);
-  auto advance = [&] {
-    if (++stage == C::kStages) {
-      stage = 0;
-      full_parity ^= 1;
-    }
-  };
   const uint32_t q_lo = tc_desc_lo(q_smem, 16), k_lo = tc_desc_lo(ring, 16),
                  v_lo = tc_desc_lo(ring, 16384);
   constexpr uint32_t kTile = C::kTileBytes >> 4;
+  auto next_stage = [&] {
+    const int at = stage;
+    if (++stage == C::kStages) stage = 0;
+    return static_cast<uint32_t>(at);
+  };
   auto scores = [&](int x, uint32_t k_at) {         // S_x = Q_x K^T
     const uint32_t q_at = q_lo + x * kTile;
 #pragma unroll
@@ -537,52 +590,34 @@ __device__ void mma_role(const TcParams& t, TcShared& s, uint32_t q_smem, uint32
     }
     tc_commit(&s.s_full[x]);
   };
+  // A wait or a commit between products leaves a gap in the tensor pipe (each costs about 100
+  // cycles), so a step has as few as it can: the group, P of each tile; S of each tile, the group.
   for (; r.open(tpi); r.next(p, tpi)) {
     const bool two = r.item * tpi + t.tpt < r.seq.n;
     if (!wait_or_abort(s, &s.q_full, q_parity)) return;
     q_parity ^= 1;
-    if (!wait_or_abort(s, &s.kv_full[stage], full_parity)) return;
-    tc_fence_after();
-    uint32_t k_at = k_lo + stage * kTile;
-    scores(0, k_at);
-    if (two) scores(1, k_at);
-    tc_commit(&s.kv_empty[stage]);
-    advance();
-    if (r.s1 - r.s0 == 1) tc_commit(&s.q_empty);
-    for (int j = r.s0; j < r.s1; ++j) {
-      const bool last = j + 1 == r.s1;
-      const uint32_t v_stage = stage;
-      if (!wait_or_abort(s, &s.kv_full[stage], full_parity)) return;
-      advance();
-      const uint32_t k_stage = stage;
-      if (!last) {
-        if (!wait_or_abort(s, &s.kv_full[stage], full_parity)) return;
-        advance();
-      }
-      const uint32_t v_at = v_lo + v_stage * kTile;
-      k_at = k_lo + k_stage * kTile;
+    for (int j = r.s0; j <= r.s1; ++j, ++group) {     // O += P(j - 1) V(j - 1), S(j) = Q K(j)^T
+      if (!wait_or_abort(s, &s.kv_full[group % kGroups], (group / kGroups) & 1)) return;
+      tc_fence_after();
+      const uint32_t v_at = j > r.s0 ? v_lo + next_stage() * kTile : 0;
+      const uint32_t k_at = j < r.s1 ? k_lo + next_stage() * kTile : 0;
       for (int x = 0; x < (two ? 2 : 1); ++x) {
-        for (int half = 0; half < 2; ++half) {        // O_x += P_x V, as P_x comes in
-          if (!wait_or_abort(s, &s.p_ready[x][half], p_parity[x])) return;
+        if (j > r.s0) {
+          if (!wait_or_abort(s, &s.p_ready[x], p_parity[x])) return;
+          p_parity[x] ^= 1;
           tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < kStep / 32; ++k)
-            tc_mma_ts(tmem + C::kColO + D * x,
-                      tmem + C::kColS + 128 * x + 8 * (half * (kStep / 32) + k),
-                      tc_desc(v_at + (2048 >> 4) * (half * (kStep / 32) + k)), kIdO,
-                      j > r.s0 || half > 0 || k > 0);
+          for (int k = 0; k < kStep / 16; ++k)
+            tc_mma_ts(tmem + C::kColO + D * x, tmem + C::kColS + 128 * x + 8 * k,
+                      tc_desc(v_at + (2048 >> 4) * k), kIdO, j > r.s0 + 1 || k > 0);
         }
-        p_parity[x] ^= 1;
-        if (last)
-          tc_commit(&s.o_full[x]);
-        else
+        if (j < r.s1)
           scores(x, k_at);
+        else
+          tc_commit(&s.o_full[x]);
       }
-      tc_commit(&s.kv_empty[v_stage]);
-      if (!last) {
-        tc_commit(&s.kv_empty[k_stage]);
-        if (j + 2 == r.s1) tc_commit(&s.q_empty);
-      }
+      tc_commit(&s.kv_empty[group % kGroups]);
+      if (j + 1 == r.s1) tc_commit(&s.q_empty);
     }
   }
 }
@@ -682,6 +717,11 @@ __device__ void softmax_role(const TcParams& t, TcShared& s) {
             for (int e = 0; e < 32; ++e)
               if (c * 32 + e >= cut) sc[c][e] = 0xff800000u;   // -inf
         }
+        // weights of the first half by the reference in hand, while the maximum is formed: it
+        // seldom grows past the slack, and then they are formed again
+        uint32_t pk[32];
+        float ref = m == -INFINITY ? 0.f : m;
+        uint64_t sum = half_weights(pk, sc[0], sc[1], scale, ref);
         float mx[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -696,7 +736,7 @@ __device__ void softmax_role(const TcParams& t, TcShared& s) {
         const bool grow = top > m + kSlack || (m == -INFINITY && top > -INFINITY);
         if (__any_sync(0xffffffffu, grow)) {
           const float old = m;
-          if (grow) m = top;
+          if (grow) m = ref = top;
           if (j > r.s0) {
             const float keep = grow ? ex2_approx(old - m) : 1.f;
             l *= keep;
@@ -712,44 +752,20 @@ __device__ void softmax_role(const TcParams& t, TcShared& s) {
               tc_st32(tm_o + 32 * c, o);
             }
           }
+          sum = half_weights(pk, sc[0], sc[1], scale, ref);
         }
-        const float ref = m == -INFINITY ? 0.f : m;
-        const uint64_t scale2 = pair(scale, scale), ref2 = pair(-ref, -ref);
-        // each half is handed over as soon as it is stored; the sum waits until then
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            uint32_t(&src)[32] = sc[half * 2 + e / 16];
-            const int at = (2 * e) % 32;
-            float a, b;
-            unpair(fma2(pair(__uint_as_float(src[at]), __uint_as_float(src[at + 1])), scale2, ref2),
-                   &a, &b);
-            a = ex2_approx(a);
-            b = ex2_approx(b);
-            pk[e] = pack_bf16(a, b);
-            src[at] = __float_as_uint(a);
-            src[at + 1] = __float_as_uint(b);
-          }
-          tc_st32(tm_s + 32 * half, pk);
-          tc_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if ((threadIdx.x & 31) == 0) mbar_arrive(&s.p_ready[x][half]);
-        }
-        uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-        for (int e = 0; e < 32; e += 2)
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            sum[c] = add2(sum[c], pair(__uint_as_float(sc[c][e]), __uint_as_float(sc[c][e + 1])));
+        tc_st32(tm_s, pk);
+        sum = add2(sum, half_weights(pk, sc[2], sc[3], scale, ref));
+        tc_st32(tm_s + 32, pk);
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&s.p_ready[x]);
         float la, lb;
-        unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), &la, &lb);
+        unpair(sum, &la, &lb);
         l += la + lb;
       } else if ((threadIdx.x & 31) == 0) {
-        mbar_arrive(&s.p_ready[x][0]);
-        mbar_arrive(&s.p_ready[x][1]);
+        mbar_arrive(&s.p_ready[x]);
       }
     }
     // ---- epilogue: the row, or its partial result
@@ -855,14 +871,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     mbar_init(&s.q_empty, 1);
     mbar_init(&s.land, 1);
     mbar_init(&s.drain, 1);
-    for (int i = 0; i < C::kStages; ++i) {
+    for (int i = 0; i < kGroups; ++i) {
       mbar_init(&s.kv_full[i], 1);
       mbar_init(&s.kv_empty[i], 1);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s.s_full[x], 1);
-      mbar_init(&s.p_ready[x][0], 4);
-      mbar_init(&s.p_ready[x][1], 4);
+      mbar_init(&s.p_ready[x], 4);
       mbar_init(&s.o_full[x], 1);
     }
     s.abort = 0;

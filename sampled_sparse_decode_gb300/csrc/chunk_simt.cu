@@ -2,16 +2,24 @@
 // arithmetic (fp32 caches).
 //
 // A KV head's G query heads share its keys, so the rows of a tile are (token, head) pairs: row
-// r of a sequence's n * G rows is token r / G, head r % G.  One block takes 64 rows and walks the
-// keys they see in tiles of 64, with the running maximum and sum of an online softmax (base 2):
-//   S = Q K^T (4 x 4 scores per thread), P = 2^(S - m), O = 2^(m_old - m) O + P V (4 x d/16).
-// K and V go through shared memory once per tile; fp32 FMA bound (about 9 FMAs per 16-byte
-// shared load).  With few tiles the keys of a tile are split over several blocks, whose partial
-// (m, l, O) a second launch joins in order.  Tiles are found from cu_q through slots, as in
-// append_chunk.cu: sequence b owns floor(cu[b] G / 64) + b onward, at least ceil(n G / 64).
+// r of a sequence's n * G rows is token r / G, head r % G.  A block takes 64 rows and the keys
+// they see, with the running maximum and sum of an online softmax (base 2), in one of two ways:
+//   many rows  keys in steps of 64 through shared memory (two blocks per SM, one copies while the
+//              other computes): S = Q K^T (4 x 4 scores per thread), P = 2^(S - m), O = 2^(m_old -
+//              m) O + P V (4 x d/16).  Bound by fp32 FMAs and their operands' shared loads (16
+//              FMAs per 16-byte load).
+//   few rows   (at most 8, so the single token of any group): a warp takes 32 keys at a time, one
+//              per lane for the scores, all of them by columns for the product with V; the warps'
+//              results are joined at the end.  With 64-row tiles 15 of 16 threads would idle.
+// The keys of a tile are split over several blocks when there are few tiles (no split below 4
+// steps); a second launch joins their partial (m, l, O) in order.  Tiles are found from cu_q
+// through slots, as in append_chunk.cu: sequence b owns floor(cu[b] G / 64) + b onward, at least
+// ceil(n G / 64).
 //
-// Masked scores never enter: P is 0 there, and in a tile that holds a masked pair (the causal
+// Masked scores never enter: P is 0 there, and in a step that holds a masked pair (the causal
 // border) the product with V is selected away too, because 0 * V is not 0 when V is not finite.
+#include <algorithm>
+
 #include "kernels.h"
 
 namespace santa {
@@ -21,13 +29,25 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRows = 64;        // query rows per tile
 constexpr int kKeys = 64;        // keys per step (divides both page sizes)
+constexpr int kMinSpan = 4;      // steps below which a tile is not split
+constexpr int kFew = 8;          // rows of the few-rows way
+constexpr int kWarps = kThreads / 32;
 
 template <int D>
 struct SimtSmem {
   float q[kRows][D + 4];         // +4: rows 16 apart would share banks
-  float k[kKeys][D + 4];
+  union {
+    float k[kKeys][D + 4];
+    float p[kRows][kKeys + 4];   // once the scores are formed
+  };
   float v[kKeys][D];
-  float p[kRows][kKeys + 4];
+};
+template <int D>
+struct FewSmem {
+  float q[kFew][D];
+  float p[kWarps][32][kFew];
+  float m[kWarps][kFew], l[kWarps][kFew];
+  float o[kWarps][kFew][D];
 };
 
 __device__ __forceinline__ float4 load4(const void* base, int64_t elem) {
@@ -42,9 +62,12 @@ struct Tile {
   int64_t first, n, len;   // first token row, new tokens, cached tokens (with the chunk)
   int64_t row0;            // first of the sequence's n * G rows in this tile
   int64_t keys;            // cached tokens that some row of the tile sees
+  int64_t steps;           // of 64 keys
+  int splits;              // blocks that share them
 };
 
-__device__ __forceinline__ bool find_tile(const ChunkParams& p, int64_t slot, int G, Tile* t) {
+__device__ __forceinline__ bool find_tile(const ChunkParams& p, int64_t slot, int G, int splits,
+                                          Tile* t) {
   // s(b) = floor(cu[b] * G / 64) + b: the search multiplies through 64-bit values
   const int lane = threadIdx.x & 31;
   int lo = 0, hi = p.batch;
@@ -77,7 +100,160 @@ __device__ __forceinline__ bool find_tile(const ChunkParams& p, int64_t slot, in
   if (j < 0 || t->row0 >= t->n * G) return false;
   const int64_t last = min(t->row0 + kRows, t->n * G) - 1;
   t->keys = t->len - t->n + last / G + 1;
+  t->steps = (t->keys + kKeys - 1) / kKeys;
+  t->splits = static_cast<int>(
+      min(static_cast<int64_t>(splits), (t->steps + kMinSpan - 1) / kMinSpan));
   return true;
+}
+
+// A row's result: the output, or the partial one of this split.  `cols` values from column c.
+__device__ __forceinline__ void finish4(const ChunkParams& p, const Tile& t, int64_t tile, int split,
+                                        int splits, int h, int G, int r, int D, int c, float4 o,
+                                        float m, float l, bool first, float* part_acc,
+                                        float* part_ml) {
+  const int64_t row = t.row0 + r;
+  if (t.splits == 1) {
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    store4(p.out, ((t.first + row / G) * p.num_q_heads + h * G + row % G) * D + c,
+           make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+  } else {
+    const int64_t at = (tile * splits + split) * kRows + r;
+    if (first) {
+      part_ml[2 * at] = m;
+      part_ml[2 * at + 1] = l;
+    }
+    *reinterpret_cast<float4*>(part_acc + at * D + c) = o;
+  }
+}
+
+// The pool element of key `tok` (0 of its row); a page out of range is reported and read as 0.
+__device__ __forceinline__ int64_t key_at(const ChunkParams& p, int b, int h, int64_t tok, int D,
+                                          bool report) {
+  int64_t page = p.page_table[static_cast<int64_t>(b) * p.max_teams + tok / p.team_size];
+  if (page < 0 || page >= p.num_pages) {
+    if (report) set_status(p.status, SANTA_DEV_BAD_PAGE);
+    page = 0;
+  }
+  return ((page * p.num_kv_heads + h) * p.team_size + tok % p.team_size) * static_cast<int64_t>(D);
+}
+
+template <int D>
+__device__ void few_rows(const ChunkParams& p, const Tile& t, FewSmem<D>& s, int G, int h,
+                         int64_t tile, int split, int splits, int64_t s0, int64_t s1,
+                         float* part_acc, float* part_ml) {
+  constexpr int kCols = D / 32;                 // columns of O per lane
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(kFew), t.n * G - t.row0));
+  for (int i = threadIdx.x; i < kFew * D; i += kThreads) {
+    const int r = i / D;
+    const int64_t row = t.row0 + r;
+    s.q[r][i % D] =
+        r < rows ? static_cast<const float*>(p.q)[((t.first + row / G) * p.num_q_heads + h * G +
+                                                   row % G) * D + i % D]
+                 : 0.f;
+  }
+  int64_t sees[kFew];
+#pragma unroll
+  for (int r = 0; r < kFew; ++r)
+    sees[r] = r < rows ? t.len - t.n + (t.row0 + r) / G + 1 : 0;
+  const int64_t all_see = t.len - t.n + t.row0 / G + 1;
+  __syncthreads();
+  float m[kFew], l[kFew], o[kFew][kCols];
+#pragma unroll
+  for (int r = 0; r < kFew; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) o[r][c] = 0.f;
+  }
+  const int64_t end = min(s1 * kKeys, t.keys);
+  for (int64_t k0 = s0 * kKeys + warp * 32; k0 < end; k0 += kWarps * 32) {
+    const int count = static_cast<int>(min(static_cast<int64_t>(32), end - k0));
+    const int64_t base = key_at(p, t.b, h, k0, D, lane == 0);      // 32 keys share a page
+    const float* k = static_cast<const float*>(p.k_pool) + base + min(lane, count - 1) * D;
+    float a[kFew];
+#pragma unroll
+    for (int r = 0; r < kFew; ++r) a[r] = 0.f;
+#pragma unroll 4
+    for (int e = 0; e < D; e += 4) {
+      const float4 kv = *reinterpret_cast<const float4*>(k + e);
+#pragma unroll
+      for (int r = 0; r < kFew; ++r) {
+        const float4 q = *reinterpret_cast<const float4*>(&s.q[r][e]);
+        a[r] = fmaf(q.x, kv.x, fmaf(q.y, kv.y, fmaf(q.z, kv.z, fmaf(q.w, kv.w, a[r]))));
+      }
+    }
+    float w[kFew];
+#pragma unroll
+    for (int r = 0; r < kFew; ++r) {
+      const float x = lane < count && k0 + lane < sees[r] ? a[r] * p.scale_log2 : -INFINITY;
+      const float mn = fmaxf(m[r], warp_max(x));
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      const float keep = exp2f(m[r] - ref);
+      w[r] = exp2f(x - ref);
+      l[r] = l[r] * keep + w[r];                // this lane's keys; summed over lanes at the end
+      m[r] = mn;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) o[r][c] *= keep;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < kFew; r += 4)
+      *reinterpret_cast<float4*>(&s.p[warp][lane][r]) =
+          make_float4(w[r], w[r + 1], w[r + 2], w[r + 3]);
+    __syncwarp();
+    const float* v = static_cast<const float*>(p.v_pool) + base + lane * kCols;
+    const bool border = k0 + 32 > all_see;
+#pragma unroll 8
+    for (int j = 0; j < count; ++j) {
+      float x[kCols];
+#pragma unroll
+      for (int c = 0; c < kCols; c += 2) {
+        const float2 v2 = *reinterpret_cast<const float2*>(v + j * D + c);
+        x[c] = v2.x;
+        x[c + 1] = v2.y;
+      }
+#pragma unroll
+      for (int r = 0; r < kFew; ++r) {
+        const float pw = s.p[warp][j][r];
+        if (!border || k0 + j < sees[r])
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) o[r][c] = fmaf(pw, x[c], o[r][c]);
+      }
+    }
+  }
+  // the warps' results, joined in order
+#pragma unroll
+  for (int r = 0; r < kFew; ++r) {
+    l[r] = warp_sum(l[r]);
+    if (lane == 0) {
+      s.m[warp][r] = m[r];
+      s.l[warp][r] = l[r];
+    }
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) s.o[warp][r][lane * kCols + c] = o[r][c];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+    const int r = i / (D / 4), c = i % (D / 4) * 4;
+    float mm = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s.m[w][r]);
+    const float ref = mm == -INFINITY ? 0.f : mm;
+    float ll = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = exp2f(s.m[w][r] - ref);
+      const float4 x = *reinterpret_cast<const float4*>(&s.o[w][r][c]);
+      ll = fmaf(f, s.l[w][r], ll);
+      acc.x = fmaf(f, x.x, acc.x);
+      acc.y = fmaf(f, x.y, acc.y);
+      acc.z = fmaf(f, x.z, acc.z);
+      acc.w = fmaf(f, x.w, acc.w);
+    }
+    finish4(p, t, tile, split, splits, h, G, r, D, c, acc, mm, ll, c == 0, part_acc, part_ml);
+  }
 }
 
 template <int D>
@@ -92,12 +268,16 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(ChunkParams p, 
   grid_dependency_wait();
   if (blockIdx.x == 0 && h == 0 && split == 0) check_bounds(p.cu_q, p.batch, p.num_tokens, p.status);
   Tile t;
-  if (!find_tile(p, blockIdx.x, G, &t)) return;
+  if (!find_tile(p, blockIdx.x, G, splits, &t) || split >= t.splits) return;
+  const int64_t tile = static_cast<int64_t>(blockIdx.x) * p.num_kv_heads + h;
+  const int64_t per = (t.steps + t.splits - 1) / t.splits;
+  const int64_t s0 = split * per, s1 = min(t.steps, s0 + per);
+  if (t.n * G - t.row0 <= kFew) {
+    few_rows<D>(p, t, *reinterpret_cast<FewSmem<D>*>(raw), G, h, tile, split, splits, s0, s1,
+                part_acc, part_ml);
+    return;
+  }
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  const int64_t steps = (t.keys + kKeys - 1) / kKeys;
-  const int64_t per = (steps + splits - 1) / splits;
-  const int64_t s0 = split * per, s1 = min(steps, s0 + per);
-
   for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
     const int r = i / (D / 4), c = i % (D / 4) * 4;
     const int64_t row = t.row0 + r;
@@ -106,12 +286,14 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(ChunkParams p, 
       x = load4(p.q, ((t.first + row / G) * p.num_q_heads + h * G + row % G) * D + c);
     *reinterpret_cast<float4*>(&s.q[r][c]) = x;
   }
-  // keys that row ty * 4 + i sees
-  int64_t sees[4];
+  // keys that row ty * 4 + i sees, from this split's first key on
+  int sees[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t row = t.row0 + ty * 4 + i;
-    sees[i] = row < t.n * G ? t.len - t.n + row / G + 1 : 0;
+    sees[i] = row < t.n * G
+                  ? static_cast<int>(max(t.len - t.n + row / G + 1 - s0 * kKeys, static_cast<int64_t>(0)))
+                  : 0;
   }
   const int64_t all_see = t.len - t.n + t.row0 / G + 1;   // keys that every row sees
 
@@ -128,25 +310,25 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(ChunkParams p, 
 
   for (int64_t step = s0; step < s1; ++step) {
     const int64_t tok0 = step * kKeys;
-    int64_t page = p.page_table[static_cast<int64_t>(t.b) * p.max_teams + tok0 / p.team_size];
-    if (page < 0 || page >= p.num_pages) {
-      if (threadIdx.x == 0) set_status(p.status, SANTA_DEV_BAD_PAGE);
-      page = 0;
-    }
-    const int64_t base =
-        ((page * p.num_kv_heads + h) * p.team_size + tok0 % p.team_size) * static_cast<int64_t>(D);
+    const int at = static_cast<int>(tok0 - s0 * kKeys);
+    const int64_t base = key_at(p, t.b, h, tok0, D, threadIdx.x == 0);
     const int valid = static_cast<int>(min(static_cast<int64_t>(kKeys), t.keys - tok0));
     __syncthreads();
-    for (int i = threadIdx.x; i < kKeys * (D / 4); i += kThreads) {
-      const int r = i / (D / 4), c = i % (D / 4) * 4;
-      float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
-      if (r < valid) {
-        kx = load4(p.k_pool, base + r * D + c);
-        vx = load4(p.v_pool, base + r * D + c);
+    // K, then V, each its own group of asynchronous copies; rows that no row sees are zeros
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      const float* src = static_cast<const float*>(kv ? p.v_pool : p.k_pool) + base;
+      for (int i = threadIdx.x; i < kKeys * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), c = i % (D / 4) * 4;
+        float* dst = kv ? &s.v[r][c] : &s.k[r][c];
+        if (r < valid)
+          cp_async16(dst, src + r * D + c);
+        else
+          *reinterpret_cast<float4*>(dst) = make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      *reinterpret_cast<float4*>(&s.k[r][c]) = kx;
-      *reinterpret_cast<float4*>(&s.v[r][c]) = vx;
+      asm volatile("cp.async.commit_group;" ::: "memory");
     }
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
     __syncthreads();
     // S = Q K^T: rows ty * 4 + i, keys tx + 16 j
     float a[4][4];
@@ -169,12 +351,14 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(ChunkParams p, 
                     fmaf(qv[i].z, kv[j].z, fmaf(qv[i].w, kv[j].w, a[i][j]))));
     }
     const bool border = tok0 + kKeys > all_see;           // some pair of this step is masked
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();                                      // K is read, V is there
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float mx = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        a[i][j] = tok0 + tx + 16 * j < sees[i] ? a[i][j] * p.scale_log2 : -INFINITY;
+        a[i][j] = at + tx + 16 * j < sees[i] ? a[i][j] * p.scale_log2 : -INFINITY;
         mx = fmaxf(mx, a[i][j]);
       }
 #pragma unroll
@@ -223,48 +407,33 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(ChunkParams p, 
           }
       }
     } else {
+#pragma unroll 2
       for (int j = 0; j < valid; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (tok0 + j < sees[i]) {
-            const float w = s.p[ty * 4 + i][j];
+        for (int c = 0; c < kCols; ++c) {
+          const float4 v = *reinterpret_cast<const float4*>(&s.v[j][tx * 4 + 64 * c]);
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) {
-              const float4 v = *reinterpret_cast<const float4*>(&s.v[j][tx * 4 + 64 * c]);
+          for (int i = 0; i < 4; ++i) {
+            const float w = s.p[ty * 4 + i][j];
+            if (at + j < sees[i]) {
               o[i][c][0] = fmaf(w, v.x, o[i][c][0]);
               o[i][c][1] = fmaf(w, v.y, o[i][c][1]);
               o[i][c][2] = fmaf(w, v.z, o[i][c][2]);
               o[i][c][3] = fmaf(w, v.w, o[i][c][3]);
             }
           }
+        }
     }
   }
 
-  const int64_t tile = static_cast<int64_t>(blockIdx.x) * p.num_kv_heads + h;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t row = t.row0 + ty * 4 + i;
-    if (row >= t.n * G) continue;
-    if (splits == 1) {
-      const float inv = l[i] > 0.f || l[i] != l[i] ? 1.f / l[i] : 0.f;
-      const int64_t out = ((t.first + row / G) * p.num_q_heads + h * G + row % G) * D;
+  for (int i = 0; i < 4; ++i)
+    if (t.row0 + ty * 4 + i < t.n * G)
 #pragma unroll
       for (int c = 0; c < kCols; ++c)
-        store4(p.out, out + tx * 4 + 64 * c,
-                     make_float4(o[i][c][0] * inv, o[i][c][1] * inv, o[i][c][2] * inv,
-                                 o[i][c][3] * inv));
-    } else {
-      const int64_t at = (tile * splits + split) * kRows + ty * 4 + i;
-      if (tx == 0) {
-        part_ml[2 * at] = m[i];
-        part_ml[2 * at + 1] = l[i];
-      }
-#pragma unroll
-      for (int c = 0; c < kCols; ++c)
-        *reinterpret_cast<float4*>(part_acc + at * D + tx * 4 + 64 * c) =
-            make_float4(o[i][c][0], o[i][c][1], o[i][c][2], o[i][c][3]);
-    }
-  }
+        finish4(p, t, tile, split, splits, h, G, ty * 4 + i, D, tx * 4 + 64 * c,
+                make_float4(o[i][c][0], o[i][c][1], o[i][c][2], o[i][c][3]), m[i], l[i],
+                tx == 0 && c == 0, part_acc, part_ml);
 }
 
 // Joins a tile's partial results in split order: one warp per row.
@@ -276,7 +445,7 @@ __global__ void __launch_bounds__(kThreads) chunk_join_kernel(ChunkParams p, int
   const int h = blockIdx.y;
   grid_dependency_wait();
   Tile t;
-  if (!find_tile(p, blockIdx.x, G, &t)) return;
+  if (!find_tile(p, blockIdx.x, G, splits, &t) || t.splits == 1) return;
   const int lane = threadIdx.x & 31;
   const int64_t tile = static_cast<int64_t>(blockIdx.x) * p.num_kv_heads + h;
   constexpr int kVals = D / 32;
@@ -287,10 +456,10 @@ __global__ void __launch_bounds__(kThreads) chunk_join_kernel(ChunkParams p, int
     float m = -INFINITY, l = 0.f, acc[kVals];
 #pragma unroll
     for (int e = 0; e < kVals; ++e) acc[e] = 0.f;
-    for (int i = 0; i < splits; ++i)
+    for (int i = 0; i < t.splits; ++i)
       m = fmaxf(m, __ldg(part_ml + 2 * ((tile * splits + i) * kRows + r)));
     const float ref = m == -INFINITY ? 0.f : m;
-    for (int i = 0; i < splits; ++i) {
+    for (int i = 0; i < t.splits; ++i) {
       const int64_t at = (tile * splits + i) * kRows + r;
       const float mi = __ldg(part_ml + 2 * at);
       const float w = exp2f(mi - ref);                    // 0 for a split that saw nothing
@@ -314,7 +483,8 @@ cudaError_t launch(const ChunkParams& p, int splits, float* part_acc, float* par
   const int G = p.num_q_heads / p.num_kv_heads;
   const int64_t slots = chunk_simt_tiles(p.num_tokens, p.batch, G, 1);
   static std::atomic<unsigned long long> done{0};
-  cudaError_t e = ensure_dynamic_smem(chunk_simt_kernel<D>, sizeof(SimtSmem<D>), done);
+  constexpr size_t kSmem = std::max(sizeof(SimtSmem<D>), sizeof(FewSmem<D>));
+  cudaError_t e = ensure_dynamic_smem(chunk_simt_kernel<D>, kSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -322,7 +492,7 @@ cudaError_t launch(const ChunkParams& p, int splits, float* part_acc, float* par
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(slots), p.num_kv_heads, splits);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = sizeof(SimtSmem<D>);
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -341,11 +511,11 @@ int64_t chunk_simt_tiles(int64_t num_tokens, int batch, int group, int num_kv_he
   return (num_tokens * group / kRows + batch) * num_kv_heads;
 }
 
-// Enough blocks to fill the device twice over (two are resident per SM), unless a block would
-// be left with fewer than 4 steps of the longest sequence.
+// Enough blocks to fill the device twice over (two are resident per SM), and no more than the
+// longest possible sequence can use.
 int chunk_simt_splits(int64_t tiles, int64_t max_len, int sms) {
   const int64_t want = (4 * static_cast<int64_t>(sms) + tiles - 1) / tiles;
-  const int64_t most = (max_len + 4 * kKeys - 1) / (4 * kKeys);
+  const int64_t most = (max_len + kMinSpan * kKeys - 1) / (kMinSpan * kKeys);
   const int64_t s = want < most ? want : most;
   return static_cast<int>(s < 1 ? 1 : s > 64 ? 64 : s);
 }

@@ -1,8 +1,8 @@
 // select_topk.cu — the M teams of best representative score, for every unit (sequence, KV head).
 //
-// One cluster per unit.  Each CTA scores a slice of the unit's teams in fp32 (16 lanes per
-// team, the group's queries in registers) and stores the scores in the first CTA's shared
-// memory; the first CTA then finds the border of the best M and writes S.
+// One cluster per unit.  Each CTA scores some of the unit's teams in fp32 (16 lanes per
+// team, two teams at a time) and stores the scores in the first CTA's shared memory; the first
+// CTA then finds the border of the best M and writes S.
 //
 // Exactness.  S is the set that 64-bit scores give.  An fp32 score of d <= 128 products, 8 per
 // lane and 16 lanes joined by a tree, is off by at most E = 16 * 2^-24 * |q||rep|: each product
@@ -34,10 +34,22 @@ __device__ __forceinline__ float key_score(uint32_t k) {
 __device__ __forceinline__ void store_cluster_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
-               ::: "memory");
+// The two halves of a cluster barrier, by every thread of every CTA of the cluster.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void cluster_wait_acquire() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+struct SelShared {
+  unsigned long long low[256], high[256];                 // keys of a digit
+  uint32_t hist[256];
+  int pick[2];                                            // digit, place within it
+  int scan[kSelThreads / 32];
+  uint32_t top[kSelThreads / 32];
+  uint32_t norm_q, norm_rep;                              // bits of the largest |q|^2, |rep|^2
+};
 
 // Exclusive prefix sum over the block's threads, and the total.
 __device__ __forceinline__ int block_scan(int v, int* buf, int* total) {
@@ -91,161 +103,255 @@ __device__ uint64_t exact_key(const SelectParams& p, int64_t page, int b, int h,
   return u >> 63 ? ~u : u | 1ull << 63;
 }
 
-// The *left-th largest of the n keys in shared memory, one byte at a time from the top; *left
-// becomes its place among the keys equal to it.  All threads get both.
-template <typename Key>
-__device__ Key kth_largest(const Key* keys, int n, int* left, uint32_t* hist, uint32_t* pick) {
-  Key prefix = 0, mask = 0;
-  int want = *left;
-  for (int shift = 8 * sizeof(Key) - 8; shift >= 0; shift -= 8) {
-    for (int i = threadIdx.x; i < 256; i += kSelThreads) hist[i] = 0u;
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kSelThreads)
-      if ((keys[i] & mask) == prefix)
-        atomicAdd(&hist[static_cast<uint32_t>(keys[i] >> shift) & 255u], 1u);
-    __syncthreads();
-    if (threadIdx.x < 32) {
-      // lane l holds the digits 255 - 8 l .. 248 - 8 l: lanes and digits go down together
-      int c[8], sum = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum += c[e] = hist[255 - (threadIdx.x * 8 + e)];
-      int before = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, before, o);
-        if (static_cast<int>(threadIdx.x) >= o) before += y;
-      }
-      before -= sum;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (before < want && want <= before + c[e]) {
-          pick[0] = 255 - (threadIdx.x * 8 + e);
-          pick[1] = want - before;
-        }
-        before += c[e];
-      }
-    }
-    __syncthreads();
-    prefix |= static_cast<Key>(pick[0]) << shift;
-    mask |= static_cast<Key>(255u) << shift;
-    want = pick[1];
+// One counting pass over the keys in [lo, hi] of the n in shared memory, digit(key) a monotone
+// map to 0 .. 255: the digit that holds the *want-th largest of them becomes the new [lo, hi]
+// (the smallest and largest key in it), *want the place within it.
+template <typename Key, typename Digit>
+__device__ __forceinline__ void narrow(const Key* keys, int n, Key& lo, Key& hi, int& want,
+                                       SelShared& s, Digit digit) {
+  Key* low = reinterpret_cast<Key*>(s.low);
+  Key* high = reinterpret_cast<Key*>(s.high);
+  for (int i = threadIdx.x; i < 256; i += kSelThreads) {
+    s.hist[i] = 0u;
+    low[i] = ~static_cast<Key>(0);
+    high[i] = 0;
   }
   __syncthreads();
-  *left = want;
-  return prefix;
+  for (int i = threadIdx.x; i < n; i += kSelThreads) {
+    const Key k = keys[i];
+    if (k >= lo && k <= hi) {
+      const uint32_t d = digit(k);
+      atomicAdd(&s.hist[d], 1u);
+      atomicMin(&low[d], k);
+      atomicMax(&high[d], k);
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    // lane l holds the digits 255 - 8 l .. 248 - 8 l: lanes and digits go down together
+    int c[8], sum = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum += c[e] = s.hist[255 - (threadIdx.x * 8 + e)];
+    int before = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, before, o);
+      if (static_cast<int>(threadIdx.x) >= o) before += y;
+    }
+    before -= sum;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (before < want && want <= before + c[e]) {
+        s.pick[0] = 255 - (threadIdx.x * 8 + e);
+        s.pick[1] = want - before;
+      }
+      before += c[e];
+    }
+  }
+  __syncthreads();
+  lo = low[s.pick[0]];
+  hi = high[s.pick[0]];
+  want = s.pick[1];
+  __syncthreads();
+}
+
+// The *left-th largest of the n keys; *left becomes its place among the keys equal to it.  All
+// threads get both.  The first pass over fp32 scores takes equal parts of their range (leading
+// bits would put nearly all scores, which share sign and exponent, into a few counters); the
+// passes after it take 8 bits from the highest in which the remaining keys differ, so at most
+// sizeof(Key) of them.  Two passes in all for most sets of scores.
+template <typename Key>
+__device__ Key kth_largest(const Key* keys, int n, int* left, SelShared& s) {
+  Key lo = 0, hi = ~static_cast<Key>(0);
+  if constexpr (sizeof(Key) == 4) {
+    lo = ~static_cast<Key>(0);
+    hi = 0;
+    for (int i = threadIdx.x; i < n; i += kSelThreads) {
+      lo = min(lo, keys[i]);
+      hi = max(hi, keys[i]);
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if ((threadIdx.x & 31) == 0) {
+      s.scan[threadIdx.x / 32] = static_cast<int>(lo);
+      s.top[threadIdx.x / 32] = hi;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kSelThreads / 32; ++w) {
+      lo = min(lo, static_cast<Key>(s.scan[w]));
+      hi = max(hi, s.top[w]);
+    }
+    const float from = key_score(lo), per = 255.f / (key_score(hi) - from);
+    // not for infinite scores, nor a range that is empty or overflows
+    if (lo < hi && from > -INFINITY && per > 0.f && per < INFINITY)
+      narrow(keys, n, lo, hi, *left, s, [&](Key k) {
+        return static_cast<uint32_t>(fminf((key_score(k) - from) * per, 255.f));
+      });
+  }
+  while (lo != hi) {
+    const int top = 64 - __clzll(static_cast<unsigned long long>(lo ^ hi));
+    const int shift = top > 8 ? top - 8 : 0;
+    narrow(keys, n, lo, hi, *left, s, [&](Key k) {
+      return static_cast<uint32_t>(k >> shift) & ((1u << (top - shift)) - 1u);
+    });
+  }
+  return hi;
 }
 
 template <bool BF16, int D>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(SelectParams p) {
+__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(SelectParams p) {
   extern __shared__ __align__(16) uint32_t keys[];        // fp32 keys, then 64-bit keys (CTA 0)
-  __shared__ float q_s[kMaxGroup * D];
-  __shared__ int buf[kSelThreads / 32];
-  __shared__ uint32_t norm_max;                           // bits of max |rep|^2 (CTA 0)
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t pick[2];                            // digit and what is left
-  constexpr int kPer = D / kLanes;                        // elements per lane (8 or 4)
+  __shared__ __align__(16) float q_s[kMaxGroup * D];
+  __shared__ SelShared s;
+  constexpr int kQuads = D / (4 * kLanes);                // float4 pieces per lane (2 or 1)
+  constexpr int kTeams = 2;                               // teams per 16 lanes in a round
+  constexpr int kRound = kSelThreads / kLanes * kTeams;   // teams per CTA in a round
   const int G = p.num_q_heads / p.num_kv_heads;
   const int rank = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int CL = gridDim.x;
   const int64_t unit = static_cast<int64_t>(b) * p.num_kv_heads + h;
-  if (threadIdx.x == 0) norm_max = 0u;
+  if (threadIdx.x == 0) s.norm_q = s.norm_rep = 0u;
+  cluster_arrive();                                       // waited for before the first store
   grid_dependency_wait();
+  grid_launch_dependents();
+  // Rounds of 32 teams are dealt out to the CTAs in turn, so which teams a thread scores does not
+  // depend on the length, and the first page ids are on their way together with it and the
+  // queries (each is a read from DRAM when the cache is larger than L2).
+  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const int32_t* table = p.page_table + static_cast<int64_t>(b) * p.max_teams;
+  auto load_ids = [&](int base, int(&to)[kTeams]) {
+#pragma unroll
+    for (int u = 0; u < kTeams; ++u) {
+      const int team = base + u * (kSelThreads / kLanes) + group;
+      to[u] = team < p.max_teams ? __ldg(table + team) : -1;
+    }
+  };
+  int page[kTeams], page_next[kTeams];
+  load_ids(rank * kRound, page);
+  load_ids((rank + CL) * kRound, page_next);
   const int64_t len = p.seq_lens[b];
+  // the unit's group of queries, zero beyond it
+  for (int i = threadIdx.x; i < kMaxGroup * D; i += kSelThreads)
+    q_s[i] = i < G * D ? q_at<BF16>(p.q, (static_cast<int64_t>(b) * p.num_q_heads + h * G) * D + i)
+                       : 0.f;
   const bool ok = len >= 1 && len <= static_cast<int64_t>(p.max_teams) * p.team_size;
   const int n = ok ? static_cast<int>((len + p.team_size - 1) / p.team_size) : 0;
-  // the unit's group of queries, zero beyond it (heads of a group of less than 8)
-  for (int i = threadIdx.x; i < kMaxGroup * D; i += kSelThreads) {
-    const int g = i / D;
-    q_s[i] = g < G ? q_at<BF16>(p.q, (static_cast<int64_t>(b) * p.num_q_heads + h * G) * D + i)
-                   : 0.f;
-  }
-  if (CL > 1) cluster_sync(); else __syncthreads();
 
-  // ---- scores of this CTA's slice of the teams
+  // ---- scores of this CTA's teams
   {
-    const int lane = threadIdx.x % kLanes, team_lane = threadIdx.x / kLanes;
-    float q[kMaxGroup][kPer];
-#pragma unroll
-    for (int g = 0; g < kMaxGroup; ++g)
-#pragma unroll
-      for (int e = 0; e < kPer; e += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(
-            q_s + g * D + (e / 4) * (4 * kLanes) + lane * 4);
-        q[g][e] = v.x; q[g][e + 1] = v.y; q[g][e + 2] = v.z; q[g][e + 3] = v.w;
-      }
     const uint32_t keys0 = cluster_addr(smem_u32(keys), 0);
-    const int per = (n + CL - 1) / CL;
-    const int lo = rank * per, hi = min(n, lo + per);
     uint32_t norm = 0u;
-    // whole warps stay together for the shuffles
-    for (int base = lo; base < hi; base += kSelThreads / kLanes) {
-      const int team = base + team_lane;
-      int64_t page = -1;
-      if (team < hi) {
-        page = p.page_table[static_cast<int64_t>(b) * p.max_teams + team];
-        if (page < 0 || page >= p.num_pages) {
+    bool waited = false;
+    float4 r[kTeams][kQuads], r_next[kTeams][kQuads];
+    // representatives of a round; a team behind the end or with a bad page id scores nothing
+    auto load_reps = [&](int base, int(&from)[kTeams], float4(&to)[kTeams][kQuads]) {
+#pragma unroll
+      for (int u = 0; u < kTeams; ++u) {
+        const int team = base + u * (kSelThreads / kLanes) + group;
+        if (team >= n) {
+          from[u] = -1;
+        } else if (from[u] < 0 || from[u] >= p.num_pages) {
           if (lane == 0) set_status(p.status, SANTA_DEV_BAD_PAGE);
-          page = -1;
+          from[u] = -1;
         }
+#pragma unroll
+        for (int e = 0; e < kQuads; ++e)
+          to[u][e] = from[u] < 0
+                         ? make_float4(0.f, 0.f, 0.f, 0.f)
+                         : __ldg(reinterpret_cast<const float4*>(
+                                     p.reps + (static_cast<int64_t>(from[u]) * p.num_kv_heads + h) * D) +
+                                 e * kLanes + lane);
       }
-      float s[kMaxGroup], nn = 0.f;
-#pragma unroll
-      for (int g = 0; g < kMaxGroup; ++g) s[g] = 0.f;
-      if (page >= 0) {
-        const float4* rep =
-            reinterpret_cast<const float4*>(p.reps + (page * p.num_kv_heads + h) * D);
-#pragma unroll
-        for (int e = 0; e < kPer; e += 4) {
-          const float4 r = __ldg(rep + (e / 4) * kLanes + lane);
-          nn = fmaf(r.x, r.x, fmaf(r.y, r.y, fmaf(r.z, r.z, fmaf(r.w, r.w, nn))));
-#pragma unroll
-          for (int g = 0; g < kMaxGroup; ++g)
-            s[g] = fmaf(q[g][e], r.x, fmaf(q[g][e + 1], r.y,
-                   fmaf(q[g][e + 2], r.z, fmaf(q[g][e + 3], r.w, s[g]))));
-        }
-      }
-      // sums over the 16 lanes: each step halves the heads a lane keeps (8, 4, 2, 1)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const bool up = lane & 8;
-        const float other = __shfl_xor_sync(0xffffffffu, up ? s[g] : s[g + 4], 8);
-        s[g] = (up ? s[g + 4] : s[g]) + other;
-      }
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const bool up = lane & 4;
-        const float other = __shfl_xor_sync(0xffffffffu, up ? s[g] : s[g + 2], 4);
-        s[g] = (up ? s[g + 2] : s[g]) + other;
-      }
-      {
-        const bool up = lane & 2;
-        const float other = __shfl_xor_sync(0xffffffffu, up ? s[0] : s[1], 2);
-        s[0] = (up ? s[1] : s[0]) + other;
-      }
-      s[0] += __shfl_xor_sync(0xffffffffu, s[0], 1);
-      // lane holds head (lane & 8 ? 4 : 0) + (lane & 4 ? 2 : 0) + (lane & 2 ? 1 : 0)
-      const int head = ((lane >> 3) & 1) * 4 + ((lane >> 2) & 1) * 2 + ((lane >> 1) & 1);
-      bool nan = head < G && s[0] != s[0];
-      float best = head < G ? s[0] : -INFINITY;
-#pragma unroll
-      for (int o = 2; o < kLanes; o <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-      const unsigned nans = __ballot_sync(0xffffffffu, nan);
-      nan = (nans >> (threadIdx.x & 16)) & 0xffffu;
-#pragma unroll
-      for (int o = 1; o < kLanes; o <<= 1) nn += __shfl_xor_sync(0xffffffffu, nn, o);
-      if (team < hi && lane == 0)
-        store_cluster_u32(keys0 + team * 4, page < 0 || nan ? 0u : score_key(best));
-      // bits of non-negative values order like the values; inf and NaN come out on top
-      if (page >= 0) norm = max(norm, __float_as_uint(nn) & 0x7fffffffu);
+    };
+    load_reps(rank * kRound, page, r);
+    __syncthreads();
+    // meanwhile |q|^2, a warp per head
+    for (int g = threadIdx.x / 32; g < G; g += kSelThreads / 32) {
+      float x = 0.f;
+      for (int e = threadIdx.x & 31; e < D; e += 32) x = fmaf(q_s[g * D + e], q_s[g * D + e], x);
+      x = warp_sum(x);
+      if ((threadIdx.x & 31) == 0) atomicMax(&s.norm_q, __float_as_uint(x) & 0x7fffffffu);
     }
+    // whole warps stay together for the shuffles; representatives are loaded one round ahead,
+    // page ids two
+#pragma unroll 1
+    for (int base = rank * kRound; base < n; base += CL * kRound) {
+      load_reps(base + CL * kRound, page_next, r_next);
+      int page_after[kTeams];
+      load_ids(base + 2 * CL * kRound, page_after);
+      float a[kTeams][kMaxGroup], nn[kTeams];
+#pragma unroll
+      for (int u = 0; u < kTeams; ++u) {
+        nn[u] = 0.f;
+#pragma unroll
+        for (int g = 0; g < kMaxGroup; ++g) a[u][g] = 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < kQuads; ++e) {
+#pragma unroll
+        for (int u = 0; u < kTeams; ++u)
+          nn[u] = fmaf(r[u][e].x, r[u][e].x, fmaf(r[u][e].y, r[u][e].y,
+                  fmaf(r[u][e].z, r[u][e].z, fmaf(r[u][e].w, r[u][e].w, nn[u]))));
+#pragma unroll
+        for (int g = 0; g < kMaxGroup; ++g) {
+          const float4 q = *reinterpret_cast<const float4*>(q_s + g * D + (e * kLanes + lane) * 4);
+#pragma unroll
+          for (int u = 0; u < kTeams; ++u)
+            a[u][g] = fmaf(q.x, r[u][e].x, fmaf(q.y, r[u][e].y,
+                      fmaf(q.z, r[u][e].z, fmaf(q.w, r[u][e].w, a[u][g]))));
+        }
+      }
+      // 16 sums over the 16 lanes, each step halving what a lane keeps: lane l ends with team
+      // (l >> 3) & 1 and head l & 7
+      const bool b3 = lane & 8, b2 = lane & 4, b1 = lane & 2, b0 = lane & 1;
+      float c[8], d[4], f[2];
+#pragma unroll
+      for (int g = 0; g < 8; ++g)
+        c[g] = (b3 ? a[1][g] : a[0][g]) + __shfl_xor_sync(0xffffffffu, b3 ? a[0][g] : a[1][g], 8);
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        d[g] = (b2 ? c[g + 4] : c[g]) + __shfl_xor_sync(0xffffffffu, b2 ? c[g] : c[g + 4], 4);
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+        f[g] = (b1 ? d[g + 2] : d[g]) + __shfl_xor_sync(0xffffffffu, b1 ? d[g] : d[g + 2], 2);
+      const float sum = (b0 ? f[1] : f[0]) + __shfl_xor_sync(0xffffffffu, b0 ? f[0] : f[1], 1);
+      const float norm2 = (b3 ? nn[1] : nn[0]) + __shfl_xor_sync(0xffffffffu, b3 ? nn[0] : nn[1], 8);
+      float best = (lane & 7) < G ? sum : -INFINITY, n2 = norm2;
+      // a NaN of any of the team's heads: its 8 lanes' bits of the warp's vote
+      const unsigned nans = __ballot_sync(0xffffffffu, (lane & 7) < G && sum != sum);
+      const bool nan = (nans >> (threadIdx.x & 24)) & 0xffu;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) {
+        best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+        n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+      }
+      // bits of non-negative values order like the values; inf and NaN come out on top
+      norm = max(norm, __float_as_uint(n2) & 0x7fffffffu);
+      if (!waited) cluster_wait_acquire();                // the first CTA is running
+      waited = true;
+      const int u = b3 ? 1 : 0, team = base + u * (kSelThreads / kLanes) + group;
+      if (team < n && (lane & 7) == 0)
+        store_cluster_u32(keys0 + team * 4,
+                          (b3 ? page[1] : page[0]) < 0 || nan ? 0u : score_key(best));
+#pragma unroll
+      for (int i = 0; i < kTeams; ++i) {
+        page[i] = page_next[i];
+        page_next[i] = page_after[i];
+#pragma unroll
+        for (int e = 0; e < kQuads; ++e) r[i][e] = r_next[i][e];
+      }
+    }
+    if (!waited) cluster_wait_acquire();
     const uint32_t top = __reduce_max_sync(0xffffffffu, norm);
     if ((threadIdx.x & 31) == 0) {
-      const uint32_t at = cluster_addr(smem_u32(&norm_max), 0);
+      const uint32_t at = cluster_addr(smem_u32(&s.norm_rep), 0);
       asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(at), "r"(top)
                    : "memory");
     }
   }
-  if (CL > 1) cluster_sync(); else __syncthreads();
+  cluster_arrive();
+  cluster_wait_acquire();
   if (rank != 0) return;
 
   // ---- the first CTA: the border of the best `keep`
@@ -268,20 +374,14 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectParams p) {
     return;
   }
   int left = keep;
-  const uint32_t border = kth_largest<uint32_t>(keys, n, &left, hist, pick);
+  const uint32_t border = kth_largest<uint32_t>(keys, n, &left, s);
 
   // ---- teams too close to the border for fp32 (see the top of the file); the norms are kept
   // away from zero so that products in the denormal range stay inside the bound
   const float t = key_score(border);
-  uint32_t qn = 0u;
-  for (int g = 0; g < G; ++g) {
-    float s = 0.f;
-    for (int e = threadIdx.x & 31; e < D; e += 32) s = fmaf(q_s[g * D + e], q_s[g * D + e], s);
-    qn = max(qn, __float_as_uint(warp_sum(s)) & 0x7fffffffu);
-  }
   const uint32_t tiny = 0x00800000u;                      // the smallest normal fp32
-  const float err = 16.f * 0x1p-24f * sqrtf(__uint_as_float(max(qn, tiny))) *
-                        sqrtf(__uint_as_float(max(norm_max, tiny))) + 0x1p-140f;
+  const float err = 16.f * 0x1p-24f * sqrtf(__uint_as_float(max(s.norm_q, tiny))) *
+                        sqrtf(__uint_as_float(max(s.norm_rep, tiny))) + 0x1p-140f;
   // an infinite or NaN bound (or a border of -inf) leaves every team to the 64-bit scores
   const bool finite = err < INFINITY && t > -INFINITY;
   const float above = finite ? t + 2.f * err : INFINITY, below = finite ? t - 2.f * err : -INFINITY;
@@ -289,19 +389,21 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectParams p) {
   const int i0 = min(n, static_cast<int>(threadIdx.x) * chunk), i1 = min(n, i0 + chunk);
   uint64_t in = 0u, near = 0u;
   for (int i = i0; i < i1; ++i) {
-    const float s = key_score(keys[i]);
-    if (s > above)
+    const float x = key_score(keys[i]);
+    if (x > above)
       in |= 1ull << (i - i0);
-    else if (s >= below)
+    else if (x >= below)
       near |= 1ull << (i - i0);
   }
-  int sure, near_total;
-  block_scan(__popcll(in), buf, &sure);
-  const int near_at = block_scan(__popcll(near), buf, &near_total);
-  int want = keep - sure;
+  // both counts in one scan (each at most 16384)
+  int total;
+  const int before = block_scan(__popcll(in) | __popcll(near) << 16, s.scan, &total);
+  const int near_at = before >> 16, near_total = total >> 16;
+  int out_at = (before & 0xffff) + near_at;               // as if every near team is taken
+  int want = keep - (total & 0xffff);
   if (near_total > want) {
     // the near teams' indices (over the fp32 keys, which are no longer needed) and 64-bit keys
-    uint64_t* exact = reinterpret_cast<uint64_t*>(keys + (p.max_teams + 3) / 4 * 4);
+    unsigned long long* exact = reinterpret_cast<unsigned long long*>(keys + (p.max_teams + 3) / 4 * 4);
     int at = near_at;
     for (uint64_t m = near; m; m &= m - 1) keys[at++] = i0 + __ffsll(m) - 1;
     __syncthreads();
@@ -315,21 +417,20 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectParams p) {
     __syncthreads();
     // the best `want` of them; `want` becomes how many of those at the border are taken, and
     // the list is in team order, so ties go to the lower index
-    const uint64_t last = kth_largest<uint64_t>(exact, near_total, &want, hist, pick);
+    const unsigned long long last = kth_largest<unsigned long long>(exact, near_total, &want, s);
     int ties = 0, all;
     for (int i = 0, e = near_at; i < __popcll(near); ++i, ++e) ties += exact[e] == last;
-    int tie_at = block_scan(ties, buf, &all);
+    int tie_at = block_scan(ties, s.scan, &all);
     at = near_at;
     for (uint64_t m = near; m; m &= m - 1, ++at)
       if (exact[at] > last || (exact[at] == last && tie_at++ < want)) in |= m & -m;
+    out_at = block_scan(__popcll(in), s.scan, &all);
   } else {
     in |= near;
   }
-  int total;
-  int at = block_scan(__popcll(in), buf, &total);
   for (; in; in &= in - 1) {
-    ids[at] = i0 + __ffsll(in) - 1;
-    pi[at++] = 1.f;
+    ids[out_at] = i0 + __ffsll(in) - 1;
+    pi[out_at++] = 1.f;
   }
 }
 

@@ -252,7 +252,7 @@ int santa_topk_decode(const santa_decode_args* a, void* stream) {
   b.mix_alpha = 0.f;
   int rc = santa::check_attend(&b);
   if (rc || (rc = santa_select_topk(&b, stream))) return rc;
-  return santa_attend(&b, stream);
+  return santa::attend_full_weights(&b, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -42,6 +42,9 @@
 //            completing on rank r's mbarrier); each CTA merges its slice in rank order.
 //            With NC > 1 the cluster partials go to global scratch and the last CTA of the
 //            unit (an atomic ticket, no waiting) merges them in cluster order.
+// Full weights (template flag FULL, bf16 attend-only steps): P enters the product with V as three
+// bf16 pieces, all its 24 bits, instead of two, and only the attend mode is compiled.
+//
 // Compact form (template flag FAST, bf16 steps with NC = 1).  FAST = 1 compiles a decode
 // step with i.i.d. Horvitz-Thompson draws alone; FAST = 2 adds the sampler variants, the
 // mixture and sampling-only steps.  Phases A and B are replaced by a shorter sequence: CTA r
@@ -429,7 +432,7 @@ __device__ __forceinline__ void score_teams(const DecodeParams& p, int b, int h,
 
 // ---------------------------------------------------------------- the kernel
 
-template <bool BF16, int D, int G, bool W, int FAST = 0>
+template <bool BF16, int D, int G, bool W, int FAST = 0, bool FULL = false>
 __global__ void __launch_bounds__(256, (DecodeTraits<BF16, D, G, W>::kMinBlocks))
     decode_kernel(const __grid_constant__ DecodeParams p) {
   using Tr = DecodeTraits<BF16, D, G, W>;
@@ -444,7 +447,8 @@ __global__ void __launch_bounds__(256, (DecodeTraits<BF16, D, G, W>::kMinBlocks)
   const int unit = b * p.num_kv_heads + h;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, lane16 = lane & 15;
   const int M = p.num_draws;
-  const int mode = FAST == 1 ? kModeDecode : p.mode;   // FAST = 2: decode or sample only
+  // FAST = 2: decode or sample only
+  const int mode = FAST == 1 ? kModeDecode : FULL ? kModeAttend : p.mode;
   const bool sampling = mode == kModeDecode || mode == kModeSample;
   const bool attending = mode != kModeSample;
   const bool writer = cidx == 0;          // the cluster that writes the sampling outputs
@@ -1461,6 +1465,13 @@ __global__ void __launch_bounds__(256, (DecodeTraits<BF16, D, G, W>::kMinBlocks)
       const uint32_t lo23 = pack_bf16(p2 - bf16_lo_f(hi23), p3 - bf16_hi_f(hi23));
       const uint32_t bh0 = movmatrix_trans(hi01), bh1 = movmatrix_trans(hi23);
       const uint32_t bl0 = movmatrix_trans(lo01), bl1 = movmatrix_trans(lo23);
+      uint32_t br0 = 0u, br1 = 0u;               // what hi + lo leave of P
+      if constexpr (FULL) {
+        br0 = movmatrix_trans(pack_bf16(p0 - bf16_lo_f(hi01) - bf16_lo_f(lo01),
+                                        p1 - bf16_hi_f(hi01) - bf16_hi_f(lo01)));
+        br1 = movmatrix_trans(pack_bf16(p2 - bf16_lo_f(hi23) - bf16_lo_f(lo23),
+                                        p3 - bf16_hi_f(hi23) - bf16_hi_f(lo23)));
+      }
 #pragma unroll
       for (int t = 0; t < kDT; ++t) {
         const int d0 = 16 * t;
@@ -1468,8 +1479,19 @@ __global__ void __launch_bounds__(256, (DecodeTraits<BF16, D, G, W>::kMinBlocks)
         const int r = 16 * tile + lr + ((mi >> 1) << 3), pc = cd + (mi & 1);
         uint32_t a[4];
         ldmatrix_x4_trans(a, vb + bx * kBox + r * 128 + ((pc ^ (r & 7)) << 4));
-        mma_bf16_16816(o[t], a, bh0, bh1);
-        mma_bf16_16816(o[t], a, bl0, bl1);
+        if constexpr (FULL) {
+          // the tile's product by itself, then one rounded addition: a long sum inside the
+          // matrix instruction, which truncates, would lose more than the third piece gives
+          float part[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_bf16_16816(part, a, br0, br1);
+          mma_bf16_16816(part, a, bl0, bl1);
+          mma_bf16_16816(part, a, bh0, bh1);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[t][e] += part[e];
+        } else {
+          mma_bf16_16816(o[t], a, bh0, bh1);
+          mma_bf16_16816(o[t], a, bl0, bl1);
+        }
       }
       // the group's barrier releases the stage (and reports a timed-out wait)
       if (bar_red_or(1 + grp, 128, timed_out)) break;
@@ -1618,6 +1640,13 @@ __global__ void __launch_bounds__(256, (DecodeTraits<BF16, D, G, W>::kMinBlocks)
       const uint32_t lo23 = pack_bf16(p2 - bf16_lo_f(hi23), p3 - bf16_hi_f(hi23));
       const uint32_t bh0 = movmatrix_trans(hi01), bh1 = movmatrix_trans(hi23);
       const uint32_t bl0 = movmatrix_trans(lo01), bl1 = movmatrix_trans(lo23);
+      uint32_t br0 = 0u, br1 = 0u;               // what hi + lo leave of P
+      if constexpr (FULL) {
+        br0 = movmatrix_trans(pack_bf16(p0 - bf16_lo_f(hi01) - bf16_lo_f(lo01),
+                                        p1 - bf16_hi_f(hi01) - bf16_hi_f(lo01)));
+        br1 = movmatrix_trans(pack_bf16(p2 - bf16_lo_f(hi23) - bf16_lo_f(lo23),
+                                        p3 - bf16_hi_f(hi23) - bf16_hi_f(lo23)));
+      }
 #pragma unroll
       for (int t = 0; t < kDT; ++t) {
         const int d0 = dh * (D / 2) + 16 * t;
@@ -1625,8 +1654,19 @@ __global__ void __launch_bounds__(256, (DecodeTraits<BF16, D, G, W>::kMinBlocks)
         const int r = 16 * tile + lr + ((mi >> 1) << 3), pc = cd + (mi & 1);
         uint32_t a[4];
         ldmatrix_x4_trans(a, vb + bx * kBox + r * 128 + ((pc ^ (r & 7)) << 4));
-        mma_bf16_16816(o[t], a, bh0, bh1);
-        mma_bf16_16816(o[t], a, bl0, bl1);
+        if constexpr (FULL) {
+          // the tile's product by itself, then one rounded addition: a long sum inside the
+          // matrix instruction, which truncates, would lose more than the third piece gives
+          float part[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_bf16_16816(part, a, br0, br1);
+          mma_bf16_16816(part, a, bl0, bl1);
+          mma_bf16_16816(part, a, bh0, bh1);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[t][e] += part[e];
+        } else {
+          mma_bf16_16816(o[t], a, bh0, bh1);
+          mma_bf16_16816(o[t], a, bl0, bl1);
+        }
       }
       if (__syncthreads_or(timed_out)) break;
       if (tid == 0 && ci + S < n_chunks) issue(ci + S);
@@ -2012,18 +2052,18 @@ __global__ void __launch_bounds__(256, (DecodeTraits<BF16, D, G, W>::kMinBlocks)
 
 // ---------------------------------------------------------------- host-side launch helpers
 
-template <bool BF16, int D, int G, bool W, int FAST = 0>
+template <bool BF16, int D, int G, bool W, int FAST = 0, bool FULL = false>
 std::atomic<unsigned long long>& decode_smem_flag() {
   static std::atomic<unsigned long long> flag{0};
   return flag;
 }
 
-template <bool BF16, int D, int G, bool W, int FAST = 0>
+template <bool BF16, int D, int G, bool W, int FAST = 0, bool FULL = false>
 cudaError_t decode_prepare_t() {
   using Tr = DecodeTraits<BF16, D, G, W>;
-  auto* kern = decode_kernel<BF16, D, G, W, FAST>;
+  auto* kern = decode_kernel<BF16, D, G, W, FAST, FULL>;
   static std::atomic<unsigned long long> cluster_flag{0};
-  cudaError_t e = ensure_dynamic_smem(kern, Tr::kSmem, decode_smem_flag<BF16, D, G, W, FAST>());
+  cudaError_t e = ensure_dynamic_smem(kern, Tr::kSmem, decode_smem_flag<BF16, D, G, W, FAST, FULL>());
   if (e != cudaSuccess) return e;
   int dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
@@ -2037,10 +2077,10 @@ cudaError_t decode_prepare_t() {
 }
 
 // How many clusters of `cluster` CTAs can be co-resident (0 if none / on error).
-template <bool BF16, int D, int G, bool W, int FAST = 0>
+template <bool BF16, int D, int G, bool W, int FAST = 0, bool FULL = false>
 int decode_max_clusters_t(int cluster) {
   using Tr = DecodeTraits<BF16, D, G, W>;
-  if (decode_prepare_t<BF16, D, G, W, FAST>() != cudaSuccess) return 0;
+  if (decode_prepare_t<BF16, D, G, W, FAST, FULL>() != cudaSuccess) return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cluster, 1, 1);
   cfg.blockDim = dim3(Tr::kThreads);
@@ -2053,26 +2093,26 @@ int decode_max_clusters_t(int cluster) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, decode_kernel<BF16, D, G, W, FAST>, &cfg) != cudaSuccess)
+  if (cudaOccupancyMaxActiveClusters(&n, decode_kernel<BF16, D, G, W, FAST, FULL>, &cfg) != cudaSuccess)
     return 0;
   return n;
 }
 
-template <bool BF16, int D, int G, bool W, int FAST = 0>
+template <bool BF16, int D, int G, bool W, int FAST = 0, bool FULL = false>
 int decode_resident_t() {
   using Tr = DecodeTraits<BF16, D, G, W>;
-  if (decode_prepare_t<BF16, D, G, W, FAST>() != cudaSuccess) return 0;
+  if (decode_prepare_t<BF16, D, G, W, FAST, FULL>() != cudaSuccess) return 0;
   int blocks = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, decode_kernel<BF16, D, G, W, FAST>,
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, decode_kernel<BF16, D, G, W, FAST, FULL>,
                                                     Tr::kThreads, Tr::kSmem) != cudaSuccess)
     return 0;
   return blocks;
 }
 
-template <bool BF16, int D, int G, bool W, int FAST = 0>
+template <bool BF16, int D, int G, bool W, int FAST = 0, bool FULL = false>
 cudaError_t decode_launch_t(const DecodeParams& p, dim3 grid, int cluster, cudaStream_t stream) {
   using Tr = DecodeTraits<BF16, D, G, W>;
-  cudaError_t e = decode_prepare_t<BF16, D, G, W, FAST>();
+  cudaError_t e = decode_prepare_t<BF16, D, G, W, FAST, FULL>();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
@@ -2090,7 +2130,7 @@ cudaError_t decode_launch_t(const DecodeParams& p, dim3 grid, int cluster, cudaS
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, decode_kernel<BF16, D, G, W, FAST>, p);
+  return cudaLaunchKernelEx(&cfg, decode_kernel<BF16, D, G, W, FAST, FULL>, p);
 }
 
 // Dispatch on the group size (1..8) for one (dtype, head_dim).

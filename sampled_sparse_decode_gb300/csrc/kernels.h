@@ -227,6 +227,11 @@ cudaError_t decode_launch_bf16_fast_var(const DecodeParams& p, int head_dim, int
 cudaError_t decode_launch_bf16_wide_fast_var(const DecodeParams& p, int head_dim, int group,
                                              dim3 grid, int cluster, cudaStream_t stream);
 int decode_resident_bf16_fast_var(int head_dim, int group);
+// attend-only steps with full weights (santa_topk_decode): the general form's layout and plan
+cudaError_t decode_launch_bf16_full(const DecodeParams& p, int head_dim, int group, dim3 grid,
+                                    int cluster, cudaStream_t stream);
+cudaError_t decode_launch_bf16_wide_full(const DecodeParams& p, int head_dim, int group,
+                                         dim3 grid, int cluster, cudaStream_t stream);
 int decode_resident_bf16_wide_fast_var(int head_dim, int group);
 
 // Helpers of the host side that both ABI files use (defined in santa_abi.cu): streaming
@@ -246,5 +251,7 @@ int pool_tensor_map(CUtensorMap* map, const void* pool, int64_t rows, int d);
 int check_and_plan_decode(const santa_decode_args* a, int* clusters_per_unit);
 // The same for santa_attend.
 int check_attend(const santa_decode_args* a);
+// santa_attend with every bit of the weights in the product with V (bf16).
+int attend_full_weights(const santa_decode_args* a, cudaStream_t stream);
 
 }  // namespace santa

@@ -448,7 +448,7 @@ int check_and_plan(const santa_decode_args* a, int mode, Plan* pl) {
   return SANTA_OK;
 }
 
-int launch(const santa_decode_args* a, int mode, cudaStream_t stream) {
+int launch(const santa_decode_args* a, int mode, cudaStream_t stream, bool full_weights = false) {
   Plan pl;
   int rc = check_and_plan(a, mode, &pl);
   if (rc) return rc;
@@ -505,6 +505,11 @@ int launch(const santa_decode_args* a, int mode, cudaStream_t stream) {
                             : santa::decode_launch_bf16_fast(p, a->head_dim, G, grid,
                                                              pl.cluster, stream));
   }
+  if (full_weights && a->dtype == SANTA_BF16)
+    return map_cuda(pl.wide ? santa::decode_launch_bf16_wide_full(p, a->head_dim, G, grid,
+                                                                  pl.cluster, stream)
+                            : santa::decode_launch_bf16_full(p, a->head_dim, G, grid,
+                                                             pl.cluster, stream));
   const cudaError_t e =
       a->dtype == SANTA_BF16
           ? (pl.wide ? santa::decode_launch_bf16_wide(p, a->head_dim, G, grid, pl.cluster, stream)
@@ -552,6 +557,10 @@ int check_and_plan_decode(const santa_decode_args* a, int* clusters_per_unit) {
   const int rc = check_and_plan(a, kModeDecode, &pl);
   if (rc == SANTA_OK && clusters_per_unit) *clusters_per_unit = pl.clusters;
   return rc;
+}
+
+int attend_full_weights(const santa_decode_args* a, cudaStream_t stream) {
+  return launch(a, kModeAttend, stream, true);
 }
 
 int check_attend(const santa_decode_args* a) {

@@ -699,7 +699,7 @@ def _token_rows(t, name, dtype, heads, d):
         return t.shape[1] * d
     if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d):
         raise SantaError(f"the heads of one token of {name} must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * d)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * d
 
 
 class _Prepared:
@@ -714,7 +714,8 @@ class _Prepared:
 
     def run(self, stream=None):
         """Enqueues the call on `stream` (the current stream by default); returns its result
-        buffers."""
+        buffers.  Buffers that the preparation made are filled on the stream that was current
+        then: another stream must wait for it before its first run."""
         if torch.cuda.current_device() != self._device:
             raise SantaError(f"{self._name} was prepared on cuda:{self._device}")
         rc = self._fn(self._aref, _stream(stream))

@@ -251,3 +251,84 @@ def test_single_token_agrees_with_dense_decode():
     half = torch.finfo(BF16).eps / 2
     vmax = c.v.abs().max().item()
     assert (out.double() - dense.double()).abs().max() <= 2e-3 + 2 * half * vmax
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_many_short_sequences(dtype):
+    """300 sequences, a fifth of them without a new token, lengths from 0 to a few pages."""
+    g = torch.Generator().manual_seed(31)
+    new = [int(x) for x in torch.randint(0, 6, (300,), generator=g)]
+    ctx = [int(x) for x in torch.randint(0, 200, (300,), generator=g)]
+    new = [0 if i % 5 == 0 else m for i, m in enumerate(new)]
+    lens = [L + m for L, m in zip(ctx, new)]
+    c = Cache(lens, 2, 64, 64, dtype, seed=31)
+    q = torch.randn(sum(new) + 2, 6, 64, generator=g).to(dtype).cuda()
+    cu_q = cu(new)
+    out, status = run(c, q, cu_q)
+    assert status == 0
+    starts = cu_q.tolist()
+    for b in range(0, 300, 7):
+        if new[b]:
+            check_rows(c, q, out, b, starts[b], new[b])
+    assert (out[starts[-1]:] == 7).all()
+    # every row of every sequence was written
+    assert not (out[:starts[-1]] == 7).any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_output_at_any_16_byte_address(dtype):
+    c = Cache([400], 2, 128, 64, dtype, seed=32)
+    q = torch.randn(77, 8, 128, generator=torch.Generator().manual_seed(4)).to(dtype).cuda()
+    want, _ = run(c, q, cu([77]))
+    off = 16 // q.element_size()
+    flat = torch.zeros(q.numel() + off, dtype=dtype, device="cuda")
+    out = flat[off:].view_as(q)
+    santa.santa_chunk_attend(q, c.k, c.v, c.table, c.seq_lens, cu([77]), out=out)
+    assert torch.equal(out, want) and (flat[:off] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_pool_larger_than_32_bit_offsets(dtype):
+    """Pages behind element 2^31 of the pools."""
+    hkv, T, d, L, new = 8, 128, 128, 300, 40
+    pages = 2**31 // (hkv * T * d) + 8
+    c = Cache([L], hkv, d, T, dtype, seed=33)
+    q = torch.randn(new, 16, 128, generator=torch.Generator().manual_seed(4)).to(dtype).cuda()
+    want, _ = run(c, q, cu([new]))
+    k = torch.empty(pages, hkv, T, d, dtype=dtype, device="cuda")
+    v = torch.empty(pages, hkv, T, d, dtype=dtype, device="cuda")
+    n = c.k.shape[0]
+    k[-n:], v[-n:] = c.k, c.v
+    table = c.table + (pages - n)
+    out = santa.santa_chunk_attend(q, k, v, table, c.seq_lens, cu([new]))
+    assert torch.equal(out, want)
+    # the single-token step and the append reach them too
+    reps = torch.zeros(pages, hkv, d, device="cuda")
+    reps[-n:] = santa.santa_build_reps(c.k, c.fill)
+    a = santa.santa_topk_decode(q[:1], c.k, c.v, reps[-n:].contiguous(), c.table, c.seq_lens, 2)
+    b = santa.santa_topk_decode(q[:1], k, v, reps, table, c.seq_lens, 2)
+    assert torch.equal(a.out, b.out) and torch.equal(a.sel_ids, b.sel_ids)
+    kn = torch.randn(50, hkv, d, generator=torch.Generator().manual_seed(5)).to(dtype).cuda()
+    for pool_k, pool_v, rep, tab in ((c.k, c.v, reps[-n:].clone(), c.table), (k, v, reps, table)):
+        santa.santa_append_chunk(None, kn, kn, cu([50]), pool_k, pool_v, rep, tab, c.seq_lens)
+        last = rep[-n:]
+        it = torch.int16 if dtype == BF16 else torch.int32
+        got = (pool_k[-n:].clone().view(it), pool_v[-n:].clone().view(it), last.clone())
+        if pool_k is c.k:
+            first = got
+    assert all(torch.equal(x, y) for x, y in zip(first, got))
+
+
+def test_keys_split_over_blocks_hold_nan_only_where_seen():
+    """A long chunk whose items are split over blocks, with NaN in the last tokens: rows before
+    them keep the bits of the clean cache, also in tiles that were joined."""
+    c = Cache([6000], 1, 128, 128, BF16, seed=34)
+    q = torch.randn(300, 4, 128, generator=torch.Generator().manual_seed(4)).to(BF16).cuda()
+    clean, _ = run(c, q, cu([300]))
+    for first in (5999, 5900, 5760):
+        page, slot = c.table[0, first // 128].long(), first % 128
+        c.k[page, 0, slot], c.v[page, 0, slot] = math.nan, math.nan
+        out, _ = run(c, q, cu([300]))
+        rows = first - 5700
+        assert torch.equal(out[:rows], clean[:rows])
+        assert out[rows:].isnan().all()

@@ -702,6 +702,11 @@ def _token_rows(t, name, dtype, heads, d):
     return t.stride(0) if t.shape[0] > 1 else t.shape[1] * d
 
 
+# The current stream's handle without a Stream object around it (several times faster).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 class _Prepared:
     """A call whose arguments are checked and marshalled once, for steps that reuse the same
     tensors: their contents may change between runs, their storage may not."""
@@ -718,7 +723,7 @@ class _Prepared:
         then: another stream must wait for it before its first run."""
         if torch.cuda.current_device() != self._device:
             raise SantaError(f"{self._name} was prepared on cuda:{self._device}")
-        rc = self._fn(self._aref, _stream(stream))
+        rc = self._fn(self._aref, _raw_stream(self._device) if stream is None else _stream(stream))
         if rc:
             _check(rc, self._name)
         return self._result

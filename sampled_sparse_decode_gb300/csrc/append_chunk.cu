@@ -40,16 +40,6 @@ __device__ __forceinline__ void unpack(const uint4& w, float (&x)[Piece<BF16>::k
     x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
   }
 }
-template <bool BF16>
-__device__ __forceinline__ uint4 pack(const float (&x)[Piece<BF16>::kVec]) {
-  if constexpr (BF16)
-    return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                      pack_bf16(x[6], x[7]));
-  else
-    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
-                      __float_as_uint(x[3]));
-}
-
 // The two pieces of a row that pair `pr` (0 .. pieces/2 - 1) stands for.  Rotation by halves:
 // pieces j and j + R/2 of the rotated part, then the rest in twos; otherwise neighbours.
 template <bool BF16>
@@ -65,23 +55,6 @@ __device__ __forceinline__ void pair_pieces(int pr, int rope_dim, bool interleav
   }
 }
 
-// Cosines and sines of a pair of pieces at one position: by halves both pieces use the
-// elements [a kVec, (a + 1) kVec); interleaved, piece a uses [a kVec / 2, ...) and piece b the
-// kVec / 2 after it, so the same kVec values again (b = a + 1).
-template <bool BF16>
-struct Turn {
-  float c[Piece<BF16>::kVec], s[Piece<BF16>::kVec];
-  __device__ __forceinline__ void load(const float* row, int half_dim, int first) {
-#pragma unroll
-    for (int e = 0; e < Piece<BF16>::kVec; e += 4) {
-      const float4 c4 = __ldg(reinterpret_cast<const float4*>(row + first + e));
-      const float4 s4 = __ldg(reinterpret_cast<const float4*>(row + half_dim + first + e));
-      c[e] = c4.x; c[e + 1] = c4.y; c[e + 2] = c4.z; c[e + 3] = c4.w;
-      s[e] = s4.x; s[e + 1] = s4.y; s[e + 2] = s4.z; s[e + 3] = s4.w;
-    }
-  }
-};
-
 // x c - y s and y c + x s with every product and sum rounded to fp32 (no contraction: the
 // stored bits are then those of the formula as any fp32 program evaluates it)
 __device__ __forceinline__ void turn_pair(float& x, float& y, float c, float s) {
@@ -89,25 +62,74 @@ __device__ __forceinline__ void turn_pair(float& x, float& y, float c, float s) 
   y = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
   x = nx;
 }
-template <bool BF16>
-__device__ __forceinline__ void rotate(uint4& wa, uint4& wb, const Turn<BF16>& t,
-                                       bool interleaved) {
-  constexpr int V = Piece<BF16>::kVec;
-  float a[V], b[V];
-  unpack<BF16>(wa, a);
-  unpack<BF16>(wb, b);
-  if (interleaved) {
+
+// Four pairs of a rotation: cosines and sines c, s of four consecutive table entries.  By halves
+// the pairs are (a_e, b_e) of two bf16 words each; interleaved they are the neighbours in four
+// bf16 words.  A pair of pieces takes two such groups (bf16) or one (fp32), and only one group's
+// table entries are in registers at a time.
+__device__ __forceinline__ void turn_halves(uint32_t& a0, uint32_t& a1, uint32_t& b0, uint32_t& b1,
+                                            const float4& c, const float4& s) {
+  float x[4] = {bf16_lo(a0), bf16_hi(a0), bf16_lo(a1), bf16_hi(a1)};
+  float y[4] = {bf16_lo(b0), bf16_hi(b0), bf16_lo(b1), bf16_hi(b1)};
+  turn_pair(x[0], y[0], c.x, s.x);
+  turn_pair(x[1], y[1], c.y, s.y);
+  turn_pair(x[2], y[2], c.z, s.z);
+  turn_pair(x[3], y[3], c.w, s.w);
+  a0 = pack_bf16(x[0], x[1]);
+  a1 = pack_bf16(x[2], x[3]);
+  b0 = pack_bf16(y[0], y[1]);
+  b1 = pack_bf16(y[2], y[3]);
+}
+__device__ __forceinline__ void turn_word(uint32_t& w, float c, float s) {
+  float x = bf16_lo(w), y = bf16_hi(w);
+  turn_pair(x, y, c, s);
+  w = pack_bf16(x, y);
+}
+__device__ __forceinline__ void turn_neighbours(uint4& w, const float4& c, const float4& s) {
+  turn_word(w.x, c.x, s.x);
+  turn_word(w.y, c.y, s.y);
+  turn_word(w.z, c.z, s.z);
+  turn_word(w.w, c.w, s.w);
+}
+__device__ __forceinline__ void turn_f32(uint32_t& a, uint32_t& b, float c, float s) {
+  float x = __uint_as_float(a), y = __uint_as_float(b);
+  turn_pair(x, y, c, s);
+  a = __float_as_uint(x);
+  b = __float_as_uint(y);
+}
+
+// Rotates N pairs of pieces that share a position, with the table row's entries from `first` on:
+// by halves both pieces of a pair use the same kVec entries; interleaved, piece a uses kVec / 2
+// and piece b (the next one) the kVec / 2 after them.
+template <bool BF16, int N>
+__device__ __forceinline__ void rotate(uint4 (&a)[N], uint4 (&b)[N], const float* row, int half_dim,
+                                       int first, bool interleaved) {
 #pragma unroll
-    for (int e = 0; e < V / 2; ++e) {
-      turn_pair(a[2 * e], a[2 * e + 1], t.c[e], t.s[e]);
-      turn_pair(b[2 * e], b[2 * e + 1], t.c[V / 2 + e], t.s[V / 2 + e]);
+  for (int group = 0; group < (BF16 ? 2 : 1); ++group) {
+    const float4 c = __ldg(reinterpret_cast<const float4*>(row + first + 4 * group));
+    const float4 s = __ldg(reinterpret_cast<const float4*>(row + half_dim + first + 4 * group));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if constexpr (BF16) {
+        if (interleaved)
+          turn_neighbours(group == 0 ? a[i] : b[i], c, s);
+        else if (group == 0)
+          turn_halves(a[i].x, a[i].y, b[i].x, b[i].y, c, s);
+        else
+          turn_halves(a[i].z, a[i].w, b[i].z, b[i].w, c, s);
+      } else if (interleaved) {
+        turn_f32(a[i].x, a[i].y, c.x, s.x);
+        turn_f32(a[i].z, a[i].w, c.y, s.y);
+        turn_f32(b[i].x, b[i].y, c.z, s.z);
+        turn_f32(b[i].z, b[i].w, c.w, s.w);
+      } else {
+        turn_f32(a[i].x, b[i].x, c.x, s.x);
+        turn_f32(a[i].y, b[i].y, c.y, s.y);
+        turn_f32(a[i].z, b[i].z, c.z, s.z);
+        turn_f32(a[i].w, b[i].w, c.w, s.w);
+      }
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e) turn_pair(a[e], b[e], t.c[e], t.s[e]);
   }
-  wa = pack<BF16>(a);
-  wb = pack<BF16>(b);
 }
 
 // Checked geometry of sequence b's chunk; false (and the status bit) if it must be skipped.
@@ -168,31 +190,42 @@ __device__ void page_item(const AppendChunkParams& p, int64_t slot, int h, float
     float sa[V], sb[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) sa[e] = sb[e] = 0.f;
-#pragma unroll 4
-    for (int r = group; r < row1; r += kGroups) {
-      uint4 wa, wb;
-      if (r < row0) {
-        wa = pool[r * kCols + ca];
-        wb = pool[r * kCols + cb];
-      } else {
-        const uint4* row = src + (tok0 + r) * stride;
-        wa = __ldg(row + ca);
-        wb = __ldg(row + cb);
-        if (turned) {
-          Turn<BF16> t;
-          t.load(p.rope + (team * T + r) * p.rope_dim, p.rope_dim / 2, first);
-          rotate<BF16>(wa, wb, t, p.interleaved);
-        }
-        pool[r * kCols + ca] = wa;
-        pool[r * kCols + cb] = wb;
-      }
-      float xa[V], xb[V];
-      unpack<BF16>(wa, xa);
-      unpack<BF16>(wb, xb);
+    // four rows at a time, all of their loads before the first use
+    constexpr int kBatch = 4;
+    for (int r0 = group; r0 < row1; r0 += kBatch * kGroups) {
+      uint4 wa[kBatch], wb[kBatch];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        sa[e] += xa[e];
-        sb[e] += xb[e];
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = r0 + i * kGroups;
+        if (r < row1) {
+          const uint4* row = r < row0 ? pool + r * kCols : src + (tok0 + r) * stride;
+          wa[i] = row[ca];
+          wb[i] = row[cb];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = r0 + i * kGroups;
+        if (r >= row1) break;
+        if (r >= row0) {
+          if (turned) {
+            uint4 a1[1] = {wa[i]}, b1[1] = {wb[i]};
+            rotate<BF16>(a1, b1, p.rope + (team * T + r) * p.rope_dim, p.rope_dim / 2, first,
+                         p.interleaved);
+            wa[i] = a1[0];
+            wb[i] = b1[0];
+          }
+          pool[r * kCols + ca] = wa[i];
+          pool[r * kCols + cb] = wb[i];
+        }
+        float xa[V], xb[V];
+        unpack<BF16>(wa[i], xa);
+        unpack<BF16>(wb[i], xb);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          sa[e] += xa[e];
+          sb[e] += xb[e];
+        }
       }
     }
 #pragma unroll
@@ -248,21 +281,19 @@ __device__ void query_item(const AppendChunkParams& p, int64_t item) {
   pair_pieces<BF16>(threadIdx.x % kPairs, p.rope_dim, p.interleaved, &ca, &cb);
   const uint4* src = static_cast<const uint4*>(p.q) + tok * (p.q_stride / V);
   uint4* dst = static_cast<uint4*>(p.q_out) + tok * p.num_q_heads * kCols;
-  uint4 wa[kHeadsPerUnit], wb[kHeadsPerUnit];
+  uint4 wa[kHeadsPerUnit] = {}, wb[kHeadsPerUnit] = {};
 #pragma unroll
   for (int i = 0; i < kHeadsPerUnit; ++i)
     if (h0 + i < p.num_q_heads) {
       wa[i] = src[(h0 + i) * kCols + ca];
       wb[i] = src[(h0 + i) * kCols + cb];
     }
-  Turn<BF16> t;
-  const bool turned = ca * V < p.rope_dim;
-  if (turned)
-    t.load(p.rope + pos * p.rope_dim, p.rope_dim / 2, p.interleaved ? ca * V / 2 : ca * V);
+  if (ca * V < p.rope_dim)
+    rotate<BF16>(wa, wb, p.rope + pos * p.rope_dim, p.rope_dim / 2,
+                 p.interleaved ? ca * V / 2 : ca * V, p.interleaved);
 #pragma unroll
   for (int i = 0; i < kHeadsPerUnit; ++i)
     if (h0 + i < p.num_q_heads) {
-      if (turned) rotate<BF16>(wa[i], wb[i], t, p.interleaved);
       dst[(h0 + i) * kCols + ca] = wa[i];
       dst[(h0 + i) * kCols + cb] = wb[i];
     }
@@ -270,7 +301,7 @@ __device__ void query_item(const AppendChunkParams& p, int64_t item) {
 
 // Page items first (they are longer), then query items.
 template <bool BF16, int D>
-__global__ void __launch_bounds__(kAppendThreads) append_chunk_kernel(AppendChunkParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 3) append_chunk_kernel(AppendChunkParams p) {
   __shared__ __align__(16) float part[kAppendThreads / (D / Piece<BF16>::kVec) * D];
   grid_dependency_wait();
   if (blockIdx.x < p.page_items)

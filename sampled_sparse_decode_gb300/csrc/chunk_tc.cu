@@ -1033,7 +1033,7 @@ TcLayout tc_layout(int blocks, int d) {
 }
 
 template <int D>
-cudaError_t launch(const TcParams& t, int blocks, cudaStream_t stream) {
+cudaError_t launch(const TcParams& t, int blocks, bool split, cudaStream_t stream) {
   using C = TcCfg<D>;
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = ensure_dynamic_smem(chunk_tc_kernel<D>, C::kSmem, done);
@@ -1049,7 +1049,7 @@ cudaError_t launch(const TcParams& t, int blocks, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, chunk_tc_kernel<D>, t);
-  if (e != cudaSuccess || blocks == 1) return e;
+  if (e != cudaSuccess || !split) return e;
   cfg.gridDim = dim3(blocks, 8);
   cfg.blockDim = dim3(D * 4);                     // a warp for every 8 columns
   cfg.dynamicSmemBytes = 0;
@@ -1097,7 +1097,10 @@ int launch_chunk_tc(const ChunkParams& p, int d, void* workspace, int sms, cudaS
   t.part_acc = reinterpret_cast<float*>(base + l.acc);
   t.part_ml = reinterpret_cast<float*>(base + l.ml);
   t.join = reinterpret_cast<int32_t*>(base + l.join);
-  const cudaError_t e = d == 128 ? launch<128>(t, blocks, stream) : launch<64>(t, blocks, stream);
+  // an item is cut only where more than one step is left on both sides (line_border)
+  const bool split = blocks > 1 && static_cast<int64_t>(p.max_teams) * p.team_size > 3 * kStep;
+  const cudaError_t e = d == 128 ? launch<128>(t, blocks, split, stream)
+                                 : launch<64>(t, blocks, split, stream);
   return e == cudaSuccess ? SANTA_OK : SANTA_ERR_CUDA;
 }
 

@@ -18,6 +18,10 @@
 //
 // Masked scores never enter: P is 0 there, and in a step that holds a masked pair (the causal
 // border) the product with V is selected away too, because 0 * V is not 0 when V is not finite.
+//
+// Measured on GB300: prompts of 1000 tokens on 4000 and 800 on 100, 8 heads of 128, 720 us, 27.8
+// TFLOP/s (the FMA pipe is 54% active); a batch of 1, 513, 64 and 1 tokens, 8 / 2 heads of 64,
+// 39 us (74 us before the few-rows way and the splits by length).
 #include <algorithm>
 
 #include "kernels.h"

@@ -11,6 +11,11 @@
 // order, the norms' own rounding and denormals.  So with t the M-th best fp32 score, a team
 // above t + 2E is in S, one below t - 2E is not, and the few between are compared in 64 bits.
 // Only if they do not all fit is any 64-bit score formed (usually the M-th alone lies there).
+//
+// Bound by latency: a launch makes two dependent reads from DRAM or L2 (the length with the
+// page ids, then the representatives), two cluster barriers and two counting passes.  Measured
+// on GB300 (d = 128): 5.3 us for 4 units of 256 teams, 9.0 us for 128 units of 256 (16.8 MB of
+// representatives), 9.8 us for 16 units of 1024.
 #include "kernels.h"
 
 namespace santa {

@@ -75,6 +75,7 @@ struct TcShared {
   uint64_t q_full, q_empty, land, drain;
   uint64_t kv_full[kGroups], kv_empty[kGroups];
   uint64_t s_full[2], p_ready[2], o_full[2];
+  uint64_t run_open[3], run_done[3];   // by item ring: a run has begun; both tiles finished it
   int group_of[10];          // by ring stage: the group of the tile in it (copying warp only)
   uint32_t tmem;
   volatile int abort;
@@ -473,6 +474,10 @@ __device__ void copy_role(const TcParams& t, TcShared& s, unsigned char* q_smem,
     ok = wait_or_abort(s, &s.q_empty, q_parity);
     q_parity ^= 1;
     if (!ok) break;
+    // the notes of three runs ago have been read (tile B may lag behind runs that A has alone)
+    ok = wait_or_abort(s, &s.run_done[turn], (runs / 3 + 1) & 1);
+    if (!ok) break;
+    if (lane == 0) mbar_arrive(&s.run_open[turn]);
     if (lane < 16) s.noted[turn][lane / 4][lane % 4] = 0u;
     if (lane == 0) {
       const uint32_t box = t.tpt * G * 128;      // bytes of one 64-element wide box
@@ -695,12 +700,18 @@ __device__ void softmax_role(const TcParams& t, TcShared& s) {
   const uint32_t tm_o = s.tmem + C::kColO + D * x + lanes;
   const float scale = p.scale_log2;
   const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
-  uint32_t s_parity = 0, o_parity = 0;
+  uint32_t parity = 0;           // bit 0: s_full, bit 1: o_full, bit 2: run_open
   Run r;
   r.begin(s, p);
   for (int turn = 0; r.open(tpi); r.next(p, tpi), turn = turn == 2 ? 0 : turn + 1) {
     const int tok0 = r.item * tpi + x * t.tpt;           // first token of this tile
-    if (tok0 >= r.seq.n) continue;
+    if (tok0 >= r.seq.n) {
+      // not before the run has begun: an early arrival would count for another run of the ring
+      if (!wait_or_abort(s, &s.run_open[turn], parity >> 2 & 1)) return;
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&s.run_done[turn]);
+      if (turn == 2) parity ^= 4;
+      continue;
+    }
     const int tok = tok0 + token_in_tile;
     const bool mine = token_in_tile < t.tpt && tok < r.seq.n;
     const int sees = mine ? r.seq.ctx + tok + 1 : 0;
@@ -708,8 +719,8 @@ __device__ void softmax_role(const TcParams& t, TcShared& s) {
     const bool warp_idle = __ballot_sync(0xffffffffu, mine) == 0u;
     float m = -INFINITY, l = 0.f;
     for (int j = r.s0; j < r.s1; ++j) {
-      if (!wait_or_abort(s, &s.s_full[x], s_parity)) return;
-      s_parity ^= 1;
+      if (!wait_or_abort(s, &s.s_full[x], parity & 1)) return;
+      parity ^= 1;
       if (!warp_idle) {
         tc_fence_after();
         uint32_t sc[4][32];
@@ -778,9 +789,12 @@ __device__ void softmax_role(const TcParams& t, TcShared& s) {
       }
     }
     // ---- epilogue: the row, or its partial result
-    if (!wait_or_abort(s, &s.o_full[x], o_parity)) return;
-    o_parity ^= 1;
-    if (warp_idle) continue;
+    if (!wait_or_abort(s, &s.o_full[x], parity >> 1 & 1)) return;
+    parity ^= turn == 2 ? 6 : 2;
+    if (warp_idle) {
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&s.run_done[turn]);
+      continue;
+    }
     tc_fence_after();
     const bool whole = r.s0 == 0 && r.s1 == r.steps;
     const int64_t out_row =
@@ -820,6 +834,7 @@ __device__ void softmax_role(const TcParams& t, TcShared& s) {
       add_noted<D>(t, r, s.noted[turn], sees, out_row, m == -INFINITY ? 0.f : m,
                    whole ? out : nullptr, part_row);
     __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&s.run_done[turn]);
     tc_fence_before();
   }
 }
@@ -888,6 +903,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&s.s_full[x], 1);
       mbar_init(&s.p_ready[x], 4);
       mbar_init(&s.o_full[x], 1);
+    }
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&s.run_open[i], 1);
+      mbar_init(&s.run_done[i], 8);              // the softmax warps
     }
     s.abort = 0;
     fence_mbar_init();

@@ -332,3 +332,65 @@ def test_keys_split_over_blocks_hold_nan_only_where_seen():
         rows = first - 5700
         assert torch.equal(out[:rows], clean[:rows])
         assert out[rows:].isnan().all()
+
+
+def test_noted_values_outlast_the_items_behind_them():
+    """One sequence in ten fills both tiles of an item and holds NaN behind its first tokens; the
+    others have one token and use the first tile alone.  The second tile's rows are finished
+    while later items are under way, and must still meet the NaN they see."""
+    new = [20 if b % 10 == 0 else 1 for b in range(2000)]
+    lens = [m + 3 for m in new]
+    c = Cache(lens, 1, 64, 64, BF16, seed=35)
+    q = torch.randn(sum(new), 8, 64, generator=torch.Generator().manual_seed(4)).to(BF16).cuda()
+    cu_q = cu(new)
+    clean, _ = run(c, q, cu_q)
+    pages = c.table[::10, 0].long()
+    c.v[pages, :, 21] = math.nan                        # token 21 of 23: rows 18 and 19 see it
+    starts = cu_q[:-1:10].long()
+    for _ in range(5):
+        out, status = run(c, q, cu_q)
+        assert status == 0
+        at = starts[:, None] + torch.arange(20, device="cuda")
+        assert out[at[:, 18:]].isnan().all()
+        rest = torch.ones(len(q), dtype=torch.bool, device="cuda")
+        rest[at[:, 18:].flatten()] = False
+        assert torch.equal(out[rest], clean[rest])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_replay_follows_lengths_and_bounds(dtype):
+    """A captured call reads lengths, bounds and pages on the device: replays after they changed
+    are calls with the new ones."""
+    c = Cache([1500, 900, 300], 2, 64, 128, dtype, seed=36)
+    q = torch.randn(200, 6, 64, generator=torch.Generator().manual_seed(4)).to(dtype).cuda()
+    cu_q, out = cu([200, 0, 0]), torch.zeros_like(q)
+    h = santa.santa_chunk_attend_prepared(q, c.k, c.v, c.table, c.seq_lens, cu_q, out=out)
+    h.run()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        h.run()
+    for new in ([1, 198, 1], [0, 0, 200], [67, 66, 67], [200, 0, 0]):
+        cu_q.copy_(cu(new))
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        want, _ = run(c, q, cu(new))
+        assert torch.equal(out, want)
+        first = 0
+        for b, m in enumerate(new):
+            if m:
+                check_rows(c, q, out, b, first, m, sorted({0, m // 2, m - 1}))
+            first += m
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_page_table_much_wider_than_the_lengths(dtype):
+    c = Cache([130, 700], 2, 128, 64, dtype, seed=37)
+    q = torch.randn(60, 4, 128, generator=torch.Generator().manual_seed(4)).to(dtype).cuda()
+    wide = torch.full((2, 16384), -7, dtype=torch.int32, device="cuda")
+    wide[:, :c.table.shape[1]] = c.table
+    c.table = wide
+    out, status = run(c, q, cu([20, 40]))
+    assert status == 0
+    check_rows(c, q, out, 0, 0, 20)
+    check_rows(c, q, out, 1, 20, 40)

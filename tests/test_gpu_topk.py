@@ -234,3 +234,58 @@ def test_prompt_then_sparse_decode(dtype):
             # the sampled step reads the same cache and representatives
             sampled = santa.santa_decode(qr, c.k, c.v, c.reps, c.table, lens, 4096, 1)
             assert sampled.status() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_chunk_tokens_as_rows_of_the_batch(dtype):
+    """Several query tokens of one sequence, as rows with the same page-table row and growing
+    lengths: each row is the step of its own length."""
+    c = Cache([1000], 2, 64, 64, dtype, seed=40)
+    c.reps = santa.santa_build_reps(c.k, c.fill)
+    rows = 6
+    q = torch.randn(rows, 8, 64, generator=torch.Generator().manual_seed(1)).to(dtype).cuda()
+    lens = torch.tensor([995 + i for i in range(rows)], dtype=torch.int32, device="cuda")
+    table = c.table.expand(rows, -1).contiguous()
+    got = santa.santa_topk_decode(q, c.k, c.v, c.reps, table, lens, 5)
+    assert got.status() == 0
+    for i in range(rows):
+        c.lens = [995 + i]
+        c.seq_lens = lens[i:i + 1].clone()
+        one = santa.santa_topk_decode(q[i:i + 1], c.k, c.v, c.reps, c.table, c.seq_lens, 5)
+        check_topk(c, q[i:i + 1], one, 5)
+        assert torch.equal(got.sel_ids[i], one.sel_ids[0])
+        assert (got.out[i] - one.out[0]).abs().max() <= TOL_OUT[NAME[dtype]]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_bad_length_gives_zeros(dtype):
+    c = Cache([300, 200], 1, 64, 64, dtype, seed=41, stale=0.0)
+    c.reps = santa.santa_build_reps(c.k, c.fill)
+    c.seq_lens[0] = 64 * c.table.shape[1] + 1
+    table = torch.where(c.table == 2**30, torch.zeros_like(c.table), c.table)
+    q = torch.randn(2, 4, 64, generator=torch.Generator().manual_seed(1)).to(dtype).cuda()
+    bufs = santa.santa_topk_decode(q, c.k, c.v, c.reps, table, c.seq_lens, 3)
+    assert bufs.status() == DEV_BAD_SEQLEN
+    assert (bufs.out[0] == 0).all() and int(bufs.sel_count[0, 0]) == 0
+    assert bufs.sel_count[1, 0] == 3 and not (bufs.out[1] == 0).all()
+
+
+def test_side_stream_and_two_steps_at_once():
+    """Two prepared steps on two streams, each with its own buffers."""
+    c = Cache([2000, 300], 2, 128, 128, BF16, seed=42)
+    c.reps = santa.santa_build_reps(c.k, c.fill)
+    qs = [torch.randn(2, 8, 128, generator=torch.Generator().manual_seed(i)).to(BF16).cuda()
+          for i in range(2)]
+    hs = [santa.santa_topk_decode_prepared(q, c.k, c.v, c.reps, c.table, c.seq_lens, 4) for q in qs]
+    want = []
+    for h in hs:
+        b = h.run()
+        torch.cuda.synchronize()
+        want.append((b.out.clone(), b.sel_ids.clone()))
+    streams = [torch.cuda.Stream() for _ in hs]
+    for _ in range(20):
+        for h, s in zip(hs, streams):
+            h.run(stream=s)
+    torch.cuda.synchronize()
+    for h, (out, ids) in zip(hs, want):
+        assert torch.equal(h.run().out, out) and torch.equal(h.run().sel_ids, ids)

@@ -19,9 +19,10 @@
 // Masked scores never enter: P is 0 there, and in a step that holds a masked pair (the causal
 // border) the product with V is selected away too, because 0 * V is not 0 when V is not finite.
 //
-// Measured on GB300: prompts of 1000 tokens on 4000 and 800 on 100, 8 heads of 128, 720 us, 27.8
-// TFLOP/s (the FMA pipe is 54% active); a batch of 1, 513, 64 and 1 tokens, 8 / 2 heads of 64,
-// 39 us (74 us before the few-rows way and the splits by length).
+// Measured on GB300: prompts of 1000 tokens on 4000 and 800 on 100, 8 heads of 128, 587 us, 34
+// TFLOP/s; a batch of 1, 513, 64 and 1 tokens, 8 / 2 heads of 64, 33 us (74 us before the few-rows
+// way and the splits by length); one token of 8 sequences on 8000, 32 / 8 heads of 128, 162 us,
+// 3.2 TB/s.
 #include <algorithm>
 
 #include "kernels.h"
@@ -51,7 +52,10 @@ struct FewSmem {
   float q[kFew][D];
   float p[kWarps][32][kFew];
   float m[kWarps][kFew], l[kWarps][kFew];
-  float o[kWarps][kFew][D];
+  union {
+    float k[kWarps][32][D / 2 + 4];      // half of the warp's 32 key rows
+    float o[kWarps][kFew][D];            // once the keys are done
+  };
 };
 
 __device__ __forceinline__ float4 load4(const void* base, int64_t elem) {
@@ -174,17 +178,31 @@ __device__ void few_rows(const ChunkParams& p, const Tile& t, FewSmem<D>& s, int
   for (int64_t k0 = s0 * kKeys + warp * 32; k0 < end; k0 += kWarps * 32) {
     const int count = static_cast<int>(min(static_cast<int64_t>(32), end - k0));
     const int64_t base = key_at(p, t.b, h, k0, D, lane == 0);      // 32 keys share a page
-    const float* k = static_cast<const float*>(p.k_pool) + base + min(lane, count - 1) * D;
+    // scores: a lane per key.  The rows come through shared memory, half of their width at a time
+    // (lanes reading their own rows from global memory touch 32 lines per load: 2.0 TB/s)
+    constexpr int kPieces = D / 8;              // 16-byte pieces of half a row
+    const float* k = static_cast<const float*>(p.k_pool) + base;
     float a[kFew];
 #pragma unroll
     for (int r = 0; r < kFew; ++r) a[r] = 0.f;
-#pragma unroll 4
-    for (int e = 0; e < D; e += 4) {
-      const float4 kv = *reinterpret_cast<const float4*>(k + e);
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      __syncwarp();
 #pragma unroll
-      for (int r = 0; r < kFew; ++r) {
-        const float4 q = *reinterpret_cast<const float4*>(&s.q[r][e]);
-        a[r] = fmaf(q.x, kv.x, fmaf(q.y, kv.y, fmaf(q.z, kv.z, fmaf(q.w, kv.w, a[r]))));
+      for (int i = 0; i < kPieces; ++i) {
+        const int at = i * 32 + lane, row = at / kPieces, c = at % kPieces * 4;
+        cp_async16(&s.k[warp][row][c], k + min(row, count - 1) * D + half * (D / 2) + c);
+      }
+      cp_async_wait_all();
+      __syncwarp();
+#pragma unroll 4
+      for (int e = 0; e < D / 2; e += 4) {
+        const float4 kv = *reinterpret_cast<const float4*>(&s.k[warp][lane][e]);
+#pragma unroll
+        for (int r = 0; r < kFew; ++r) {
+          const float4 q = *reinterpret_cast<const float4*>(&s.q[r][half * (D / 2) + e]);
+          a[r] = fmaf(q.x, kv.x, fmaf(q.y, kv.y, fmaf(q.z, kv.z, fmaf(q.w, kv.w, a[r]))));
+        }
       }
     }
     float w[kFew];
@@ -227,6 +245,7 @@ __device__ void few_rows(const ChunkParams& p, const Tile& t, FewSmem<D>& s, int
     }
   }
   // the warps' results, joined in order
+  __syncthreads();
 #pragma unroll
   for (int r = 0; r < kFew; ++r) {
     l[r] = warp_sum(l[r]);

@@ -9,8 +9,8 @@
 //   O += P V    (128 x d x 128, P from TMEM, V in shared memory)     -> TMEM
 // Roles of a block (one per SM, persistent): warps 0-3 softmax of tile A and warps 4-7 of tile B
 // (a thread owns a row, so maxima and sums need no exchange), warp 8 issues the products, warp 9
-// feeds K and V through a ring of tensor copies (warps 10 and 11 only give up registers).  While one tile's softmax runs, the tensor
-// pipe works on the other tile.  O is rescaled only when a row's maximum has grown by more than
+// feeds K and V through a ring of tensor copies (warps 10 and 11 only give up registers).  While
+// one tile's softmax runs, the tensor pipe works on the other tile.  O is rescaled only when a row's maximum has grown by more than
 // 2^8 since the last time (the stored m is then any upper reference, not the maximum; weights
 // stay below 2^8), so most steps touch O by the product alone.
 //
@@ -941,8 +941,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int snap = static_cast<int>(
         max(static_cast<int64_t>(1), min(static_cast<int64_t>(kSnap), total / (2 * blocks))));
     int start[4] = {p.batch, 0, 0, 0};
-    const int64_t at =
-        line_border(p, tpi, total, blocks, snap, min(static_cast<int>(blockIdx.x) + warp, blocks), start);
+    const int border = min(static_cast<int>(blockIdx.x) + warp, blocks);
+    const int64_t at = line_border(p, tpi, total, blocks, snap, border, start);
     if (lane == 0 && warp == 0) {
       for (int i = 0; i < 4; ++i) s.start[i] = start[i];
       s.begin = at;

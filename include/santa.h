@@ -491,6 +491,8 @@ typedef struct santa_chunk_args {
  *     initialisation and serves one call at a time.  Results do not depend on its contents
  *     or on timing: equal calls give equal bits.
  *   - num_tokens may be 0 (nothing is launched).
+ *   - SANTA_DEV_TIMEOUT (bf16): a bounded wait inside the kernel gave up; the call's results are
+ *     not meaningful, the context stays usable.
  */
 size_t santa_chunk_workspace_bytes(int dtype, int batch, int64_t num_tokens, int num_q_heads,
                                    int num_kv_heads, int head_dim, int team_size,

@@ -8,9 +8,10 @@
 //              other computes): S = Q K^T (4 x 4 scores per thread), P = 2^(S - m), O = 2^(m_old -
 //              m) O + P V (4 x d/16).  Bound by fp32 FMAs and their operands' shared loads (16
 //              FMAs per 16-byte load).
-//   few rows   (at most 8, so the single token of any group): a warp takes 32 keys at a time, one
-//              per lane for the scores, all of them by columns for the product with V; the warps'
-//              results are joined at the end.  With 64-row tiles 15 of 16 threads would idle.
+//   few rows   (8 at a time, so the single token of any group at once): a warp takes 32 keys at a
+//              time, one per lane for the scores, all of them by columns for the product with V;
+//              the warps' results are joined at the end.  With 64-row tiles 15 of 16 threads
+//              would idle.
 // The keys of a tile are split over several blocks when there are few tiles (no split below 4
 // steps); a second launch joins their partial (m, l, O) in order.  Tiles are found from cu_q
 // through slots, as in append_chunk.cu: sequence b owns floor(cu[b] G / 64) + b onward, at least
@@ -35,7 +36,10 @@ constexpr int kThreads = 256;
 constexpr int kRows = 64;        // query rows per tile
 constexpr int kKeys = 64;        // keys per step (divides both page sizes)
 constexpr int kMinSpan = 4;      // steps below which a tile is not split
-constexpr int kFew = 8;          // rows of the few-rows way
+constexpr int kFew = 8;          // rows that the few-rows way takes at a time
+// Tiles of more rows than these go the other way: with two KV heads of 128 on 12505 tokens, 16 rows
+// take 49 us here (two passes) and 54 us there, 24 rows 65 and 54 us.
+constexpr int kFewMost = 16;
 constexpr int kWarps = kThreads / 32;
 
 template <int D>
@@ -147,14 +151,15 @@ __device__ __forceinline__ int64_t key_at(const ChunkParams& p, int b, int h, in
 
 template <int D>
 __device__ void few_rows(const ChunkParams& p, const Tile& t, FewSmem<D>& s, int G, int h,
-                         int64_t tile, int split, int splits, int64_t s0, int64_t s1,
+                         int64_t tile, int split, int splits, int64_t s0, int64_t s1, int first,
                          float* part_acc, float* part_ml) {
   constexpr int kCols = D / 32;                 // columns of O per lane
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  const int rows = static_cast<int>(min(static_cast<int64_t>(kFew), t.n * G - t.row0));
+  const int64_t row0 = t.row0 + first;          // of the (up to) 8 rows of this pass
+  const int rows = static_cast<int>(min(static_cast<int64_t>(kFew), t.n * G - row0));
   for (int i = threadIdx.x; i < kFew * D; i += kThreads) {
     const int r = i / D;
-    const int64_t row = t.row0 + r;
+    const int64_t row = row0 + r;
     s.q[r][i % D] =
         r < rows ? static_cast<const float*>(p.q)[((t.first + row / G) * p.num_q_heads + h * G +
                                                    row % G) * D + i % D]
@@ -163,8 +168,8 @@ __device__ void few_rows(const ChunkParams& p, const Tile& t, FewSmem<D>& s, int
   int64_t sees[kFew];
 #pragma unroll
   for (int r = 0; r < kFew; ++r)
-    sees[r] = r < rows ? t.len - t.n + (t.row0 + r) / G + 1 : 0;
-  const int64_t all_see = t.len - t.n + t.row0 / G + 1;
+    sees[r] = r < rows ? t.len - t.n + (row0 + r) / G + 1 : 0;
+  const int64_t all_see = t.len - t.n + row0 / G + 1;
   __syncthreads();
   float m[kFew], l[kFew], o[kFew][kCols];
 #pragma unroll
@@ -275,7 +280,7 @@ __device__ void few_rows(const ChunkParams& p, const Tile& t, FewSmem<D>& s, int
       acc.z = fmaf(f, x.z, acc.z);
       acc.w = fmaf(f, x.w, acc.w);
     }
-    finish4(p, t, tile, split, splits, h, G, r, D, c, acc, mm, ll, c == 0, part_acc, part_ml);
+    finish4(p, t, tile, split, splits, h, G, first + r, D, c, acc, mm, ll, c == 0, part_acc, part_ml);
   }
 }
 
@@ -295,9 +300,12 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(ChunkParams p, 
   const int64_t tile = static_cast<int64_t>(blockIdx.x) * p.num_kv_heads + h;
   const int64_t per = (t.steps + t.splits - 1) / t.splits;
   const int64_t s0 = split * per, s1 = min(t.steps, s0 + per);
-  if (t.n * G - t.row0 <= kFew) {
-    few_rows<D>(p, t, *reinterpret_cast<FewSmem<D>*>(raw), G, h, tile, split, splits, s0, s1,
-                part_acc, part_ml);
+  if (t.n * G - t.row0 <= kFewMost) {
+    for (int first = 0; first < t.n * G - t.row0; first += kFew) {
+      if (first > 0) __syncthreads();
+      few_rows<D>(p, t, *reinterpret_cast<FewSmem<D>*>(raw), G, h, tile, split, splits, s0, s1,
+                  first, part_acc, part_ml);
+    }
     return;
   }
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;

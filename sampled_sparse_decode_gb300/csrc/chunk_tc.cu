@@ -10,16 +10,16 @@
 // Roles of a block (one per SM, persistent): warps 0-3 softmax of tile A and warps 4-7 of tile B
 // (a thread owns a row, so maxima and sums need no exchange), warp 8 issues the products, warp 9
 // feeds K and V through a ring of tensor copies (warps 10 and 11 only give up registers).  While
-// one tile's softmax runs, the tensor pipe works on the other tile.  O is rescaled only when a row's maximum has grown by more than
-// 2^8 since the last time (the stored m is then any upper reference, not the maximum; weights
-// stay below 2^8), so most steps touch O by the product alone.
+// one tile's softmax runs, the tensor pipe works on the other tile.  O is rescaled only when a
+// row's maximum has grown by more than 2^8 since the last time (the stored m is a reference, not
+// the maximum; weights stay below 2^8), so most steps touch O by the product alone.
 //
 // Work split.  The steps of all items, in the order (sequence, KV head, item, step), are one line
 // of W units, a few more for each item's opening; block c of N takes the units [W c / N,
-// W (c + 1) / N).  An item that crosses a
-// border leaves partial (m, l, O) rows in the workspace, at most two per block, and a second
-// launch joins them in order: every block has the same work to within a step, for one long
-// sequence as for many short ones, and nothing depends on timing.
+// W (c + 1) / N), give or take a few that spare a cut (line_border).  An item that is cut leaves
+// partial (m, l, O) rows in the workspace, at most two per block, and a second launch joins them
+// in order: every block has the same work to within a few steps, for one long sequence as for
+// many short ones, and nothing depends on timing.
 //
 // Unseen values.  P is 0 for a masked pair, but 0 * V is not 0 for an infinite or NaN V.  Steps
 // that hold masked pairs (the causal border and the sequence's end) therefore pass through the

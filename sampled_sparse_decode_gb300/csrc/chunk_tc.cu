@@ -189,6 +189,12 @@ __device__ __forceinline__ bool wait_or_abort(TcShared& s, uint64_t* bar, uint32
   return true;
 }
 
+// The same by all lanes of a warp, with one answer: a lane that left alone would leave the others
+// waiting for it in the warp's next common instruction.
+__device__ __forceinline__ bool warp_wait(TcShared& s, uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait_or_abort(s, bar, parity));
+}
+
 // Two fp32 values in a register pair, and the instructions that work on both.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
   uint64_t r;
@@ -458,7 +464,7 @@ __device__ void copy_role(const TcParams& t, TcShared& s, unsigned char* q_smem,
   auto claim = [&] {
     if (tiles >= C::kStages) {
       const int g = s.group_of[stage];
-      ok = wait_or_abort(s, &s.kv_empty[g % kGroups], (g / kGroups) & 1);
+      ok = warp_wait(s, &s.kv_empty[g % kGroups], (g / kGroups) & 1);
       __syncwarp();
     }
     if (lane == 0) s.group_of[stage] = group;
@@ -471,11 +477,11 @@ __device__ void copy_role(const TcParams& t, TcShared& s, unsigned char* q_smem,
   for (int turn = 0; ok && r.open(tpi); r.next(p, tpi), turn = turn == 2 ? 0 : turn + 1) {
     const int tok = r.item * tpi;
     const bool two = tok + t.tpt < r.seq.n;
-    ok = wait_or_abort(s, &s.q_empty, q_parity);
+    ok = warp_wait(s, &s.q_empty, q_parity);
     q_parity ^= 1;
     if (!ok) break;
     // the notes of three runs ago have been read (tile B may lag behind runs that A has alone)
-    ok = wait_or_abort(s, &s.run_done[turn], (runs / 3 + 1) & 1);
+    ok = warp_wait(s, &s.run_done[turn], (runs / 3 + 1) & 1);
     if (!ok) break;
     if (lane == 0) mbar_arrive(&s.run_open[turn]);
     if (lane < 16) s.noted[turn][lane / 4][lane % 4] = 0u;
@@ -546,7 +552,7 @@ __device__ void copy_role(const TcParams& t, TcShared& s, unsigned char* q_smem,
         load(k_dst, &t.tmap_k, bar);
       }
       if (check) {
-        ok = wait_or_abort(s, &s.land, land_parity);
+        ok = warp_wait(s, &s.land, land_parity);
         land_parity ^= 1;
         if (!ok) break;
         // rows [lo, hi) are seen by some rows of the item only, rows from hi on by none
@@ -559,8 +565,8 @@ __device__ void copy_role(const TcParams& t, TcShared& s, unsigned char* q_smem,
       if (lane == 0) mbar_arrive(bar);
     }
   }
-  if (!ok && lane == 0) {
-    // drain: what was issued lands before the block may end (bounded)
+  if (lane == 0) {
+    // what was issued lands before the block may end (bounded; it has, unless a wait gave up)
     const uint64_t start = global_timer_ns();
     while (runs && !mbar_try_wait(&s.q_full, (runs - 1) & 1) &&
            global_timer_ns() - start < kWaitLimitNs) {
@@ -570,7 +576,7 @@ __device__ void copy_role(const TcParams& t, TcShared& s, unsigned char* q_smem,
              global_timer_ns() - start < kWaitLimitNs) {
       }
     // copies of a group that was not completed: nothing signals them, so the time is waited out
-    while (global_timer_ns() - start < kDrainNs) {
+    while (!ok && global_timer_ns() - start < kDrainNs) {
     }
   }
 }
@@ -707,7 +713,7 @@ __device__ void softmax_role(const TcParams& t, TcShared& s) {
     const int tok0 = r.item * tpi + x * t.tpt;           // first token of this tile
     if (tok0 >= r.seq.n) {
       // not before the run has begun: an early arrival would count for another run of the ring
-      if (!wait_or_abort(s, &s.run_open[turn], parity >> 2 & 1)) return;
+      if (!warp_wait(s, &s.run_open[turn], parity >> 2 & 1)) return;
       if ((threadIdx.x & 31) == 0) mbar_arrive(&s.run_done[turn]);
       if (turn == 2) parity ^= 4;
       continue;
@@ -719,7 +725,7 @@ __device__ void softmax_role(const TcParams& t, TcShared& s) {
     const bool warp_idle = __ballot_sync(0xffffffffu, mine) == 0u;
     float m = -INFINITY, l = 0.f;
     for (int j = r.s0; j < r.s1; ++j) {
-      if (!wait_or_abort(s, &s.s_full[x], parity & 1)) return;
+      if (!warp_wait(s, &s.s_full[x], parity & 1)) return;
       parity ^= 1;
       if (!warp_idle) {
         tc_fence_after();
@@ -789,7 +795,7 @@ __device__ void softmax_role(const TcParams& t, TcShared& s) {
       }
     }
     // ---- epilogue: the row, or its partial result
-    if (!wait_or_abort(s, &s.o_full[x], parity >> 1 & 1)) return;
+    if (!warp_wait(s, &s.o_full[x], parity >> 1 & 1)) return;
     parity ^= turn == 2 ? 6 : 2;
     if (warp_idle) {
       if ((threadIdx.x & 31) == 0) mbar_arrive(&s.run_done[turn]);
@@ -964,11 +970,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (warp == 8) {
       if (lane == 0) {
         mma_role<D>(t, s, smem_u32(q_smem), smem_u32(ring));
-        if (s.abort) {                           // no product is in flight when TMEM is freed
-          tc_commit(&s.drain);
-          const uint64_t begin = global_timer_ns();
-          while (!mbar_try_wait(&s.drain, 0) && global_timer_ns() - begin < kWaitLimitNs) {
-          }
+        tc_commit(&s.drain);                     // no product is in flight when TMEM is freed
+        const uint64_t begin = global_timer_ns();
+        while (!mbar_try_wait(&s.drain, 0) && global_timer_ns() - begin < kWaitLimitNs) {
         }
       }
       __syncwarp();

@@ -119,9 +119,9 @@ __device__ __forceinline__ bool find_tile(const ChunkParams& p, int64_t slot, in
 }
 
 // A row's result: the output, or the partial one of this split.  `cols` values from column c.
-__device__ __forceinline__ void finish4(const ChunkParams& p, const Tile& t, int64_t tile, int split,
-                                        int splits, int h, int G, int r, int D, int c, float4 o,
-                                        float m, float l, bool first, float* part_acc,
+__device__ __forceinline__ void finish4(const ChunkParams& p, const Tile& t, int64_t tile,
+                                        int split, int splits, int h, int G, int r, int D, int c,
+                                        float4 o, float m, float l, bool first, float* part_acc,
                                         float* part_ml) {
   const int64_t row = t.row0 + r;
   if (t.splits == 1) {
@@ -280,7 +280,8 @@ __device__ void few_rows(const ChunkParams& p, const Tile& t, FewSmem<D>& s, int
       acc.z = fmaf(f, x.z, acc.z);
       acc.w = fmaf(f, x.w, acc.w);
     }
-    finish4(p, t, tile, split, splits, h, G, first + r, D, c, acc, mm, ll, c == 0, part_acc, part_ml);
+    finish4(p, t, tile, split, splits, h, G, first + r, D, c, acc, mm, ll, c == 0, part_acc,
+            part_ml);
   }
 }
 
@@ -294,7 +295,8 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(ChunkParams p, 
   const int G = p.num_q_heads / p.num_kv_heads;
   const int h = blockIdx.y, split = blockIdx.z;
   grid_dependency_wait();
-  if (blockIdx.x == 0 && h == 0 && split == 0) check_bounds(p.cu_q, p.batch, p.num_tokens, p.status);
+  if (blockIdx.x == 0 && h == 0 && split == 0)
+    check_bounds(p.cu_q, p.batch, p.num_tokens, p.status);
   Tile t;
   if (!find_tile(p, blockIdx.x, G, splits, &t) || split >= t.splits) return;
   const int64_t tile = static_cast<int64_t>(blockIdx.x) * p.num_kv_heads + h;
@@ -322,9 +324,8 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_simt_kernel(ChunkParams p, 
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t row = t.row0 + ty * 4 + i;
-    sees[i] = row < t.n * G
-                  ? static_cast<int>(max(t.len - t.n + row / G + 1 - s0 * kKeys, static_cast<int64_t>(0)))
-                  : 0;
+    const int64_t ahead = t.len - t.n + row / G + 1 - s0 * kKeys;
+    sees[i] = row < t.n * G && ahead > 0 ? static_cast<int>(ahead) : 0;
   }
   const int64_t all_see = t.len - t.n + t.row0 / G + 1;   // keys that every row sees
 

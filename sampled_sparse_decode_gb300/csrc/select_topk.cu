@@ -260,13 +260,12 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(SelectParams p) 
           if (lane == 0) set_status(p.status, SANTA_DEV_BAD_PAGE);
           from[u] = -1;
         }
+        const float4* rep = reinterpret_cast<const float4*>(
+            p.reps + (static_cast<int64_t>(from[u]) * p.num_kv_heads + h) * D);
 #pragma unroll
         for (int e = 0; e < kQuads; ++e)
-          to[u][e] = from[u] < 0
-                         ? make_float4(0.f, 0.f, 0.f, 0.f)
-                         : __ldg(reinterpret_cast<const float4*>(
-                                     p.reps + (static_cast<int64_t>(from[u]) * p.num_kv_heads + h) * D) +
-                                 e * kLanes + lane);
+          to[u][e] = from[u] < 0 ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                 : __ldg(rep + e * kLanes + lane);
       }
     };
     load_reps(rank * kRound, page, r);
@@ -321,8 +320,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(SelectParams p) 
       for (int g = 0; g < 2; ++g)
         f[g] = (b1 ? d[g + 2] : d[g]) + __shfl_xor_sync(0xffffffffu, b1 ? d[g] : d[g + 2], 2);
       const float sum = (b0 ? f[1] : f[0]) + __shfl_xor_sync(0xffffffffu, b0 ? f[0] : f[1], 1);
-      const float norm2 = (b3 ? nn[1] : nn[0]) + __shfl_xor_sync(0xffffffffu, b3 ? nn[0] : nn[1], 8);
-      float best = (lane & 7) < G ? sum : -INFINITY, n2 = norm2;
+      float n2 = (b3 ? nn[1] : nn[0]) + __shfl_xor_sync(0xffffffffu, b3 ? nn[0] : nn[1], 8);
+      float best = (lane & 7) < G ? sum : -INFINITY;
       // a NaN of any of the team's heads: its 8 lanes' bits of the warp's vote
       const unsigned nans = __ballot_sync(0xffffffffu, (lane & 7) < G && sum != sum);
       const bool nan = (nans >> (threadIdx.x & 24)) & 0xffu;
@@ -408,7 +407,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(SelectParams p) 
   int want = keep - (total & 0xffff);
   if (near_total > want) {
     // the near teams' indices (over the fp32 keys, which are no longer needed) and 64-bit keys
-    unsigned long long* exact = reinterpret_cast<unsigned long long*>(keys + (p.max_teams + 3) / 4 * 4);
+    unsigned long long* exact =
+        reinterpret_cast<unsigned long long*>(keys + (p.max_teams + 3) / 4 * 4);
     int at = near_at;
     for (uint64_t m = near; m; m &= m - 1) keys[at++] = i0 + __ffsll(m) - 1;
     __syncthreads();

@@ -805,8 +805,9 @@ __device__ void softmax_role(const TcParams& t, TcShared& s) {
     const bool whole = r.s0 == 0 && r.s1 == r.steps;
     const int64_t out_row =
         (static_cast<int64_t>(r.seq.first + tok) * p.num_q_heads + r.h * G + g) * D;
+    // notes are taken from the keys on that the item's (not the tile's) first token does not see
     bool noted = false;
-    if ((r.s1) * kStep > all_see)
+    if (r.s1 * kStep > r.seq.ctx + r.item * tpi + 1)
 #pragma unroll
       for (int e = 0; e < 16; ++e) noted |= s.noted[turn][e / 4][e % 4] != 0u;
     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;

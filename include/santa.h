@@ -502,12 +502,14 @@ int santa_chunk_attend(const santa_chunk_args* a, void* stream);
 /*
  * santa_select_topk — the deterministic counterpart of santa_sample: the score of team i for
  * unit (b, h) is s_i = max over the group's heads g of q_g . rep_i, and S is the min(M, n)
- * teams of largest s_i (ties to the lower index; a NaN score ranks last).  M = num_draws.
+ * teams of largest s_i (ties to the lower index).  A team with a NaN score or with a page id out
+ * of range ranks below every score, -inf included; a bad page sets SANTA_DEV_BAD_PAGE.
+ * M = num_draws.
  * Scores are fp32; teams whose scores lie too close to the border of S for fp32 to order are
  * compared in 64 bits, so S is the set that 64-bit scores give.  Writes sel_ids (ascending,
  * padded with -1), sel_count and pi (1 for each selected team, padded with 0).  Reads q, reps,
  * page_table, seq_lens; k_pool, v_pool, seed, sampler, draw_ids, team_probs and workspace are
- * not used.  A team with a page id out of range ranks last and sets SANTA_DEV_BAD_PAGE.
+ * not used.
  */
 int santa_select_topk(const santa_decode_args* a, void* stream);
 

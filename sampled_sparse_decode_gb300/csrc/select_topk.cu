@@ -25,9 +25,10 @@ namespace {
 constexpr int kSelThreads = 256;
 constexpr int kLanes = 16;                                // lanes per team
 
-// Order-preserving map of fp32 to unsigned; NaN and -inf map to the lowest value.
+// Order-preserving map of fp32 to unsigned: NaN maps to 0 (as a bad page does), -inf to the value
+// above it that any score has.
 __device__ __forceinline__ uint32_t score_key(float s) {
-  if (!(s > -INFINITY)) return 0u;
+  if (s != s) return 0u;
   const uint32_t u = __float_as_uint(s + 0.f);            // -0 and 0 are one score
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
@@ -85,7 +86,7 @@ __device__ __forceinline__ float q_at(const void* q, int64_t i) {
 }
 
 // 64-bit score of team `page` by one warp (all lanes get it), as an order-preserving key: the
-// largest product over the heads; 0 for NaN and -inf.
+// largest product over the heads; 0 for NaN.
 template <bool BF16, int D>
 __device__ uint64_t exact_key(const SelectParams& p, int64_t page, int b, int h, int G) {
   const int lane = threadIdx.x & 31;
@@ -103,7 +104,7 @@ __device__ uint64_t exact_key(const SelectParams& p, int64_t page, int b, int h,
     nan |= s != s;
     best = s > best ? s : best;
   }
-  if (nan || best == -INFINITY) return 0u;
+  if (nan) return 0u;
   const uint64_t u = static_cast<uint64_t>(__double_as_longlong(best + 0.0));
   return u >> 63 ? ~u : u | 1ull << 63;
 }

@@ -709,24 +709,47 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 class _Prepared:
     """A call whose arguments are checked and marshalled once, for steps that reuse the same
-    tensors: their contents may change between runs, their storage may not."""
+    tensors: their contents may change between runs, their storage may not.  The runs of one
+    handle share its buffers (workspace and results): a run on another stream must wait for the
+    run before it, and work at the same time takes a handle each.  A CUDA graph that captured a
+    run uses the handle's buffers: keep the handle as long as the graph is replayed."""
 
-    def __init__(self, name, args, keep, result):
+    def __init__(self, name, args, keep, result, stream=None):
         self._name, self._fn = name, getattr(lib(), name)
         self._a, self._aref = args, ctypes.byref(args)
         self._keep, self._result = keep, result
         self._device = torch.cuda.current_device()
+        # streams that the allocator waits for by itself before it reuses the memory: the one
+        # that the buffers were made for, then those that _record names to it
+        self._known = {self._raw(stream)} if keep else set()
+
+    def _raw(self, stream):
+        return _raw_stream(self._device) if stream is None else _stream(stream)
 
     def run(self, stream=None):
         """Enqueues the call on `stream` (the current stream by default); returns its result
         buffers.  Buffers that the preparation made are filled on the stream that was current
-        then: another stream must wait for it before its first run."""
+        then: another stream must wait for it before its first run.  The handle may be dropped
+        while runs are in flight on any stream."""
         if torch.cuda.current_device() != self._device:
             raise SantaError(f"{self._name} was prepared on cuda:{self._device}")
-        rc = self._fn(self._aref, _raw_stream(self._device) if stream is None else _stream(stream))
+        raw = self._raw(stream)
+        if raw not in self._known:
+            self._record(raw, stream)
+        rc = self._fn(self._aref, raw)
         if rc:
             _check(rc, self._name)
         return self._result
+
+    def _record(self, raw, stream):
+        """Memory behind the call is reused only after the work that this stream has been given
+        by the time it is freed."""
+        for t in self._keep:
+            if t is not None:
+                if not isinstance(stream, torch.cuda.Stream):
+                    stream = torch.cuda.ExternalStream(raw) if raw else torch.cuda.default_stream()
+                t.record_stream(stream)
+        self._known.add(raw)
 
 
 def santa_rope_table(positions: int, rope_dim: int, theta: float = 10000.0, device="cuda",
@@ -798,9 +821,9 @@ def _append_chunk(q, k_new, v_new, cu_q, k_pool, v_pool, reps, page_table, seq_l
     a.interleaved = int(bool(interleaved))
     a.k_pool, a.v_pool, a.reps = _ptr(k_pool), _ptr(v_pool), _ptr(reps)
     a.seq_lens_next, a.device_status = _ptr(seq_lens_next), _ptr(device_status)
-    keep = (q, k_new, v_new, cu_q, k_pool, v_pool, reps, page_table, seq_lens, rope,
+    keep = (q, k_new, v_new, cu_q, k_pool, v_pool, reps, page_table, seq_lens, rope, q_out,
             seq_lens_next, device_status)
-    return _Prepared("santa_append_chunk", a, keep, q_out)
+    return _Prepared("santa_append_chunk", a, keep, q_out, stream)
 
 
 def santa_append_chunk(q, k_new, v_new, cu_q, k_pool, v_pool, reps, page_table, seq_lens,
@@ -874,8 +897,8 @@ def _chunk_attend(q, k_pool, v_pool, page_table, seq_lens, cu_q, out, workspace,
     a.team_size, a.max_teams = T, page_table.shape[1]
     a.out, a.workspace, a.workspace_bytes = _ptr(out), _ptr(workspace), workspace.numel()
     a.device_status = _ptr(device_status)
-    keep = (q, k_pool, v_pool, page_table, seq_lens, cu_q, workspace, device_status)
-    return _Prepared("santa_chunk_attend", a, keep, out)
+    keep = (q, k_pool, v_pool, page_table, seq_lens, cu_q, out, workspace, device_status)
+    return _Prepared("santa_chunk_attend", a, keep, out, stream)
 
 
 def santa_chunk_attend(q, k_pool, v_pool, page_table, seq_lens, cu_q,
@@ -922,10 +945,12 @@ def _topk(name, q, k_pool, v_pool, reps, page_table, seq_lens, num_teams, bufs, 
         if tuple(getattr(bufs, field).shape) != shape:
             raise SantaError(f"bufs.{field} must be {shape}")
     a = _args(q, k_pool, v_pool, reps, page_table, seq_lens, num_teams, 0, bufs)
+    # the tensors themselves: bufs' fields may be replaced later
+    made = tuple(vars(bufs).values())
     _same_device(q=q, k_pool=k_pool, v_pool=v_pool, reps=reps, page_table=page_table,
                  seq_lens=seq_lens, out=bufs.out, workspace=bufs.workspace)
-    keep = (q, k_pool, v_pool, reps, page_table, seq_lens)
-    return _Prepared(name, a, keep, bufs)
+    keep = (q, k_pool, v_pool, reps, page_table, seq_lens, *made)
+    return _Prepared(name, a, keep, bufs, stream)
 
 
 def santa_select_topk(q, k_pool, v_pool, reps, page_table, seq_lens, num_teams: int,

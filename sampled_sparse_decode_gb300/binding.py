@@ -948,7 +948,9 @@ def _topk(name, q, k_pool, v_pool, reps, page_table, seq_lens, num_teams, bufs, 
     # the tensors themselves: bufs' fields may be replaced later
     made = tuple(vars(bufs).values())
     _same_device(q=q, k_pool=k_pool, v_pool=v_pool, reps=reps, page_table=page_table,
-                 seq_lens=seq_lens, out=bufs.out, workspace=bufs.workspace)
+                 seq_lens=seq_lens, out=bufs.out, sel_ids=bufs.sel_ids,
+                 sel_count=bufs.sel_count, pi=bufs.pi, workspace=bufs.workspace,
+                 device_status=bufs.device_status)
     keep = (q, k_pool, v_pool, reps, page_table, seq_lens, *made)
     return _Prepared(name, a, keep, bufs, stream)
 

@@ -421,11 +421,13 @@ typedef struct santa_append_chunk_args {
   int rope_dim;                /* R: 0 (no rotation) or a multiple of 16 up to head_dim */
   int interleaved;             /* 0: pairs (j, j + R/2); 1: pairs (2j, 2j + 1) */
   void* q_out;                 /* [num_tokens][Hq][d] contiguous, rotated queries; may be q
-                                  itself when q_stride = Hq * d; NULL with q */
+                                  itself when q_stride = Hq * d, and overlaps no row of q,
+                                  k_new or v_new otherwise; NULL with q */
   void* k_pool;                /* [P][Hkv][T][d] */
   void* v_pool;
   float* reps;                 /* [P][Hkv][d] */
-  int32_t* seq_lens_next;      /* [B] receives the new lengths (may be NULL; not seq_lens) */
+  int32_t* seq_lens_next;      /* [B] receives the new lengths (may be NULL; does not overlap
+                                  seq_lens or cu_q) */
   int32_t* device_status;      /* may be NULL */
 } santa_append_chunk_args;
 
@@ -467,7 +469,7 @@ typedef struct santa_chunk_args {
   int head_dim;
   int team_size;
   int max_teams;
-  void* out;                   /* [num_tokens][Hq][d] dtype */
+  void* out;                   /* [num_tokens][Hq][d] dtype; does not overlap q */
   void* workspace;             /* santa_chunk_workspace_bytes; contents need not be set */
   size_t workspace_bytes;
   int32_t* device_status;      /* may be NULL */

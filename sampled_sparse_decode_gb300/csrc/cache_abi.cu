@@ -34,6 +34,16 @@ int check_tokens(int64_t num_tokens) {
   if (num_tokens < 0) return SANTA_ERR_INVALID_ARG;
   return num_tokens > kMaxTokens ? SANTA_ERR_UNSUPPORTED : SANTA_OK;
 }
+// Whether [a, a + bytes) meets one of the `rows` rows of row_bytes that lie stride_bytes
+// (>= row_bytes) apart from b on.
+bool meets(const void* a, int64_t bytes, const void* b, int64_t rows, int64_t row_bytes,
+           int64_t stride_bytes) {
+  if (!a || !b || bytes <= 0 || rows <= 0 || row_bytes <= 0) return false;
+  const __int128 lo = reinterpret_cast<uintptr_t>(a), at = reinterpret_cast<uintptr_t>(b);
+  // the first row that ends behind lo
+  const __int128 r = at + row_bytes > lo ? 0 : (lo - at - row_bytes) / stride_bytes + 1;
+  return r < rows && at + r * stride_bytes < lo + bytes;
+}
 
 // Workspace of a chunk attention: bf16 has one of its own; fp32 keeps the partial results of
 // its split tiles, accumulators, then (m, l).
@@ -114,10 +124,19 @@ int santa_append_chunk(const santa_append_chunk_args* a, void* stream) {
       !aligned(a->reps, 16) || !aligned(a->cu_q, 4) || !aligned(a->page_table, 4) ||
       !aligned(a->seq_lens, 4) || !aligned(a->seq_lens_next, 4) || !aligned(a->device_status, 4))
     return SANTA_ERR_INVALID_ARG;
-  if (a->seq_lens_next == a->seq_lens) return SANTA_ERR_INVALID_ARG;   // read while written
   if (santa::append_chunk_blocks(a->num_tokens, a->batch, a->q ? a->num_q_heads : 0,
                                  a->num_kv_heads, a->head_dim, a->team_size, bf16) > 0x7fffffffll)
     return SANTA_ERR_UNSUPPORTED;
+  // what is written while other blocks still read: rotated queries over the new rows (but for a
+  // rotation in place), new lengths over the batch's lengths and bounds
+  const int64_t es = bf16 ? 2 : 4, n = a->num_tokens, len_bytes = int64_t(a->batch) * 4;
+  const int64_t q_bytes = a->q ? n * q_row * es : 0;
+  if ((a->q_out != a->q && meets(a->q_out, q_bytes, a->q, n, q_row * es, a->q_stride * es)) ||
+      meets(a->q_out, q_bytes, a->k_new, n, kv_row * es, a->k_stride * es) ||
+      meets(a->q_out, q_bytes, a->v_new, n, kv_row * es, a->v_stride * es) ||
+      meets(a->seq_lens_next, len_bytes, a->seq_lens, 1, len_bytes, len_bytes) ||
+      meets(a->seq_lens_next, len_bytes, a->cu_q, 1, len_bytes + 4, len_bytes + 4))
+    return SANTA_ERR_INVALID_ARG;
   santa::AppendChunkParams p = {};
   p.q = a->q;
   p.k_new = a->k_new;
@@ -175,6 +194,11 @@ int santa_chunk_attend(const santa_chunk_args* a, void* stream) {
       !aligned(a->cu_q, 4) || !aligned(a->device_status, 4))
     return SANTA_ERR_INVALID_ARG;
   if (a->num_tokens == 0) return SANTA_OK;
+  // queries are read again after rows of `out` are written
+  const int64_t row = static_cast<int64_t>(a->num_q_heads) * a->head_dim *
+                      (a->dtype == SANTA_BF16 ? 2 : 4);
+  if (meets(a->out, a->num_tokens * row, a->q, a->num_tokens, row, row))
+    return SANTA_ERR_INVALID_ARG;
   ChunkLayout l;
   if ((rc = chunk_layout(a->dtype, a->batch, a->num_tokens, a->num_q_heads, a->num_kv_heads,
                          a->head_dim, a->team_size, a->max_teams, &l)))

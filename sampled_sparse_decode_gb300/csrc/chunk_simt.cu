@@ -485,21 +485,22 @@ __global__ void __launch_bounds__(kThreads) chunk_join_kernel(ChunkParams p, int
        r += gridDim.z * (kThreads / 32)) {
     const int64_t row = t.row0 + r;
     if (row >= t.n * G) break;
+    // plain loads: the launch before this one wrote the parts (see grid_dependency_wait)
     const float2* ml = reinterpret_cast<const float2*>(part_ml) + tile * splits * kRows + r;
     float m = -INFINITY, l = 0.f, acc[kVals];
 #pragma unroll
     for (int e = 0; e < kVals; ++e) acc[e] = 0.f;
-    for (int i = lane; i < t.splits; i += 32) m = fmaxf(m, __ldg(ml + i * kRows).x);
+    for (int i = lane; i < t.splits; i += 32) m = fmaxf(m, ml[i * kRows].x);
     m = warp_max(m);
     const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll 8
     for (int i = 0; i < t.splits; ++i) {
-      const float2 e2 = __ldg(ml + i * kRows);
+      const float2 e2 = ml[i * kRows];
       const float* src = part_acc + ((tile * splits + i) * kRows + r) * D + lane;
       const float w = exp2f(e2.x - ref);                  // 0 for a split that saw nothing
       l = fmaf(w, e2.y, l);
 #pragma unroll
-      for (int e = 0; e < kVals; ++e) acc[e] = fmaf(w, __ldg(src + e * 32), acc[e]);
+      for (int e = 0; e < kVals; ++e) acc[e] = fmaf(w, src[e * 32], acc[e]);
     }
     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
     const int64_t out = ((t.first + row / G) * p.num_q_heads + h * G + row % G) * D;

@@ -1010,10 +1010,12 @@ __global__ void __launch_bounds__(D * 4) chunk_tc_join_kernel(ChunkParams p, int
   if (in_tile >= tpt || tok >= n) return;
   // part 0 is the second partial of block c0, part i the first one of block c0 + i
   auto at = [&](int i) { return static_cast<int64_t>(c0 + i) * 2 + (i == 0 ? 1 : 0); };
+  // plain loads: this kernel may have been resident while the parts were written, so they are no
+  // read-only data to it
   const float2* ml = reinterpret_cast<const float2*>(part_ml);
   float m = -INFINITY;
 #pragma unroll 4
-  for (int i = 0; i < parts; ++i) m = fmaxf(m, __ldg(ml + at(i) * 256 + row).x);
+  for (int i = 0; i < parts; ++i) m = fmaxf(m, ml[at(i) * 256 + row].x);
   const float ref = m == -INFINITY ? 0.f : m;
   // this warp's 8 columns
   const int q0 = (threadIdx.x / 32) * 2;
@@ -1021,9 +1023,9 @@ __global__ void __launch_bounds__(D * 4) chunk_tc_join_kernel(ChunkParams p, int
   float l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
   for (int i = 0; i < parts; ++i) {
-    const float2 e = __ldg(ml + at(i) * 256 + row);
-    const float4 a = __ldg(acc + (at(i) * (D / 4) + q0) * 256 + row);
-    const float4 b = __ldg(acc + (at(i) * (D / 4) + q0 + 1) * 256 + row);
+    const float2 e = ml[at(i) * 256 + row];
+    const float4 a = acc[(at(i) * (D / 4) + q0) * 256 + row];
+    const float4 b = acc[(at(i) * (D / 4) + q0 + 1) * 256 + row];
     const float w = ex2_approx(e.x - ref);
     l = fmaf(w, e.y, l);
     o[0] = fmaf(w, a.x, o[0]);

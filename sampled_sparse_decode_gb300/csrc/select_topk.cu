@@ -225,12 +225,14 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(SelectParams p) 
   // depend on the length, and the first page ids are on their way together with it and the
   // queries (each is a read from DRAM when the cache is larger than L2).
   const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  // plain loads: the launch before this one may have written the table and the representatives
+  // while this one was resident, so they are no read-only data to it
   const int32_t* table = p.page_table + static_cast<int64_t>(b) * p.max_teams;
   auto load_ids = [&](int base, int(&to)[kTeams]) {
 #pragma unroll
     for (int u = 0; u < kTeams; ++u) {
       const int team = base + u * (kSelThreads / kLanes) + group;
-      to[u] = team < p.max_teams ? __ldg(table + team) : -1;
+      to[u] = team < p.max_teams ? table[team] : -1;
     }
   };
   int page[kTeams], page_next[kTeams];
@@ -250,7 +252,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(SelectParams p) 
     uint32_t norm = 0u;
     bool waited = false;
     float4 r[kTeams][kQuads], r_next[kTeams][kQuads];
-    // representatives of a round; a team behind the end or with a bad page id scores nothing
+    // representatives of a round; a team behind the end or with a bad page id scores nothing (the
+    // ids are judged first: a status write between the loads would hold the later ones back)
     auto load_reps = [&](int base, int(&from)[kTeams], float4(&to)[kTeams][kQuads]) {
 #pragma unroll
       for (int u = 0; u < kTeams; ++u) {
@@ -261,12 +264,13 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(SelectParams p) 
           if (lane == 0) set_status(p.status, SANTA_DEV_BAD_PAGE);
           from[u] = -1;
         }
+      }
+#pragma unroll
+      for (int u = 0; u < kTeams; ++u) {
         const float4* rep = reinterpret_cast<const float4*>(
             p.reps + (static_cast<int64_t>(from[u]) * p.num_kv_heads + h) * D);
 #pragma unroll
-        for (int e = 0; e < kQuads; ++e)
-          to[u][e] = from[u] < 0 ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                 : __ldg(rep + e * kLanes + lane);
+        for (int e = 0; e < kQuads; ++e) to[u][e] = from[u] < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : rep[e * kLanes + lane];
       }
     };
     load_reps(rank * kRound, page, r);

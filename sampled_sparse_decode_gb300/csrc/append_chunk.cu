@@ -107,6 +107,8 @@ __device__ __forceinline__ void turn_f32(uint32_t& a, uint32_t& b, float c, floa
 // Rotates N pairs of pieces that share a position, with the table row's entries from `first` on:
 // by halves both pieces of a pair use the same kVec entries; interleaved, piece a uses kVec / 2
 // and piece b (the next one) the kVec / 2 after them.
+// Its read-only loads ask that no launch that lets the next one start early writes the table:
+// santa_rope_table does not.
 template <bool BF16, int N>
 __device__ __forceinline__ void rotate(uint4 (&a)[N], uint4 (&b)[N], const float* row, int half_dim,
                                        int first, bool interleaved) {
@@ -246,9 +248,22 @@ __device__ void page_item(const AppendChunkParams& p, int64_t slot, int h, float
     uint4* pool = static_cast<uint4*>(p.v_pool) + blk;
     const uint4* src = static_cast<const uint4*>(p.v_new) + h * kCols;
     const int64_t stride = p.v_stride / V;
-#pragma unroll 8
-    for (int i = row0 * kCols + t; i < row1 * kCols; i += kAppendThreads / 2)
-      pool[i] = __ldg(src + (tok0 + i / kCols) * stride + i % kCols);
+    // eight pieces at a time, all of their loads first (plain ones: what the launch before this one
+    // writes is no read-only data to it)
+    constexpr int kBatch = 8, kStep = kAppendThreads / 2;
+    for (int i0 = row0 * kCols + t; i0 < row1 * kCols; i0 += kBatch * kStep) {
+      uint4 w[kBatch];
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        const int i = i0 + e * kStep;
+        if (i < row1 * kCols) w[e] = src[(tok0 + i / kCols) * stride + i % kCols];
+      }
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        const int i = i0 + e * kStep;
+        if (i < row1 * kCols) pool[i] = w[e];
+      }
+    }
   }
   __syncthreads();
   for (int e = threadIdx.x; e < D; e += kAppendThreads) {

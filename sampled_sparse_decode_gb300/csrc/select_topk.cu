@@ -270,7 +270,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(SelectParams p) 
         const float4* rep = reinterpret_cast<const float4*>(
             p.reps + (static_cast<int64_t>(from[u]) * p.num_kv_heads + h) * D);
 #pragma unroll
-        for (int e = 0; e < kQuads; ++e) to[u][e] = from[u] < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : rep[e * kLanes + lane];
+        for (int e = 0; e < kQuads; ++e)
+          to[u][e] = from[u] < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : rep[e * kLanes + lane];
       }
     };
     load_reps(rank * kRound, page, r);

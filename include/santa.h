@@ -518,9 +518,9 @@ int santa_select_topk(const santa_decode_args* a, void* stream);
 /*
  * santa_topk_decode — santa_select_topk followed by santa_attend on `stream`: exact attention
  * inside the M teams of best representative score.  (With bf16 caches the weights enter the
- * product with V in full, where santa_attend keeps about 16 bits of them.)  A chunk of several query tokens of one
- * sequence is served as that many rows of the batch, with the same page-table row and
- * growing lengths.  Workspace as for santa_decode.
+ * product with V in full, where santa_attend keeps about 16 bits of them.)  A chunk of several
+ * query tokens of one sequence is served as that many rows of the batch, with the same page-table
+ * row and growing lengths.  Workspace as for santa_decode.
  */
 int santa_topk_decode(const santa_decode_args* a, void* stream);
 

@@ -837,7 +837,7 @@ def santa_append_chunk(q, k_new, v_new, cu_q, k_pool, v_pool, reps, page_table, 
     seq_lens_next (if given) receives the new lengths.  q, k_new and v_new may be strided from
     token to token (views of a fused projection).  Returns the rotated queries: q_out, or a new
     tensor whose rows outside every sequence are zero; q_out may be q itself if q is
-    contiguous."""
+    contiguous, and overlaps none of q, k_new and v_new otherwise."""
     return _append_chunk(q, k_new, v_new, cu_q, k_pool, v_pool, reps, page_table, seq_lens,
                          rope, seq_lens_next, q_out, interleaved, device_status,
                          stream).run(stream)
@@ -906,7 +906,8 @@ def santa_chunk_attend(q, k_pool, v_pool, page_table, seq_lens, cu_q,
                        device_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Exact causal attention of a ragged chunk (q [tokens][Hq][d], cu_q [B + 1]; the last
     cu_q[b + 1] - cu_q[b] of sequence b's seq_lens[b] cached tokens) over the paged cache.
-    Returns out [tokens][Hq][d] in q's dtype (a new tensor: zero outside every sequence)."""
+    Returns out [tokens][Hq][d] in q's dtype, which does not overlap q (a new tensor: zero outside
+    every sequence)."""
     return _chunk_attend(q, k_pool, v_pool, page_table, seq_lens, cu_q, out, workspace,
                          device_status, stream).run(stream)
 

@@ -18,8 +18,8 @@
 // cosine and a sine serve both of its elements and the 128 threads cover the same split.
 //
 // Bound by HBM for prompts and by latency for single tokens.  Measured on GB300: 8 sequences of
-// 4096 tokens (32 query and 8 KV heads of 128, bf16) 133 us, 6.2 TB/s of what must move; one token
-// for each of 8 sequences 4.0 us.  The page items' key loop takes four rows at a time with all of
+// 4096 tokens (32 query and 8 KV heads of 128, bf16) 134 us, 6.1 TB/s of what must move; one token
+// for each of 8 sequences 3.9 us.  The page items' key loop takes four rows at a time with all of
 // their loads first (single tokens 4.4 -> 4.0 us), and three blocks per SM rather than two or four
 // (145, 133, 143 us for the prompts).
 #include "kernels.h"

@@ -6,8 +6,8 @@
 // they see, with the running maximum and sum of an online softmax (base 2), in one of two ways:
 //   many rows  keys in steps of 64 through shared memory (two blocks per SM, one copies while the
 //              other computes): S = Q K^T (4 x 4 scores per thread), P = 2^(S - m), O = 2^(m_old -
-//              m) O + P V (4 x d/16).  Bound by fp32 FMAs and their operands' shared loads (16
-//              FMAs per 16-byte load).
+//              m) O + P V (4 x d/16).  Bound by fp32 FMAs and their operands' shared loads (8 FMAs
+//              per 16-byte load in the scores; 8 in the product with V at d = 64, 10.7 at 128).
 //   few rows   (8 at a time, so the single token of any group at once): a warp takes 32 keys at a
 //              time, one per lane for the scores, all of them by columns for the product with V;
 //              the warps' results are joined at the end.  With 64-row tiles 15 of 16 threads
@@ -20,10 +20,10 @@
 // Masked scores never enter: P is 0 there, and in a step that holds a masked pair (the causal
 // border) the product with V is selected away too, because 0 * V is not 0 when V is not finite.
 //
-// Measured on GB300: prompts of 1000 tokens on 4000 and 800 on 100, 8 heads of 128, 587 us, 34
-// TFLOP/s; a batch of 1, 513, 64 and 1 tokens, 8 / 2 heads of 64, 33 us (74 us before the few-rows
-// way and the splits by length); one token of 8 sequences on 8000, 32 / 8 heads of 128, 162 us,
-// 3.2 TB/s.
+// Measured on GB300 in a stream of calls on changing inputs: prompts of 1000 tokens on 4000 and 800
+// on 100, 8 heads of 128, 602 us, 33 TFLOP/s; a batch of 1, 513, 64 and 1 tokens, 8 / 2 heads of 64,
+// 33 us (74 us before the few-rows way and the splits by length); one token of 8 sequences on 8000,
+// 32 / 8 heads of 128, 183 us, 2.9 TB/s.
 #include <algorithm>
 
 #include "kernels.h"

@@ -27,11 +27,20 @@
 // that only some see, non-finite elements are cleared and noted; the rows that do see them add
 // their product in the epilogue.
 //
+// Roundings.  Scores, m, l and O are fp32.  P is rounded to bf16 (half a step is 2^-9 of a weight),
+// because the product with bf16 V takes no wider operand; l sums the weights before the rounding.
+// Over bf16 results the error against 64 bits is 2.0e-3 to 2.4e-3 of their size, of which 1.5e-3 to
+// 1.7e-3 is the output's own rounding.  A second bf16 piece of P would leave that alone, at the
+// price of twice the products with V, a softmax that spills and as much again of it to TMEM:
+// measured, 2048 tokens on 32K 671 -> 1222 us, ragged prompts 779 -> 1418, 4 tokens of 16 sequences
+// on 32K (bound by the cache otherwise) 323 -> 513, head size 64 240 -> 410.
+//
 // Bound by the chain S -> softmax -> P -> product within a tile, which two tiles per block hide
 // in part: a step takes 2950 cycles of which the tensor pipe works 2048 (65.7% active over the
-// kernel).  Measured on GB300 (d = 128): 2048 tokens on 32K, 28 / 4 heads, 630 us, 1575 TFLOP/s
-// (83% of a measured library product); 8192 tokens from empty, 32 / 8 heads, 381 us, 1440 TFLOP/s;
-// 4 tokens of 16 sequences on 32K 320 us, 6.7 TB/s.
+// kernel).  Measured on GB300 in a stream of calls on changing inputs: 2048 tokens on 32K, 28 / 4
+// heads of 128, 672 us, 1476 TFLOP/s (77% of a measured library product); prompts from empty, 32 / 8
+// heads of 128, 512, 1216 and 4096 tokens 19.8, 27.6 and 131 us; 4 tokens of 16 sequences on 32K
+// 326 us, 6.6 TB/s; 4096 tokens on 4096, 32 / 8 heads of 64, 245 us, 842 TFLOP/s.
 #include <algorithm>
 
 #include "kernels.h"
@@ -42,8 +51,8 @@ namespace {
 
 constexpr int kTcThreads = 384;         // three warpgroups: softmax A, softmax B, the rest
 // Registers per thread of a softmax and of the last warpgroup: 2 * 200 + 104 = 3 * 168, what 384
-// threads are launched with.  192 / 120 spills in the softmax (834 us where 200 / 104 takes 630),
-// 208 / 88 in the issuing warp (660 us).
+// threads are launched with.  192 / 120 spills in the softmax (2048 tokens on 32K, the same inputs in
+// every call: 834 us where 200 / 104 takes 630), 208 / 88 in the issuing warp (660 us).
 constexpr int kSoftmaxRegs = 200;
 constexpr int kIssueRegs = 104;
 constexpr int kStep = 128;              // keys per step
@@ -1132,7 +1141,9 @@ int launch_chunk_tc(const ChunkParams& p, int d, void* workspace, int sms, cudaS
   t.part_acc = reinterpret_cast<float*>(base + l.acc);
   t.part_ml = reinterpret_cast<float*>(base + l.ml);
   t.join = reinterpret_cast<int32_t*>(base + l.join);
-  // an item is cut only where more than one step is left on both sides (line_border)
+  // An item is cut only where more than one step is left on both sides (line_border), so tables of
+  // up to three steps need no join: 33 tokens on 100, 28 / 4 heads of 128, 12.0 us with a table of 2
+  // or 3 pages, 13.6 with one of 4 (whose join finds nothing), 14.1 with one of 256.
   const bool split = blocks > 1 && static_cast<int64_t>(p.max_teams) * p.team_size > 3 * kStep;
   const cudaError_t e = d == 128 ? launch<128>(t, blocks, split, stream)
                                  : launch<64>(t, blocks, split, stream);

@@ -28,7 +28,9 @@ def tensors(x):
         return [x]
     if isinstance(x, (tuple, list)):
         return [t for y in x for t in tensors(y)]
-    return [t for y in vars(x).values() for t in tensors(y)] if isinstance(x, santa.DecodeBuffers) else []
+    if isinstance(x, santa.DecodeBuffers):
+        return tensors(list(vars(x).values()))
+    return []
 
 
 def held(h):

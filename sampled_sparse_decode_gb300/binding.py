@@ -714,14 +714,15 @@ class _Prepared:
     run before it, and work at the same time takes a handle each.  A CUDA graph that captured a
     run uses the handle's buffers: keep the handle as long as the graph is replayed."""
 
-    def __init__(self, name, args, keep, result, stream=None):
+    def __init__(self, name, args, keep, result, made=(), stream=None):
         self._name, self._fn = name, getattr(lib(), name)
         self._a, self._aref = args, ctypes.byref(args)
         self._keep, self._result = keep, result
         self._device = torch.cuda.current_device()
-        # streams that the allocator waits for by itself before it reuses the memory: the one
-        # that the buffers were made for, then those that _record names to it
-        self._known = {self._raw(stream)} if keep else set()
+        # tensors that the preparation made, and the streams that the allocator waits for before
+        # it reuses their memory: the one they were made for, then those that _record names to it
+        self._made = made
+        self._known = {self._raw(stream)} if made else set()
 
     def _raw(self, stream):
         return _raw_stream(self._device) if stream is None else _stream(stream)
@@ -729,12 +730,13 @@ class _Prepared:
     def run(self, stream=None):
         """Enqueues the call on `stream` (the current stream by default); returns its result
         buffers.  Buffers that the preparation made are filled on the stream that was current
-        then: another stream must wait for it before its first run.  The handle may be dropped
-        while runs are in flight on any stream."""
+        then: another stream must wait for it before its first run.  The handle and those buffers
+        may be dropped while runs are in flight (a stream given as a raw handle must outlive
+        them); tensors that the caller gave are the caller's to keep until the runs are done."""
         if torch.cuda.current_device() != self._device:
             raise SantaError(f"{self._name} was prepared on cuda:{self._device}")
         raw = self._raw(stream)
-        if raw not in self._known:
+        if self._made and raw not in self._known:
             self._record(raw, stream)
         rc = self._fn(self._aref, raw)
         if rc:
@@ -742,13 +744,12 @@ class _Prepared:
         return self._result
 
     def _record(self, raw, stream):
-        """Memory behind the call is reused only after the work that this stream has been given
-        by the time it is freed."""
-        for t in self._keep:
-            if t is not None:
-                if not isinstance(stream, torch.cuda.Stream):
-                    stream = torch.cuda.ExternalStream(raw) if raw else torch.cuda.default_stream()
-                t.record_stream(stream)
+        """Memory that the preparation made is reused only after the work that this stream has
+        been given by the time it is freed."""
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(raw) if raw else torch.cuda.default_stream()
+        for t in self._made:
+            t.record_stream(stream)
         self._known.add(raw)
 
 
@@ -781,7 +782,7 @@ def _append_chunk(q, k_new, v_new, cu_q, k_pool, v_pool, reps, page_table, seq_l
     a = _AppendChunkArgs()
     a.k_stride = _token_rows(k_new, "k_new", dt, Hkv, d)
     a.v_stride = _token_rows(v_new, "v_new", dt, Hkv, d)
-    n = k_new.shape[0]
+    n, made = k_new.shape[0], ()
     if v_new.shape[0] != n:
         raise SantaError("k_new and v_new must hold the same tokens")
     if q is not None:
@@ -794,6 +795,7 @@ def _append_chunk(q, k_new, v_new, cu_q, k_pool, v_pool, reps, page_table, seq_l
             with _allocating(stream):
                 # rows that belong to no sequence are not written
                 q_out = torch.zeros((n, q.shape[1], d), dtype=dt, device=q.device)
+            made = (q_out,)
         _req(q_out, "q_out", dt, 3)
         if q_out.shape != q.shape:
             raise SantaError("q_out must have q's shape")
@@ -823,7 +825,7 @@ def _append_chunk(q, k_new, v_new, cu_q, k_pool, v_pool, reps, page_table, seq_l
     a.seq_lens_next, a.device_status = _ptr(seq_lens_next), _ptr(device_status)
     keep = (q, k_new, v_new, cu_q, k_pool, v_pool, reps, page_table, seq_lens, rope, q_out,
             seq_lens_next, device_status)
-    return _Prepared("santa_append_chunk", a, keep, q_out, stream)
+    return _Prepared("santa_append_chunk", a, keep, q_out, made, stream)
 
 
 def santa_append_chunk(q, k_new, v_new, cu_q, k_pool, v_pool, reps, page_table, seq_lens,
@@ -879,16 +881,19 @@ def _chunk_attend(q, k_pool, v_pool, page_table, seq_lens, cu_q, out, workspace,
         _req(workspace, "workspace", torch.uint8, 1)
     _same_device(q=q, k_pool=k_pool, v_pool=v_pool, page_table=page_table, seq_lens=seq_lens,
                  cu_q=cu_q, out=out, workspace=workspace, device_status=device_status)
+    made = []
     with _allocating(stream):
         if out is None:
             # rows that belong to no sequence are not written
             out = torch.zeros_like(q)
+            made.append(out)
         if workspace is None:
             need = santa_chunk_workspace_bytes(q.dtype, B, n, Hq, Hkv, d, T,
                                                page_table.shape[1])
             if need == 0:
                 raise SantaError("unsupported shape for santa_chunk_attend")
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            made.append(workspace)
     a = _ChunkArgs()
     a.q, a.k_pool, a.v_pool = _ptr(q), _ptr(k_pool), _ptr(v_pool)
     a.page_table, a.seq_lens, a.cu_q = _ptr(page_table), _ptr(seq_lens), _ptr(cu_q)
@@ -898,7 +903,7 @@ def _chunk_attend(q, k_pool, v_pool, page_table, seq_lens, cu_q, out, workspace,
     a.out, a.workspace, a.workspace_bytes = _ptr(out), _ptr(workspace), workspace.numel()
     a.device_status = _ptr(device_status)
     keep = (q, k_pool, v_pool, page_table, seq_lens, cu_q, out, workspace, device_status)
-    return _Prepared("santa_chunk_attend", a, keep, out, stream)
+    return _Prepared("santa_chunk_attend", a, keep, out, tuple(made), stream)
 
 
 def santa_chunk_attend(q, k_pool, v_pool, page_table, seq_lens, cu_q,
@@ -930,12 +935,14 @@ def _topk(name, q, k_pool, v_pool, reps, page_table, seq_lens, num_teams, bufs, 
     _req(page_table, "page_table", torch.int32, 2)
     if tuple(reps.shape) != (k_pool.shape[0], k_pool.shape[1], k_pool.shape[3]):
         raise SantaError("reps must be [P][Hkv][d] of the pools")
+    made = ()
     if bufs is None:
         if q.dtype not in _DTYPES:
             raise SantaError("q must be float32 or bfloat16")
         _same_device(q=q)
         with _allocating(stream):
             bufs = _bufs_for(q, k_pool, page_table, num_teams, None)
+        made = tuple(t for t in vars(bufs).values() if t is not None)
     B, Hq, d = q.shape
     Hkv = k_pool.shape[1]
     for field, shape, dt in (("out", (B, Hq, d), torch.float32),
@@ -946,14 +953,13 @@ def _topk(name, q, k_pool, v_pool, reps, page_table, seq_lens, num_teams, bufs, 
         if tuple(getattr(bufs, field).shape) != shape:
             raise SantaError(f"bufs.{field} must be {shape}")
     a = _args(q, k_pool, v_pool, reps, page_table, seq_lens, num_teams, 0, bufs)
-    # the tensors themselves: bufs' fields may be replaced later
-    made = tuple(vars(bufs).values())
     _same_device(q=q, k_pool=k_pool, v_pool=v_pool, reps=reps, page_table=page_table,
                  seq_lens=seq_lens, out=bufs.out, sel_ids=bufs.sel_ids,
                  sel_count=bufs.sel_count, pi=bufs.pi, workspace=bufs.workspace,
                  device_status=bufs.device_status)
-    keep = (q, k_pool, v_pool, reps, page_table, seq_lens, *made)
-    return _Prepared(name, a, keep, bufs, stream)
+    # the buffers' tensors themselves: the fields of bufs may be replaced later
+    keep = (q, k_pool, v_pool, reps, page_table, seq_lens, *vars(bufs).values())
+    return _Prepared(name, a, keep, bufs, made, stream)
 
 
 def santa_select_topk(q, k_pool, v_pool, reps, page_table, seq_lens, num_teams: int,

@@ -29,11 +29,11 @@
 //
 // Roundings.  Scores, m, l and O are fp32.  P is rounded to bf16 (half a step is 2^-9 of a weight),
 // because the product with bf16 V takes no wider operand; l sums the weights before the rounding.
-// Over bf16 results the error against 64 bits is 2.0e-3 to 2.4e-3 of their size, of which 1.5e-3 to
-// 1.7e-3 is the output's own rounding.  A second bf16 piece of P would leave that alone, at the
-// price of twice the products with V, a softmax that spills and as much again of it to TMEM:
-// measured, 2048 tokens on 32K 671 -> 1222 us, ragged prompts 779 -> 1418, 4 tokens of 16 sequences
-// on 32K (bound by the cache otherwise) 323 -> 513, head size 64 240 -> 410.
+// The error against 64 bits is 2.0e-3 to 2.4e-3 of the results' size; with a second bf16 piece of P
+// it is 1.5e-3 to 1.7e-3, the output's own rounding.  That takes twice the products with V, and a
+// softmax that spills and stores twice as much: 2048 tokens on 32K 671 -> 1222 us, ragged prompts
+// 779 -> 1418, 4 tokens of 16 sequences on 32K (bound by the cache otherwise) 323 -> 513, 4096
+// tokens on 4096 with heads of 64 240 -> 410.
 //
 // Bound by the chain S -> softmax -> P -> product within a tile, which two tiles per block hide
 // in part: a step takes 2950 cycles of which the tensor pipe works 2048 (65.7% active over the

@@ -167,7 +167,9 @@ def work(case):
 # ---------------------------------------------------------------- inputs
 
 def _scale(x, top):
-    return x.abs().amax(-1).clamp(min=TINY) / top
+    # divided by a tensor: torch multiplies by a plain number's rounded reciprocal instead
+    a = x.abs().amax(-1).clamp(min=TINY)
+    return a / torch.full_like(a, top)
 
 
 def _codes(x, scale, kind):

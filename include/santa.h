@@ -74,7 +74,12 @@ typedef enum santa_status {
                                   santa_noalloc_scratch_bytes() */
 } santa_status;
 
-typedef enum santa_dtype { SANTA_F32 = 0, SANTA_BF16 = 1 } santa_dtype;
+typedef enum santa_dtype {
+  SANTA_F32 = 0,
+  SANTA_BF16 = 1,
+  SANTA_I8 = 2,                /* rows of 8-bit caches only (see "The cache in 8 bits") */
+  SANTA_E4M3 = 3
+} santa_dtype;
 
 /* Bits ORed into *device_status by the kernels. */
 #define SANTA_DEV_BAD_PAGE 1u    /* a page id outside [0, num_pages) */
@@ -523,6 +528,135 @@ int santa_select_topk(const santa_decode_args* a, void* stream);
  * row and growing lengths.  Workspace as for santa_decode.
  */
 int santa_topk_decode(const santa_decode_args* a, void* stream);
+
+/*
+ * ---- The cache in 8 bits ----
+ *
+ * A row (the key or the value of one token and KV head) of d elements x is held as d codes c of one
+ * byte and one fp32 scale s, and stands for c s:
+ *   s = max(max_j |x_j|, 2^-90) / top,   c_j = x_j / s rounded to the nearest code (ties to even),
+ * top = 127 for SANTA_I8 (two's complement) and 448 for SANTA_E4M3 (the finite 4-3 format).  A row
+ * with an infinity or a NaN gets s = NaN and codes 0.  Codes of a cache filled in another way may be
+ * any byte; an e4m3 NaN code makes what sees it NaN.
+ *   codes   k, v             [P][Hkv][T][d] bytes, 16-byte aligned
+ *   scales  k_scale, v_scale [P][Hkv][T] fp32, 16-byte aligned
+ * Page tables, lengths and representatives are those of the other caches: reps are fp32 means of the
+ * keys that the rows stand for, so santa_sample and santa_select_topk work unchanged beside it.
+ */
+
+/* One append with norms (see santa_append_norm). */
+typedef struct santa_append_norm_args {
+  santa_append_chunk_args chunk;  /* as for santa_append_chunk; chunk.dtype is the type of q, k_new,
+                                     v_new and q_out; k_pool and v_pool hold the codes of an 8-bit
+                                     cache */
+  int cache_type;                 /* chunk.dtype, SANTA_I8 or SANTA_E4M3 */
+  float eps;                      /* of the norms: >= 0 and finite */
+  const float* q_norm;            /* [d] fp32 weights, or NULL: queries are not normed */
+  const float* k_norm;            /* [d] fp32 weights, or NULL: keys are not normed */
+  float* k_scale;                 /* 8-bit caches; NULL otherwise */
+  float* v_scale;
+} santa_append_norm_args;
+
+/*
+ * santa_append_norm — santa_append_chunk with the norms of the heads in the same pass, into a cache
+ * of the activations' type or of 8 bits.  A query or key x of one head becomes
+ *   y = x / sqrt(mean_j(x_j^2) + eps) * w
+ * (q_norm for queries, k_norm for keys), then its pairs are turned as in santa_append_chunk, all in
+ * fp32, and the result is rounded once: queries to their type, keys to the cache's.  Values are
+ * neither normed nor turned.  With a cache of the activations' type and no norms the results are
+ * santa_append_chunk's, bit for bit.
+ *   - The representative of a touched page is the mean of its keys as stored; it does not depend on
+ *     how the tokens were divided among calls.
+ *   - Everything else (ragged chunks, lengths, refusals, device status, skipped sequences and pages)
+ *     is as for santa_append_chunk.  Scales and weights are 16-byte aligned.
+ */
+int santa_append_norm(const santa_append_norm_args* a, void* stream);
+
+/* The cache of 8 bits that the santa_q8_* attention reads beside santa_decode_args, and the options
+ * of its scores. */
+typedef struct santa_q8_args {
+  const void* k;               /* codes and scales as above */
+  const void* v;
+  const float* k_scale;
+  const float* v_scale;
+  int type;                    /* SANTA_I8 or SANTA_E4M3 */
+  int window;                  /* 0: none; else a token sees the last `window` cached tokens only */
+  float softcap;               /* 0: none; else scores s become softcap * tanh(s / softcap) */
+} santa_q8_args;
+
+/*
+ * santa_q8_dense_decode / santa_q8_attend — attention of one new token per sequence over an 8-bit
+ * cache: every cached token, or the teams listed in a->sel_ids[0 .. sel_count) with weight 1/pi
+ * (santa_dense_decode and santa_attend over the values that the rows stand for).  With the score
+ * s_j = q . k_j / sqrt(d), capped if asked, over the tokens j < seq_len that the window leaves,
+ *   out = sum_j w_j e^{s_j} v_j / sum_j w_j e^{s_j}     (w_j = 1, or 1 / pi of j's team).
+ * Products and sums are held in fp32 or better: q enters as fp16 pieces that carry it to 2^-22 of
+ * its head's largest element, weights as fp16 pieces that carry them to 2^-22 of the largest.
+ *   a    q, page_table, seq_lens, dtype (of q), shapes, num_pages, out, workspace, device_status;
+ *        santa_q8_attend also sel_ids, sel_count, pi and num_draws (1 .. 4096).  k_pool, v_pool, reps
+ *        and the other fields are not read.
+ *   - A sequence of length 0 and a unit without a seen token get zeros.  A length outside
+ *     [0, max_teams * T] sets SANTA_DEV_BAD_SEQLEN and its rows get zeros; a page id out of range
+ *     sets SANTA_DEV_BAD_PAGE and its tokens are left out; a listed team out of range, a weight that
+ *     is not finite and positive or a count outside [0, num_draws] sets SANTA_DEV_BAD_SEL, and that
+ *     team is left out (a count is clamped).  A team listed twice counts twice.
+ *   - What is not seen has no influence, whatever its bytes and scales hold.
+ *   - out does not overlap what the call reads or the workspace.  The workspace
+ *     (santa_q8_workspace_bytes) needs no initialisation and serves one call at a time.  Equal calls
+ *     give equal bits.
+ */
+size_t santa_q8_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                                int team_size, int max_teams);
+int santa_q8_dense_decode(const santa_decode_args* a, const santa_q8_args* c, void* stream);
+int santa_q8_attend(const santa_decode_args* a, const santa_q8_args* c, void* stream);
+
+/*
+ * santa_q8_topk_decode / santa_q8_decode — santa_select_topk or santa_sample followed by
+ * santa_q8_attend on `stream`: the sparse steps over an 8-bit cache.  a as for santa_topk_decode and
+ * santa_decode but for k_pool and v_pool, which are not read, and the workspace, which is
+ * santa_q8_attend's.  The selection takes every team of the sequence and plain scores; softcap and
+ * window act in the attention.
+ */
+int santa_q8_topk_decode(const santa_decode_args* a, const santa_q8_args* c, void* stream);
+int santa_q8_decode(const santa_decode_args* a, const santa_q8_args* c, void* stream);
+
+/* One reading back (see santa_q8_read). */
+typedef struct santa_q8_read_args {
+  const void* k;               /* codes and scales as above */
+  const void* v;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* page_table;   /* [B][max_teams] */
+  const int32_t* seq_lens;     /* [B] */
+  const int32_t* first;        /* [B] first token to read, or NULL: 0 */
+  const int32_t* dst_table;    /* [B][max_teams] pages of the destination */
+  int64_t num_pages;
+  int64_t dst_pages;
+  int type;                    /* SANTA_I8 or SANTA_E4M3 */
+  int out_dtype;               /* SANTA_F32 or SANTA_BF16 */
+  int batch;
+  int num_kv_heads;
+  int head_dim;
+  int team_size;
+  int max_teams;
+  void* k_out;                 /* [dst_pages][Hkv][T][d] out_dtype */
+  void* v_out;
+  int32_t* device_status;      /* may be NULL */
+} santa_q8_read_args;
+
+/*
+ * santa_q8_read — tokens first[b] .. seq_lens[b] - 1 of every sequence out of an 8-bit cache into the
+ * same slots of the pages dst_table names, as bf16 or fp32: c s in fp32, rounded once.  The result is
+ * a cache that santa_chunk_attend, santa_build_reps and the other calls read; `first` lets a prompt's
+ * next chunk read back only what it added.
+ *   - Slots of other tokens are left as they were.
+ *   - first[b] < 0, seq_lens[b] < first[b] or a length above max_teams * T sets
+ *     SANTA_DEV_BAD_SEQLEN (that sequence is skipped), a page id out of range on either side
+ *     SANTA_DEV_BAD_PAGE (that page is skipped).
+ *   - No two pages of a call's destinations may be the same; the outputs overlap neither each other
+ *     nor what is read.
+ */
+int santa_q8_read(const santa_q8_read_args* a, void* stream);
 
 /* Size in bytes of the scratch array santa_decode_noalloc uses. */
 size_t santa_noalloc_scratch_bytes(void);

@@ -2,10 +2,11 @@
 
 ``santa_build_reps``, ``santa_update_reps``, ``santa_append_kv``, ``santa_sample``,
 ``santa_attend``, ``santa_decode``, ``santa_dense_decode``, ``santa_append_chunk``,
-``santa_chunk_attend`` and ``santa_topk_decode`` call the entry points of ``libsanta.so`` with
-torch CUDA tensors; every step of the path runs in that library's kernels.  The library is
-loaded on first use and a missing or unbuildable library raises an error: there is no CPU
-fallback.  ``workloads`` builds seeded synthetic inputs and can be imported without a GPU.
+``santa_chunk_attend``, ``santa_topk_decode``, ``santa_append_norm`` and the ``santa_q8_*`` calls
+over 8-bit caches call the entry points of ``libsanta.so`` with torch CUDA tensors; every step of
+the path runs in that library's kernels.  The library is loaded on first use and a missing or
+unbuildable library raises an error: there is no CPU fallback.  ``workloads`` builds seeded
+synthetic inputs and can be imported without a GPU.
 """
 from __future__ import annotations
 
@@ -18,6 +19,10 @@ _BINDING_NAMES = (
     "santa_rope_table", "santa_append_chunk", "santa_append_chunk_prepared",
     "santa_chunk_attend", "santa_chunk_attend_prepared", "santa_chunk_workspace_bytes",
     "santa_select_topk", "santa_topk_decode", "santa_topk_decode_prepared",
+    "Q8Cache", "santa_append_norm", "santa_append_norm_prepared", "santa_q8_workspace_bytes",
+    "santa_q8_dense_decode", "santa_q8_dense_decode_prepared", "santa_q8_attend",
+    "santa_q8_attend_prepared", "santa_q8_topk_decode", "santa_q8_topk_decode_prepared",
+    "santa_q8_decode", "santa_q8_read", "santa_q8_read_prepared",
     "santa_attend_vs", "StepInputs", "HostOutputs", "PreparedDecode", "santa_decode_prepared",
 )
 

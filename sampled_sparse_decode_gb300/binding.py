@@ -73,6 +73,35 @@ class _ChunkArgs(ctypes.Structure):
     ]
 
 
+class _AppendNormArgs(ctypes.Structure):
+    _fields_ = [
+        ("chunk", _AppendChunkArgs), ("cache_type", ctypes.c_int), ("eps", ctypes.c_float),
+        ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+    ]
+
+
+class _Q8Args(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p), ("type", ctypes.c_int), ("window", ctypes.c_int),
+        ("softcap", ctypes.c_float),
+    ]
+
+
+class _Q8ReadArgs(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+        ("seq_lens", ctypes.c_void_p), ("first", ctypes.c_void_p), ("dst_table", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int64), ("dst_pages", ctypes.c_int64), ("type", ctypes.c_int),
+        ("out_dtype", ctypes.c_int), ("batch", ctypes.c_int), ("num_kv_heads", ctypes.c_int),
+        ("head_dim", ctypes.c_int), ("team_size", ctypes.c_int), ("max_teams", ctypes.c_int),
+        ("k_out", ctypes.c_void_p), ("v_out", ctypes.c_void_p),
+        ("device_status", ctypes.c_void_p),
+    ]
+
+
 # Samplers (santa_sampler): i.i.d. draws with Horvitz-Thompson weights (the method),
 # systematic draws with Horvitz-Thompson weights, i.i.d. draws with Hansen-Hurwitz weights.
 SAMPLERS = {"iid_ht": 0, "systematic": 1, "iid_hh": 2}
@@ -117,6 +146,13 @@ def lib():
             "santa_chunk_attend": (i32, [ctypes.POINTER(_ChunkArgs), vp]),
             "santa_select_topk": (i32, [A, vp]),
             "santa_topk_decode": (i32, [A, vp]),
+            "santa_append_norm": (i32, [ctypes.POINTER(_AppendNormArgs), vp]),
+            "santa_q8_workspace_bytes": (sz, [i32] * 6),
+            "santa_q8_dense_decode": (i32, [A, ctypes.POINTER(_Q8Args), vp]),
+            "santa_q8_attend": (i32, [A, ctypes.POINTER(_Q8Args), vp]),
+            "santa_q8_topk_decode": (i32, [A, ctypes.POINTER(_Q8Args), vp]),
+            "santa_q8_decode": (i32, [A, ctypes.POINTER(_Q8Args), vp]),
+            "santa_q8_read": (i32, [ctypes.POINTER(_Q8ReadArgs), vp]),
         }
         for name, (res, args) in sigs.items():
             f = getattr(L, name)
@@ -716,7 +752,8 @@ class _Prepared:
 
     def __init__(self, name, args, keep, result, made=(), stream=None):
         self._name, self._fn = name, getattr(lib(), name)
-        self._a, self._aref = args, ctypes.byref(args)
+        args = args if isinstance(args, tuple) else (args,)
+        self._a, self._aref = args[0], tuple(ctypes.byref(a) for a in args)
         self._keep, self._result = keep, result
         self._device = torch.cuda.current_device()
         # tensors that the preparation made, and the streams that the allocator waits for before
@@ -738,7 +775,7 @@ class _Prepared:
         raw = self._raw(stream)
         if self._made and raw not in self._known:
             self._record(raw, stream)
-        rc = self._fn(self._aref, raw)
+        rc = self._fn(*self._aref, raw)
         if rc:
             _check(rc, self._name)
         return self._result
@@ -769,12 +806,12 @@ def santa_rope_table(positions: int, rope_dim: int, theta: float = 10000.0, devi
     return table
 
 
-def _append_chunk(q, k_new, v_new, cu_q, k_pool, v_pool, reps, page_table, seq_lens, rope,
-                  seq_lens_next, q_out, interleaved, device_status, stream):
-    if not isinstance(k_pool, torch.Tensor) or k_pool.dtype not in _DTYPES:
-        raise SantaError("k_pool must be a float32 or bfloat16 tensor")
-    dt = k_pool.dtype
-    P, Hkv, T, d = _pools(k_pool, v_pool, dt)
+def _append_args(q, k_new, v_new, cu_q, pools, dt, reps, page_table, seq_lens, rope,
+                 seq_lens_next, q_out, interleaved, device_status, stream, **more):
+    """The argument structure of an append of dt tokens into `pools`, the tensors it points into,
+    q_out and whether it was made here; `more`: further tensors of the call."""
+    k_pool, v_pool = pools
+    P, Hkv, T, d = k_pool.shape
     B = _ragged(cu_q, page_table, seq_lens)
     _req(reps, "reps", torch.float32, 3)
     if tuple(reps.shape) != (P, Hkv, d):
@@ -812,7 +849,7 @@ def _append_chunk(q, k_new, v_new, cu_q, k_pool, v_pool, reps, page_table, seq_l
     _status_word(device_status)
     _same_device(q=q, k_new=k_new, v_new=v_new, cu_q=cu_q, k_pool=k_pool, v_pool=v_pool,
                  reps=reps, page_table=page_table, seq_lens=seq_lens, rope=rope, q_out=q_out,
-                 seq_lens_next=seq_lens_next, device_status=device_status)
+                 seq_lens_next=seq_lens_next, device_status=device_status, **more)
     # an empty chunk has tensors without storage
     a.q, a.q_out = (_ptr(q), _ptr(q_out)) if n else (None, None)
     a.k_new, a.v_new = _ptr(k_new), _ptr(v_new)
@@ -824,7 +861,19 @@ def _append_chunk(q, k_new, v_new, cu_q, k_pool, v_pool, reps, page_table, seq_l
     a.k_pool, a.v_pool, a.reps = _ptr(k_pool), _ptr(v_pool), _ptr(reps)
     a.seq_lens_next, a.device_status = _ptr(seq_lens_next), _ptr(device_status)
     keep = (q, k_new, v_new, cu_q, k_pool, v_pool, reps, page_table, seq_lens, rope, q_out,
-            seq_lens_next, device_status)
+            seq_lens_next, device_status, *more.values())
+    return a, keep, q_out, made
+
+
+def _append_chunk(q, k_new, v_new, cu_q, k_pool, v_pool, reps, page_table, seq_lens, rope,
+                  seq_lens_next, q_out, interleaved, device_status, stream):
+    if not isinstance(k_pool, torch.Tensor) or k_pool.dtype not in _DTYPES:
+        raise SantaError("k_pool must be a float32 or bfloat16 tensor")
+    dt = k_pool.dtype
+    _pools(k_pool, v_pool, dt)
+    a, keep, q_out, made = _append_args(
+        q, k_new, v_new, cu_q, (k_pool, v_pool), dt, reps, page_table, seq_lens, rope,
+        seq_lens_next, q_out, interleaved, device_status, stream)
     return _Prepared("santa_append_chunk", a, keep, q_out, made, stream)
 
 
@@ -983,3 +1032,358 @@ def santa_topk_decode_prepared(q, k_pool, v_pool, reps, page_table, seq_lens, nu
     .run(stream=None)."""
     return _topk("santa_topk_decode", q, k_pool, v_pool, reps, page_table, seq_lens, num_teams,
                  bufs, None)
+
+
+# ---------------------------------------------------------------- caches in 8 bits
+
+_CODE_TYPES = {torch.int8: 2, torch.float8_e4m3fn: 3}
+
+
+@dataclass
+class Q8Cache:
+    """A paged cache of 8-bit rows: codes k, v [P][Hkv][T][d] (int8 or float8_e4m3fn) and one
+    scale for each row, k_scale, v_scale [P][Hkv][T] float32.  A row stands for codes * scale."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+    @staticmethod
+    def allocate(num_pages, num_kv_heads, team_size, head_dim, dtype=torch.int8,
+                 device="cuda") -> "Q8Cache":
+        """Rows of zeros."""
+        if dtype not in _CODE_TYPES:
+            raise SantaError("a cache of 8 bits is int8 or float8_e4m3fn")
+        shape = (num_pages, num_kv_heads, team_size, head_dim)
+        k, v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(dtype) for _ in "kv")
+        k_scale, v_scale = (torch.zeros(shape[:3], dtype=torch.float32, device=device) for _ in "kv")
+        return Q8Cache(k, v, k_scale, v_scale)
+
+    def _check(self):
+        """Checks the four tensors; returns [P][Hkv][T][d]."""
+        if not isinstance(self.k, torch.Tensor) or self.k.dtype not in _CODE_TYPES:
+            raise SantaError("cache.k must be an int8 or float8_e4m3fn tensor")
+        _req(self.k, "cache.k", ndim=4)
+        _req(self.v, "cache.v", self.k.dtype, 4)
+        _req(self.k_scale, "cache.k_scale", torch.float32, 3)
+        _req(self.v_scale, "cache.v_scale", torch.float32, 3)
+        if self.v.shape != self.k.shape or self.k_scale.shape != self.k.shape[:3] or \
+                self.v_scale.shape != self.k.shape[:3]:
+            raise SantaError("a cache holds k and v [P][Hkv][T][d] and scales [P][Hkv][T]")
+        return self.k.shape
+
+    def _tensors(self):
+        return dict(cache_k=self.k, cache_v=self.v, cache_k_scale=self.k_scale,
+                    cache_v_scale=self.v_scale)
+
+
+def _norm_weight(w, name, d):
+    if w is not None:
+        _req(w, name, torch.float32, 1)
+        if w.shape[0] != d:
+            raise SantaError(f"{name} must be [{d}]")
+
+
+def _append_norm(q, k_new, v_new, cu_q, cache, reps, page_table, seq_lens, rope, q_norm, k_norm,
+                 eps, seq_lens_next, q_out, interleaved, device_status, stream):
+    a = _AppendNormArgs()
+    if isinstance(cache, Q8Cache):
+        cache._check()
+        pools, scales = (cache.k, cache.v), (cache.k_scale, cache.v_scale)
+        if not isinstance(k_new, torch.Tensor) or k_new.dtype not in _DTYPES:
+            raise SantaError("k_new must be a float32 or bfloat16 tensor")
+        dt = k_new.dtype
+        a.cache_type = _CODE_TYPES[cache.k.dtype]
+    else:
+        if not isinstance(cache, (tuple, list)) or len(cache) != 2:
+            raise SantaError("cache must be a Q8Cache or (k_pool, v_pool)")
+        pools, scales = tuple(cache), (None, None)
+        if not isinstance(pools[0], torch.Tensor) or pools[0].dtype not in _DTYPES:
+            raise SantaError("k_pool must be a float32 or bfloat16 tensor")
+        dt = pools[0].dtype
+        _pools(*pools, dt)
+        a.cache_type = _DTYPES[dt]
+    d = pools[0].shape[3]
+    _norm_weight(q_norm, "q_norm", d)
+    _norm_weight(k_norm, "k_norm", d)
+    if q_norm is not None and q is None:
+        raise SantaError("q_norm without q")
+    a.chunk, keep, q_out, made = _append_args(
+        q, k_new, v_new, cu_q, pools, dt, reps, page_table, seq_lens, rope, seq_lens_next, q_out,
+        interleaved, device_status, stream, q_norm=q_norm, k_norm=k_norm, k_scale=scales[0],
+        v_scale=scales[1])
+    a.eps, a.q_norm, a.k_norm = float(eps), _ptr(q_norm), _ptr(k_norm)
+    a.k_scale, a.v_scale = _ptr(scales[0]), _ptr(scales[1])
+    return _Prepared("santa_append_norm", a, keep, q_out, made, stream)
+
+
+def santa_append_norm(q, k_new, v_new, cu_q, cache, reps, page_table, seq_lens,
+                      rope: torch.Tensor | None = None, q_norm: torch.Tensor | None = None,
+                      k_norm: torch.Tensor | None = None, eps: float = 1e-6,
+                      seq_lens_next: torch.Tensor | None = None,
+                      q_out: torch.Tensor | None = None, interleaved: bool = False,
+                      device_status: torch.Tensor | None = None, stream=None):
+    """santa_append_chunk with the norms of the heads in the same pass (q_norm, k_norm: weights [d]
+    float32 of x / sqrt(mean(x^2) + eps) * w for queries and keys, before the rotation; None: not
+    normed), into `cache`: a Q8Cache, whose rows are rounded to 8 bits as they are written, or the
+    pair (k_pool, v_pool) of the tokens' type."""
+    return _append_norm(q, k_new, v_new, cu_q, cache, reps, page_table, seq_lens, rope, q_norm,
+                        k_norm, eps, seq_lens_next, q_out, interleaved, device_status,
+                        stream).run(stream)
+
+
+def santa_append_norm_prepared(q, k_new, v_new, cu_q, cache, reps, page_table, seq_lens,
+                               rope: torch.Tensor | None = None,
+                               q_norm: torch.Tensor | None = None,
+                               k_norm: torch.Tensor | None = None, eps: float = 1e-6,
+                               seq_lens_next: torch.Tensor | None = None,
+                               q_out: torch.Tensor | None = None, interleaved: bool = False,
+                               device_status: torch.Tensor | None = None) -> _Prepared:
+    """santa_append_norm's checks and argument structure done once; .run(stream=None)."""
+    return _append_norm(q, k_new, v_new, cu_q, cache, reps, page_table, seq_lens, rope, q_norm,
+                        k_norm, eps, seq_lens_next, q_out, interleaved, device_status, None)
+
+
+def santa_q8_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, team_size,
+                             max_teams) -> int:
+    """Of the santa_q8_* attention; 0 for an unsupported shape."""
+    return lib().santa_q8_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, team_size,
+                                          max_teams)
+
+
+def _q8_step(q, cache, page_table, seq_lens, softcap, window):
+    """Checks and marshals what every attention over an 8-bit cache takes."""
+    if not isinstance(cache, Q8Cache):
+        raise SantaError("cache must be a Q8Cache")
+    P, Hkv, T, d = cache._check()
+    _req(q, "q", ndim=3)
+    if q.dtype not in _DTYPES:
+        raise SantaError("q must be float32 or bfloat16")
+    _req(page_table, "page_table", torch.int32, 2)
+    _req(seq_lens, "seq_lens", torch.int32, 1)
+    B, Hq, d2 = q.shape
+    if d2 != d or page_table.shape[0] != B or seq_lens.shape[0] != B:
+        raise SantaError("shape mismatch between q, cache, page_table and seq_lens")
+    a, c = _DecodeArgs(), _Q8Args()
+    a.q, a.page_table, a.seq_lens = _ptr(q), _ptr(page_table), _ptr(seq_lens)
+    a.dtype, a.batch, a.num_q_heads, a.num_kv_heads = _DTYPES[q.dtype], B, Hq, Hkv
+    a.head_dim, a.team_size, a.max_teams, a.num_pages = d, T, page_table.shape[1], P
+    c.k, c.v, c.k_scale, c.v_scale = (_ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale),
+                                      _ptr(cache.v_scale))
+    c.type, c.window, c.softcap = _CODE_TYPES[cache.k.dtype], int(window), float(softcap)
+    return a, c
+
+
+def _q8_workspace(a, device):
+    need = santa_q8_workspace_bytes(a.batch, a.num_q_heads, a.num_kv_heads, a.head_dim,
+                                    a.team_size, a.max_teams)
+    if need == 0:
+        raise SantaError("unsupported shape for the attention over an 8-bit cache")
+    return torch.empty(need, dtype=torch.uint8, device=device)
+
+
+def _q8_attend(q, cache, page_table, seq_lens, sel, softcap, window, out, workspace,
+               device_status, stream):
+    a, c = _q8_step(q, cache, page_table, seq_lens, softcap, window)
+    B, Hq, d = q.shape
+    Hkv = cache.k.shape[1]
+    name, lists = "santa_q8_dense_decode", {}
+    if sel is not None:
+        name = "santa_q8_attend"
+        lists = dict(zip(("sel_ids", "sel_count", "pi"), sel))
+        _req(lists["sel_ids"], "sel_ids", torch.int32, 3)
+        _req(lists["sel_count"], "sel_count", torch.int32, 2)
+        _req(lists["pi"], "pi", torch.float32, 3)
+        M = lists["sel_ids"].shape[2]
+        if tuple(lists["sel_ids"].shape) != (B, Hkv, M) or \
+                tuple(lists["sel_count"].shape) != (B, Hkv) or \
+                tuple(lists["pi"].shape) != (B, Hkv, M):
+            raise SantaError("sel_ids and pi must be [B][Hkv][M] and sel_count [B][Hkv]")
+        a.num_draws = M
+        a.sel_ids, a.sel_count, a.pi = (_ptr(t) for t in lists.values())
+    if out is not None:
+        _req(out, "out", torch.float32, 3)
+        if out.shape != q.shape:
+            raise SantaError("out must have q's shape")
+    if workspace is not None:
+        _req(workspace, "workspace", torch.uint8, 1)
+    _status_word(device_status)
+    _same_device(q=q, page_table=page_table, seq_lens=seq_lens, out=out, workspace=workspace,
+                 device_status=device_status, **cache._tensors(), **lists)
+    made = []
+    with _allocating(stream):
+        if out is None:
+            out = torch.empty((B, Hq, d), dtype=torch.float32, device=q.device)
+            made.append(out)
+        if workspace is None:
+            workspace = _q8_workspace(a, q.device)
+            made.append(workspace)
+    a.out, a.workspace, a.workspace_bytes = _ptr(out), _ptr(workspace), workspace.numel()
+    a.device_status = _ptr(device_status)
+    keep = (q, page_table, seq_lens, out, workspace, device_status, *cache._tensors().values(),
+            *lists.values())
+    return _Prepared(name, (a, c), keep, out, tuple(made), stream)
+
+
+def santa_q8_dense_decode(q, cache: Q8Cache, page_table, seq_lens, softcap: float = 0.0,
+                          window: int = 0, out: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None,
+                          device_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of one new token per sequence (q [B][Hq][d]) over every cached token of an 8-bit
+    cache; softcap > 0: scores s become softcap * tanh(s / softcap); window > 0: the last `window`
+    cached tokens only.  Returns out [B][Hq][d] float32."""
+    return _q8_attend(q, cache, page_table, seq_lens, None, softcap, window, out, workspace,
+                      device_status, stream).run(stream)
+
+
+def santa_q8_dense_decode_prepared(q, cache: Q8Cache, page_table, seq_lens, softcap: float = 0.0,
+                                   window: int = 0, out: torch.Tensor | None = None,
+                                   workspace: torch.Tensor | None = None,
+                                   device_status: torch.Tensor | None = None) -> _Prepared:
+    """santa_q8_dense_decode's checks, buffers and argument structures done once;
+    .run(stream=None)."""
+    return _q8_attend(q, cache, page_table, seq_lens, None, softcap, window, out, workspace,
+                      device_status, None)
+
+
+def santa_q8_attend(q, cache: Q8Cache, page_table, seq_lens, sel_ids, sel_count, pi,
+                    softcap: float = 0.0, window: int = 0, out: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None,
+                    device_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """santa_attend over an 8-bit cache: the listed teams (sel_ids [B][Hkv][M], sel_count [B][Hkv])
+    with weight 1 / pi [B][Hkv][M].  Returns out [B][Hq][d] float32."""
+    return _q8_attend(q, cache, page_table, seq_lens, (sel_ids, sel_count, pi), softcap, window,
+                      out, workspace, device_status, stream).run(stream)
+
+
+def santa_q8_attend_prepared(q, cache: Q8Cache, page_table, seq_lens, sel_ids, sel_count, pi,
+                             softcap: float = 0.0, window: int = 0,
+                             out: torch.Tensor | None = None,
+                             workspace: torch.Tensor | None = None,
+                             device_status: torch.Tensor | None = None) -> _Prepared:
+    """santa_q8_attend's checks, buffers and argument structures done once; .run(stream=None)."""
+    return _q8_attend(q, cache, page_table, seq_lens, (sel_ids, sel_count, pi), softcap, window,
+                      out, workspace, device_status, None)
+
+
+def _q8_sparse(name, q, cache, reps, page_table, seq_lens, num_teams, softcap, window, bufs,
+               stream, seed=0, sampler="iid_ht", mix_alpha=0.0):
+    a, c = _q8_step(q, cache, page_table, seq_lens, softcap, window)
+    P, Hkv, T, d = cache.k.shape
+    B, Hq, _ = q.shape
+    _req(reps, "reps", torch.float32, 3)
+    if tuple(reps.shape) != (P, Hkv, d):
+        raise SantaError("reps must be [P][Hkv][d] of the cache")
+    if sampler not in SAMPLERS:
+        raise SantaError(f"unknown sampler {sampler!r} (one of {sorted(SAMPLERS)})")
+    made = ()
+    if bufs is None:
+        _same_device(q=q)
+        with _allocating(stream):
+            views, _ = _output_views(B, Hq, Hkv, d, num_teams, q.device, False)
+            bufs = DecodeBuffers(*views[:5], None, _q8_workspace(a, q.device), views[5])
+        made = tuple(t for t in vars(bufs).values() if t is not None)
+    fields = [("out", (B, Hq, d), torch.float32), ("sel_ids", (B, Hkv, num_teams), torch.int32),
+              ("sel_count", (B, Hkv), torch.int32), ("pi", (B, Hkv, num_teams), torch.float32)]
+    if name == "santa_q8_decode":
+        fields.append(("draw_ids", (B, Hkv, num_teams), torch.int32))
+        if bufs.team_probs is not None:
+            fields.append(("team_probs", (B, Hkv, page_table.shape[1]), torch.float32))
+    for field, shape, dt in fields:
+        _req(getattr(bufs, field), f"bufs.{field}", dt)
+        if tuple(getattr(bufs, field).shape) != shape:
+            raise SantaError(f"bufs.{field} must be {shape}")
+    _req(bufs.workspace, "bufs.workspace", torch.uint8, 1)
+    _status_word(bufs.device_status)
+    _same_device(q=q, reps=reps, page_table=page_table, seq_lens=seq_lens, **cache._tensors(),
+                 **{f: getattr(bufs, f) for f, _, _ in fields}, workspace=bufs.workspace,
+                 device_status=bufs.device_status)
+    a.reps, a.num_draws, a.seed = _ptr(reps), num_teams, seed & 0xFFFFFFFFFFFFFFFF
+    a.sampler, a.mix_alpha = SAMPLERS[sampler], float(mix_alpha)
+    for field, _, _ in fields:
+        setattr(a, field, _ptr(getattr(bufs, field)))
+    a.workspace, a.workspace_bytes = _ptr(bufs.workspace), bufs.workspace.numel()
+    a.device_status = _ptr(bufs.device_status)
+    keep = (q, reps, page_table, seq_lens, *cache._tensors().values(), *vars(bufs).values())
+    return _Prepared(name, (a, c), keep, bufs, made, stream)
+
+
+def santa_q8_topk_decode(q, cache: Q8Cache, reps, page_table, seq_lens, num_teams: int,
+                         softcap: float = 0.0, window: int = 0,
+                         bufs: DecodeBuffers | None = None, stream=None) -> DecodeBuffers:
+    """santa_topk_decode over an 8-bit cache: santa_select_topk, then santa_q8_attend."""
+    return _q8_sparse("santa_q8_topk_decode", q, cache, reps, page_table, seq_lens, num_teams,
+                      softcap, window, bufs, stream).run(stream)
+
+
+def santa_q8_topk_decode_prepared(q, cache: Q8Cache, reps, page_table, seq_lens, num_teams: int,
+                                  softcap: float = 0.0, window: int = 0,
+                                  bufs: DecodeBuffers | None = None) -> _Prepared:
+    """santa_q8_topk_decode's checks, buffers and argument structures done once;
+    .run(stream=None)."""
+    return _q8_sparse("santa_q8_topk_decode", q, cache, reps, page_table, seq_lens, num_teams,
+                      softcap, window, bufs, None)
+
+
+def santa_q8_decode(q, cache: Q8Cache, reps, page_table, seq_lens, num_draws: int, seed: int,
+                    softcap: float = 0.0, window: int = 0, bufs: DecodeBuffers | None = None,
+                    stream=None, sampler: str = "iid_ht", mix_alpha: float = 0.0) -> DecodeBuffers:
+    """santa_decode over an 8-bit cache: santa_sample, then santa_q8_attend."""
+    return _q8_sparse("santa_q8_decode", q, cache, reps, page_table, seq_lens, num_draws, softcap,
+                      window, bufs, stream, seed, sampler, mix_alpha).run(stream)
+
+
+def _q8_read(cache, page_table, seq_lens, k_out, v_out, dst_table, first, device_status, stream):
+    if not isinstance(cache, Q8Cache):
+        raise SantaError("cache must be a Q8Cache")
+    P, Hkv, T, d = cache._check()
+    if not isinstance(k_out, torch.Tensor) or k_out.dtype not in _DTYPES:
+        raise SantaError("k_out must be a float32 or bfloat16 tensor")
+    _req(k_out, "k_out", ndim=4)
+    _req(v_out, "v_out", k_out.dtype, 4)
+    if tuple(k_out.shape[1:]) != (Hkv, T, d) or v_out.shape != k_out.shape:
+        raise SantaError("k_out and v_out must be [pages][Hkv][T][d] of the cache")
+    _req(page_table, "page_table", torch.int32, 2)
+    _req(dst_table, "dst_table", torch.int32, 2)
+    _req(seq_lens, "seq_lens", torch.int32, 1)
+    B = seq_lens.shape[0]
+    if page_table.shape[0] != B or dst_table.shape != page_table.shape:
+        raise SantaError("page_table and dst_table must be [B][max_teams] and seq_lens [B]")
+    if first is not None:
+        _req(first, "first", torch.int32, 1)
+        if first.shape[0] != B:
+            raise SantaError("first must be [B]")
+    _status_word(device_status)
+    _same_device(page_table=page_table, dst_table=dst_table, seq_lens=seq_lens, first=first,
+                 k_out=k_out, v_out=v_out, device_status=device_status, **cache._tensors())
+    a = _Q8ReadArgs()
+    a.k, a.v, a.k_scale, a.v_scale = (_ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale),
+                                      _ptr(cache.v_scale))
+    a.page_table, a.seq_lens, a.first, a.dst_table = (_ptr(page_table), _ptr(seq_lens),
+                                                      _ptr(first), _ptr(dst_table))
+    a.num_pages, a.dst_pages, a.type, a.out_dtype = (P, k_out.shape[0], _CODE_TYPES[cache.k.dtype],
+                                                     _DTYPES[k_out.dtype])
+    a.batch, a.num_kv_heads, a.head_dim, a.team_size, a.max_teams = B, Hkv, d, T, page_table.shape[1]
+    a.k_out, a.v_out, a.device_status = _ptr(k_out), _ptr(v_out), _ptr(device_status)
+    keep = (page_table, dst_table, seq_lens, first, k_out, v_out, device_status,
+            *cache._tensors().values())
+    return _Prepared("santa_q8_read", a, keep, (k_out, v_out), (), stream)
+
+
+def santa_q8_read(cache: Q8Cache, page_table, seq_lens, k_out, v_out, dst_table,
+                  first: torch.Tensor | None = None, device_status: torch.Tensor | None = None,
+                  stream=None):
+    """Tokens first[b] (None: 0) .. seq_lens[b] - 1 of every sequence out of an 8-bit cache into the
+    same slots of the pages that dst_table [B][max_teams] names in k_out, v_out [pages][Hkv][T][d]
+    (float32 or bfloat16): a cache for santa_chunk_attend and the other calls.  Other slots are left
+    as they were.  Returns (k_out, v_out)."""
+    return _q8_read(cache, page_table, seq_lens, k_out, v_out, dst_table, first, device_status,
+                    stream).run(stream)
+
+
+def santa_q8_read_prepared(cache: Q8Cache, page_table, seq_lens, k_out, v_out, dst_table,
+                           first: torch.Tensor | None = None,
+                           device_status: torch.Tensor | None = None) -> _Prepared:
+    """santa_q8_read's checks and argument structure done once; .run(stream=None)."""
+    return _q8_read(cache, page_table, seq_lens, k_out, v_out, dst_table, first, device_status,
+                    None)

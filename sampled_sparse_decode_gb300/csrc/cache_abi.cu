@@ -4,46 +4,12 @@
 #include <cmath>
 #include <cstdint>
 
-#include "kernels.h"
+#include "abi_checks.h"
+#include "q8.cuh"
+
+using namespace santa::abi;
 
 namespace {
-
-constexpr int kMaxTeams = 16384;
-constexpr int kMaxDraws = 4096;
-constexpr int kMaxRopeDim = 128;
-constexpr int64_t kMaxTokens = int64_t(1) << 24;    // tokens of one chunk call
-constexpr size_t kAlign = 256;
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-int map_cuda(cudaError_t e) { return e == cudaSuccess ? SANTA_OK : SANTA_ERR_CUDA; }
-
-int check_cache_shape(int dtype, int batch, int hkv, int d, int T, int max_teams) {
-  if (dtype != SANTA_F32 && dtype != SANTA_BF16) return SANTA_ERR_UNSUPPORTED;
-  if (batch < 1 || hkv < 1 || max_teams < 1) return SANTA_ERR_INVALID_ARG;
-  if (d != 64 && d != 128) return SANTA_ERR_UNSUPPORTED;
-  if (T != 64 && T != 128) return SANTA_ERR_UNSUPPORTED;
-  if (max_teams > kMaxTeams || batch > 65535 || hkv > 65535) return SANTA_ERR_UNSUPPORTED;
-  return SANTA_OK;
-}
-int check_heads(int hq, int hkv) {
-  if (hq < 1 || hq % hkv != 0) return SANTA_ERR_INVALID_ARG;
-  return hq / hkv > santa::kMaxGroup ? SANTA_ERR_UNSUPPORTED : SANTA_OK;
-}
-int check_tokens(int64_t num_tokens) {
-  if (num_tokens < 0) return SANTA_ERR_INVALID_ARG;
-  return num_tokens > kMaxTokens ? SANTA_ERR_UNSUPPORTED : SANTA_OK;
-}
-// Whether [a, a + bytes) meets one of the `rows` rows of row_bytes that lie stride_bytes
-// (>= row_bytes) apart from b on.
-bool meets(const void* a, int64_t bytes, const void* b, int64_t rows, int64_t row_bytes,
-           int64_t stride_bytes) {
-  if (!a || !b || bytes <= 0 || rows <= 0 || row_bytes <= 0) return false;
-  const __int128 lo = reinterpret_cast<uintptr_t>(a), at = reinterpret_cast<uintptr_t>(b);
-  // the first row that ends behind lo
-  const __int128 r = at + row_bytes > lo ? 0 : (lo - at - row_bytes) / stride_bytes + 1;
-  return r < rows && at + r * stride_bytes < lo + bytes;
-}
 
 // Workspace of a chunk attention: bf16 has one of its own; fp32 keeps the partial results of
 // its split tiles, accumulators, then (m, l).
@@ -78,22 +44,8 @@ int check_chunk_shape(int dtype, int batch, int64_t num_tokens, int hq, int hkv,
   return SANTA_OK;
 }
 
-}  // namespace
-
-#pragma GCC visibility push(default)
-extern "C" {
-
-int santa_rope_table(float* table, int64_t positions, int rope_dim, double theta,
-                     void* stream) {
-  if (!table || !aligned(table, 16) || positions < 1) return SANTA_ERR_INVALID_ARG;
-  if (!(theta > 1.0) || !std::isfinite(theta)) return SANTA_ERR_INVALID_ARG;
-  if (rope_dim < 16 || rope_dim > kMaxRopeDim || rope_dim % 16) return SANTA_ERR_UNSUPPORTED;
-  if (positions > 0x7fffffffll) return SANTA_ERR_UNSUPPORTED;
-  return map_cuda(santa::launch_rope_table(table, positions, rope_dim, theta,
-                                           static_cast<cudaStream_t>(stream)));
-}
-
-int santa_append_chunk(const santa_append_chunk_args* a, void* stream) {
+// What santa_append_chunk and santa_append_norm refuse alike.
+int check_append(const santa_append_chunk_args* a) {
   if (!a) return SANTA_ERR_INVALID_ARG;
   int rc = check_cache_shape(a->dtype, a->batch, a->num_kv_heads, a->head_dim, a->team_size,
                              a->max_teams);
@@ -137,35 +89,84 @@ int santa_append_chunk(const santa_append_chunk_args* a, void* stream) {
       meets(a->seq_lens_next, len_bytes, a->seq_lens, 1, len_bytes, len_bytes) ||
       meets(a->seq_lens_next, len_bytes, a->cu_q, 1, len_bytes + 4, len_bytes + 4))
     return SANTA_ERR_INVALID_ARG;
+  return SANTA_OK;
+}
+
+void fill_append(const santa_append_chunk_args* a, santa::AppendChunkParams* p) {
+  p->q = a->q;
+  p->k_new = a->k_new;
+  p->v_new = a->v_new;
+  p->q_stride = a->q_stride;
+  p->k_stride = a->k_stride;
+  p->v_stride = a->v_stride;
+  p->cu_q = a->cu_q;
+  p->page_table = a->page_table;
+  p->seq_lens = a->seq_lens;
+  p->rope = a->rope;
+  p->rope_positions = a->rope_positions;
+  p->num_tokens = a->num_tokens;
+  p->num_pages = a->num_pages;
+  p->batch = a->batch;
+  p->num_q_heads = a->num_q_heads;
+  p->num_kv_heads = a->num_kv_heads;
+  p->team_size = a->team_size;
+  p->max_teams = a->max_teams;
+  p->rope_dim = a->rope_dim;
+  p->interleaved = a->interleaved != 0;
+  p->q_out = a->q_out;
+  p->k_pool = a->k_pool;
+  p->v_pool = a->v_pool;
+  p->reps = a->reps;
+  p->seq_lens_next = a->seq_lens_next;
+  p->status = a->device_status;
+}
+
+}  // namespace
+
+#pragma GCC visibility push(default)
+extern "C" {
+
+int santa_rope_table(float* table, int64_t positions, int rope_dim, double theta,
+                     void* stream) {
+  if (!table || !aligned(table, 16) || positions < 1) return SANTA_ERR_INVALID_ARG;
+  if (!(theta > 1.0) || !std::isfinite(theta)) return SANTA_ERR_INVALID_ARG;
+  if (rope_dim < 16 || rope_dim > kMaxRopeDim || rope_dim % 16) return SANTA_ERR_UNSUPPORTED;
+  if (positions > 0x7fffffffll) return SANTA_ERR_UNSUPPORTED;
+  return map_cuda(santa::launch_rope_table(table, positions, rope_dim, theta,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+int santa_append_chunk(const santa_append_chunk_args* a, void* stream) {
+  const int rc = check_append(a);
+  if (rc) return rc;
   santa::AppendChunkParams p = {};
-  p.q = a->q;
-  p.k_new = a->k_new;
-  p.v_new = a->v_new;
-  p.q_stride = a->q_stride;
-  p.k_stride = a->k_stride;
-  p.v_stride = a->v_stride;
-  p.cu_q = a->cu_q;
-  p.page_table = a->page_table;
-  p.seq_lens = a->seq_lens;
-  p.rope = a->rope;
-  p.rope_positions = a->rope_positions;
-  p.num_tokens = a->num_tokens;
-  p.num_pages = a->num_pages;
-  p.batch = a->batch;
-  p.num_q_heads = a->num_q_heads;
-  p.num_kv_heads = a->num_kv_heads;
-  p.team_size = a->team_size;
-  p.max_teams = a->max_teams;
-  p.rope_dim = a->rope_dim;
-  p.interleaved = a->interleaved != 0;
-  p.q_out = a->q_out;
-  p.k_pool = a->k_pool;
-  p.v_pool = a->v_pool;
-  p.reps = a->reps;
-  p.seq_lens_next = a->seq_lens_next;
-  p.status = a->device_status;
-  return map_cuda(santa::launch_append_chunk(p, a->head_dim, bf16,
+  fill_append(a, &p);
+  return map_cuda(santa::launch_append_chunk(p, a->head_dim, a->dtype == SANTA_BF16,
                                              static_cast<cudaStream_t>(stream)));
+}
+
+int santa_append_norm(const santa_append_norm_args* a, void* stream) {
+  if (!a) return SANTA_ERR_INVALID_ARG;
+  const santa_append_chunk_args* c = &a->chunk;
+  int rc = check_append(c);
+  if (rc) return rc;
+  int code = santa::kCodeNone;
+  if (a->cache_type != c->dtype && (rc = code_of(a->cache_type, &code))) return rc;
+  if (code != santa::kCodeNone && (!a->k_scale || !a->v_scale)) return SANTA_ERR_INVALID_ARG;
+  if (code == santa::kCodeNone && (a->k_scale || a->v_scale)) return SANTA_ERR_INVALID_ARG;
+  if (!aligned(a->k_scale, 16) || !aligned(a->v_scale, 16) || !aligned(a->q_norm, 16) ||
+      !aligned(a->k_norm, 16))
+    return SANTA_ERR_INVALID_ARG;
+  if (!(a->eps >= 0.f) || !std::isfinite(a->eps)) return SANTA_ERR_INVALID_ARG;
+  santa::AppendNormParams p = {};
+  fill_append(c, &p);
+  p.q_norm = a->q_norm;
+  p.k_norm = a->k_norm;
+  p.eps = a->eps;
+  p.k_scale = a->k_scale;
+  p.v_scale = a->v_scale;
+  return map_cuda(santa::launch_append_norm(p, c->head_dim, c->dtype == SANTA_BF16, code,
+                                            static_cast<cudaStream_t>(stream)));
 }
 
 size_t santa_chunk_workspace_bytes(int dtype, int batch, int64_t num_tokens, int num_q_heads,

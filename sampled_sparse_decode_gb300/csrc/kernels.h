@@ -104,6 +104,63 @@ cudaError_t launch_append_chunk(const AppendChunkParams& p, int head_dim, bool b
 cudaError_t launch_rope_table(float* table, int64_t positions, int rope_dim, double theta,
                               cudaStream_t stream);
 
+// The same with norms of the heads and a cache of the activations' type or of 8-bit rows.
+struct AppendNormParams : AppendChunkParams {
+  const float* q_norm;        // [d] or nullptr
+  const float* k_norm;
+  float eps;
+  float* k_scale;             // [P][Hkv][T], 8-bit caches
+  float* v_scale;
+};
+// code: CodeType of the cache
+cudaError_t launch_append_norm(const AppendNormParams& p, int head_dim, bool bf16, int code,
+                               cudaStream_t stream);
+
+// ---------------------------------------------------------------- 8-bit cache: reading back
+struct Q8ReadParams {
+  const void* k;              // [P][Hkv][T][d] codes
+  const void* v;
+  const float* k_scale;       // [P][Hkv][T]
+  const float* v_scale;
+  const int32_t* page_table;  // [B][max_teams]
+  const int32_t* seq_lens;    // [B]
+  const int32_t* first;       // [B] or nullptr
+  const int32_t* dst_table;   // [B][max_teams]
+  int64_t num_pages, dst_pages;
+  int batch, num_kv_heads, team_size, max_teams;
+  void* k_out;                // [dst_pages][Hkv][T][d]
+  void* v_out;
+  int32_t* status;
+};
+cudaError_t launch_q8_read(const Q8ReadParams& p, int head_dim, bool bf16, int code, int sms,
+                           cudaStream_t stream);
+
+// ---------------------------------------------------------------- 8-bit cache: attention
+struct Q8AttendParams {
+  const void* q;              // [B][Hq][d]
+  const void* k;              // [P][Hkv][T][d] codes
+  const void* v;
+  const float* k_scale;       // [P][Hkv][T]
+  const float* v_scale;
+  const int32_t* page_table;  // [B][max_teams]
+  const int32_t* seq_lens;    // [B]
+  const int32_t* sel_ids;     // [B][Hkv][M], or nullptr: every team with weight 1
+  const int32_t* sel_count;   // [B][Hkv]
+  const float* pi;            // [B][Hkv][M]
+  int64_t num_pages;
+  int batch, num_q_heads, num_kv_heads, team_size, max_teams, num_draws;
+  float scale;                // 1 / sqrt(d)
+  float softcap;              // 0: none
+  int window;                 // 0: none
+  int splits;                 // blocks per unit
+  float* part;                // [B * Hkv][splits][G][d + 2]
+  float* out;                 // [B][Hq][d]
+  int32_t* status;
+};
+int q8_attend_splits(int64_t units, int64_t max_tokens, int sms);
+cudaError_t launch_q8_attend(const Q8AttendParams& p, int head_dim, bool bf16, int code,
+                             cudaStream_t stream);
+
 // ---------------------------------------------------------------- top-k selection
 struct SelectParams {
   const void* q;

@@ -1,0 +1,230 @@
+// q8_abi.cu — the C entry points over 8-bit caches but for the append (cache_abi.cu): argument checks,
+// workspace layout and launches.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "abi_checks.h"
+
+using namespace santa::abi;
+
+namespace {
+
+constexpr int64_t kMaxPages = 0x7fffffff;   // page ids are int32
+
+// A buffer of a call, for the overlap checks.
+struct Span {
+  const void* at;
+  int64_t bytes;
+};
+template <int N>
+bool meets_any(const Span& out, const Span (&in)[N]) {
+  return std::any_of(in, in + N, [&](const Span& s) {
+    return meets(out.at, out.bytes, s.at, 1, s.bytes, s.bytes);
+  });
+}
+
+int check_q8_cache(const void* k, const void* v, const float* k_scale, const float* v_scale,
+                   int type, int* code) {
+  const int rc = code_of(type, code);
+  if (rc) return rc;
+  if (!k || !v || !k_scale || !v_scale) return SANTA_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_scale, 16) || !aligned(v_scale, 16))
+    return SANTA_ERR_INVALID_ARG;
+  return SANTA_OK;
+}
+
+int check_q8_shape(int batch, int hq, int hkv, int d, int T, int max_teams) {
+  const int rc = check_cache_shape(SANTA_F32, batch, hkv, d, T, max_teams);
+  return rc ? rc : check_heads(hq, hkv);
+}
+
+struct Q8Layout {
+  int splits;
+  size_t bytes;
+};
+int q8_layout(int batch, int hq, int hkv, int d, int T, int max_teams, Q8Layout* l) {
+  const int sms = santa::device_sms();
+  if (sms <= 0) return SANTA_ERR_CUDA;
+  const int64_t units = static_cast<int64_t>(batch) * hkv;
+  l->splits = santa::q8_attend_splits(units, static_cast<int64_t>(max_teams) * T, sms);
+  l->bytes = kAlign + static_cast<size_t>(units) * l->splits * (hq / hkv) * (d + 2) * sizeof(float);
+  return SANTA_OK;
+}
+
+// Every check of an attention; listed: over sel_ids.
+int check_q8_attend(const santa_decode_args* a, const santa_q8_args* c, bool listed, int* code,
+                    Q8Layout* l) {
+  if (!a || !c) return SANTA_ERR_INVALID_ARG;
+  int rc = check_cache_shape(a->dtype, a->batch, a->num_kv_heads, a->head_dim, a->team_size,
+                             a->max_teams);
+  if (rc || (rc = check_heads(a->num_q_heads, a->num_kv_heads))) return rc;
+  if ((rc = check_q8_cache(c->k, c->v, c->k_scale, c->v_scale, c->type, code))) return rc;
+  if (a->num_pages < 1 || !a->q || !a->page_table || !a->seq_lens || !a->out)
+    return SANTA_ERR_INVALID_ARG;
+  if (a->num_pages > kMaxPages) return SANTA_ERR_UNSUPPORTED;
+  if (!aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->page_table, 4) ||
+      !aligned(a->seq_lens, 4) || !aligned(a->device_status, 4))
+    return SANTA_ERR_INVALID_ARG;
+  if (!(c->softcap >= 0.f) || !std::isfinite(c->softcap) || c->window < 0)
+    return SANTA_ERR_INVALID_ARG;
+  if (listed) {
+    if (a->num_draws < 1 || a->num_draws > kMaxDraws) return SANTA_ERR_UNSUPPORTED;
+    if (!a->sel_ids || !a->sel_count || !a->pi) return SANTA_ERR_INVALID_ARG;
+    if (!aligned(a->sel_ids, 4) || !aligned(a->sel_count, 4) || !aligned(a->pi, 4))
+      return SANTA_ERR_INVALID_ARG;
+  }
+  if ((rc = q8_layout(a->batch, a->num_q_heads, a->num_kv_heads, a->head_dim, a->team_size,
+                      a->max_teams, l)))
+    return rc;
+  if (!a->workspace || a->workspace_bytes < l->bytes) return SANTA_ERR_INVALID_ARG;
+  const int64_t rows = a->num_pages * a->num_kv_heads * static_cast<int64_t>(a->team_size);
+  const int64_t units = static_cast<int64_t>(a->batch) * a->num_kv_heads;
+  const int64_t row = static_cast<int64_t>(a->num_q_heads) * a->head_dim;
+  const int64_t list = listed ? units * a->num_draws * 4 : 0;
+  const Span in[] = {{a->q, a->batch * row * (a->dtype == SANTA_BF16 ? 2 : 4)},
+                     {c->k, rows * a->head_dim},
+                     {c->v, rows * a->head_dim},
+                     {c->k_scale, rows * 4},
+                     {c->v_scale, rows * 4},
+                     {a->page_table, static_cast<int64_t>(a->batch) * a->max_teams * 4},
+                     {a->seq_lens, static_cast<int64_t>(a->batch) * 4},
+                     {a->sel_ids, list},
+                     {a->sel_count, listed ? units * 4 : 0},
+                     {a->pi, list}};
+  const Span out = {a->out, a->batch * row * 4};
+  const Span ws = {a->workspace, static_cast<int64_t>(l->bytes)};
+  if (meets_any(out, in) || meets_any(ws, in) || meets(out.at, out.bytes, ws.at, 1, ws.bytes, ws.bytes))
+    return SANTA_ERR_INVALID_ARG;
+  return SANTA_OK;
+}
+
+int launch_q8(const santa_decode_args* a, const santa_q8_args* c, bool listed, void* stream) {
+  int code = 0;
+  Q8Layout l;
+  const int rc = check_q8_attend(a, c, listed, &code, &l);
+  if (rc) return rc;
+  santa::Q8AttendParams p = {};
+  p.q = a->q;
+  p.k = c->k;
+  p.v = c->v;
+  p.k_scale = c->k_scale;
+  p.v_scale = c->v_scale;
+  p.page_table = a->page_table;
+  p.seq_lens = a->seq_lens;
+  p.sel_ids = listed ? a->sel_ids : nullptr;
+  p.sel_count = a->sel_count;
+  p.pi = a->pi;
+  p.num_pages = a->num_pages;
+  p.batch = a->batch;
+  p.num_q_heads = a->num_q_heads;
+  p.num_kv_heads = a->num_kv_heads;
+  p.team_size = a->team_size;
+  p.max_teams = a->max_teams;
+  p.num_draws = a->num_draws;
+  p.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(a->head_dim)));
+  p.softcap = c->softcap;
+  p.window = c->window;
+  p.splits = l.splits;
+  p.part = reinterpret_cast<float*>(round_up(reinterpret_cast<uintptr_t>(a->workspace), kAlign));
+  p.out = a->out;
+  p.status = a->device_status;
+  return map_cuda(santa::launch_q8_attend(p, a->head_dim, a->dtype == SANTA_BF16, code,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+#pragma GCC visibility push(default)
+extern "C" {
+
+size_t santa_q8_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                                int team_size, int max_teams) {
+  Q8Layout l;
+  if (check_q8_shape(batch, num_q_heads, num_kv_heads, head_dim, team_size, max_teams) ||
+      q8_layout(batch, num_q_heads, num_kv_heads, head_dim, team_size, max_teams, &l))
+    return 0;
+  return l.bytes;
+}
+
+int santa_q8_dense_decode(const santa_decode_args* a, const santa_q8_args* c, void* stream) {
+  return launch_q8(a, c, false, stream);
+}
+
+int santa_q8_attend(const santa_decode_args* a, const santa_q8_args* c, void* stream) {
+  return launch_q8(a, c, true, stream);
+}
+
+int santa_q8_topk_decode(const santa_decode_args* a, const santa_q8_args* c, void* stream) {
+  // everything the attention refuses is refused before the selection is launched
+  int code = 0;
+  Q8Layout l;
+  int rc = check_q8_attend(a, c, true, &code, &l);
+  if (rc || (rc = santa_select_topk(a, stream))) return rc;
+  return launch_q8(a, c, true, stream);
+}
+
+int santa_q8_decode(const santa_decode_args* a, const santa_q8_args* c, void* stream) {
+  int code = 0;
+  Q8Layout l;
+  int rc = check_q8_attend(a, c, true, &code, &l);
+  if (rc) return rc;
+  // the sampling reads representatives only; its checks ask for pools all the same
+  santa_decode_args b = *a;
+  b.k_pool = c->k;
+  b.v_pool = c->v;
+  if ((rc = santa_sample(&b, stream))) return rc;
+  return launch_q8(a, c, true, stream);
+}
+
+int santa_q8_read(const santa_q8_read_args* a, void* stream) {
+  if (!a) return SANTA_ERR_INVALID_ARG;
+  int rc = check_cache_shape(a->out_dtype, a->batch, a->num_kv_heads, a->head_dim, a->team_size,
+                             a->max_teams);
+  int code = 0;
+  if (rc || (rc = check_q8_cache(a->k, a->v, a->k_scale, a->v_scale, a->type, &code))) return rc;
+  if (a->num_pages < 1 || a->dst_pages < 1 || !a->page_table || !a->seq_lens || !a->dst_table ||
+      !a->k_out || !a->v_out)
+    return SANTA_ERR_INVALID_ARG;
+  if (a->num_pages > kMaxPages || a->dst_pages > kMaxPages) return SANTA_ERR_UNSUPPORTED;
+  if (!aligned(a->k_out, 16) || !aligned(a->v_out, 16) || !aligned(a->page_table, 4) ||
+      !aligned(a->seq_lens, 4) || !aligned(a->first, 4) || !aligned(a->dst_table, 4) ||
+      !aligned(a->device_status, 4))
+    return SANTA_ERR_INVALID_ARG;
+  const int64_t page = static_cast<int64_t>(a->num_kv_heads) * a->team_size;
+  const int64_t rows = a->num_pages * page, bytes = a->dst_pages * page * a->head_dim *
+                                                    (a->out_dtype == SANTA_BF16 ? 2 : 4);
+  const int64_t table = static_cast<int64_t>(a->batch) * a->max_teams * 4, lens = a->batch * 4ll;
+  const Span in[] = {{a->k, rows * a->head_dim}, {a->v, rows * a->head_dim},
+                     {a->k_scale, rows * 4},     {a->v_scale, rows * 4},
+                     {a->page_table, table},     {a->dst_table, table},
+                     {a->seq_lens, lens},        {a->first, lens}};
+  const Span k = {a->k_out, bytes}, v = {a->v_out, bytes};
+  if (meets_any(k, in) || meets_any(v, in) || meets(k.at, bytes, v.at, 1, bytes, bytes))
+    return SANTA_ERR_INVALID_ARG;
+  const int sms = santa::device_sms();
+  if (sms <= 0) return SANTA_ERR_CUDA;
+  santa::Q8ReadParams p = {};
+  p.k = a->k;
+  p.v = a->v;
+  p.k_scale = a->k_scale;
+  p.v_scale = a->v_scale;
+  p.page_table = a->page_table;
+  p.seq_lens = a->seq_lens;
+  p.first = a->first;
+  p.dst_table = a->dst_table;
+  p.num_pages = a->num_pages;
+  p.dst_pages = a->dst_pages;
+  p.batch = a->batch;
+  p.num_kv_heads = a->num_kv_heads;
+  p.team_size = a->team_size;
+  p.max_teams = a->max_teams;
+  p.k_out = a->k_out;
+  p.v_out = a->v_out;
+  p.status = a->device_status;
+  return map_cuda(santa::launch_q8_read(p, a->head_dim, a->out_dtype == SANTA_BF16, code, sms,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+#pragma GCC visibility pop

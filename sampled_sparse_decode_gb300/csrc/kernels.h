@@ -152,13 +152,15 @@ struct Q8AttendParams {
   float scale;                // 1 / sqrt(d)
   float softcap;              // 0: none
   int window;                 // 0: none
-  int splits;                 // blocks per unit
-  float* part;                // [B * Hkv][splits][G][d + 2]
+  // partial results, two slots of each block: of which unit (-1: none), accumulators, (m, l)
+  int64_t* part_unit;         // [blocks][2]
+  float* part_acc;            // [blocks][2][kMaxGroup][d]
+  float* part_ml;             // [blocks][2][kMaxGroup][2]
   float* out;                 // [B][Hq][d]
   int32_t* status;
 };
-int q8_attend_splits(int64_t units, int64_t max_tokens, int sms);
-cudaError_t launch_q8_attend(const Q8AttendParams& p, int head_dim, bool bf16, int code,
+// One block per multiprocessor; two launches.
+cudaError_t launch_q8_attend(const Q8AttendParams& p, int head_dim, bool bf16, int code, int sms,
                              cudaStream_t stream);
 
 // ---------------------------------------------------------------- top-k selection

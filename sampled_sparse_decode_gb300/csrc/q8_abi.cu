@@ -39,16 +39,18 @@ int check_q8_shape(int batch, int hq, int hkv, int d, int T, int max_teams) {
   return rc ? rc : check_heads(hq, hkv);
 }
 
+// Workspace of an attention: the blocks' partial results (see Q8AttendParams).
 struct Q8Layout {
-  int splits;
-  size_t bytes;
+  int sms;
+  size_t unit_bytes, ml_bytes, bytes;
 };
-int q8_layout(int batch, int hq, int hkv, int d, int T, int max_teams, Q8Layout* l) {
-  const int sms = santa::device_sms();
-  if (sms <= 0) return SANTA_ERR_CUDA;
-  const int64_t units = static_cast<int64_t>(batch) * hkv;
-  l->splits = santa::q8_attend_splits(units, static_cast<int64_t>(max_teams) * T, sms);
-  l->bytes = kAlign + static_cast<size_t>(units) * l->splits * (hq / hkv) * (d + 2) * sizeof(float);
+int q8_layout(int d, Q8Layout* l) {
+  l->sms = santa::device_sms();
+  if (l->sms <= 0) return SANTA_ERR_CUDA;
+  const size_t parts = static_cast<size_t>(l->sms) * 2;
+  l->unit_bytes = round_up(parts * sizeof(int64_t), kAlign);
+  l->ml_bytes = round_up(parts * santa::kMaxGroup * 2 * sizeof(float), kAlign);
+  l->bytes = kAlign + l->unit_bytes + l->ml_bytes + parts * santa::kMaxGroup * d * sizeof(float);
   return SANTA_OK;
 }
 
@@ -74,9 +76,7 @@ int check_q8_attend(const santa_decode_args* a, const santa_q8_args* c, bool lis
     if (!aligned(a->sel_ids, 4) || !aligned(a->sel_count, 4) || !aligned(a->pi, 4))
       return SANTA_ERR_INVALID_ARG;
   }
-  if ((rc = q8_layout(a->batch, a->num_q_heads, a->num_kv_heads, a->head_dim, a->team_size,
-                      a->max_teams, l)))
-    return rc;
+  if ((rc = q8_layout(a->head_dim, l))) return rc;
   if (!a->workspace || a->workspace_bytes < l->bytes) return SANTA_ERR_INVALID_ARG;
   const int64_t rows = a->num_pages * a->num_kv_heads * static_cast<int64_t>(a->team_size);
   const int64_t units = static_cast<int64_t>(a->batch) * a->num_kv_heads;
@@ -125,11 +125,14 @@ int launch_q8(const santa_decode_args* a, const santa_q8_args* c, bool listed, v
   p.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(a->head_dim)));
   p.softcap = c->softcap;
   p.window = c->window;
-  p.splits = l.splits;
-  p.part = reinterpret_cast<float*>(round_up(reinterpret_cast<uintptr_t>(a->workspace), kAlign));
+  unsigned char* base = reinterpret_cast<unsigned char*>(
+      round_up(reinterpret_cast<uintptr_t>(a->workspace), kAlign));
+  p.part_unit = reinterpret_cast<int64_t*>(base);
+  p.part_ml = reinterpret_cast<float*>(base + l.unit_bytes);
+  p.part_acc = reinterpret_cast<float*>(base + l.unit_bytes + l.ml_bytes);
   p.out = a->out;
   p.status = a->device_status;
-  return map_cuda(santa::launch_q8_attend(p, a->head_dim, a->dtype == SANTA_BF16, code,
+  return map_cuda(santa::launch_q8_attend(p, a->head_dim, a->dtype == SANTA_BF16, code, l.sms,
                                           static_cast<cudaStream_t>(stream)));
 }
 
@@ -142,7 +145,7 @@ size_t santa_q8_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, in
                                 int team_size, int max_teams) {
   Q8Layout l;
   if (check_q8_shape(batch, num_q_heads, num_kv_heads, head_dim, team_size, max_teams) ||
-      q8_layout(batch, num_q_heads, num_kv_heads, head_dim, team_size, max_teams, &l))
+      q8_layout(head_dim, &l))
     return 0;
   return l.bytes;
 }

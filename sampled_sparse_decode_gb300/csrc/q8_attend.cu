@@ -9,8 +9,28 @@
 // scale of a key multiplies its whole score and the scale of a value its weight, so that no element
 // is scaled by itself.
 //
-// A warp takes one token at a time; a lane holds d / 32 elements of every query head of the group.
-// The second launch adds a unit's partial results in the order of the splits.
+// Work.  The tiles (32 tokens) of all units (sequence, KV head) lie on one line, which the blocks
+// share evenly, whatever the lengths of the batch are; the lengths are read on the device.  A block's
+// warps take the tiles of its part in turn, each through a ring of its own in shared memory
+// (asynchronous 16-byte copies, two tiles ahead of the one in use, no barrier among warps), and merge
+// their results at the end of each unit's part.  A unit that lies within one block is finished there;
+// the others' partial results are joined by a second launch in the order of the line.
+//
+// A tile.  Codes become fp16 exactly (int8 by the bits of 1024 + code, e4m3 by conversion) and go to
+// the matrix units as the A operand of m16n8k16, tokens x dimensions for the scores and dimensions x
+// tokens for the output, so that the group's up to 8 query heads are the n = 8 columns and a warp
+// needs no other padding.  Which dimension stands at which k is free as long as both operands agree:
+// a lane reads 16 bytes of one row and has the operands of four products.  Rows are placed so that
+// both kinds of read are free of bank conflicts.
+//   - q enters as fp16 pieces (one for bf16, two for fp32) of q 2^-e, e the exponent of the head's
+//     largest element: fp16's range holds everything down to 2^-24 of it.
+//   - The weights enter the second product as two fp16 pieces (22 bits; one would leave 2^-12 of
+//     error in an fp32 result) of p_j vs_j over a power of two near the largest p vs so far: the scales of
+//     values may lie any powers of two apart.
+//   - The reference of the exponentials is raised only when a score passes it by 8 (powers of two),
+//     which is seldom after a few tiles, so a tile has no reduction among lanes.
+//   - The matrix units cut what they add; each tile's products start from zero and are added to the
+//     running sums in fp32 with rounding.
 #include <algorithm>
 
 #include "kernels.h"
@@ -20,201 +40,742 @@ namespace santa {
 
 namespace {
 
+constexpr int kTile = 32;                  // tokens of a tile
 constexpr int kQ8Threads = 256;
 constexpr int kQ8Warps = kQ8Threads / 32;
+constexpr int kStages = 3;                 // tiles of a warp's ring
+constexpr int kMinShare = kQ8Warps;        // tiles of a block's part: at least one for each warp
+constexpr int kMergeDims = 64;             // dimensions that one merging pass takes
+constexpr int kMergeRow = kMergeDims + 4;
+constexpr float kSlack = 8.f;              // how far a score may pass the reference (base 2)
+constexpr float kTopWeight = 256.f;        // the same for a weight
 
-// The tokens that a unit may see: positions lo .. len - 1 (dense), or `count` listed teams.
+template <int D>
+struct Ring {
+  static constexpr int kCodes = kTile * D;                     // bytes of a tile's keys or values
+  static constexpr int kStage = 2 * kCodes + 2 * kTile * 4;    // keys, values, scales
+  static constexpr int kWarp = kStages * kStage;
+  static constexpr int kMerge = kQ8Warps * kMaxGroup * kMergeRow * 4;
+  static constexpr int kBytes = kQ8Warps * kWarp + kMerge;
+};
+
+// Byte of 16-byte piece `chunk` of row r in a tile's block of rows.  Scores are read by 8 lanes from
+// pieces c .. c + 3 of rows 2j and 2j + 1, values from pieces 2j and 2j + 1 (d = 128; the halves of a
+// piece for d = 64) of four rows two apart: either way the 8 pieces lie in 8 different banks' groups.
+template <int D>
+__device__ __forceinline__ int piece_at(int r, int chunk) {
+  if constexpr (D == 128) {
+    return r * 128 + ((chunk ^ (((r >> 2 ^ r) & 1) << 2 | (r & 2))) << 4);
+  } else {
+    const int half = (r ^ r >> 1) & 1;
+    return (r >> 1) * 128 + (half << 6) + ((chunk ^ ((r >> 2 & 1) << 1)) << 4);
+  }
+}
+
+__device__ __forceinline__ void cp_async16_fill(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+      " {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The two code pairs of a word, bytes (0, 1) and (2, 3), as fp16.  int8: with its sign bit turned
+// a code is u = code + 128, 0x6400 | u is 1024 + u, and 1152 less is the code; exact.
+template <int C>
+__device__ __forceinline__ void pairs_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (C == kCodeI8) {
+    const uint32_t u = w ^ 0x80808080u;
+    lo = sub_f16x2(__byte_perm(u, 0x64646464u, 0x4140), 0x64806480u);
+    hi = sub_f16x2(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u);
+  } else {
+    lo = e4m3_to_f16x2(static_cast<uint16_t>(w));
+    hi = e4m3_to_f16x2(static_cast<uint16_t>(w >> 16));
+  }
+}
+
+// ---------------------------------------------------------------- the line of tiles
+
+// A unit's tokens: positions lo .. len - 1 (dense), or `count` listed teams; `tiles` on the line.
 struct Unit {
   int64_t len, lo;
   int count;
+  int64_t tiles;
 };
-__device__ __forceinline__ bool load_unit(const Q8AttendParams& p, int b, int h, Unit* u) {
-  u->len = p.seq_lens[b];
-  if (u->len < 0 || u->len > static_cast<int64_t>(p.max_teams) * p.team_size) return false;
-  u->lo = p.window > 0 && u->len > p.window ? u->len - p.window : 0;
-  u->count = 0;
+// Reads sequence b (dense) or unit (b, h) (listed); what is out of range is judged here and told if
+// `tell`.
+__device__ __forceinline__ Unit load_unit(const Q8AttendParams& p, int b, int h, bool tell) {
+  Unit u;
+  u.len = p.seq_lens[b];
+  u.count = 0;
+  if (u.len < 0 || u.len > static_cast<int64_t>(p.max_teams) * p.team_size) {
+    if (tell) set_status(p.status, SANTA_DEV_BAD_SEQLEN);
+    u.len = 0;
+  }
+  u.lo = p.window > 0 && u.len > p.window ? u.len - p.window : 0;
   if (p.sel_ids) {
-    u->count = p.sel_count[static_cast<int64_t>(b) * p.num_kv_heads + h];
-    if (u->count < 0 || u->count > p.num_draws) {
-      set_status(p.status, SANTA_DEV_BAD_SEL);
-      u->count = u->count < 0 ? 0 : p.num_draws;
+    const int count = p.sel_count[static_cast<int64_t>(b) * p.num_kv_heads + h];
+    u.count = min(max(count, 0), p.num_draws);
+    if (count != u.count && tell) set_status(p.status, SANTA_DEV_BAD_SEL);
+    if (u.len == 0) u.count = 0;
+    u.tiles = static_cast<int64_t>(u.count) * (p.team_size / kTile);
+  } else {
+    u.tiles = (u.len + kTile - 1) / kTile - u.lo / kTile;
+  }
+  return u;
+}
+
+// A place on the line: unit (b, h), whose tiles start at `base`.
+struct Walk {
+  int b, h;
+  int64_t base;
+  Unit u;
+};
+__device__ __forceinline__ void next_unit(const Q8AttendParams& p, Walk& w) {
+  w.base += w.u.tiles;
+  if (w.b == p.batch - 1 && w.h == p.num_kv_heads - 1) {
+    // not reached while lengths and lists stay as they are; if not, the walk ends here
+    w.u = Unit{0, 0, 0, INT64_MAX / 2};
+    return;
+  }
+  const bool wrap = ++w.h == p.num_kv_heads;
+  if (wrap) {
+    w.h = 0;
+    ++w.b;
+  }
+  if (wrap || p.sel_ids) w.u = load_unit(p, w.b, w.h, false);
+}
+
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += up;
+  }
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  int64_t before = 0;
+#pragma unroll
+  for (int w = 0; w < kQ8Warps; ++w)
+    if (w < warp) before += warp_sums[w];
+  return v + before;
+}
+
+// ---------------------------------------------------------------- the attention
+
+// What a warp knows of its next tiles' pages: 32 consecutive teams of a sequence (dense) or slots of a
+// unit's list, one per lane.
+struct PageCache {
+  int b, h;            // of which sequence (and unit, listed); b = -1: nothing yet
+  int first;           // team or slot of lane 0
+  int team;            // listed: -1 for one that is left out
+  int page;            // -1: out of range
+  float bias;          // listed: -log2 pi
+};
+
+template <int NQ, int C, int D>
+struct Warp {
+  static constexpr int kSteps = D / 16;              // k steps of a score
+  static constexpr int kOut = D / 16;                // 16-dimension tiles of the output
+  uint32_t q[NQ][kSteps][2];
+  float acc[kOut][4];
+  float ref[2], top[2];      // of heads 2t and 2t + 1: reference, and the score that raises it
+  float sum[2];              // this lane's share of the sum of weights
+  float big[2], inv[2];      // largest |p vs| (at least), and the power of two that scales weights
+  float qs[2];               // score of a unit product, base 2 (or over the cap)
+};
+
+// Copies tile `t` of the line into a stage and returns what the consumer must know of it: the range of
+// its tokens that are seen and the bias.
+template <int D>
+__device__ __forceinline__ void issue_tile(const Q8AttendParams& p, const Walk& w, int64_t t,
+                                           PageCache& pc, uint8_t* stage, int2* note) {
+  const int lane = threadIdx.x & 31;
+  const int T = p.team_size, per = T / kTile;
+  const int64_t i = t - w.base;                      // tile of the unit
+  const int64_t at = p.sel_ids ? i / per : (w.u.lo / kTile + i) / per;     // slot or team
+  const int row = static_cast<int>(p.sel_ids ? i % per : (w.u.lo / kTile + i) % per) * kTile;
+  if (pc.b != w.b || (p.sel_ids && pc.h != w.h) || at < pc.first || at >= pc.first + 32) {
+    pc.b = w.b;
+    pc.h = w.h;
+    pc.first = static_cast<int>(at);
+    const int64_t mine = at + lane;
+    pc.bias = 0.f;
+    pc.page = -1;
+    pc.team = -1;
+    if (!p.sel_ids) {
+      if (mine * T < w.u.len) pc.team = static_cast<int>(mine);
+    } else if (mine < w.u.count) {
+      const int64_t slot = (static_cast<int64_t>(w.b) * p.num_kv_heads + w.h) * p.num_draws + mine;
+      const int team = p.sel_ids[slot];
+      const float pi = p.pi[slot];
+      if (team >= 0 && static_cast<int64_t>(team) * T < w.u.len && pi > 0.f && pi < INFINITY) {
+        pc.team = team;
+        pc.bias = -log2f(pi);
+      } else {
+        set_status(p.status, SANTA_DEV_BAD_SEL);
+      }
+    }
+    if (pc.team >= 0) {
+      pc.page = p.page_table[static_cast<int64_t>(w.b) * p.max_teams + pc.team];
+      if (pc.page < 0 || pc.page >= p.num_pages) {
+        set_status(p.status, SANTA_DEV_BAD_PAGE);
+        pc.page = -1;
+      }
     }
   }
-  return true;
+  const int from = static_cast<int>(at - pc.first);
+  const int team = __shfl_sync(0xffffffffu, pc.team, from);
+  const int page = __shfl_sync(0xffffffffu, pc.page, from);
+  const float bias = __shfl_sync(0xffffffffu, pc.bias, from);
+  const int64_t t0 = static_cast<int64_t>(team) * T + row;
+  int n0 = static_cast<int>(min(max(w.u.lo - t0, int64_t(0)), int64_t(kTile)));
+  int n1 = static_cast<int>(min(max(w.u.len - t0, int64_t(0)), int64_t(kTile)));
+  if (page < 0 || n0 >= n1) n0 = n1 = 0;
+  if (lane == 0) *note = make_int2(n0 | n1 << 16, __float_as_int(bias));
+  if (n1 > 0) {
+    constexpr int kCols = D / 16, kRows = 32 / kCols;   // pieces of a row; rows per round
+    const int64_t first = (static_cast<int64_t>(page) * p.num_kv_heads + w.h) * T + row;
+    const uint8_t* k = static_cast<const uint8_t*>(p.k) + first * D;
+    const uint8_t* v = static_cast<const uint8_t*>(p.v) + first * D;
+    const uint32_t to = smem_u32(stage);
+#pragma unroll
+    for (int e = 0; e < kTile / kRows; ++e) {
+      const int r = e * kRows + lane / kCols, chunk = lane % kCols;
+      const bool on = r >= n0 && r < n1;              // rows that are not seen become zeros
+      cp_async16_fill(to + piece_at<D>(r, chunk), k + r * D + chunk * 16, on);
+      cp_async16_fill(to + kTile * D + piece_at<D>(r, chunk), v + r * D + chunk * 16, on);
+    }
+    if (lane < 2 * kTile / 4) {
+      const float* s = (lane < kTile / 4 ? p.k_scale : p.v_scale) + first + lane % (kTile / 4) * 4;
+      cp_async16_fill(to + 2 * kTile * D + lane * 16, s, true);
+    }
+  }
 }
 
-template <int C, int W>
-__device__ __forceinline__ void load_row(const void* codes, int64_t row, int lane, float (&x)[W]) {
-  const uint8_t* at = static_cast<const uint8_t*>(codes) + row * (32 * W) + lane * W;
-  float y[4];
-  if constexpr (W == 4) {
-    q8_decode<C>(*reinterpret_cast<const uint32_t*>(at), y);
-  } else {
-    q8_decode<C>(*reinterpret_cast<const uint16_t*>(at), y);
+// The group's queries as B operands: k index of step (c, w) are bytes 16 (t + 4 c) + 4 w + ... of a
+// row, t = lane % 4 (d = 64: c = 0 only).
+template <int NQ, int C, int D>
+__device__ void load_queries(const Q8AttendParams& p, int b, int h, Warp<NQ, C, D>& w) {
+  const int lane = threadIdx.x & 31, head = lane >> 2, t = lane & 3;
+  const int G = p.num_q_heads / p.num_kv_heads;
+  const int64_t at = (static_cast<int64_t>(b) * p.num_q_heads + h * G + head) * D;
+  float x[D / 4];
+  uint32_t top = 0;
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int64_t e = at + 16 * (t + 4 * c) + i;
+      float* y = x + 16 * c + i;
+      if (head >= G) {
+        y[0] = y[1] = y[2] = y[3] = 0.f;
+      } else if constexpr (NQ == 1) {
+        const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + e);
+        y[0] = bf16_lo(v.x), y[1] = bf16_hi(v.x), y[2] = bf16_lo(v.y), y[3] = bf16_hi(v.y);
+      } else {
+        const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + e);
+        y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
+      }
+    }
   }
 #pragma unroll
-  for (int e = 0; e < W; ++e) x[e] = y[e];
+  for (int i = 0; i < D / 4; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  // 2^-e and 2^e as exponent fields; zeros and queries near fp32's ends keep a factor inside its range
+  const uint32_t e = min(max(top >> 23, 16u), 253u);
+  const float down = __uint_as_float((254u - e) << 23), up = __uint_as_float(e << 23);
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float a = x[4 * s + 2 * i] * down, c = x[4 * s + 2 * i + 1] * down;
+      w.q[0][s][i] = pack_f16(a, c);
+      if constexpr (NQ == 2) {
+        const float2 got = f16x2_to_f32(w.q[0][s][i]);
+        w.q[NQ - 1][s][i] = pack_f16(a - got.x, c - got.y);
+      }
+    }
+  }
+  constexpr float kLog2e = 1.4426950408889634f;
+  const float f = up * (p.softcap > 0.f ? p.scale / p.softcap : p.scale * kLog2e);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    w.qs[i] = __shfl_sync(0xffffffffu, f, (2 * t + i) * 4);
+    w.ref[i] = 0.f;
+    w.top[i] = -INFINITY;
+    w.sum[i] = w.big[i] = 0.f;
+    w.inv[i] = 1.f;
+  }
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w.acc[j][i] = 0.f;
 }
 
-template <bool BF16, int C, int D>
-__global__ void __launch_bounds__(kQ8Threads) q8_attend_kernel(Q8AttendParams p) {
-  constexpr int W = D / 32;
+// Raises the references to this tile's largest score and weight: x[4 m + 2 r + i] is the score of token
+// 16 m + 8 r + lane / 4 and head 2 t + i, vs[2 m + r] the token's value scale.
+template <int NQ, int C, int D>
+__device__ __forceinline__ void raise(Warp<NQ, C, D>& w, const float (&x)[8], const float (&vs)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float top = fmaxf(fmaxf(x[i], x[2 + i]), fmaxf(x[4 + i], x[6 + i]));
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const bool fresh = w.top[i] == -INFINITY;
+    float keep = 1.f;
+    if (top != -INFINITY && (fresh || top > w.ref[i])) {
+      keep = fresh ? 0.f : ex2_approx(w.ref[i] - top);
+      w.ref[i] = top;
+      w.top[i] = top + kSlack;
+    }
+    float big = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) big = fmaxf(big, fabsf(ex2_approx(x[2 * k + i] - w.ref[i]) * vs[k]));
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+    big = fmaxf(big, w.big[i] * keep);
+    w.big[i] = big;
+    float inv = w.inv[i];
+    if (big > 0.f) inv = __uint_as_float((254u - min(max(__float_as_uint(big) >> 23, 1u), 253u)) << 23);
+    // inv / w.inv as a power of two inside fp32's range
+    const int d = static_cast<int>(__float_as_uint(inv) >> 23) - static_cast<int>(__float_as_uint(w.inv[i]) >> 23);
+    const float f = keep * __uint_as_float(static_cast<uint32_t>(min(max(d, -126), 127) + 127) << 23);
+    w.inv[i] = inv;
+    w.sum[i] *= keep;
+    if (f != 1.f) {
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        w.acc[j][i] *= f;
+        w.acc[j][2 + i] *= f;
+      }
+    }
+  }
+}
+
+template <int NQ, int C, int D>
+__device__ __forceinline__ void attend_tile(const Q8AttendParams& p, Warp<NQ, C, D>& w,
+                                            const uint8_t* stage, int2 note) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const float* scales = reinterpret_cast<const float*>(stage + 2 * kTile * D);
+  const int n0 = note.x & 0xffff, n1 = note.x >> 16;
+  if (n1 == 0) return;
+  float x[8], vs[4];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h) {
+      const uint4 a = *reinterpret_cast<const uint4*>(stage + piece_at<D>(16 * m + g, t + 4 * h));
+      const uint4 b = *reinterpret_cast<const uint4*>(stage + piece_at<D>(16 * m + 8 + g, t + 4 * h));
+      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t f[4];
+        pairs_to_f16<C>(aw[k], f[0], f[2]);
+        pairs_to_f16<C>(bw[k], f[1], f[3]);
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) mma_f16_16816(c, f, w.q[n][4 * h + k][0], w.q[n][4 * h + k][1]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int tok = 16 * m + 8 * r + g;
+      const float ks = scales[tok];
+      vs[2 * m + r] = scales[kTile + tok];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) x[4 * m + 2 * r + i] = c[2 * r + i] * ks * w.qs[i];
+    }
+  }
+  if (p.softcap > 0.f) {
+    const float cap = p.softcap * 1.4426950408889634f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = cap * tanhf(x[i]);
+  }
+  const float bias = __int_as_float(note.y);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] += bias;
+  if (n0 > 0 || n1 < kTile) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int tok = 8 * k + g;
+      if (tok < n0 || tok >= n1) {
+        x[2 * k] = x[2 * k + 1] = -INFINITY;
+        vs[k] = 0.f;
+      }
+    }
+  }
+  float e[8], pw[8];
+  auto weigh = [&]() {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        e[2 * k + i] = ex2_approx(x[2 * k + i] - w.ref[i]);
+        pw[2 * k + i] = e[2 * k + i] * vs[k] * w.inv[i];
+      }
+  };
+  weigh();
+  bool over = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) over |= x[i] > w.top[i & 1] || fabsf(pw[i]) > kTopWeight;
+  if (__any_sync(0xffffffffu, over)) {
+    raise(w, x, vs);
+    weigh();
+  }
+  uint32_t hi[4], lo[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    w.sum[0] += e[2 * k];
+    w.sum[1] += e[2 * k + 1];
+    hi[k] = pack_f16(pw[2 * k], pw[2 * k + 1]);
+    const float2 got = f16x2_to_f32(hi[k]);
+    lo[k] = pack_f16(pw[2 * k] - got.x, pw[2 * k + 1] - got.y);
+    hi[k] = movmatrix_trans(hi[k]);
+    lo[k] = movmatrix_trans(lo[k]);
+  }
+  // values: 16 tokens at a time; a lane has D / 8 dimensions of four tokens
+  constexpr int kWords = D / 32;
+  uint32_t v[2][4][kWords];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int tok = 16 * m + 8 * (r >> 1) + 2 * t + (r & 1);
+      const uint8_t* at = stage + kTile * D;
+      if constexpr (D == 128) {
+        const uint4 a = *reinterpret_cast<const uint4*>(at + piece_at<D>(tok, g));
+        v[m][r][0] = a.x, v[m][r][1] = a.y, v[m][r][kWords - 2] = a.z, v[m][r][kWords - 1] = a.w;
+      } else {
+        const uint2 a = *reinterpret_cast<const uint2*>(at + piece_at<D>(tok, g >> 1) + (g & 1) * 8);
+        v[m][r][0] = a.x, v[m][r][1] = a.y;
+      }
+    }
+#pragma unroll
+  for (int k = 0; k < kWords; ++k) {
+    float c[2][4] = {};
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      uint32_t f[2][4];                              // dimensions (4k, 4k + 1) and (4k + 2, 4k + 3)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t a = v[m][2 * r][k], b = v[m][2 * r + 1][k];
+        pairs_to_f16<C>(__byte_perm(a, b, 0x5140), f[0][2 * r], f[0][2 * r + 1]);
+        pairs_to_f16<C>(__byte_perm(a, b, 0x7362), f[1][2 * r], f[1][2 * r + 1]);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        mma_f16_16816(c[j], f[j], hi[2 * m], hi[2 * m + 1]);
+        mma_f16_16816(c[j], f[j], lo[2 * m], lo[2 * m + 1]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w.acc[2 * k + j][i] += c[j][i];
+  }
+}
+
+template <int NQ, int C, int D>
+__global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t sums[2][kQ8Warps];
+  __shared__ int64_t start_s[2];                     // element of the line's start, its first tile
+  __shared__ int2 notes[kQ8Warps][kStages];
+  __shared__ float ml[kQ8Warps][kMaxGroup][2];
+  using R = Ring<D>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int G = p.num_q_heads / p.num_kv_heads;
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  // the length of the line, and where this block's part of it starts: by sequences (dense) or units
+  const int64_t elems = static_cast<int64_t>(p.batch) * (p.sel_ids ? p.num_kv_heads : 1);
+  const int heads = p.sel_ids ? 1 : p.num_kv_heads;
+  auto tiles_of = [&](int64_t e, bool tell) -> int64_t {
+    if (e >= elems) return 0;
+    const int b = static_cast<int>(p.sel_ids ? e / p.num_kv_heads : e);
+    return load_unit(p, b, static_cast<int>(e - static_cast<int64_t>(b) * p.num_kv_heads), tell).tiles *
+           heads;
+  };
+  int64_t total = 0, mine = 0, upto = 0;
+  for (int64_t e0 = 0; e0 < elems; e0 += kQ8Threads) {
+    mine = tiles_of(e0 + threadIdx.x, blockIdx.x == 0);
+    upto = total + block_scan(mine, sums[(e0 / kQ8Threads) & 1]);
+    if (threadIdx.x == kQ8Threads - 1) start_s[0] = upto;
+    __syncthreads();
+    total = start_s[0];
+    __syncthreads();
+  }
+  const int64_t share = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kMinShare));
+  const int64_t c0 = blockIdx.x * share, c1 = min(c0 + share, total);
+  if (threadIdx.x < 2) p.part_unit[blockIdx.x * 2 + threadIdx.x] = -1;
+  if (c0 >= c1) return;
+  if (elems <= kQ8Threads) {
+    if (upto > c0 && upto - mine <= c0) {
+      start_s[0] = threadIdx.x;
+      start_s[1] = upto - mine;
+    }
+  } else {
+    int64_t before = 0;
+    for (int64_t e0 = 0; e0 < elems; e0 += kQ8Threads) {
+      mine = tiles_of(e0 + threadIdx.x, false);
+      upto = before + block_scan(mine, sums[(e0 / kQ8Threads) & 1]);
+      if (upto > c0 && upto - mine <= c0) {
+        start_s[0] = e0 + threadIdx.x;
+        start_s[1] = upto - mine;
+      }
+      const bool found = __syncthreads_or(upto > c0);
+      if (found) break;
+      __syncthreads();
+      if (threadIdx.x == kQ8Threads - 1) sums[0][0] = upto;
+      __syncthreads();
+      before = sums[0][0];
+      __syncthreads();
+    }
+  }
+  __syncthreads();
+  Walk use;
+  use.b = static_cast<int>(p.sel_ids ? start_s[0] / p.num_kv_heads : start_s[0]);
+  use.h = static_cast<int>(p.sel_ids ? start_s[0] % p.num_kv_heads : 0);
+  use.base = start_s[1];
+  use.u = load_unit(p, use.b, use.h, false);
+  while (use.base + use.u.tiles <= c0) next_unit(p, use);
+  Walk ask = use;
+
+  uint8_t* ring = smem + warp * R::kWarp;
+  float* merge = reinterpret_cast<float*>(smem + kQ8Warps * R::kWarp);
+  PageCache pc;
+  pc.b = -1;
+  int64_t next = c0 + warp;                          // the next tile to ask for
+  int put = 0, get = 0;
+  auto ask_next = [&]() {
+    if (next < c1) {
+      while (ask.base + ask.u.tiles <= next) next_unit(p, ask);
+      issue_tile<D>(p, ask, next, pc, ring + put * R::kStage, &notes[warp][put]);
+      next += kQ8Warps;
+    }
+    cp_async_commit();
+    put = put + 1 == kStages ? 0 : put + 1;
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) ask_next();
+
+  Warp<NQ, C, D> w;
+  int64_t at = c0 + warp;
+  for (;;) {
+    const int64_t end = min(c1, use.base + use.u.tiles);
+    load_queries(p, use.b, use.h, w);
+    for (; at < end; at += kQ8Warps) {
+      cp_async_wait<kStages - 2>();
+      __syncwarp();
+      ask_next();
+      attend_tile(p, w, ring + get * R::kStage, notes[warp][get]);
+      get = get + 1 == kStages ? 0 : get + 1;
+      __syncwarp();
+    }
+    // merge the warps' results of this unit
+    const bool whole = use.base >= c0 && use.base + use.u.tiles <= c1;
+    const int slot = use.base < c0 ? 0 : 1;
+    const int64_t unit = static_cast<int64_t>(use.b) * p.num_kv_heads + use.h;
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float s = w.sum[i];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (g == 0) {
+        ml[warp][2 * t + i][0] = w.top[i] == -INFINITY ? -INFINITY : w.ref[i];
+        ml[warp][2 * t + i][1] = s;
+      }
+      const float back = 1.f / w.inv[i];
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        w.acc[j][i] *= back;
+        w.acc[j][2 + i] *= back;
+      }
+    }
+    // dimension D/8 g + 2j + r of the lane's D/8; a pass takes 8 of them from every lane
+#pragma unroll
+    for (int pass = 0; pass < D / kMergeDims; ++pass) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float* row = merge + (warp * kMaxGroup + 2 * t + i) * kMergeRow + g * 8;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          *reinterpret_cast<float4*>(row + 4 * j) =
+              make_float4(w.acc[4 * pass + 2 * j][i], w.acc[4 * pass + 2 * j][2 + i],
+                          w.acc[4 * pass + 2 * j + 1][i], w.acc[4 * pass + 2 * j + 1][2 + i]);
+      }
+      __syncthreads();
+      for (int e = threadIdx.x; e < G * kMergeDims; e += kQ8Threads) {
+        const int head = e / kMergeDims, col = e % kMergeDims;
+        const int dim = col / 8 * (D / 8) + 8 * pass + col % 8;
+        float top = -INFINITY, sum = 0.f, z = 0.f;
+#pragma unroll
+        for (int i = 0; i < kQ8Warps; ++i) top = fmaxf(top, ml[i][head][0]);
+        const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int i = 0; i < kQ8Warps; ++i) {
+          const float keep = ex2_approx(ml[i][head][0] - ref);
+          sum += merge[(i * kMaxGroup + head) * kMergeRow + col] * keep;
+          z += ml[i][head][1] * keep;
+        }
+        if (whole) {
+          p.out[(static_cast<int64_t>(use.b) * p.num_q_heads + use.h * G + head) * D + dim] =
+              z == 0.f ? 0.f : sum / z;
+        } else {
+          const int64_t part = static_cast<int64_t>(blockIdx.x * 2 + slot) * kMaxGroup + head;
+          p.part_acc[part * D + dim] = sum;
+          if (dim == 0) {
+            p.part_ml[part * 2] = top;
+            p.part_ml[part * 2 + 1] = z;
+          }
+        }
+      }
+      __syncthreads();
+    }
+    if (!whole && threadIdx.x == 0) p.part_unit[blockIdx.x * 2 + slot] = unit;
+    if (end >= c1) break;
+    do next_unit(p, use);
+    while (use.u.tiles == 0);
+  }
+}
+
+// One block per (unit, query head): adds the unit's partial results in the order of the line, a
+// warp each in turn.  Units without a tile get zeros here; those that one block finished have no
+// partial result.
+template <int D>
+__global__ void __launch_bounds__(kQ8Threads) q8_join_kernel(Q8AttendParams p, int blocks) {
+  constexpr int W = D / 32;                          // dimensions of a lane
   __shared__ float acc_s[kQ8Warps][D];
   __shared__ float ml_s[kQ8Warps][2];
-  grid_dependency_wait();
-  const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z, T = p.team_size;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int G = p.num_q_heads / p.num_kv_heads;
-  const int64_t unit = static_cast<int64_t>(b) * p.num_kv_heads + h;
-  float q[kMaxGroup][W], acc[kMaxGroup][W], m[kMaxGroup], l[kMaxGroup];
-#pragma unroll
-  for (int g = 0; g < kMaxGroup; ++g) {
-    m[g] = -INFINITY;
-    l[g] = 0.f;
-#pragma unroll
-    for (int e = 0; e < W; ++e) {
-      acc[g][e] = q[g][e] = 0.f;
-      if (g < G) {
-        const int64_t at = (static_cast<int64_t>(b) * p.num_q_heads + h * G + g) * D + lane * W + e;
-        q[g][e] = BF16 ? bf16_to_f32(static_cast<const uint16_t*>(p.q)[at])
-                       : static_cast<const float*>(p.q)[at];
-      }
-    }
-  }
-  Unit u;
-  const bool ok = load_unit(p, b, h, &u);
-  if (!ok && threadIdx.x == 0) set_status(p.status, SANTA_DEV_BAD_SEQLEN);
-  const int64_t n = !ok ? 0 : p.sel_ids ? static_cast<int64_t>(u.count) * T : u.len - u.lo;
-  const int64_t begin = n * split / p.splits, end = n * (split + 1) / p.splits;
-  for (int64_t i = begin + warp; i < end; i += kQ8Warps) {
-    int64_t t = u.lo + i;
-    float bias = 0.f;
-    if (p.sel_ids) {
-      const int64_t at = unit * p.num_draws + i / T;
-      const int64_t team = p.sel_ids[at];
-      const float pi = p.pi[at];
-      if (team < 0 || team * T >= u.len || !(pi > 0.f) || pi == INFINITY) {
-        set_status(p.status, SANTA_DEV_BAD_SEL);
-        continue;
-      }
-      t = team * T + i % T;
-      bias = -logf(pi);
-      if (t >= u.len || t < u.lo) continue;
-    }
-    const int64_t page = p.page_table[static_cast<int64_t>(b) * p.max_teams + t / T];
-    if (page < 0 || page >= p.num_pages) {
-      set_status(p.status, SANTA_DEV_BAD_PAGE);
-      continue;
-    }
-    const int64_t row = (page * p.num_kv_heads + h) * T + t % T;
-    float k[W], v[W];
-    load_row<C, W>(p.k, row, lane, k);
-    load_row<C, W>(p.v, row, lane, v);
-    const float ks = p.k_scale[row] * p.scale, vs = p.v_scale[row];
-#pragma unroll
-    for (int g = 0; g < kMaxGroup; ++g) {
-      if (g >= G) break;
-      float s = 0.f;
-#pragma unroll
-      for (int e = 0; e < W; ++e) s = fmaf(q[g][e], k[e], s);
-      s = warp_sum(s) * ks;
-      if (p.softcap > 0.f) s = p.softcap * tanhf(s / p.softcap);
-      s += bias;
-      const float top = fmaxf(m[g], s);
-      const float ref = top == -INFINITY ? 0.f : top;
-      const float keep = expf(m[g] - ref), w = expf(s - ref);
-      m[g] = top;
-      l[g] = l[g] * keep + w;
-#pragma unroll
-      for (int e = 0; e < W; ++e) acc[g][e] = acc[g][e] * keep + w * vs * v[e];
-    }
-  }
-#pragma unroll
-  for (int g = 0; g < kMaxGroup; ++g) {
-    if (g >= G) break;
-#pragma unroll
-    for (int e = 0; e < W; ++e) acc_s[warp][lane * W + e] = acc[g][e];
-    if (lane == 0) {
-      ml_s[warp][0] = m[g];
-      ml_s[warp][1] = l[g];
-    }
-    __syncthreads();
-    float* part = p.part + ((unit * p.splits + split) * G + g) * (D + 2);
-    if (threadIdx.x < D) {
-      float top = -INFINITY, sum = 0.f, z = 0.f;
-      for (int w = 0; w < kQ8Warps; ++w) top = fmaxf(top, ml_s[w][0]);
-      const float ref = top == -INFINITY ? 0.f : top;
-      for (int w = 0; w < kQ8Warps; ++w) {
-        const float keep = expf(ml_s[w][0] - ref);
-        sum += acc_s[w][threadIdx.x] * keep;
-        z += ml_s[w][1] * keep;
-      }
-      part[threadIdx.x] = sum;
-      if (threadIdx.x == 0) {
-        part[D] = top;
-        part[D + 1] = z;
-      }
-    }
-    __syncthreads();
-  }
-}
-
-// One block per (unit, query head), a thread per element.
-template <int D>
-__global__ void q8_join_kernel(Q8AttendParams p) {
-  grid_dependency_wait();
+  __shared__ int first_s, last_s;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = p.num_q_heads / p.num_kv_heads;
   const int64_t unit = blockIdx.x / G;
-  const int g = blockIdx.x % G;
-  const float* part = p.part + (unit * p.splits * G + g) * (D + 2);
-  const int64_t step = static_cast<int64_t>(G) * (D + 2);
-  float top = -INFINITY, sum = 0.f, z = 0.f;
-  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, part[s * step + D]);
-  const float ref = top == -INFINITY ? 0.f : top;
-  for (int s = 0; s < p.splits; ++s) {
-    const float keep = expf(part[s * step + D] - ref);
-    sum += part[s * step + threadIdx.x] * keep;
-    z += part[s * step + D + 1] * keep;
+  const int head = blockIdx.x % G;
+  const int b = static_cast<int>(unit / p.num_kv_heads), h = static_cast<int>(unit % p.num_kv_heads);
+  if (threadIdx.x == 0) {
+    first_s = INT32_MAX;
+    last_s = -1;
   }
-  const int64_t b = unit / p.num_kv_heads, h = unit % p.num_kv_heads;
-  p.out[(b * p.num_q_heads + h * G + g) * D + threadIdx.x] = z == 0.f ? 0.f : sum / z;
+  __syncthreads();
+  grid_dependency_wait();
+  const bool none = load_unit(p, b, h, false).tiles == 0;
+  for (int i = threadIdx.x; i < 2 * blocks; i += kQ8Threads)
+    if (p.part_unit[i] == unit) {
+      atomicMin(&first_s, i);
+      atomicMax(&last_s, i);
+    }
+  __syncthreads();
+  float* out = p.out + (static_cast<int64_t>(b) * p.num_q_heads + h * G + head) * D;
+  if (last_s < 0) {
+    if (none && threadIdx.x < D) out[threadIdx.x] = 0.f;
+    return;
+  }
+  // part 0 is the unit's first, in either slot of its block; the others continue it in slot 0
+  const int first = first_s, count = last_s / 2 - first / 2 + 1;
+  float m = -INFINITY, l = 0.f, acc[W];
+#pragma unroll
+  for (int e = 0; e < W; ++e) acc[e] = 0.f;
+  for (int k = warp; k < count; k += kQ8Warps) {
+    const int64_t part = static_cast<int64_t>(k == 0 ? first : 2 * (first / 2 + k)) * kMaxGroup + head;
+    const float pm = p.part_ml[part * 2], pl = p.part_ml[part * 2 + 1];
+    float x[W];
+#pragma unroll
+    for (int e = 0; e < W; ++e) x[e] = p.part_acc[part * D + lane * W + e];
+    const float top = fmaxf(m, pm), ref = top == -INFINITY ? 0.f : top;
+    const float keep = ex2_approx(m - ref), add = ex2_approx(pm - ref);
+    m = top;
+    l = l * keep + pl * add;
+#pragma unroll
+    for (int e = 0; e < W; ++e) acc[e] = acc[e] * keep + x[e] * add;
+  }
+#pragma unroll
+  for (int e = 0; e < W; ++e) acc_s[warp][lane * W + e] = acc[e];
+  if (lane == 0) {
+    ml_s[warp][0] = m;
+    ml_s[warp][1] = l;
+  }
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float top = -INFINITY, sum = 0.f, z = 0.f;
+#pragma unroll
+    for (int i = 0; i < kQ8Warps; ++i) top = fmaxf(top, ml_s[i][0]);
+    const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int i = 0; i < kQ8Warps; ++i) {
+      const float keep = ex2_approx(ml_s[i][0] - ref);
+      sum += acc_s[i][threadIdx.x] * keep;
+      z += ml_s[i][1] * keep;
+    }
+    out[threadIdx.x] = z == 0.f ? 0.f : sum / z;
+  }
 }
 
-template <bool BF16, int C, int D>
-cudaError_t launch_typed(const Q8AttendParams& p, cudaStream_t stream) {
+template <int NQ, int C, int D>
+cudaError_t launch_typed(const Q8AttendParams& p, int blocks, cudaStream_t stream) {
+  static std::atomic<unsigned long long> done{0};
+  auto* kernel = q8_attend_kernel<NQ, C, D>;
+  cudaError_t e = ensure_dynamic_smem(kernel, Ring<D>::kBytes, done);
+  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.splits, p.num_kv_heads, p.batch);
+  cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(kQ8Threads);
+  cfg.dynamicSmemBytes = Ring<D>::kBytes;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, q8_attend_kernel<BF16, C, D>, p);
-  if (e != cudaSuccess) return e;
+  if ((e = cudaLaunchKernelEx(&cfg, kernel, p)) != cudaSuccess) return e;
   cfg.gridDim = dim3(static_cast<unsigned>(p.batch * static_cast<int64_t>(p.num_q_heads)));
-  cfg.blockDim = dim3(D);
-  return cudaLaunchKernelEx(&cfg, q8_join_kernel<D>, p);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, q8_join_kernel<D>, p, blocks);
 }
 
-template <int C>
-cudaError_t launch_code(const Q8AttendParams& p, int d, bool bf16, cudaStream_t stream) {
-  if (bf16) return d == 128 ? launch_typed<true, C, 128>(p, stream) : launch_typed<true, C, 64>(p, stream);
-  return d == 128 ? launch_typed<false, C, 128>(p, stream) : launch_typed<false, C, 64>(p, stream);
+template <int NQ, int C>
+cudaError_t launch_code(const Q8AttendParams& p, int d, int blocks, cudaStream_t stream) {
+  return d == 128 ? launch_typed<NQ, C, 128>(p, blocks, stream)
+                  : launch_typed<NQ, C, 64>(p, blocks, stream);
 }
 
 }  // namespace
 
-int q8_attend_splits(int64_t units, int64_t max_tokens, int sms) {
-  const int64_t want = (4ll * sms + units - 1) / units, most = (max_tokens + 63) / 64;
-  return static_cast<int>(std::max<int64_t>(1, std::min(want, most)));
-}
-
-cudaError_t launch_q8_attend(const Q8AttendParams& p, int head_dim, bool bf16, int code,
+cudaError_t launch_q8_attend(const Q8AttendParams& p, int head_dim, bool bf16, int code, int sms,
                              cudaStream_t stream) {
-  return code == kCodeI8 ? launch_code<kCodeI8>(p, head_dim, bf16, stream)
-                         : launch_code<kCodeE4M3>(p, head_dim, bf16, stream);
+  if (code == kCodeI8)
+    return bf16 ? launch_code<1, kCodeI8>(p, head_dim, sms, stream)
+                : launch_code<2, kCodeI8>(p, head_dim, sms, stream);
+  return bf16 ? launch_code<1, kCodeE4M3>(p, head_dim, sms, stream)
+              : launch_code<2, kCodeE4M3>(p, head_dim, sms, stream);
 }
 
 }  // namespace santa

@@ -152,8 +152,10 @@ struct Q8AttendParams {
   float scale;                // 1 / sqrt(d)
   float softcap;              // 0: none
   int window;                 // 0: none
-  // partial results, two slots of each block: of which unit (-1: none), accumulators, (m, l)
-  int64_t* part_unit;         // [blocks][2]
+  // of each block: the unit that starts there and ends elsewhere (-1: none) with its parts; two slots
+  // of partial results (a unit that goes on from the block before, one that starts): accumulators, (m, l)
+  int64_t* split_unit;        // [blocks]
+  int32_t* split_parts;       // [blocks]
   float* part_acc;            // [blocks][2][kMaxGroup][d]
   float* part_ml;             // [blocks][2][kMaxGroup][2]
   float* out;                 // [B][Hq][d]

@@ -48,7 +48,7 @@ int q8_layout(int d, Q8Layout* l) {
   l->sms = santa::device_sms();
   if (l->sms <= 0) return SANTA_ERR_CUDA;
   const size_t parts = static_cast<size_t>(l->sms) * 2;
-  l->unit_bytes = round_up(parts * sizeof(int64_t), kAlign);
+  l->unit_bytes = round_up(l->sms * (sizeof(int64_t) + sizeof(int32_t)), kAlign);
   l->ml_bytes = round_up(parts * santa::kMaxGroup * 2 * sizeof(float), kAlign);
   l->bytes = kAlign + l->unit_bytes + l->ml_bytes + parts * santa::kMaxGroup * d * sizeof(float);
   return SANTA_OK;
@@ -127,7 +127,8 @@ int launch_q8(const santa_decode_args* a, const santa_q8_args* c, bool listed, v
   p.window = c->window;
   unsigned char* base = reinterpret_cast<unsigned char*>(
       round_up(reinterpret_cast<uintptr_t>(a->workspace), kAlign));
-  p.part_unit = reinterpret_cast<int64_t*>(base);
+  p.split_unit = reinterpret_cast<int64_t*>(base);
+  p.split_parts = reinterpret_cast<int32_t*>(p.split_unit + l.sms);
   p.part_ml = reinterpret_cast<float*>(base + l.unit_bytes);
   p.part_acc = reinterpret_cast<float*>(base + l.unit_bytes + l.ml_bytes);
   p.out = a->out;

@@ -41,12 +41,14 @@ namespace santa {
 namespace {
 
 constexpr int kTile = 32;                  // tokens of a tile
-constexpr int kQ8Threads = 256;
-constexpr int kQ8Warps = kQ8Threads / 32;
+constexpr int kQ8Warps = 8;
+constexpr int kQ8Threads = kQ8Warps * 32;
 constexpr int kStages = 3;                 // tiles of a warp's ring
 constexpr int kMinShare = kQ8Warps;        // tiles of a block's part: at least one for each warp
+constexpr int kScanRounds = 8;             // 32 sequences or units each that a warp reads by itself
 constexpr int kMergeDims = 64;             // dimensions that one merging pass takes
 constexpr int kMergeRow = kMergeDims + 4;
+constexpr float kNoScore = -1e38f;         // a reference before the first score
 constexpr float kSlack = 8.f;              // how far a score may pass the reference (base 2)
 constexpr float kTopWeight = 256.f;        // the same for a weight
 
@@ -72,6 +74,9 @@ __device__ __forceinline__ int piece_at(int r, int chunk) {
   }
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async16_fill(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
                : "memory");
@@ -103,6 +108,11 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// The leading 11 bits of x (fp16 holds them from 2^-14 on; below, it rounds at 2^-25).
+__device__ __forceinline__ float cut_f16(float x) {
+  return __uint_as_float(__float_as_uint(x) & 0xffffe000u);
+}
+
 // The two code pairs of a word, bytes (0, 1) and (2, 3), as fp16.  int8: with its sign bit turned
 // a code is u = code + 128, 0x6400 | u is 1024 + u, and 1152 less is the code; exact.
 template <int C>
@@ -121,7 +131,7 @@ __device__ __forceinline__ void pairs_to_f16(uint32_t w, uint32_t& lo, uint32_t&
 
 // A unit's tokens: positions lo .. len - 1 (dense), or `count` listed teams; `tiles` on the line.
 struct Unit {
-  int64_t len, lo;
+  int len, lo;         // at most 2^14 pages of 2^7 tokens
   int count;
   int64_t tiles;
 };
@@ -131,7 +141,7 @@ __device__ __forceinline__ Unit load_unit(const Q8AttendParams& p, int b, int h,
   Unit u;
   u.len = p.seq_lens[b];
   u.count = 0;
-  if (u.len < 0 || u.len > static_cast<int64_t>(p.max_teams) * p.team_size) {
+  if (u.len < 0 || u.len > p.max_teams * p.team_size) {
     if (tell) set_status(p.status, SANTA_DEV_BAD_SEQLEN);
     u.len = 0;
   }
@@ -203,7 +213,7 @@ struct Warp {
   static constexpr int kOut = D / 16;                // 16-dimension tiles of the output
   uint32_t q[NQ][kSteps][2];
   float acc[kOut][4];
-  float ref[2], top[2];      // of heads 2t and 2t + 1: reference, and the score that raises it
+  float ref[2];              // of heads 2t and 2t + 1: reference of the exponentials
   float sum[2];              // this lane's share of the sum of weights
   float big[2], inv[2];      // largest |p vs| (at least), and the power of two that scales weights
   float qs[2];               // score of a unit product, base 2 (or over the cap)
@@ -215,25 +225,25 @@ template <int D>
 __device__ __forceinline__ void issue_tile(const Q8AttendParams& p, const Walk& w, int64_t t,
                                            PageCache& pc, uint8_t* stage, int2* note) {
   const int lane = threadIdx.x & 31;
-  const int T = p.team_size, per = T / kTile;
-  const int64_t i = t - w.base;                      // tile of the unit
-  const int64_t at = p.sel_ids ? i / per : (w.u.lo / kTile + i) / per;     // slot or team
-  const int row = static_cast<int>(p.sel_ids ? i % per : (w.u.lo / kTile + i) % per) * kTile;
-  if (pc.b != w.b || (p.sel_ids && pc.h != w.h) || at < pc.first || at >= pc.first + 32) {
+  const int T = p.team_size, per = T == 128 ? 2 : 1;  // log2 of a page's tiles
+  // tile of the unit, or of the sequence (at most 2^16 of them); then slot or team, and row in it
+  const int i = static_cast<int>(t - w.base) + (p.sel_ids ? 0 : w.u.lo / kTile);
+  const int at = i >> per, row = (i & ((1 << per) - 1)) * kTile;
+  if (__builtin_expect(pc.b != w.b || (p.sel_ids && pc.h != w.h) || at < pc.first || at >= pc.first + 32, 0)) {
     pc.b = w.b;
     pc.h = w.h;
-    pc.first = static_cast<int>(at);
-    const int64_t mine = at + lane;
+    pc.first = at;
+    const int mine = at + lane;
     pc.bias = 0.f;
     pc.page = -1;
     pc.team = -1;
     if (!p.sel_ids) {
-      if (mine * T < w.u.len) pc.team = static_cast<int>(mine);
+      if (mine * T < w.u.len) pc.team = mine;
     } else if (mine < w.u.count) {
       const int64_t slot = (static_cast<int64_t>(w.b) * p.num_kv_heads + w.h) * p.num_draws + mine;
       const int team = p.sel_ids[slot];
       const float pi = p.pi[slot];
-      if (team >= 0 && static_cast<int64_t>(team) * T < w.u.len && pi > 0.f && pi < INFINITY) {
+      if (team >= 0 && team < p.max_teams && team * T < w.u.len && pi > 0.f && pi < INFINITY) {
         pc.team = team;
         pc.bias = -log2f(pi);
       } else {
@@ -248,31 +258,40 @@ __device__ __forceinline__ void issue_tile(const Q8AttendParams& p, const Walk& 
       }
     }
   }
-  const int from = static_cast<int>(at - pc.first);
+  const int from = at - pc.first;
   const int team = __shfl_sync(0xffffffffu, pc.team, from);
   const int page = __shfl_sync(0xffffffffu, pc.page, from);
   const float bias = __shfl_sync(0xffffffffu, pc.bias, from);
-  const int64_t t0 = static_cast<int64_t>(team) * T + row;
-  int n0 = static_cast<int>(min(max(w.u.lo - t0, int64_t(0)), int64_t(kTile)));
-  int n1 = static_cast<int>(min(max(w.u.len - t0, int64_t(0)), int64_t(kTile)));
+  const int t0 = team * T + row;
+  int n0 = min(max(w.u.lo - t0, 0), kTile);
+  int n1 = min(max(w.u.len - t0, 0), kTile);
   if (page < 0 || n0 >= n1) n0 = n1 = 0;
   if (lane == 0) *note = make_int2(n0 | n1 << 16, __float_as_int(bias));
   if (n1 > 0) {
     constexpr int kCols = D / 16, kRows = 32 / kCols;   // pieces of a row; rows per round
     const int64_t first = (static_cast<int64_t>(page) * p.num_kv_heads + w.h) * T + row;
-    const uint8_t* k = static_cast<const uint8_t*>(p.k) + first * D;
-    const uint8_t* v = static_cast<const uint8_t*>(p.v) + first * D;
+    const int r0 = lane / kCols, chunk = lane % kCols;
+    const uint8_t* k = static_cast<const uint8_t*>(p.k) + first * D + lane * 16;
+    const uint8_t* v = static_cast<const uint8_t*>(p.v) + first * D + lane * 16;
     const uint32_t to = smem_u32(stage);
+    if (__builtin_expect(n0 == 0 && n1 == kTile, 1)) {
 #pragma unroll
-    for (int e = 0; e < kTile / kRows; ++e) {
-      const int r = e * kRows + lane / kCols, chunk = lane % kCols;
-      const bool on = r >= n0 && r < n1;              // rows that are not seen become zeros
-      cp_async16_fill(to + piece_at<D>(r, chunk), k + r * D + chunk * 16, on);
-      cp_async16_fill(to + kTile * D + piece_at<D>(r, chunk), v + r * D + chunk * 16, on);
+      for (int e = 0; e < kTile / kRows; ++e) {
+        cp_async16(to + piece_at<D>(e * kRows + r0, chunk), k + e * 512);
+        cp_async16(to + kTile * D + piece_at<D>(e * kRows + r0, chunk), v + e * 512);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kTile / kRows; ++e) {
+        const int r = e * kRows + r0;
+        const bool on = r >= n0 && r < n1;              // rows that are not seen become zeros
+        cp_async16_fill(to + piece_at<D>(r, chunk), k + e * 512, on);
+        cp_async16_fill(to + kTile * D + piece_at<D>(r, chunk), v + e * 512, on);
+      }
     }
     if (lane < 2 * kTile / 4) {
       const float* s = (lane < kTile / 4 ? p.k_scale : p.v_scale) + first + lane % (kTile / 4) * 4;
-      cp_async16_fill(to + 2 * kTile * D + lane * 16, s, true);
+      cp_async16(to + 2 * kTile * D + lane * 16, s);
     }
   }
 }
@@ -327,8 +346,7 @@ __device__ void load_queries(const Q8AttendParams& p, int b, int h, Warp<NQ, C, 
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     w.qs[i] = __shfl_sync(0xffffffffu, f, (2 * t + i) * 4);
-    w.ref[i] = 0.f;
-    w.top[i] = -INFINITY;
+    w.ref[i] = kNoScore;
     w.sum[i] = w.big[i] = 0.f;
     w.inv[i] = 1.f;
   }
@@ -338,8 +356,8 @@ __device__ void load_queries(const Q8AttendParams& p, int b, int h, Warp<NQ, C, 
     for (int i = 0; i < 4; ++i) w.acc[j][i] = 0.f;
 }
 
-// Raises the references to this tile's largest score and weight: x[4 m + 2 r + i] is the score of token
-// 16 m + 8 r + lane / 4 and head 2 t + i, vs[2 m + r] the token's value scale.
+// Raises the references to this tile's largest score and weight: x[2 k + i] is the score of token
+// 8 k + lane / 4 and head 2 t + i, vs[k] the token's value scale.
 template <int NQ, int C, int D>
 __device__ __forceinline__ void raise(Warp<NQ, C, D>& w, const float (&x)[8], const float (&vs)[4]) {
 #pragma unroll
@@ -347,13 +365,9 @@ __device__ __forceinline__ void raise(Warp<NQ, C, D>& w, const float (&x)[8], co
     float top = fmaxf(fmaxf(x[i], x[2 + i]), fmaxf(x[4 + i], x[6 + i]));
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const bool fresh = w.top[i] == -INFINITY;
-    float keep = 1.f;
-    if (top != -INFINITY && (fresh || top > w.ref[i])) {
-      keep = fresh ? 0.f : ex2_approx(w.ref[i] - top);
-      w.ref[i] = top;
-      w.top[i] = top + kSlack;
-    }
+    const bool up = top > w.ref[i];
+    const float keep = up ? ex2_approx(w.ref[i] - top) : 1.f;
+    if (up) w.ref[i] = top;
     float big = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) big = fmaxf(big, fabsf(ex2_approx(x[2 * k + i] - w.ref[i]) * vs[k]));
@@ -368,12 +382,10 @@ __device__ __forceinline__ void raise(Warp<NQ, C, D>& w, const float (&x)[8], co
     const float f = keep * __uint_as_float(static_cast<uint32_t>(min(max(d, -126), 127) + 127) << 23);
     w.inv[i] = inv;
     w.sum[i] *= keep;
-    if (f != 1.f) {
 #pragma unroll
-      for (int j = 0; j < D / 16; ++j) {
-        w.acc[j][i] *= f;
-        w.acc[j][2 + i] *= f;
-      }
+    for (int j = 0; j < D / 16; ++j) {
+      w.acc[j][i] *= f;
+      w.acc[j][2 + i] *= f;
     }
   }
 }
@@ -385,7 +397,7 @@ __device__ __forceinline__ void attend_tile(const Q8AttendParams& p, Warp<NQ, C,
   const float* scales = reinterpret_cast<const float*>(stage + 2 * kTile * D);
   const int n0 = note.x & 0xffff, n1 = note.x >> 16;
   if (n1 == 0) return;
-  float x[8], vs[4];
+  float x[8], ks[4], vs[4];                          // token 8 k + g; score 2 k + i: head 2 t + i
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
     float c[4] = {0.f, 0.f, 0.f, 0.f};
@@ -405,47 +417,53 @@ __device__ __forceinline__ void attend_tile(const Q8AttendParams& p, Warp<NQ, C,
     }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int tok = 16 * m + 8 * r + g;
-      const float ks = scales[tok];
-      vs[2 * m + r] = scales[kTile + tok];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) x[4 * m + 2 * r + i] = c[2 * r + i] * ks * w.qs[i];
+      ks[2 * m + r] = scales[16 * m + 8 * r + g];
+      vs[2 * m + r] = scales[kTile + 16 * m + 8 * r + g];
+      x[4 * m + 2 * r] = c[2 * r];
+      x[4 * m + 2 * r + 1] = c[2 * r + 1];
     }
   }
-  if (p.softcap > 0.f) {
-    const float cap = p.softcap * 1.4426950408889634f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = cap * tanhf(x[i]);
-  }
-  const float bias = __int_as_float(note.y);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] += bias;
-  if (n0 > 0 || n1 < kTile) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int tok = 8 * k + g;
-      if (tok < n0 || tok >= n1) {
-        x[2 * k] = x[2 * k + 1] = -INFINITY;
-        vs[k] = 0.f;
-      }
-    }
-  }
-  float e[8], pw[8];
-  auto weigh = [&]() {
+  const bool part = n0 > 0 || n1 < kTile;
+  if (__builtin_expect(part, 0)) {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
+      if (8 * k + g < n0 || 8 * k + g >= n1) vs[k] = 0.f;
+  }
+  // differences from the reference, one rounding each
+  const float bias = __int_as_float(note.y);
+  float y[8], e[8], pw[8];
+  auto scores = [&](float r0, float r1) {
+    const float off[2] = {bias - r0, bias - r1};
+    if (__builtin_expect(p.softcap > 0.f, 0)) {
+      const float cap = p.softcap * 1.4426950408889634f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        e[2 * k + i] = ex2_approx(x[2 * k + i] - w.ref[i]);
-        pw[2 * k + i] = e[2 * k + i] * vs[k] * w.inv[i];
-      }
+      for (int i = 0; i < 8; ++i) y[i] = fmaf(cap, tanhf(x[i] * (ks[i >> 1] * w.qs[i & 1])), off[i & 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i], ks[i >> 1] * w.qs[i & 1], off[i & 1]);
+    }
+    if (__builtin_expect(part, 0)) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (8 * (i >> 1) + g < n0 || 8 * (i >> 1) + g >= n1) y[i] = -INFINITY;
+    }
   };
+  auto weigh = [&]() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      e[i] = ex2_approx(y[i]);
+      pw[i] = e[i] * vs[i >> 1] * w.inv[i & 1];
+    }
+  };
+  scores(w.ref[0], w.ref[1]);
   weigh();
   bool over = false;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) over |= x[i] > w.top[i & 1] || fabsf(pw[i]) > kTopWeight;
-  if (__any_sync(0xffffffffu, over)) {
-    raise(w, x, vs);
+  for (int i = 0; i < 8; ++i) over |= y[i] > kSlack || fabsf(pw[i]) > kTopWeight;
+  if (__builtin_expect(__any_sync(0xffffffffu, over), 0)) {
+    scores(0.f, 0.f);
+    raise(w, y, vs);
+    scores(w.ref[0], w.ref[1]);
     weigh();
   }
   uint32_t hi[4], lo[4];
@@ -453,9 +471,10 @@ __device__ __forceinline__ void attend_tile(const Q8AttendParams& p, Warp<NQ, C,
   for (int k = 0; k < 4; ++k) {
     w.sum[0] += e[2 * k];
     w.sum[1] += e[2 * k + 1];
-    hi[k] = pack_f16(pw[2 * k], pw[2 * k + 1]);
-    const float2 got = f16x2_to_f32(hi[k]);
-    lo[k] = pack_f16(pw[2 * k] - got.x, pw[2 * k + 1] - got.y);
+    // the first piece is cut, not rounded: what it leaves out is then exact in fp32 at once
+    const float a = cut_f16(pw[2 * k]), b = cut_f16(pw[2 * k + 1]);
+    hi[k] = pack_f16(a, b);
+    lo[k] = pack_f16(pw[2 * k] - a, pw[2 * k + 1] - b);
     hi[k] = movmatrix_trans(hi[k]);
     lo[k] = movmatrix_trans(lo[k]);
   }
@@ -523,47 +542,85 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
     return load_unit(p, b, static_cast<int>(e - static_cast<int64_t>(b) * p.num_kv_heads), tell).tiles *
            heads;
   };
-  int64_t total = 0, mine = 0, upto = 0;
-  for (int64_t e0 = 0; e0 < elems; e0 += kQ8Threads) {
-    mine = tiles_of(e0 + threadIdx.x, blockIdx.x == 0);
-    upto = total + block_scan(mine, sums[(e0 / kQ8Threads) & 1]);
-    if (threadIdx.x == kQ8Threads - 1) start_s[0] = upto;
-    __syncthreads();
-    total = start_s[0];
-    __syncthreads();
-  }
-  const int64_t share = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kMinShare));
-  const int64_t c0 = blockIdx.x * share, c1 = min(c0 + share, total);
-  if (threadIdx.x < 2) p.part_unit[blockIdx.x * 2 + threadIdx.x] = -1;
-  if (c0 >= c1) return;
-  if (elems <= kQ8Threads) {
-    if (upto > c0 && upto - mine <= c0) {
-      start_s[0] = threadIdx.x;
-      start_s[1] = upto - mine;
+  const bool tell = blockIdx.x == 0;
+  int64_t total = 0, share, c0, elem = 0, elem_base = 0;
+  auto split = [&]() {
+    share = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kMinShare));
+    c0 = blockIdx.x * share;
+  };
+  if (elems <= 32 * kScanRounds) {
+    // every warp for itself, without a barrier
+    int64_t v[kScanRounds], upto[kScanRounds];
+#pragma unroll
+    for (int i = 0; i < kScanRounds; ++i) v[i] = tiles_of(32 * i + lane, tell && warp == 0);
+#pragma unroll
+    for (int i = 0; i < kScanRounds; ++i) {
+      upto[i] = v[i];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, upto[i], o);
+        if (lane >= o) upto[i] += up;
+      }
+      upto[i] += total;
+      total = __shfl_sync(0xffffffffu, upto[i], 31);
+    }
+    split();
+#pragma unroll
+    for (int i = 0; i < kScanRounds; ++i) {
+      const unsigned hit = __ballot_sync(0xffffffffu, upto[i] > c0 && upto[i] - v[i] <= c0);
+      if (hit) {
+        elem = 32 * i + __ffs(hit) - 1;
+        elem_base = __shfl_sync(0xffffffffu, upto[i] - v[i], __ffs(hit) - 1);
+      }
     }
   } else {
-    int64_t before = 0;
     for (int64_t e0 = 0; e0 < elems; e0 += kQ8Threads) {
-      mine = tiles_of(e0 + threadIdx.x, false);
-      upto = before + block_scan(mine, sums[(e0 / kQ8Threads) & 1]);
+      const int64_t upto =
+          total + block_scan(tiles_of(e0 + threadIdx.x, tell), sums[(e0 / kQ8Threads) & 1]);
+      if (threadIdx.x == kQ8Threads - 1) start_s[0] = upto;
+      __syncthreads();
+      total = start_s[0];
+      __syncthreads();
+    }
+    split();
+    int64_t before = 0;
+    for (int64_t e0 = 0; e0 < elems && c0 < total; e0 += kQ8Threads) {
+      const int64_t mine = tiles_of(e0 + threadIdx.x, false);
+      const int64_t upto = before + block_scan(mine, sums[(e0 / kQ8Threads) & 1]);
       if (upto > c0 && upto - mine <= c0) {
         start_s[0] = e0 + threadIdx.x;
         start_s[1] = upto - mine;
       }
-      const bool found = __syncthreads_or(upto > c0);
-      if (found) break;
-      __syncthreads();
+      if (__syncthreads_or(upto > c0)) break;
       if (threadIdx.x == kQ8Threads - 1) sums[0][0] = upto;
       __syncthreads();
       before = sums[0][0];
       __syncthreads();
     }
+    __syncthreads();
+    elem = start_s[0];
+    elem_base = start_s[1];
   }
-  __syncthreads();
+  const int64_t c1 = min(c0 + share, total);
+  int64_t split_unit = -1;                           // a unit that starts here and ends elsewhere
+  int split_parts = 0;
+  // units that see nothing
+  auto zero_units = [&]() {
+    for (int64_t e = blockIdx.x; e < elems; e += gridDim.x) {
+      if (tiles_of(e, false)) continue;
+      float* row = p.out + e * heads * G * D;
+      for (int i = threadIdx.x; i < heads * G * D; i += kQ8Threads) row[i] = 0.f;
+    }
+  };
+  if (c0 >= c1) {
+    zero_units();
+    if (threadIdx.x == 0) p.split_unit[blockIdx.x] = -1;
+    return;
+  }
   Walk use;
-  use.b = static_cast<int>(p.sel_ids ? start_s[0] / p.num_kv_heads : start_s[0]);
-  use.h = static_cast<int>(p.sel_ids ? start_s[0] % p.num_kv_heads : 0);
-  use.base = start_s[1];
+  use.b = static_cast<int>(p.sel_ids ? elem / p.num_kv_heads : elem);
+  use.h = static_cast<int>(p.sel_ids ? elem % p.num_kv_heads : 0);
+  use.base = elem_base;
   use.u = load_unit(p, use.b, use.h, false);
   while (use.base + use.u.tiles <= c0) next_unit(p, use);
   Walk ask = use;
@@ -585,6 +642,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
   };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) ask_next();
+  zero_units();
 
   Warp<NQ, C, D> w;
   int64_t at = c0 + warp;
@@ -601,8 +659,11 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
     }
     // merge the warps' results of this unit
     const bool whole = use.base >= c0 && use.base + use.u.tiles <= c1;
-    const int slot = use.base < c0 ? 0 : 1;
-    const int64_t unit = static_cast<int64_t>(use.b) * p.num_kv_heads + use.h;
+    const int slot = use.base < c0 ? 0 : 1;          // goes on from the block before, or starts here
+    if (!whole && slot == 1) {
+      split_unit = static_cast<int64_t>(use.b) * p.num_kv_heads + use.h;
+      split_parts = static_cast<int>((use.base + use.u.tiles - 1) / share) - blockIdx.x + 1;
+    }
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -610,7 +671,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       if (g == 0) {
-        ml[warp][2 * t + i][0] = w.top[i] == -INFINITY ? -INFINITY : w.ref[i];
+        ml[warp][2 * t + i][0] = w.ref[i];
         ml[warp][2 * t + i][1] = s;
       }
       const float back = 1.f / w.inv[i];
@@ -620,22 +681,24 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
         w.acc[j][2 + i] *= back;
       }
     }
-    // dimension D/8 g + 2j + r of the lane's D/8; a pass takes 8 of them from every lane
+    // dimension D/8 g + 2j + r of the lane's D/8; a pass takes kLane of them from every lane
+    constexpr int kLane = kMergeDims / 8;
 #pragma unroll
     for (int pass = 0; pass < D / kMergeDims; ++pass) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float* row = merge + (warp * kMaxGroup + 2 * t + i) * kMergeRow + g * 8;
+        float* row = merge + (warp * kMaxGroup + 2 * t + i) * kMergeRow + g * kLane;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < kLane / 4; ++j) {
+          const int o = pass * kLane / 2 + 2 * j;
           *reinterpret_cast<float4*>(row + 4 * j) =
-              make_float4(w.acc[4 * pass + 2 * j][i], w.acc[4 * pass + 2 * j][2 + i],
-                          w.acc[4 * pass + 2 * j + 1][i], w.acc[4 * pass + 2 * j + 1][2 + i]);
+              make_float4(w.acc[o][i], w.acc[o][2 + i], w.acc[o + 1][i], w.acc[o + 1][2 + i]);
+        }
       }
       __syncthreads();
       for (int e = threadIdx.x; e < G * kMergeDims; e += kQ8Threads) {
         const int head = e / kMergeDims, col = e % kMergeDims;
-        const int dim = col / 8 * (D / 8) + 8 * pass + col % 8;
+        const int dim = col / kLane * (D / 8) + kLane * pass + col % kLane;
         float top = -INFINITY, sum = 0.f, z = 0.f;
 #pragma unroll
         for (int i = 0; i < kQ8Warps; ++i) top = fmaxf(top, ml[i][head][0]);
@@ -660,52 +723,38 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
       }
       __syncthreads();
     }
-    if (!whole && threadIdx.x == 0) p.part_unit[blockIdx.x * 2 + slot] = unit;
     if (end >= c1) break;
     do next_unit(p, use);
     while (use.u.tiles == 0);
   }
+  if (threadIdx.x == 0) {
+    p.split_unit[blockIdx.x] = split_unit;
+    p.split_parts[blockIdx.x] = split_parts;
+  }
 }
 
-// One block per (unit, query head): adds the unit's partial results in the order of the line, a
-// warp each in turn.  Units without a tile get zeros here; those that one block finished have no
-// partial result.
+// One block per (block of the first launch, query head of a group): joins the unit that starts there and
+// ends elsewhere, if there is one, by adding its partial results in the order of the line, a warp each
+// in turn.
 template <int D>
-__global__ void __launch_bounds__(kQ8Threads) q8_join_kernel(Q8AttendParams p, int blocks) {
+__global__ void __launch_bounds__(kQ8Threads) q8_join_kernel(Q8AttendParams p) {
   constexpr int W = D / 32;                          // dimensions of a lane
   __shared__ float acc_s[kQ8Warps][D];
   __shared__ float ml_s[kQ8Warps][2];
-  __shared__ int first_s, last_s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = p.num_q_heads / p.num_kv_heads;
-  const int64_t unit = blockIdx.x / G;
-  const int head = blockIdx.x % G;
-  const int b = static_cast<int>(unit / p.num_kv_heads), h = static_cast<int>(unit % p.num_kv_heads);
-  if (threadIdx.x == 0) {
-    first_s = INT32_MAX;
-    last_s = -1;
-  }
-  __syncthreads();
+  const int block = blockIdx.x / G, head = blockIdx.x % G;
   grid_dependency_wait();
-  const bool none = load_unit(p, b, h, false).tiles == 0;
-  for (int i = threadIdx.x; i < 2 * blocks; i += kQ8Threads)
-    if (p.part_unit[i] == unit) {
-      atomicMin(&first_s, i);
-      atomicMax(&last_s, i);
-    }
-  __syncthreads();
-  float* out = p.out + (static_cast<int64_t>(b) * p.num_q_heads + h * G + head) * D;
-  if (last_s < 0) {
-    if (none && threadIdx.x < D) out[threadIdx.x] = 0.f;
-    return;
-  }
-  // part 0 is the unit's first, in either slot of its block; the others continue it in slot 0
-  const int first = first_s, count = last_s / 2 - first / 2 + 1;
+  const int64_t unit = p.split_unit[block];
+  if (unit < 0) return;
+  const int count = p.split_parts[block];
+  float* out = p.out + (unit * G + head) * D;
   float m = -INFINITY, l = 0.f, acc[W];
 #pragma unroll
   for (int e = 0; e < W; ++e) acc[e] = 0.f;
   for (int k = warp; k < count; k += kQ8Warps) {
-    const int64_t part = static_cast<int64_t>(k == 0 ? first : 2 * (first / 2 + k)) * kMaxGroup + head;
+    // the first part is the second slot of its block, the others the first slots of theirs
+    const int64_t part = static_cast<int64_t>(2 * (block + k) + (k == 0)) * kMaxGroup + head;
     const float pm = p.part_ml[part * 2], pl = p.part_ml[part * 2 + 1];
     float x[W];
 #pragma unroll
@@ -756,9 +805,9 @@ cudaError_t launch_typed(const Q8AttendParams& p, int blocks, cudaStream_t strea
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, kernel, p)) != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(p.batch * static_cast<int64_t>(p.num_q_heads)));
+  cfg.gridDim = dim3(blocks * (p.num_q_heads / p.num_kv_heads));
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, q8_join_kernel<D>, p, blocks);
+  return cudaLaunchKernelEx(&cfg, q8_join_kernel<D>, p);
 }
 
 template <int NQ, int C>

@@ -152,15 +152,18 @@ struct Q8AttendParams {
   float scale;                // 1 / sqrt(d)
   float softcap;              // 0: none
   int window;                 // 0: none
-  // of each block: the unit that starts there and ends elsewhere (-1: none) with its parts; two slots
-  // of partial results (a unit that goes on from the block before, one that starts): accumulators, (m, l)
+  bool short_line;            // few units and tiles (set by the launcher)
+  // per block (one per multiprocessor): the unit that begins there and ends elsewhere (-1: none) with the
+  // number of its parts; two parts, sums and (reference, sum of weights); per warp a piece
   int64_t* split_unit;        // [blocks]
   int32_t* split_parts;       // [blocks]
   float* part_acc;            // [blocks][2][kMaxGroup][d]
   float* part_ml;             // [blocks][2][kMaxGroup][2]
+  float* piece;               // [blocks][q8_attend_warps()][kMaxGroup][d]
   float* out;                 // [B][Hq][d]
   int32_t* status;
 };
+int q8_attend_warps();
 // One block per multiprocessor; two launches.
 cudaError_t launch_q8_attend(const Q8AttendParams& p, int head_dim, bool bf16, int code, int sms,
                              cudaStream_t stream);

@@ -39,18 +39,20 @@ int check_q8_shape(int batch, int hq, int hkv, int d, int T, int max_teams) {
   return rc ? rc : check_heads(hq, hkv);
 }
 
-// Workspace of an attention: the blocks' partial results (see Q8AttendParams).
+// Workspace of an attention (see Q8AttendParams): split units, parts, pieces.
 struct Q8Layout {
   int sms;
-  size_t unit_bytes, ml_bytes, bytes;
+  size_t split_bytes, ml_bytes, acc_bytes, bytes;
 };
 int q8_layout(int d, Q8Layout* l) {
   l->sms = santa::device_sms();
   if (l->sms <= 0) return SANTA_ERR_CUDA;
-  const size_t parts = static_cast<size_t>(l->sms) * 2;
-  l->unit_bytes = round_up(l->sms * (sizeof(int64_t) + sizeof(int32_t)), kAlign);
-  l->ml_bytes = round_up(parts * santa::kMaxGroup * 2 * sizeof(float), kAlign);
-  l->bytes = kAlign + l->unit_bytes + l->ml_bytes + parts * santa::kMaxGroup * d * sizeof(float);
+  const size_t rows = static_cast<size_t>(l->sms) * santa::kMaxGroup;
+  l->split_bytes = round_up(l->sms * (sizeof(int64_t) + sizeof(int32_t)), kAlign);
+  l->ml_bytes = round_up(2 * rows * 2 * sizeof(float), kAlign);
+  l->acc_bytes = 2 * rows * d * sizeof(float);
+  l->bytes = kAlign + l->split_bytes + l->ml_bytes + l->acc_bytes +
+             santa::q8_attend_warps() * rows * d * sizeof(float);
   return SANTA_OK;
 }
 
@@ -129,8 +131,9 @@ int launch_q8(const santa_decode_args* a, const santa_q8_args* c, bool listed, v
       round_up(reinterpret_cast<uintptr_t>(a->workspace), kAlign));
   p.split_unit = reinterpret_cast<int64_t*>(base);
   p.split_parts = reinterpret_cast<int32_t*>(p.split_unit + l.sms);
-  p.part_ml = reinterpret_cast<float*>(base + l.unit_bytes);
-  p.part_acc = reinterpret_cast<float*>(base + l.unit_bytes + l.ml_bytes);
+  p.part_ml = reinterpret_cast<float*>(base += l.split_bytes);
+  p.part_acc = reinterpret_cast<float*>(base += l.ml_bytes);
+  p.piece = reinterpret_cast<float*>(base + l.acc_bytes);
   p.out = a->out;
   p.status = a->device_status;
   return map_cuda(santa::launch_q8_attend(p, a->head_dim, a->dtype == SANTA_BF16, code, l.sms,

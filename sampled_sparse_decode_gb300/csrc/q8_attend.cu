@@ -9,19 +9,19 @@
 // scale of a key multiplies its whole score and the scale of a value its weight, so that no element
 // is scaled by itself.
 //
-// Work.  The tiles (32 tokens) of all units (sequence, KV head) lie on one line, which the blocks
-// share evenly, whatever the lengths of the batch are; the lengths are read on the device.  A block's
-// warps take the tiles of its part in turn, each through a ring of its own in shared memory
-// (asynchronous 16-byte copies, two tiles ahead of the one in use, no barrier among warps), and merge
-// their results at the end of each unit's part.  A unit that lies within one block is finished there;
-// the others' partial results are joined by a second launch in the order of the line.
+// Work.  The tiles (32 tokens) of all units (sequence, KV head) lie on one line, which the warps of
+// the grid share evenly, whatever the lengths of the batch are; the lengths are read on the device, and
+// opening a unit counts like a tile.  A warp takes its stretch of the line through a ring of its own in
+// shared memory (asynchronous 16-byte copies), without a barrier.  A unit that lies within one
+// stretch is finished by its warp; of the others a warp holds a piece.  At its end a block merges its
+// warps' pieces; a unit that goes beyond the block leaves a part in the workspace, and a second launch
+// joins the parts in the order of the line.
 //
 // A tile.  Codes become fp16 exactly (int8 by the bits of 1024 + code, e4m3 by conversion) and go to
 // the matrix units as the A operand of m16n8k16, tokens x dimensions for the scores and dimensions x
-// tokens for the output, so that the group's up to 8 query heads are the n = 8 columns and a warp
-// needs no other padding.  Which dimension stands at which k is free as long as both operands agree:
-// a lane reads 16 bytes of one row and has the operands of four products.  Rows are placed so that
-// both kinds of read are free of bank conflicts.
+// tokens for the output, so that the group's up to 8 query heads are the n = 8 columns.  Both are read
+// by ldmatrix as pairs of bytes: four dimensions of a key, or (transposed) two dimensions of two
+// values' tokens, stand in a register, and which dimension stands at which k is free.
 //   - q enters as fp16 pieces (one for bf16, two for fp32) of q 2^-e, e the exponent of the head's
 //     largest element: fp16's range holds everything down to 2^-24 of it.
 //   - The weights enter the second product as two fp16 pieces (22 bits; one would leave 2^-12 of
@@ -44,10 +44,8 @@ constexpr int kTile = 32;                  // tokens of a tile
 constexpr int kQ8Warps = 8;
 constexpr int kQ8Threads = kQ8Warps * 32;
 constexpr int kStages = 3;                 // tiles of a warp's ring
-constexpr int kMinShare = kQ8Warps;        // tiles of a block's part: at least one for each warp
+constexpr int kOpen = 1;                   // what opening a unit counts, in tiles
 constexpr int kScanRounds = 8;             // 32 sequences or units each that a warp reads by itself
-constexpr int kMergeDims = 64;             // dimensions that one merging pass takes
-constexpr int kMergeRow = kMergeDims + 4;
 constexpr float kNoScore = -1e38f;         // a reference before the first score
 constexpr float kSlack = 8.f;              // how far a score may pass the reference (base 2)
 constexpr float kTopWeight = 256.f;        // the same for a weight
@@ -57,21 +55,17 @@ struct Ring {
   static constexpr int kCodes = kTile * D;                     // bytes of a tile's keys or values
   static constexpr int kStage = 2 * kCodes + 2 * kTile * 4;    // keys, values, scales
   static constexpr int kWarp = kStages * kStage;
-  static constexpr int kMerge = kQ8Warps * kMaxGroup * kMergeRow * 4;
-  static constexpr int kBytes = kQ8Warps * kWarp + kMerge;
+  static constexpr int kBytes = kQ8Warps * kWarp;
+  static constexpr int kPieceRow = D + 4;                      // floats of a head in a piece
+  static_assert(kMaxGroup * kPieceRow * 4 <= kWarp, "a piece fits its warp's ring");
 };
 
-// Byte of 16-byte piece `chunk` of row r in a tile's block of rows.  Scores are read by 8 lanes from
-// pieces c .. c + 3 of rows 2j and 2j + 1, values from pieces 2j and 2j + 1 (d = 128; the halves of a
-// piece for d = 64) of four rows two apart: either way the 8 pieces lie in 8 different banks' groups.
+// Byte of 16-byte piece `chunk` of row r in a tile's block of rows: eight consecutive rows' pieces of
+// one chunk lie in eight different groups of four banks.
 template <int D>
 __device__ __forceinline__ int piece_at(int r, int chunk) {
-  if constexpr (D == 128) {
-    return r * 128 + ((chunk ^ (((r >> 2 ^ r) & 1) << 2 | (r & 2))) << 4);
-  } else {
-    const int half = (r ^ r >> 1) & 1;
-    return (r >> 1) * 128 + (half << 6) + ((chunk ^ ((r >> 2 & 1) << 1)) << 4);
-  }
+  if constexpr (D == 128) return r * 128 + ((chunk ^ (r & 7)) << 4);
+  return (r >> 1) * 128 + (r & 1) * 64 + ((chunk ^ (r >> 1 & 3)) << 4);
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -126,14 +120,26 @@ __device__ __forceinline__ void pairs_to_f16(uint32_t w, uint32_t& lo, uint32_t&
     hi = e4m3_to_f16x2(static_cast<uint16_t>(w >> 16));
   }
 }
+// The same of a register with two dimensions of two tokens, bytes (d, d + 1) of one and of the next:
+// each dimension's pair of tokens.
+template <int C>
+__device__ __forceinline__ void tokens_to_f16(uint32_t w, uint32_t& d0, uint32_t& d1) {
+  if constexpr (C == kCodeI8) {
+    const uint32_t u = w ^ 0x80808080u;
+    d0 = sub_f16x2(__byte_perm(u, 0x64646464u, 0x4240), 0x64806480u);
+    d1 = sub_f16x2(__byte_perm(u, 0x64646464u, 0x4341), 0x64806480u);
+  } else {
+    pairs_to_f16<C>(__byte_perm(w, 0, 0x3120), d0, d1);
+  }
+}
 
 // ---------------------------------------------------------------- the line of tiles
 
-// A unit's tokens: positions lo .. len - 1 (dense), or `count` listed teams; `tiles` on the line.
+// A unit's tokens: positions lo .. len - 1 (dense), or `count` listed teams, in `tiles` tiles.
 struct Unit {
   int len, lo;         // at most 2^14 pages of 2^7 tokens
   int count;
-  int64_t tiles;
+  int tiles;
 };
 // Reads sequence b (dense) or unit (b, h) (listed); what is out of range is judged here and told if
 // `tell`.
@@ -151,24 +157,27 @@ __device__ __forceinline__ Unit load_unit(const Q8AttendParams& p, int b, int h,
     u.count = min(max(count, 0), p.num_draws);
     if (count != u.count && tell) set_status(p.status, SANTA_DEV_BAD_SEL);
     if (u.len == 0) u.count = 0;
-    u.tiles = static_cast<int64_t>(u.count) * (p.team_size / kTile);
+    u.tiles = u.count * (p.team_size / kTile);
   } else {
     u.tiles = (u.len + kTile - 1) / kTile - u.lo / kTile;
   }
   return u;
 }
+// A unit's length on the line: its tiles and its opening.
+__device__ __forceinline__ int64_t span(const Unit& u) { return u.tiles ? u.tiles + kOpen : 0; }
 
-// A place on the line: unit (b, h), whose tiles start at `base`.
+// A place on the line: unit (b, h), which begins at `base`; its tile k stands at base + kOpen + k.
 struct Walk {
   int b, h;
   int64_t base;
   Unit u;
 };
 __device__ __forceinline__ void next_unit(const Q8AttendParams& p, Walk& w) {
-  w.base += w.u.tiles;
+  w.base += span(w.u);
   if (w.b == p.batch - 1 && w.h == p.num_kv_heads - 1) {
     // not reached while lengths and lists stay as they are; if not, the walk ends here
-    w.u = Unit{0, 0, 0, INT64_MAX / 2};
+    w.base = INT64_MAX / 2;
+    w.u = Unit{0, 0, 0, 0};
     return;
   }
   const bool wrap = ++w.h == p.num_kv_heads;
@@ -178,21 +187,30 @@ __device__ __forceinline__ void next_unit(const Q8AttendParams& p, Walk& w) {
   }
   if (wrap || p.sel_ids) w.u = load_unit(p, w.b, w.h, false);
 }
+// To the unit that owns place `at` (at < the line's length).
+__device__ __forceinline__ void walk_to(const Q8AttendParams& p, Walk& w, int64_t at) {
+  while (w.base + span(w.u) <= at) next_unit(p, w);
+}
 
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+template <typename T>
+__device__ __forceinline__ T warp_scan(T v) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t up = __shfl_up_sync(0xffffffffu, v, o);
+    const T up = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += up;
   }
-  if (lane == 31) warp_sums[warp] = v;
+  return v;
+}
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums) {
+  const int warp = threadIdx.x >> 5;
+  v = warp_scan(v);
+  if ((threadIdx.x & 31) == 31) warp_sums[warp] = v;
   __syncthreads();
-  int64_t before = 0;
 #pragma unroll
   for (int w = 0; w < kQ8Warps; ++w)
-    if (w < warp) before += warp_sums[w];
-  return v + before;
+    if (w < warp) v += warp_sums[w];
+  return v;
 }
 
 // ---------------------------------------------------------------- the attention
@@ -209,25 +227,24 @@ struct PageCache {
 
 template <int NQ, int C, int D>
 struct Warp {
-  static constexpr int kSteps = D / 16;              // k steps of a score
-  static constexpr int kOut = D / 16;                // 16-dimension tiles of the output
+  static constexpr int kSteps = D / 16;      // 16-dimension pieces: k steps of a score, tiles of out
   uint32_t q[NQ][kSteps][2];
-  float acc[kOut][4];
+  float acc[kSteps][4];      // dimensions 16 j + 2 g (+ 1) of heads 2t, 2t + 1 (g, t: lane / 4, lane % 4)
   float ref[2];              // of heads 2t and 2t + 1: reference of the exponentials
   float sum[2];              // this lane's share of the sum of weights
   float big[2], inv[2];      // largest |p vs| (at least), and the power of two that scales weights
   float qs[2];               // score of a unit product, base 2 (or over the cap)
 };
 
-// Copies tile `t` of the line into a stage and returns what the consumer must know of it: the range of
-// its tokens that are seen and the bias.
+// Copies tile `k` of a unit into a stage and notes what the consumer must know of it: the range of its
+// tokens that are seen and the bias.
 template <int D>
-__device__ __forceinline__ void issue_tile(const Q8AttendParams& p, const Walk& w, int64_t t,
+__device__ __forceinline__ void issue_tile(const Q8AttendParams& p, const Walk& w, int k_unit,
                                            PageCache& pc, uint8_t* stage, int2* note) {
   const int lane = threadIdx.x & 31;
   const int T = p.team_size, per = T == 128 ? 2 : 1;  // log2 of a page's tiles
   // tile of the unit, or of the sequence (at most 2^16 of them); then slot or team, and row in it
-  const int i = static_cast<int>(t - w.base) + (p.sel_ids ? 0 : w.u.lo / kTile);
+  const int i = k_unit + (p.sel_ids ? 0 : w.u.lo / kTile);
   const int at = i >> per, row = (i & ((1 << per) - 1)) * kTile;
   if (__builtin_expect(pc.b != w.b || (p.sel_ids && pc.h != w.h) || at < pc.first || at >= pc.first + 32, 0)) {
     pc.b = w.b;
@@ -296,30 +313,27 @@ __device__ __forceinline__ void issue_tile(const Q8AttendParams& p, const Walk& 
   }
 }
 
-// The group's queries as B operands: k index of step (c, w) are bytes 16 (t + 4 c) + 4 w + ... of a
-// row, t = lane % 4 (d = 64: c = 0 only).
+// The group's queries as B operands of the score: step s has dimensions 16 s + 4 t + 0 .. 3 of head
+// g, as a key's register has them.
 template <int NQ, int C, int D>
-__device__ void load_queries(const Q8AttendParams& p, int b, int h, Warp<NQ, C, D>& w) {
+__device__ __forceinline__ void load_queries(const Q8AttendParams& p, int b, int h,
+                                             Warp<NQ, C, D>& w) {
   const int lane = threadIdx.x & 31, head = lane >> 2, t = lane & 3;
   const int G = p.num_q_heads / p.num_kv_heads;
-  const int64_t at = (static_cast<int64_t>(b) * p.num_q_heads + h * G + head) * D;
+  const int64_t at = (static_cast<int64_t>(b) * p.num_q_heads + h * G + head) * D + 4 * t;
   float x[D / 4];
   uint32_t top = 0;
 #pragma unroll
-  for (int c = 0; c < D / 64; ++c) {
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const int64_t e = at + 16 * (t + 4 * c) + i;
-      float* y = x + 16 * c + i;
-      if (head >= G) {
-        y[0] = y[1] = y[2] = y[3] = 0.f;
-      } else if constexpr (NQ == 1) {
-        const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + e);
-        y[0] = bf16_lo(v.x), y[1] = bf16_hi(v.x), y[2] = bf16_lo(v.y), y[3] = bf16_hi(v.y);
-      } else {
-        const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + e);
-        y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
-      }
+  for (int s = 0; s < D / 16; ++s) {
+    float* y = x + 4 * s;
+    if (head >= G) {
+      y[0] = y[1] = y[2] = y[3] = 0.f;
+    } else if constexpr (NQ == 1) {
+      const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + at + 16 * s);
+      y[0] = bf16_lo(v.x), y[1] = bf16_hi(v.x), y[2] = bf16_lo(v.y), y[3] = bf16_hi(v.y);
+    } else {
+      const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at + 16 * s);
+      y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
     }
   }
 #pragma unroll
@@ -393,8 +407,9 @@ __device__ __forceinline__ void raise(Warp<NQ, C, D>& w, const float (&x)[8], co
 template <int NQ, int C, int D>
 __device__ __forceinline__ void attend_tile(const Q8AttendParams& p, Warp<NQ, C, D>& w,
                                             const uint8_t* stage, int2 note) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int lane = threadIdx.x & 31, g = lane >> 2;
   const float* scales = reinterpret_cast<const float*>(stage + 2 * kTile * D);
+  const uint32_t at = smem_u32(stage);
   const int n0 = note.x & 0xffff, n1 = note.x >> 16;
   if (n1 == 0) return;
   float x[8], ks[4], vs[4];                          // token 8 k + g; score 2 k + i: head 2 t + i
@@ -402,17 +417,17 @@ __device__ __forceinline__ void attend_tile(const Q8AttendParams& p, Warp<NQ, C,
   for (int m = 0; m < 2; ++m) {
     float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int h = 0; h < D / 64; ++h) {
-      const uint4 a = *reinterpret_cast<const uint4*>(stage + piece_at<D>(16 * m + g, t + 4 * h));
-      const uint4 b = *reinterpret_cast<const uint4*>(stage + piece_at<D>(16 * m + 8 + g, t + 4 * h));
-      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+    for (int s = 0; s < D / 16; s += 2) {
+      // rows 16 m + 0 .. 7 and 8 .. 15, pieces s and s + 1: matrix lane / 8's row is given by the lane
+      uint32_t a[4];
+      ldmatrix_x4(a, at + piece_at<D>(16 * m + (lane & 15), s + (lane >> 4)));
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 2; ++k) {
         uint32_t f[4];
-        pairs_to_f16<C>(aw[k], f[0], f[2]);
-        pairs_to_f16<C>(bw[k], f[1], f[3]);
+        pairs_to_f16<C>(a[2 * k], f[0], f[2]);
+        pairs_to_f16<C>(a[2 * k + 1], f[1], f[3]);
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) mma_f16_16816(c, f, w.q[n][4 * h + k][0], w.q[n][4 * h + k][1]);
+        for (int n = 0; n < NQ; ++n) mma_f16_16816(c, f, w.q[n][s + k][0], w.q[n][s + k][1]);
       }
     }
 #pragma unroll
@@ -478,102 +493,161 @@ __device__ __forceinline__ void attend_tile(const Q8AttendParams& p, Warp<NQ, C,
     hi[k] = movmatrix_trans(hi[k]);
     lo[k] = movmatrix_trans(lo[k]);
   }
-  // values: 16 tokens at a time; a lane has D / 8 dimensions of four tokens
-  constexpr int kWords = D / 32;
-  uint32_t v[2][4][kWords];
+  // values: matrix lane / 8 is token group lane / 8; a register has two dimensions of two tokens
 #pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int tok = 16 * m + 8 * (r >> 1) + 2 * t + (r & 1);
-      const uint8_t* at = stage + kTile * D;
-      if constexpr (D == 128) {
-        const uint4 a = *reinterpret_cast<const uint4*>(at + piece_at<D>(tok, g));
-        v[m][r][0] = a.x, v[m][r][1] = a.y, v[m][r][kWords - 2] = a.z, v[m][r][kWords - 1] = a.w;
-      } else {
-        const uint2 a = *reinterpret_cast<const uint2*>(at + piece_at<D>(tok, g >> 1) + (g & 1) * 8);
-        v[m][r][0] = a.x, v[m][r][1] = a.y;
-      }
-    }
-#pragma unroll
-  for (int k = 0; k < kWords; ++k) {
-    float c[2][4] = {};
+  for (int j = 0; j < D / 16; ++j) {
+    uint32_t a[4];
+    ldmatrix_x4_trans(a, at + kTile * D + piece_at<D>(lane, j));
+    float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      uint32_t f[2][4];                              // dimensions (4k, 4k + 1) and (4k + 2, 4k + 3)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const uint32_t a = v[m][2 * r][k], b = v[m][2 * r + 1][k];
-        pairs_to_f16<C>(__byte_perm(a, b, 0x5140), f[0][2 * r], f[0][2 * r + 1]);
-        pairs_to_f16<C>(__byte_perm(a, b, 0x7362), f[1][2 * r], f[1][2 * r + 1]);
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        mma_f16_16816(c[j], f[j], hi[2 * m], hi[2 * m + 1]);
-        mma_f16_16816(c[j], f[j], lo[2 * m], lo[2 * m + 1]);
-      }
+      uint32_t f[4];
+      tokens_to_f16<C>(a[2 * m], f[0], f[1]);
+      tokens_to_f16<C>(a[2 * m + 1], f[2], f[3]);
+      mma_f16_16816(c, f, hi[2 * m], hi[2 * m + 1]);
+      mma_f16_16816(c, f, lo[2 * m], lo[2 * m + 1]);
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w.acc[2 * k + j][i] += c[j][i];
+    for (int i = 0; i < 4; ++i) w.acc[j][i] += c[i];
   }
 }
+
+// The weights' sums of a warp's unit, over the lanes that share its heads.
+template <int NQ, int C, int D>
+__device__ __forceinline__ void close_sums(Warp<NQ, C, D>& w) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) w.sum[i] += __shfl_xor_sync(0xffffffffu, w.sum[i], o);
+}
+
+// Writes a piece: rows of `stride` floats, one for each head of the group, and (reference, sum).
+template <int NQ, int C, int D>
+__device__ __forceinline__ void store_piece(Warp<NQ, C, D>& w, int G, float* rows, int stride,
+                                            float (*ml)[2]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  close_sums(w);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (2 * t + i >= G) continue;
+    const float back = 1.f / w.inv[i];
+    float* row = rows + (2 * t + i) * stride + 2 * g;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j)
+      *reinterpret_cast<float2*>(row + 16 * j) =
+          make_float2(w.acc[j][i] * back, w.acc[j][2 + i] * back);
+    if (g == 0) {
+      ml[2 * t + i][0] = w.ref[i];
+      ml[2 * t + i][1] = w.sum[i];
+    }
+  }
+}
+
+// Writes a whole unit's rows of out.
+template <int NQ, int C, int D>
+__device__ __forceinline__ void store_unit(Warp<NQ, C, D>& w, int G, float* out) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  close_sums(w);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (2 * t + i >= G) continue;
+    const float back = 1.f / w.inv[i], z = w.sum[i];
+    float* row = out + (2 * t + i) * D + 2 * g;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j)
+      *reinterpret_cast<float2*>(row + 16 * j) =
+          z == 0.f ? make_float2(0.f, 0.f)
+                   : make_float2(w.acc[j][i] * back / z, w.acc[j][2 + i] * back / z);
+  }
+}
+
+// Adds (x, m, l) to a running (sum, top, z): sums relative to the largest reference.
+template <int N>
+__device__ __forceinline__ void add_part(float (&sum)[N], float& top, float& z, const float (&x)[N],
+                                         float m, float l) {
+  const float best = fmaxf(top, m);
+  const float keep = ex2_approx(top - best), f = ex2_approx(m - best);
+  top = best;
+  z = z * keep + l * f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) sum[i] = sum[i] * keep + x[i] * f;
+}
+
+// A unit that a warp holds a piece of, or a block a part: where it stands on the line.
+struct Owner {
+  int64_t unit, base;   // unit -1: none
+  int tiles;
+  bool first;           // whether the piece has the unit's first tile
+};
 
 template <int NQ, int C, int D>
 __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t sums[2][kQ8Warps];
-  __shared__ int64_t start_s[2];                     // element of the line's start, its first tile
+  __shared__ int64_t start_s[2];                     // element of the block's start, its place
   __shared__ int2 notes[kQ8Warps][kStages];
-  __shared__ float ml[kQ8Warps][kMaxGroup][2];
+  // each warp's piece that closes a unit which another warp opened (0, in the workspace), and its
+  // piece that goes on beyond its stretch (1, in its ring), with their (reference, sum)
+  __shared__ Owner owner_s[2][kQ8Warps];
+  __shared__ float ml_s[2][kQ8Warps][kMaxGroup][2];
   using R = Ring<D>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = p.num_q_heads / p.num_kv_heads;
   grid_dependency_wait();
-  grid_launch_dependents();
 
-  // the length of the line, and where this block's part of it starts: by sequences (dense) or units
+  // the line's length, and where this warp's stretch of it starts: by sequences (dense) or units
   const int64_t elems = static_cast<int64_t>(p.batch) * (p.sel_ids ? p.num_kv_heads : 1);
   const int heads = p.sel_ids ? 1 : p.num_kv_heads;
-  auto tiles_of = [&](int64_t e, bool tell) -> int64_t {
-    if (e >= elems) return 0;
-    const int b = static_cast<int>(p.sel_ids ? e / p.num_kv_heads : e);
-    return load_unit(p, b, static_cast<int>(e - static_cast<int64_t>(b) * p.num_kv_heads), tell).tiles *
-           heads;
-  };
   const bool tell = blockIdx.x == 0;
-  int64_t total = 0, share, c0, elem = 0, elem_base = 0;
-  auto split = [&]() {
-    share = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kMinShare));
-    c0 = blockIdx.x * share;
-  };
-  if (elems <= 32 * kScanRounds) {
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * kQ8Warps;
+  int64_t total, share, c0;
+  Walk use;
+  use.h = 0;
+  if (p.short_line) {
     // every warp for itself, without a barrier
-    int64_t v[kScanRounds], upto[kScanRounds];
-#pragma unroll
-    for (int i = 0; i < kScanRounds; ++i) v[i] = tiles_of(32 * i + lane, tell && warp == 0);
+    int v[kScanRounds], upto[kScanRounds], sum = 0;
 #pragma unroll
     for (int i = 0; i < kScanRounds; ++i) {
-      upto[i] = v[i];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, upto[i], o);
-        if (lane >= o) upto[i] += up;
+      v[i] = upto[i] = 0;
+      if (32 * i >= elems) continue;
+      const int e = 32 * i + lane;
+      if (e < elems) {
+        const int b = p.sel_ids ? e / p.num_kv_heads : e;
+        v[i] = static_cast<int>(span(load_unit(p, b, e - b * p.num_kv_heads, tell && warp == 0))) * heads;
       }
-      upto[i] += total;
-      total = __shfl_sync(0xffffffffu, upto[i], 31);
     }
-    split();
 #pragma unroll
     for (int i = 0; i < kScanRounds; ++i) {
+      if (32 * i >= elems) continue;
+      upto[i] = warp_scan(v[i]) + sum;
+      sum = __shfl_sync(0xffffffffu, upto[i], 31);
+    }
+    total = sum;
+    const int each = static_cast<int>((static_cast<unsigned>(sum) + static_cast<unsigned>(warps) - 1) /
+                                      static_cast<unsigned>(warps));
+    share = each;
+    c0 = (static_cast<int64_t>(blockIdx.x) * kQ8Warps + warp) * share;
+    int elem = 0, base = 0;
+#pragma unroll
+    for (int i = 0; i < kScanRounds; ++i) {
+      if (32 * i >= elems) continue;
       const unsigned hit = __ballot_sync(0xffffffffu, upto[i] > c0 && upto[i] - v[i] <= c0);
       if (hit) {
         elem = 32 * i + __ffs(hit) - 1;
-        elem_base = __shfl_sync(0xffffffffu, upto[i] - v[i], __ffs(hit) - 1);
+        base = __shfl_sync(0xffffffffu, upto[i] - v[i], __ffs(hit) - 1);
       }
     }
+    use.b = p.sel_ids ? elem / p.num_kv_heads : elem;
+    if (p.sel_ids) use.h = elem - use.b * p.num_kv_heads;
+    use.base = base;
   } else {
+    auto tiles_of = [&](int64_t e, bool say) -> int64_t {
+      if (e >= elems) return 0;
+      const int b = static_cast<int>(p.sel_ids ? e / p.num_kv_heads : e);
+      const int h = static_cast<int>(e - static_cast<int64_t>(b) * p.num_kv_heads);
+      return span(load_unit(p, b, p.sel_ids ? h : 0, say)) * heads;
+    };
+    total = 0;
     for (int64_t e0 = 0; e0 < elems; e0 += kQ8Threads) {
       const int64_t upto =
           total + block_scan(tiles_of(e0 + threadIdx.x, tell), sums[(e0 / kQ8Threads) & 1]);
@@ -582,7 +656,8 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
       total = start_s[0];
       __syncthreads();
     }
-    split();
+    share = (total + warps - 1) / warps;
+    c0 = static_cast<int64_t>(blockIdx.x) * kQ8Warps * share;      // of the block, first
     int64_t before = 0;
     for (int64_t e0 = 0; e0 < elems && c0 < total; e0 += kQ8Threads) {
       const int64_t mine = tiles_of(e0 + threadIdx.x, false);
@@ -598,134 +673,139 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
       __syncthreads();
     }
     __syncthreads();
-    elem = start_s[0];
-    elem_base = start_s[1];
+    use.b = static_cast<int>(p.sel_ids ? start_s[0] / p.num_kv_heads : start_s[0]);
+    if (p.sel_ids) use.h = static_cast<int>(start_s[0] - static_cast<int64_t>(use.b) * p.num_kv_heads);
+    use.base = start_s[1];
+    c0 += warp * share;
   }
+  const int64_t block_share = share * kQ8Warps;
   const int64_t c1 = min(c0 + share, total);
-  int64_t split_unit = -1;                           // a unit that starts here and ends elsewhere
-  int split_parts = 0;
-  // units that see nothing
-  auto zero_units = [&]() {
-    for (int64_t e = blockIdx.x; e < elems; e += gridDim.x) {
-      if (tiles_of(e, false)) continue;
-      float* row = p.out + e * heads * G * D;
-      for (int i = threadIdx.x; i < heads * G * D; i += kQ8Threads) row[i] = 0.f;
-    }
-  };
-  if (c0 >= c1) {
-    zero_units();
-    if (threadIdx.x == 0) p.split_unit[blockIdx.x] = -1;
-    return;
-  }
-  Walk use;
-  use.b = static_cast<int>(p.sel_ids ? elem / p.num_kv_heads : elem);
-  use.h = static_cast<int>(p.sel_ids ? elem % p.num_kv_heads : 0);
-  use.base = elem_base;
-  use.u = load_unit(p, use.b, use.h, false);
-  while (use.base + use.u.tiles <= c0) next_unit(p, use);
-  Walk ask = use;
+  const int64_t block_c0 = static_cast<int64_t>(blockIdx.x) * block_share;
 
+  if (threadIdx.x < 2 * kQ8Warps) owner_s[threadIdx.x & 1][threadIdx.x >> 1].unit = -1;
+  __syncthreads();
   uint8_t* ring = smem + warp * R::kWarp;
-  float* merge = reinterpret_cast<float*>(smem + kQ8Warps * R::kWarp);
-  PageCache pc;
-  pc.b = -1;
-  int64_t next = c0 + warp;                          // the next tile to ask for
-  int put = 0, get = 0;
-  auto ask_next = [&]() {
-    if (next < c1) {
-      while (ask.base + ask.u.tiles <= next) next_unit(p, ask);
-      issue_tile<D>(p, ask, next, pc, ring + put * R::kStage, &notes[warp][put]);
-      next += kQ8Warps;
-    }
-    cp_async_commit();
-    put = put + 1 == kStages ? 0 : put + 1;
-  };
+  float* closing = p.piece + (static_cast<int64_t>(blockIdx.x) * kQ8Warps + warp) * kMaxGroup * D;
+  if (c0 < c1) {
+    use.u = load_unit(p, use.b, use.h, false);
+    walk_to(p, use, c0);
+    Walk ask = use;
+    int ask_k = static_cast<int>(max(c0 - use.base - kOpen, int64_t(0)));   // next tile of ask's unit
+    PageCache pc;
+    pc.b = -1;
+    bool more = true;
+    int put = 0, get = 0;
+    auto ask_next = [&]() {
+      if (more) {
+        while (ask_k >= ask.u.tiles) {               // on to the next unit with a tile
+          next_unit(p, ask);
+          ask_k = 0;
+          if (ask.base >= c1) break;
+        }
+        more = ask.base + kOpen + ask_k < c1;
+        if (more) {
+          issue_tile<D>(p, ask, ask_k, pc, ring + put * R::kStage, &notes[warp][put]);
+          ++ask_k;
+        }
+      }
+      cp_async_commit();
+      put = put + 1 == kStages ? 0 : put + 1;
+    };
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) ask_next();
-  zero_units();
+    for (int i = 0; i < kStages - 1; ++i) ask_next();
 
-  Warp<NQ, C, D> w;
-  int64_t at = c0 + warp;
-  for (;;) {
-    const int64_t end = min(c1, use.base + use.u.tiles);
-    load_queries(p, use.b, use.h, w);
-    for (; at < end; at += kQ8Warps) {
-      cp_async_wait<kStages - 2>();
-      __syncwarp();
-      ask_next();
-      attend_tile(p, w, ring + get * R::kStage, notes[warp][get]);
-      get = get + 1 == kStages ? 0 : get + 1;
-      __syncwarp();
-    }
-    // merge the warps' results of this unit
-    const bool whole = use.base >= c0 && use.base + use.u.tiles <= c1;
-    const int slot = use.base < c0 ? 0 : 1;          // goes on from the block before, or starts here
-    if (!whole && slot == 1) {
-      split_unit = static_cast<int64_t>(use.b) * p.num_kv_heads + use.h;
-      split_parts = static_cast<int>((use.base + use.u.tiles - 1) / share) - blockIdx.x + 1;
-    }
-    const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float s = w.sum[i];
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (g == 0) {
-        ml[warp][2 * t + i][0] = w.ref[i];
-        ml[warp][2 * t + i][1] = s;
-      }
-      const float back = 1.f / w.inv[i];
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j) {
-        w.acc[j][i] *= back;
-        w.acc[j][2 + i] *= back;
-      }
-    }
-    // dimension D/8 g + 2j + r of the lane's D/8; a pass takes kLane of them from every lane
-    constexpr int kLane = kMergeDims / 8;
-#pragma unroll
-    for (int pass = 0; pass < D / kMergeDims; ++pass) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float* row = merge + (warp * kMaxGroup + 2 * t + i) * kMergeRow + g * kLane;
-#pragma unroll
-        for (int j = 0; j < kLane / 4; ++j) {
-          const int o = pass * kLane / 2 + 2 * j;
-          *reinterpret_cast<float4*>(row + 4 * j) =
-              make_float4(w.acc[o][i], w.acc[o][2 + i], w.acc[o + 1][i], w.acc[o + 1][2 + i]);
+    Warp<NQ, C, D> w;
+    for (;;) {
+      const int k0 = static_cast<int>(max(c0 - use.base - kOpen, int64_t(0)));
+      const int k1 = static_cast<int>(min(c1 - use.base - kOpen, static_cast<int64_t>(use.u.tiles)));
+      if (k0 < k1) {
+        load_queries(p, use.b, use.h, w);
+        for (int k = k0; k < k1; ++k) {
+          cp_async_wait<kStages - 2>();
+          __syncwarp();
+          ask_next();
+          attend_tile(p, w, ring + get * R::kStage, notes[warp][get]);
+          get = get + 1 == kStages ? 0 : get + 1;
+          __syncwarp();
         }
-      }
-      __syncthreads();
-      for (int e = threadIdx.x; e < G * kMergeDims; e += kQ8Threads) {
-        const int head = e / kMergeDims, col = e % kMergeDims;
-        const int dim = col / kLane * (D / 8) + kLane * pass + col % kLane;
-        float top = -INFINITY, sum = 0.f, z = 0.f;
-#pragma unroll
-        for (int i = 0; i < kQ8Warps; ++i) top = fmaxf(top, ml[i][head][0]);
-        const float ref = top == -INFINITY ? 0.f : top;
-#pragma unroll
-        for (int i = 0; i < kQ8Warps; ++i) {
-          const float keep = ex2_approx(ml[i][head][0] - ref);
-          sum += merge[(i * kMaxGroup + head) * kMergeRow + col] * keep;
-          z += ml[i][head][1] * keep;
-        }
-        if (whole) {
-          p.out[(static_cast<int64_t>(use.b) * p.num_q_heads + use.h * G + head) * D + dim] =
-              z == 0.f ? 0.f : sum / z;
+        const int64_t unit = static_cast<int64_t>(use.b) * p.num_kv_heads + use.h;
+        const Owner own = {unit, use.base, use.u.tiles, k0 == 0};
+        if (k1 < use.u.tiles) {
+          if (lane == 0) owner_s[1][warp] = own;
+          store_piece(w, G, reinterpret_cast<float*>(ring), R::kPieceRow, ml_s[1][warp]);
+        } else if (k0 > 0) {
+          if (lane == 0) owner_s[0][warp] = own;
+          store_piece(w, G, closing, D, ml_s[0][warp]);
         } else {
-          const int64_t part = static_cast<int64_t>(blockIdx.x * 2 + slot) * kMaxGroup + head;
-          p.part_acc[part * D + dim] = sum;
-          if (dim == 0) {
-            p.part_ml[part * 2] = top;
-            p.part_ml[part * 2 + 1] = z;
-          }
+          store_unit(w, G, p.out + unit * G * D);
         }
       }
-      __syncthreads();
+      if (use.base + span(use.u) >= c1) break;
+      do next_unit(p, use);
+      while (use.u.tiles == 0 && use.base < c1);
     }
-    if (end >= c1) break;
-    do next_unit(p, use);
-    while (use.u.tiles == 0);
+  }
+  // units that see nothing
+  for (int64_t e = blockIdx.x; e < elems; e += gridDim.x) {
+    const int b = static_cast<int>(p.sel_ids ? e / p.num_kv_heads : e);
+    if (load_unit(p, b, p.sel_ids ? static_cast<int>(e - static_cast<int64_t>(b) * p.num_kv_heads) : 0, false).tiles)
+      continue;
+    float* row = p.out + e * heads * G * D;
+    for (int i = threadIdx.x; i < heads * G * D; i += kQ8Threads) row[i] = 0.f;
+  }
+  __syncthreads();
+  int64_t split_unit = -1;                           // a unit that begins in this block and ends elsewhere
+  int split_parts = 0;
+
+  // The block's chains: pieces that go on, up to one that closes the unit or to the block's end; before
+  // them a piece at the block's start that only closes (w = -1).
+  for (int w = -1; w < kQ8Warps;) {
+    const bool lone = w < 0;
+    if (owner_s[!lone][max(w, 0)].unit < 0) {
+      ++w;
+      continue;
+    }
+    const Owner own = owner_s[!lone][max(w, 0)];
+    int end = max(w, 0);                             // pieces w .. end - 1 go on
+    if (!lone)
+      do ++end;
+      while (end < kQ8Warps && owner_s[1][end].unit >= 0 && owner_s[0][end].unit < 0);
+    const bool closed = end < kQ8Warps && owner_s[0][end].unit >= 0;
+    const int begin = max(w, 0), slot = !lone && own.first;
+    const bool whole = closed && slot;
+    const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * kMaxGroup;
+    const int count = end - begin + closed;
+    // a head's four dimensions per thread; a short loop, since the code is run once and must be fetched
+    for (int e = threadIdx.x; e < G * (D / 4); e += kQ8Threads) {
+      const int head = e / (D / 4), dim = e % (D / 4) * 4;
+      float sum[4] = {}, top = kNoScore, z = 0.f;
+#pragma unroll 1
+      for (int i = 0; i < count; ++i) {
+        const bool on = begin + i < end;
+        const float* row =
+            on ? reinterpret_cast<const float*>(smem + (begin + i) * R::kWarp) + head * R::kPieceRow
+               : p.piece + ((static_cast<int64_t>(blockIdx.x) * kQ8Warps + end) * kMaxGroup + head) * D;
+        const float4 v = *reinterpret_cast<const float4*>(row + dim);
+        const float x[4] = {v.x, v.y, v.z, v.w};
+        add_part(sum, top, z, x, ml_s[on][begin + i][head][0], ml_s[on][begin + i][head][1]);
+      }
+      if (whole) {
+        const float f = z == 0.f ? 0.f : 1.f / z;
+        *reinterpret_cast<float4*>(p.out + (own.unit * G + head) * D + dim) =
+            make_float4(sum[0] * f, sum[1] * f, sum[2] * f, sum[3] * f);
+      } else {
+        *reinterpret_cast<float4*>(p.part_acc + (part + head) * D + dim) =
+            make_float4(sum[0], sum[1], sum[2], sum[3]);
+        if (dim == 0)
+          *reinterpret_cast<float2*>(p.part_ml + (part + head) * 2) = make_float2(top, z);
+      }
+    }
+    if (!whole && slot) {
+      split_unit = own.unit;
+      split_parts = static_cast<int>((own.base + kOpen + own.tiles - 1) / block_share -
+                                     (own.base + kOpen) / block_share) + 1;
+    }
+    w = lone ? 0 : end;
   }
   if (threadIdx.x == 0) {
     p.split_unit[blockIdx.x] = split_unit;
@@ -733,9 +813,8 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
   }
 }
 
-// One block per (block of the first launch, query head of a group): joins the unit that starts there and
-// ends elsewhere, if there is one, by adding its partial results in the order of the line, a warp each
-// in turn.
+// One block per (block of the first launch, query head of a group): joins the unit that begins there and
+// ends elsewhere, if there is one: a warp takes every eighth part, eight of them at a time.
 template <int D>
 __global__ void __launch_bounds__(kQ8Threads) q8_join_kernel(Q8AttendParams p) {
   constexpr int W = D / 32;                          // dimensions of a lane
@@ -746,45 +825,49 @@ __global__ void __launch_bounds__(kQ8Threads) q8_join_kernel(Q8AttendParams p) {
   const int block = blockIdx.x / G, head = blockIdx.x % G;
   grid_dependency_wait();
   const int64_t unit = p.split_unit[block];
-  if (unit < 0) return;
   const int count = p.split_parts[block];
-  float* out = p.out + (unit * G + head) * D;
-  float m = -INFINITY, l = 0.f, acc[W];
+  if (unit < 0) return;
+  float sum[W] = {}, top = kNoScore, z = 0.f;
+  constexpr int kAhead = 8;
+  for (int k0 = warp; k0 < count; k0 += kAhead * kQ8Warps) {
+    float x[kAhead][W];
+    float2 ml[kAhead];
 #pragma unroll
-  for (int e = 0; e < W; ++e) acc[e] = 0.f;
-  for (int k = warp; k < count; k += kQ8Warps) {
-    // the first part is the second slot of its block, the others the first slots of theirs
-    const int64_t part = static_cast<int64_t>(2 * (block + k) + (k == 0)) * kMaxGroup + head;
-    const float pm = p.part_ml[part * 2], pl = p.part_ml[part * 2 + 1];
-    float x[W];
+    for (int i = 0; i < kAhead; ++i) {
+      const int k = k0 + i * kQ8Warps;
+      if (k < count) {
+        // the first part is the second slot of its block, the others are the first slots of theirs
+        const int64_t part = static_cast<int64_t>(2 * (block + k) + (k == 0)) * kMaxGroup + head;
+        const float* row = p.part_acc + part * D + lane * W;
+        if constexpr (W == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(row);
+          x[i][0] = v.x, x[i][1] = v.y, x[i][W - 2] = v.z, x[i][W - 1] = v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(row);
+          x[i][0] = v.x, x[i][1] = v.y;
+        }
+        ml[i] = *reinterpret_cast<const float2*>(p.part_ml + part * 2);
+      }
+    }
 #pragma unroll
-    for (int e = 0; e < W; ++e) x[e] = p.part_acc[part * D + lane * W + e];
-    const float top = fmaxf(m, pm), ref = top == -INFINITY ? 0.f : top;
-    const float keep = ex2_approx(m - ref), add = ex2_approx(pm - ref);
-    m = top;
-    l = l * keep + pl * add;
-#pragma unroll
-    for (int e = 0; e < W; ++e) acc[e] = acc[e] * keep + x[e] * add;
+    for (int i = 0; i < kAhead; ++i)
+      if (k0 + i * kQ8Warps < count) add_part(sum, top, z, x[i], ml[i].x, ml[i].y);
   }
 #pragma unroll
-  for (int e = 0; e < W; ++e) acc_s[warp][lane * W + e] = acc[e];
+  for (int e = 0; e < W; ++e) acc_s[warp][lane * W + e] = sum[e];
   if (lane == 0) {
-    ml_s[warp][0] = m;
-    ml_s[warp][1] = l;
+    ml_s[warp][0] = top;
+    ml_s[warp][1] = z;
   }
   __syncthreads();
   if (threadIdx.x < D) {
-    float top = -INFINITY, sum = 0.f, z = 0.f;
-#pragma unroll
-    for (int i = 0; i < kQ8Warps; ++i) top = fmaxf(top, ml_s[i][0]);
-    const float ref = top == -INFINITY ? 0.f : top;
+    float all[1] = {0.f}, best = kNoScore, l = 0.f;
 #pragma unroll
     for (int i = 0; i < kQ8Warps; ++i) {
-      const float keep = ex2_approx(ml_s[i][0] - ref);
-      sum += acc_s[i][threadIdx.x] * keep;
-      z += ml_s[i][1] * keep;
+      const float x[1] = {acc_s[i][threadIdx.x]};
+      add_part(all, best, l, x, ml_s[i][0], ml_s[i][1]);
     }
-    out[threadIdx.x] = z == 0.f ? 0.f : sum / z;
+    p.out[(unit * G + head) * D + threadIdx.x] = l == 0.f ? 0.f : all[0] / l;
   }
 }
 
@@ -818,8 +901,16 @@ cudaError_t launch_code(const Q8AttendParams& p, int d, int blocks, cudaStream_t
 
 }  // namespace
 
-cudaError_t launch_q8_attend(const Q8AttendParams& p, int head_dim, bool bf16, int code, int sms,
+int q8_attend_warps() { return kQ8Warps; }
+
+cudaError_t launch_q8_attend(const Q8AttendParams& params, int head_dim, bool bf16, int code, int sms,
                              cudaStream_t stream) {
+  Q8AttendParams p = params;
+  const int64_t elems = static_cast<int64_t>(p.batch) * (p.sel_ids ? p.num_kv_heads : 1);
+  const int64_t teams = p.sel_ids ? p.num_draws : p.max_teams;
+  const int64_t places = static_cast<int64_t>(p.batch) * p.num_kv_heads *
+                         (teams * (p.team_size / kTile) + kOpen + 1);
+  p.short_line = elems <= 32 * kScanRounds && places < (1ll << 30);
   if (code == kCodeI8)
     return bf16 ? launch_code<1, kCodeI8>(p, head_dim, sms, stream)
                 : launch_code<2, kCodeI8>(p, head_dim, sms, stream);

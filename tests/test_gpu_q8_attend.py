@@ -278,9 +278,15 @@ def test_equal_calls_give_equal_bits():
     first = h.run().clone()
     for _ in range(20):
         assert torch.equal(h.run(), first)
+    # one workspace for calls of different shapes, one after the other
     ws = torch.full((santa.santa_q8_workspace_bytes(5, 16, 4, 128, 128, c.table.shape[1]),), 0xff,
                     dtype=torch.uint8, device="cuda")
-    assert torch.equal(santa.santa_q8_dense_decode(q, c.cache, c.table, c.seq_lens, workspace=ws), first)
+    other = Q8([7000, 3000], 2, 64, 64, I8, seed=3)
+    qo = queries(other, 6, F32)
+    for _ in range(3):
+        assert torch.equal(santa.santa_q8_dense_decode(q, c.cache, c.table, c.seq_lens, workspace=ws), first)
+        check_dense(other, qo, santa.santa_q8_dense_decode(qo, other.cache, other.table, other.seq_lens,
+                                                           workspace=ws))
 
 
 def test_replayed_for_other_lengths_on_another_stream():

@@ -153,10 +153,11 @@ struct Q8AttendParams {
   float softcap;              // 0: none
   int window;                 // 0: none
   bool short_line;            // few units and tiles (set by the launcher)
-  // per block (one per multiprocessor): the unit that begins there and ends elsewhere (-1: none) with the
-  // number of its parts; two parts, sums and (reference, sum of weights); per warp a piece
-  int64_t* split_unit;        // [blocks]
-  int32_t* split_parts;       // [blocks]
+  // per block (at most q8_attend_most_blocks()): the unit that goes on there from the block before and
+  // the unit that begins there and goes on (-1: none), as far as it does not end there; their parts, sums
+  // and (reference, sum of weights); per warp a piece
+  int64_t* goes_on;           // [blocks]
+  int64_t* begins;            // [blocks]
   float* part_acc;            // [blocks][2][kMaxGroup][d]
   float* part_ml;             // [blocks][2][kMaxGroup][2]
   float* piece;               // [blocks][q8_attend_warps()][kMaxGroup][d]
@@ -164,7 +165,8 @@ struct Q8AttendParams {
   int32_t* status;
 };
 int q8_attend_warps();
-// One block per multiprocessor; two launches.
+int q8_attend_most_blocks();
+// `sms` blocks (one per multiprocessor); two launches.
 cudaError_t launch_q8_attend(const Q8AttendParams& p, int head_dim, bool bf16, int code, int sms,
                              cudaStream_t stream);
 

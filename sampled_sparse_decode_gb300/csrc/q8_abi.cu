@@ -45,10 +45,10 @@ struct Q8Layout {
   size_t split_bytes, ml_bytes, acc_bytes, bytes;
 };
 int q8_layout(int d, Q8Layout* l) {
-  l->sms = santa::device_sms();
+  l->sms = std::min(santa::device_sms(), santa::q8_attend_most_blocks());
   if (l->sms <= 0) return SANTA_ERR_CUDA;
   const size_t rows = static_cast<size_t>(l->sms) * santa::kMaxGroup;
-  l->split_bytes = round_up(l->sms * (sizeof(int64_t) + sizeof(int32_t)), kAlign);
+  l->split_bytes = round_up(2 * l->sms * sizeof(int64_t), kAlign);
   l->ml_bytes = round_up(2 * rows * 2 * sizeof(float), kAlign);
   l->acc_bytes = 2 * rows * d * sizeof(float);
   l->bytes = kAlign + l->split_bytes + l->ml_bytes + l->acc_bytes +
@@ -129,8 +129,8 @@ int launch_q8(const santa_decode_args* a, const santa_q8_args* c, bool listed, v
   p.window = c->window;
   unsigned char* base = reinterpret_cast<unsigned char*>(
       round_up(reinterpret_cast<uintptr_t>(a->workspace), kAlign));
-  p.split_unit = reinterpret_cast<int64_t*>(base);
-  p.split_parts = reinterpret_cast<int32_t*>(p.split_unit + l.sms);
+  p.goes_on = reinterpret_cast<int64_t*>(base);
+  p.begins = p.goes_on + l.sms;
   p.part_ml = reinterpret_cast<float*>(base += l.split_bytes);
   p.part_acc = reinterpret_cast<float*>(base += l.ml_bytes);
   p.piece = reinterpret_cast<float*>(base + l.acc_bytes);

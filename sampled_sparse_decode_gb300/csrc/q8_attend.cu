@@ -44,8 +44,9 @@ constexpr int kTile = 32;                  // tokens of a tile
 constexpr int kQ8Warps = 8;
 constexpr int kQ8Threads = kQ8Warps * 32;
 constexpr int kStages = 3;                 // tiles of a warp's ring
-constexpr int kOpen = 1;                   // what opening a unit counts, in tiles
+constexpr int kOpen = 2;                   // what opening a unit counts, in tiles
 constexpr int kScanRounds = 8;             // 32 sequences or units each that a warp reads by itself
+constexpr int kJoinRounds = 8;             // 32 blocks each that a unit may reach over
 constexpr float kNoScore = -1e38f;         // a reference before the first score
 constexpr float kSlack = 8.f;              // how far a score may pass the reference (base 2)
 constexpr float kTopWeight = 256.f;        // the same for a weight
@@ -141,19 +142,18 @@ struct Unit {
   int count;
   int tiles;
 };
-// Reads sequence b (dense) or unit (b, h) (listed); what is out of range is judged here and told if
-// `tell`.
-__device__ __forceinline__ Unit load_unit(const Q8AttendParams& p, int b, int h, bool tell) {
+// From a sequence's length and (listed) a unit's count of teams; what is out of range is judged here and
+// told if `tell`.
+__device__ __forceinline__ Unit judge_unit(const Q8AttendParams& p, int len, int count, bool tell) {
   Unit u;
-  u.len = p.seq_lens[b];
+  u.len = len;
   u.count = 0;
-  if (u.len < 0 || u.len > p.max_teams * p.team_size) {
+  if (len < 0 || len > p.max_teams * p.team_size) {
     if (tell) set_status(p.status, SANTA_DEV_BAD_SEQLEN);
     u.len = 0;
   }
   u.lo = p.window > 0 && u.len > p.window ? u.len - p.window : 0;
   if (p.sel_ids) {
-    const int count = p.sel_count[static_cast<int64_t>(b) * p.num_kv_heads + h];
     u.count = min(max(count, 0), p.num_draws);
     if (count != u.count && tell) set_status(p.status, SANTA_DEV_BAD_SEL);
     if (u.len == 0) u.count = 0;
@@ -162,6 +162,10 @@ __device__ __forceinline__ Unit load_unit(const Q8AttendParams& p, int b, int h,
     u.tiles = (u.len + kTile - 1) / kTile - u.lo / kTile;
   }
   return u;
+}
+__device__ __forceinline__ Unit load_unit(const Q8AttendParams& p, int b, int h, bool tell) {
+  return judge_unit(p, p.seq_lens[b],
+                    p.sel_ids ? p.sel_count[static_cast<int64_t>(b) * p.num_kv_heads + h] : 0, tell);
 }
 // A unit's length on the line: its tiles and its opening.
 __device__ __forceinline__ int64_t span(const Unit& u) { return u.tiles ? u.tiles + kOpen : 0; }
@@ -313,27 +317,48 @@ __device__ __forceinline__ void issue_tile(const Q8AttendParams& p, const Walk& 
   }
 }
 
-// The group's queries as B operands of the score: step s has dimensions 16 s + 4 t + 0 .. 3 of head
-// g, as a key's register has them.
-template <int NQ, int C, int D>
-__device__ __forceinline__ void load_queries(const Q8AttendParams& p, int b, int h,
-                                             Warp<NQ, C, D>& w) {
+// A unit's queries as they are in memory: a lane's share of the B operands of its scores.  Step s has
+// dimensions 16 s + 4 t + 0 .. 3 of head g, as a key's register has them.
+template <int NQ, int D>
+struct Queries {
+  uint32_t w[D / 16][2 * NQ];
+};
+template <int NQ, int D>
+__device__ __forceinline__ void fetch_queries(const Q8AttendParams& p, int b, int h,
+                                              Queries<NQ, D>& raw) {
   const int lane = threadIdx.x & 31, head = lane >> 2, t = lane & 3;
   const int G = p.num_q_heads / p.num_kv_heads;
   const int64_t at = (static_cast<int64_t>(b) * p.num_q_heads + h * G + head) * D + 4 * t;
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s) {
+    if constexpr (NQ == 1) {
+      uint2 v = make_uint2(0, 0);
+      if (head < G) v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + at + 16 * s);
+      raw.w[s][0] = v.x, raw.w[s][1] = v.y;
+    } else {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (head < G) v = *reinterpret_cast<const uint4*>(static_cast<const float*>(p.q) + at + 16 * s);
+      raw.w[s][0] = v.x, raw.w[s][1] = v.y, raw.w[s][2 * NQ - 2] = v.z, raw.w[s][2 * NQ - 1] = v.w;
+    }
+  }
+}
+
+// A unit's beginning: its queries as pieces, no score yet.
+template <int NQ, int C, int D>
+__device__ __forceinline__ void open_unit(const Q8AttendParams& p, const Queries<NQ, D>& raw,
+                                          Warp<NQ, C, D>& w) {
+  const int t = threadIdx.x & 3;
   float x[D / 4];
   uint32_t top = 0;
 #pragma unroll
   for (int s = 0; s < D / 16; ++s) {
     float* y = x + 4 * s;
-    if (head >= G) {
-      y[0] = y[1] = y[2] = y[3] = 0.f;
-    } else if constexpr (NQ == 1) {
-      const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + at + 16 * s);
-      y[0] = bf16_lo(v.x), y[1] = bf16_hi(v.x), y[2] = bf16_lo(v.y), y[3] = bf16_hi(v.y);
+    if constexpr (NQ == 1) {
+      y[0] = bf16_lo(raw.w[s][0]), y[1] = bf16_hi(raw.w[s][0]);
+      y[2] = bf16_lo(raw.w[s][1]), y[3] = bf16_hi(raw.w[s][1]);
     } else {
-      const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at + 16 * s);
-      y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = __uint_as_float(raw.w[s][i]);
     }
   }
 #pragma unroll
@@ -512,6 +537,11 @@ __device__ __forceinline__ void attend_tile(const Q8AttendParams& p, Warp<NQ, C,
   }
 }
 
+// Of a power of two between 2^-126 and 2^126.
+__device__ __forceinline__ float reciprocal(float two_to_k) {
+  return __uint_as_float((254u << 23) - __float_as_uint(two_to_k));
+}
+
 // The weights' sums of a warp's unit, over the lanes that share its heads.
 template <int NQ, int C, int D>
 __device__ __forceinline__ void close_sums(Warp<NQ, C, D>& w) {
@@ -530,7 +560,7 @@ __device__ __forceinline__ void store_piece(Warp<NQ, C, D>& w, int G, float* row
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     if (2 * t + i >= G) continue;
-    const float back = 1.f / w.inv[i];
+    const float back = reciprocal(w.inv[i]);
     float* row = rows + (2 * t + i) * stride + 2 * g;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j)
@@ -551,13 +581,12 @@ __device__ __forceinline__ void store_unit(Warp<NQ, C, D>& w, int G, float* out)
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     if (2 * t + i >= G) continue;
-    const float back = 1.f / w.inv[i], z = w.sum[i];
+    const float back = reciprocal(w.inv[i]), f = w.sum[i] == 0.f ? 0.f : 1.f / w.sum[i];
     float* row = out + (2 * t + i) * D + 2 * g;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j)
       *reinterpret_cast<float2*>(row + 16 * j) =
-          z == 0.f ? make_float2(0.f, 0.f)
-                   : make_float2(w.acc[j][i] * back / z, w.acc[j][2 + i] * back / z);
+          make_float2(w.acc[j][i] * back * f, w.acc[j][2 + i] * back * f);
   }
 }
 
@@ -604,21 +633,23 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
   Walk use;
   use.h = 0;
   if (p.short_line) {
-    // every warp for itself, without a barrier
-    int v[kScanRounds], upto[kScanRounds], sum = 0;
+    // every warp for itself, without a barrier; all loads first
+    int len[kScanRounds], count[kScanRounds], v[kScanRounds], upto[kScanRounds], sum = 0;
 #pragma unroll
     for (int i = 0; i < kScanRounds; ++i) {
-      v[i] = upto[i] = 0;
+      len[i] = count[i] = 0;
       if (32 * i >= elems) continue;
-      const int e = 32 * i + lane;
+      const unsigned e = 32 * i + lane;
       if (e < elems) {
-        const int b = p.sel_ids ? e / p.num_kv_heads : e;
-        v[i] = static_cast<int>(span(load_unit(p, b, e - b * p.num_kv_heads, tell && warp == 0))) * heads;
+        len[i] = p.seq_lens[p.sel_ids ? e / static_cast<unsigned>(p.num_kv_heads) : e];
+        if (p.sel_ids) count[i] = p.sel_count[e];
       }
     }
 #pragma unroll
     for (int i = 0; i < kScanRounds; ++i) {
+      v[i] = upto[i] = 0;
       if (32 * i >= elems) continue;
+      v[i] = static_cast<int>(span(judge_unit(p, len[i], count[i], tell && warp == 0))) * heads;
       upto[i] = warp_scan(v[i]) + sum;
       sum = __shfl_sync(0xffffffffu, upto[i], 31);
     }
@@ -633,8 +664,11 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
       if (32 * i >= elems) continue;
       const unsigned hit = __ballot_sync(0xffffffffu, upto[i] > c0 && upto[i] - v[i] <= c0);
       if (hit) {
-        elem = 32 * i + __ffs(hit) - 1;
-        base = __shfl_sync(0xffffffffu, upto[i] - v[i], __ffs(hit) - 1);
+        const int from = __ffs(hit) - 1;
+        elem = 32 * i + from;
+        base = __shfl_sync(0xffffffffu, upto[i] - v[i], from);
+        use.u = judge_unit(p, __shfl_sync(0xffffffffu, len[i], from),
+                           __shfl_sync(0xffffffffu, count[i], from), false);
       }
     }
     use.b = p.sel_ids ? elem / p.num_kv_heads : elem;
@@ -676,6 +710,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
     use.b = static_cast<int>(p.sel_ids ? start_s[0] / p.num_kv_heads : start_s[0]);
     if (p.sel_ids) use.h = static_cast<int>(start_s[0] - static_cast<int64_t>(use.b) * p.num_kv_heads);
     use.base = start_s[1];
+    if (c0 < total) use.u = load_unit(p, use.b, use.h, false);
     c0 += warp * share;
   }
   const int64_t block_share = share * kQ8Warps;
@@ -687,7 +722,6 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
   uint8_t* ring = smem + warp * R::kWarp;
   float* closing = p.piece + (static_cast<int64_t>(blockIdx.x) * kQ8Warps + warp) * kMaxGroup * D;
   if (c0 < c1) {
-    use.u = load_unit(p, use.b, use.h, false);
     walk_to(p, use, c0);
     Walk ask = use;
     int ask_k = static_cast<int>(max(c0 - use.base - kOpen, int64_t(0)));   // next tile of ask's unit
@@ -695,6 +729,8 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
     pc.b = -1;
     bool more = true;
     int put = 0, get = 0;
+    Queries<NQ, D> raw;
+    fetch_queries<NQ, D>(p, use.b, use.h, raw);
     auto ask_next = [&]() {
       if (more) {
         while (ask_k >= ask.u.tiles) {               // on to the next unit with a tile
@@ -719,7 +755,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
       const int k0 = static_cast<int>(max(c0 - use.base - kOpen, int64_t(0)));
       const int k1 = static_cast<int>(min(c1 - use.base - kOpen, static_cast<int64_t>(use.u.tiles)));
       if (k0 < k1) {
-        load_queries(p, use.b, use.h, w);
+        open_unit(p, raw, w);
         for (int k = k0; k < k1; ++k) {
           cp_async_wait<kStages - 2>();
           __syncwarp();
@@ -728,9 +764,19 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
           get = get + 1 == kStages ? 0 : get + 1;
           __syncwarp();
         }
-        const int64_t unit = static_cast<int64_t>(use.b) * p.num_kv_heads + use.h;
-        const Owner own = {unit, use.base, use.u.tiles, k0 == 0};
-        if (k1 < use.u.tiles) {
+      }
+      // on to the next unit with a tile, whose queries are asked for before this one's results are stored
+      const Walk now = use;
+      const bool last = now.base + span(now.u) >= c1;
+      if (!last) {
+        do next_unit(p, use);
+        while (use.u.tiles == 0 && use.base < c1);
+        fetch_queries<NQ, D>(p, use.b, use.h, raw);
+      }
+      if (k0 < k1) {
+        const int64_t unit = static_cast<int64_t>(now.b) * p.num_kv_heads + now.h;
+        const Owner own = {unit, now.base, now.u.tiles, k0 == 0};
+        if (k1 < now.u.tiles) {
           if (lane == 0) owner_s[1][warp] = own;
           store_piece(w, G, reinterpret_cast<float*>(ring), R::kPieceRow, ml_s[1][warp]);
         } else if (k0 > 0) {
@@ -740,22 +786,11 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
           store_unit(w, G, p.out + unit * G * D);
         }
       }
-      if (use.base + span(use.u) >= c1) break;
-      do next_unit(p, use);
-      while (use.u.tiles == 0 && use.base < c1);
+      if (last) break;
     }
   }
-  // units that see nothing
-  for (int64_t e = blockIdx.x; e < elems; e += gridDim.x) {
-    const int b = static_cast<int>(p.sel_ids ? e / p.num_kv_heads : e);
-    if (load_unit(p, b, p.sel_ids ? static_cast<int>(e - static_cast<int64_t>(b) * p.num_kv_heads) : 0, false).tiles)
-      continue;
-    float* row = p.out + e * heads * G * D;
-    for (int i = threadIdx.x; i < heads * G * D; i += kQ8Threads) row[i] = 0.f;
-  }
   __syncthreads();
-  int64_t split_unit = -1;                           // a unit that begins in this block and ends elsewhere
-  int split_parts = 0;
+  int64_t part_of[2] = {-1, -1};                     // units of the block's parts
 
   // The block's chains: pieces that go on, up to one that closes the unit or to the block's end; before
   // them a piece at the block's start that only closes (w = -1).
@@ -800,16 +835,20 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
           *reinterpret_cast<float2*>(p.part_ml + (part + head) * 2) = make_float2(top, z);
       }
     }
-    if (!whole && slot) {
-      split_unit = own.unit;
-      split_parts = static_cast<int>((own.base + kOpen + own.tiles - 1) / block_share -
-                                     (own.base + kOpen) / block_share) + 1;
-    }
+    if (!whole) part_of[slot] = own.unit;
     w = lone ? 0 : end;
   }
   if (threadIdx.x == 0) {
-    p.split_unit[blockIdx.x] = split_unit;
-    p.split_parts[blockIdx.x] = split_parts;
+    p.goes_on[blockIdx.x] = part_of[0];
+    p.begins[blockIdx.x] = part_of[1];
+  }
+  // units that see nothing
+  for (int64_t e = blockIdx.x; e < elems; e += gridDim.x) {
+    const int b = static_cast<int>(p.sel_ids ? e / p.num_kv_heads : e);
+    if (load_unit(p, b, p.sel_ids ? static_cast<int>(e - static_cast<int64_t>(b) * p.num_kv_heads) : 0, false).tiles)
+      continue;
+    float* row = p.out + e * heads * G * D;
+    for (int i = threadIdx.x; i < heads * G * D; i += kQ8Threads) row[i] = 0.f;
   }
 }
 
@@ -824,9 +863,23 @@ __global__ void __launch_bounds__(kQ8Threads) q8_join_kernel(Q8AttendParams p) {
   const int G = p.num_q_heads / p.num_kv_heads;
   const int block = blockIdx.x / G, head = blockIdx.x % G;
   grid_dependency_wait();
-  const int64_t unit = p.split_unit[block];
-  const int count = p.split_parts[block];
+  const int blocks = gridDim.x / G;
+  const int64_t unit = p.begins[block];
+  // the unit's parts: of this block and of those after it in which it goes on
+  int count = 1;
+  int64_t after[kJoinRounds];
+#pragma unroll
+  for (int i = 0; i < kJoinRounds; ++i) {
+    const int k = block + 1 + 32 * i + lane;
+    after[i] = k < blocks ? p.goes_on[k] : -1;
+  }
   if (unit < 0) return;
+#pragma unroll
+  for (int i = 0; i < kJoinRounds; ++i) {
+    const unsigned miss = __ballot_sync(0xffffffffu, after[i] != unit);
+    count += miss ? __ffs(miss) - 1 : 32;
+    if (miss) break;
+  }
   float sum[W] = {}, top = kNoScore, z = 0.f;
   constexpr int kAhead = 8;
   for (int k0 = warp; k0 < count; k0 += kAhead * kQ8Warps) {
@@ -902,6 +955,7 @@ cudaError_t launch_code(const Q8AttendParams& p, int d, int blocks, cudaStream_t
 }  // namespace
 
 int q8_attend_warps() { return kQ8Warps; }
+int q8_attend_most_blocks() { return 32 * kJoinRounds; }
 
 cudaError_t launch_q8_attend(const Q8AttendParams& params, int head_dim, bool bf16, int code, int sms,
                              cudaStream_t stream) {

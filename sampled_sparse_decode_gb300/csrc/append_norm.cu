@@ -7,12 +7,17 @@
 //   rotation
 //   representative = mean of the page's keys as stored
 //
-// The work items are those of append_chunk.cu: page items (half of the block for the keys, half for
-// the values) and query items, with the same search for a block's sequence.  A row lies in the
-// registers of 4 to 16 neighbouring lanes, two 16-byte pieces each, so the norm's sum and the row's
-// largest magnitude are shuffles among them, and every element is read once and written once.
+// The work items are those of append_chunk.cu, page items (touched page, KV head) and query items, with
+// the same search for a block's sequence.  A row lies in the registers of 8 or 16 neighbouring lanes,
+// two quads of elements each: the two that a rotation by halves pairs up, or neighbours.  The norm's sum
+// and the row's largest magnitude are shuffles among them; every element is read once and written once.
+// Quads rather than 16-byte pieces keep a thread's row, sums and weights in 8 registers each, so that
+// three blocks stay on a multiprocessor.
+//
 // With a cache of the activations' type the mean is summed in the order of reps.cu (its bits are
-// santa_build_reps's); with 8 bits in the same order over the values that the codes stand for.
+// santa_build_reps's): rows group, group + kGroups, ... of a quad in row order, then the groups.  bf16 rows
+// fill a block with the groups of reps.cu, and the values are blocks of their own; fp32 rows fill half of
+// one, and the other half takes the values.
 #include "append.cuh"
 #include "q8.cuh"
 
@@ -20,180 +25,386 @@ namespace santa {
 
 namespace {
 
-// Where a thread's two pieces of a row stand, and what becomes of them.
-struct Lane {
-  int ca, cb;        // pieces
-  int first;         // of the table row, for rotated pieces
-  bool turned;
+constexpr int kQuad = 4;                             // elements
+
+template <bool BF16, int D>
+struct Rows {
+  static constexpr int kQuads = D / kQuad;           // of a row
+  static constexpr int kLanes = kQuads / 2;          // of a row
+  static constexpr int kGroups = 256 / (D * (BF16 ? 2 : 4) / 16);   // row groups of reps.cu
+  static constexpr int kTeam = kGroups * kLanes;     // threads that share a page's keys or values
+  static constexpr bool kApart = kTeam == kAppendThreads;   // keys and values in blocks of their own
+  static constexpr int kLoad = BF16 ? 4 : 2;         // rows whose loads go out together
+  static constexpr int kHeads = BF16 ? 8 : 4;        // query heads that share cosines and sines
+  static_assert(kApart || kTeam == kAppendThreads / 2, "the block is one team or two");
 };
 
+// A quad as it is in memory: two words (bf16) or four.
 template <bool BF16>
+struct Raw {
+  uint32_t w[BF16 ? 2 : 4];
+};
+template <bool BF16>
+__device__ __forceinline__ Raw<BF16> load_raw(const void* base, int64_t element) {
+  Raw<BF16> r;
+  if constexpr (BF16) {
+    const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + element);
+    r.w[0] = v.x, r.w[1] = v.y;
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const float*>(base) + element);
+    r.w[0] = v.x, r.w[1] = v.y, r.w[2] = v.z, r.w[3] = v.w;
+  }
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ void store_raw(void* base, int64_t element, const Raw<BF16>& r) {
+  if constexpr (BF16)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + element) = make_uint2(r.w[0], r.w[1]);
+  else
+    *reinterpret_cast<uint4*>(static_cast<float*>(base) + element) =
+        make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+}
+// A lane's part of a row: two quads, (x[0], x[1]) and (x[2], x[3]), each x two neighbours in a register
+// pair, so that one instruction works on both.
+struct Part {
+  uint64_t x[4];
+};
+template <bool BF16>
+__device__ __forceinline__ void values_of(const Raw<BF16>& r, uint64_t& lo, uint64_t& hi) {
+  if constexpr (BF16) {
+    lo = pair(bf16_lo(r.w[0]), bf16_hi(r.w[0]));
+    hi = pair(bf16_lo(r.w[1]), bf16_hi(r.w[1]));
+  } else {
+    lo = pair(__uint_as_float(r.w[0]), __uint_as_float(r.w[1]));
+    hi = pair(__uint_as_float(r.w[2]), __uint_as_float(r.w[3]));
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ Part values_of(const Raw<BF16>& a, const Raw<BF16>& b) {
+  Part r;
+  values_of<BF16>(a, r.x[0], r.x[1]);
+  values_of<BF16>(b, r.x[2], r.x[3]);
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ Raw<BF16> round_to(uint64_t lo, uint64_t hi) {
+  const float2 a = halves(lo), b = halves(hi);
+  Raw<BF16> r;
+  if constexpr (BF16) {
+    r.w[0] = pack_bf16(a.x, a.y), r.w[1] = pack_bf16(b.x, b.y);
+  } else {
+    r.w[0] = __float_as_uint(a.x), r.w[1] = __float_as_uint(a.y);
+    r.w[2] = __float_as_uint(b.x), r.w[3] = __float_as_uint(b.y);
+  }
+  return r;
+}
+
+// Where a lane's two quads stand in a row (elements), and where its angles start in a table row.
+struct Lane {
+  int a, b;
+  int first;
+  bool turned;
+};
 __device__ __forceinline__ Lane lane_of(const AppendChunkParams& p, int pr) {
-  constexpr int V = Piece<BF16>::kVec;
+  const int half = p.interleaved ? 0 : p.rope_dim / (2 * kQuad);
   Lane l;
-  pair_pieces<BF16>(pr, p.rope_dim, p.interleaved, &l.ca, &l.cb);
-  l.first = p.interleaved ? l.ca * V / 2 : l.ca * V;
-  l.turned = l.ca * V < p.rope_dim;
+  if (pr < half) {
+    l.a = kQuad * pr;
+    l.b = l.a + kQuad * half;
+  } else {
+    l.a = 2 * kQuad * pr;                            // neighbours, behind the paired ones
+    l.b = l.a + kQuad;
+  }
+  l.first = p.interleaved ? l.a / 2 : l.a;
+  l.turned = l.a < p.rope_dim;
   return l;
 }
 
-// Sum and largest word over the `kLanes` neighbouring lanes that hold a row (every lane of the warp
-// takes part).
-template <int kLanes>
-__device__ __forceinline__ float row_sum(float v) {
+// Largest magnitudes of N rows over the kLanes neighbouring lanes that hold a row (the whole warp calls).
+template <int kLanes, int N>
+__device__ __forceinline__ void row_max(float (&v)[N]) {
 #pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float u = __shfl_xor_sync(0xffffffffu, v[i], o);
+      v[i] = max_abs(v[i], u, u);
+    }
 }
-template <int kLanes>
-__device__ __forceinline__ uint32_t row_max(uint32_t v) {
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-
-template <int V>
-__device__ __forceinline__ uint32_t magnitude(const float (&a)[V], const float (&b)[V]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int e = 0; e < V; ++e)
-    m = max(m, max(__float_as_uint(a[e]) & 0x7fffffffu, __float_as_uint(b[e]) & 0x7fffffffu));
-  return m;
+__device__ __forceinline__ float magnitude(const Part& v) {
+  const float2 a = halves(v.x[0]), b = halves(v.x[1]), c = halves(v.x[2]), d = halves(v.x[3]);
+  return max_abs(max_abs(max_abs(a.x, a.y, b.x), b.y, c.x), max_abs(c.y, d.x, d.y), 0.f);
 }
 
-// A thread's part of a norm's weights.
-template <int V>
-__device__ __forceinline__ void load_weights(const float* w, const Lane& l, float (&wa)[V],
-                                             float (&wb)[V]) {
+// A lane's part of a norm's weights.
+__device__ __forceinline__ Part load_weights(const float* w, const Lane& l) {
+  Part r;
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    wa[e] = w ? w[l.ca * V + e] : 1.f;
-    wb[e] = w ? w[l.cb * V + e] : 1.f;
+  for (int i = 0; i < 4; ++i) r.x[i] = twice(1.f);
+  if (w) {
+    const float4 a = *reinterpret_cast<const float4*>(w + l.a);
+    const float4 b = *reinterpret_cast<const float4*>(w + l.b);
+    r = {{pair(a.x, a.y), pair(a.z, a.w), pair(b.x, b.y), pair(b.z, b.w)}};
+  }
+  return r;
+}
+// N rows at a time, so that their chains of shuffles overlap.
+template <int kLanes, int D, int N>
+__device__ __forceinline__ void norm_rows(Part (&v)[N], const Part& w, float eps) {
+  float ss[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    uint64_t s = mul_pair(v[i].x[0], v[i].x[0]);
+#pragma unroll
+    for (int e = 1; e < 4; ++e) s = fma_pair(v[i].x[e], v[i].x[e], s);
+    const float2 h = halves(s);
+    ss[i] = h.x + h.y;
+  }
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], o);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint64_t r = twice(rsqrtf(ss[i] * (1.f / D) + eps));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[i].x[e] = mul_pair(mul_pair(v[i].x[e], r), w.x[e]);
   }
 }
 
-template <int V, int kLanes>
-__device__ __forceinline__ void norm_row(float (&a)[V], float (&b)[V], const float (&wa)[V],
-                                         const float (&wb)[V], int d, float eps) {
-  float ss = 0.f;
-#pragma unroll
-  for (int e = 0; e < V; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
-  const float r = __frsqrt_rn(row_sum<kLanes>(ss) / d + eps);
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-    a[e] = a[e] * r * wa[e];
-    b[e] = b[e] * r * wb[e];
-  }
+// Cosines and sines of a lane's four pairs of elements at one position.
+struct Angles {
+  float4 c, s;
+};
+__device__ __forceinline__ Angles load_angles(const float* row, int half_dim) {
+  return {*reinterpret_cast<const float4*>(row), *reinterpret_cast<const float4*>(row + half_dim)};
 }
-
-// The rotation of a thread's pieces by the table row's entries from `first` on: by halves the pairs
-// are (a_e, b_e); interleaved they are neighbours, V / 2 entries for each piece.
-template <int V>
-__device__ __forceinline__ void turn_row(float (&a)[V], float (&b)[V], const float* row,
-                                         int half_dim, int first, bool interleaved) {
-#pragma unroll
-  for (int g = 0; g < V / 4; ++g) {
-    const float4 c4 = *reinterpret_cast<const float4*>(row + first + 4 * g);
-    const float4 s4 = *reinterpret_cast<const float4*>(row + half_dim + first + 4 * g);
-    const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+// By halves the rotated pairs are (a_e, b_e) of the two quads, interleaved they are neighbours.  EXACT:
+// products and sums rounded one by one, as in append_chunk.cu, for calls without norms (one by one also in
+// the instructions: a product and a sum of register pairs may be contracted); else the first product in the
+// sum's rounding.
+template <bool EXACT>
+__device__ __forceinline__ void turn_row(Part& v, const Angles& t, bool interleaved) {
+  const float c[4] = {t.c.x, t.c.y, t.c.z, t.c.w}, s[4] = {t.s.x, t.s.y, t.s.z, t.s.w};
+  if constexpr (EXACT) {
+    float x[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (!interleaved) {
-        turn_pair(a[4 * g + i], b[4 * g + i], c[i], s[i]);
-      } else {
-        const int e = 2 * (4 * g + i);
-        if (e < V)
-          turn_pair(a[e], a[e + 1], c[i], s[i]);
-        else
-          turn_pair(b[e - V], b[e - V + 1], c[i], s[i]);
+      const float2 h = halves(v.x[i]);
+      x[2 * i] = h.x, x[2 * i + 1] = h.y;
+    }
+    if (interleaved) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) turn_pair(x[2 * i], x[2 * i + 1], c[i], s[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) turn_pair(x[i], x[4 + i], c[i], s[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v.x[i] = pair(x[2 * i], x[2 * i + 1]);
+  } else if (interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 h = halves(v.x[i]);
+      v.x[i] = fma_pair(v.x[i], twice(c[i]), mul_pair(pair(h.y, h.x), pair(-s[i], s[i])));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t x = v.x[i], y = v.x[2 + i], cc = pair(c[2 * i], c[2 * i + 1]);
+      v.x[i] = fma_pair(x, cc, mul_pair(y, pair(-s[2 * i], -s[2 * i + 1])));
+      v.x[2 + i] = fma_pair(y, cc, mul_pair(x, pair(s[2 * i], s[2 * i + 1])));
+    }
+  }
+}
+
+// A touched page: its rows before row0 are cached already, row0 .. row1 - 1 are new.
+struct Page {
+  int row0, row1;
+  int64_t tok0;        // token row of page row 0 (may be before the chunk's first)
+  int64_t at;          // row 0 among the cache's rows
+  int64_t pos;         // position of row 0
+};
+
+template <bool BF16, int C, int D, bool NORM>
+__device__ __forceinline__ void key_rows(const AppendNormParams& p, const Page& pg, int h, int thread,
+                                         float* part) {
+  using R = Rows<BF16, D>;
+  constexpr int kElement = BF16 ? 2 : 4, kCached = C == kCodeNone ? kElement : 1;   // bytes
+  const int group = thread / R::kLanes;
+  const Lane l = lane_of(p, thread % R::kLanes);
+  const Part w = load_weights(NORM ? p.k_norm : nullptr, l);
+  // this lane's quads of page row `group` among the new rows (may be before the first) and in the cache
+  const char* src =
+      static_cast<const char*>(p.k_new) + ((pg.tok0 + group) * p.k_stride + h * D) * kElement;
+  const int64_t src_step = R::kGroups * p.k_stride * kElement;
+  char* pool = static_cast<char*>(p.k_pool) + (pg.at + group) * D * kCached;
+  float* scales = p.k_scale + pg.at + group;
+  const float* angles = p.rope + (pg.pos + group) * p.rope_dim + l.first;
+  Part sum;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sum.x[e] = 0;
+  for (int base = group; base - group < pg.row1; base += R::kLoad * R::kGroups) {
+    Raw<BF16> xa[R::kLoad] = {}, xb[R::kLoad] = {};
+    float old[R::kLoad] = {};                        // scales of earlier rows
+#pragma unroll
+    for (int i = 0; i < R::kLoad; ++i) {
+      const int r = base + i * R::kGroups;
+      const char* row = src + i * src_step;
+      const char* cached = pool + i * R::kGroups * D * kCached;
+      if (r >= pg.row0 && r < pg.row1) {
+        xa[i] = load_raw<BF16>(row, l.a);
+        xb[i] = load_raw<BF16>(row, l.b);
+      } else if (r < pg.row1) {
+        if constexpr (C == kCodeNone) {
+          xa[i] = load_raw<BF16>(cached, l.a);
+          xb[i] = load_raw<BF16>(cached, l.b);
+        } else {
+          xa[i].w[0] = *reinterpret_cast<const uint32_t*>(cached + l.a);
+          xb[i].w[0] = *reinterpret_cast<const uint32_t*>(cached + l.b);
+          old[i] = scales[i * R::kGroups];
+        }
       }
     }
-  }
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint4 pack(const float (&x)[Piece<BF16>::kVec]) {
-  if constexpr (BF16)
-    return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                      pack_bf16(x[6], x[7]));
-  else
-    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
-                      __float_as_uint(x[3]));
-}
-
-// V codes of a piece: one or two words.
-template <int C, int V>
-__device__ __forceinline__ void store_codes(uint8_t* at, float (&x)[V], float scale) {
-  uint32_t w[V / 4];
 #pragma unroll
-  for (int i = 0; i < V / 4; ++i) {
-    float y[4] = {x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
-    w[i] = q8_encode<C>(y, scale);
-    x[4 * i] = y[0], x[4 * i + 1] = y[1], x[4 * i + 2] = y[2], x[4 * i + 3] = y[3];
-  }
-  if constexpr (V == 8)
-    *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
-  else
-    *reinterpret_cast<uint32_t*>(at) = w[0];
-}
-
-// Stores a row's pieces at cache row `at` (a row index over all pages and heads); a and b become
-// the values as stored.  Every lane of the warp takes part, `on` says which have a row.
-template <bool BF16, int C, int D>
-__device__ __forceinline__ void store_row(void* pool, float* scales, int64_t at, const Lane& l,
-                                          bool on, float (&a)[Piece<BF16>::kVec],
-                                          float (&b)[Piece<BF16>::kVec]) {
-  constexpr int V = Piece<BF16>::kVec;
-  if constexpr (C == kCodeNone) {
-    const uint4 wa = pack<BF16>(a), wb = pack<BF16>(b);
-    if (on) {
-      uint4* row = static_cast<uint4*>(pool) + at * (D / V);
-      row[l.ca] = wa;
-      row[l.cb] = wb;
+    for (int i = 0; i < R::kLoad; ++i) {
+      const int r = base + i * R::kGroups;
+      if (r - group >= pg.row1) break;               // no lane of the team has such a row
+      const bool on = r >= pg.row0 && r < pg.row1;
+      // what is added to the mean: the row as stored, codes' values with their scale
+      Part v[1];
+      float scale = 1.f;
+      if (r - group + R::kGroups > pg.row0) {        // new rows among the team's: all lanes take part
+        v[0] = values_of<BF16>(xa[i], xb[i]);
+        Angles t = {};
+        if (on && l.turned) t = load_angles(angles + i * R::kGroups * p.rope_dim, p.rope_dim / 2);
+        if (NORM && p.k_norm) norm_rows<R::kLanes, D>(v, w, p.eps);
+        if (l.turned) turn_row<!NORM>(v[0], t, p.interleaved);
+        char* cached = pool + i * R::kGroups * D * kCached;
+        if constexpr (C == kCodeNone) {
+          if (on) {
+            const Raw<BF16> a = round_to<BF16>(v[0].x[0], v[0].x[1]), b = round_to<BF16>(v[0].x[2], v[0].x[3]);
+            store_raw<BF16>(cached, l.a, a);
+            store_raw<BF16>(cached, l.b, b);
+            v[0] = values_of<BF16>(a, b);
+          }
+        } else {
+          float amax[1] = {magnitude(v[0])};
+          row_max<R::kLanes>(amax);
+          if (on) {
+            const Scale s = q8_scale<C>(amax[0]);
+            uint64_t a[2] = {v[0].x[0], v[0].x[1]}, b[2] = {v[0].x[2], v[0].x[3]};
+            *reinterpret_cast<uint32_t*>(cached + l.a) = q8_encode<C>(a, s);
+            *reinterpret_cast<uint32_t*>(cached + l.b) = q8_encode<C>(b, s);
+            if (l.a == 0) scales[i * R::kGroups] = s.s;
+            v[0] = {{a[0], a[1], b[0], b[1]}};
+            scale = s.s;
+          }
+        }
+      }
+      if (r < pg.row0) {
+        if constexpr (C == kCodeNone) {
+          v[0] = values_of<BF16>(xa[i], xb[i]);
+        } else {
+          float a[kQuad], b[kQuad];
+          q8_decode<C>(xa[i].w[0], a);
+          q8_decode<C>(xb[i].w[0], b);
+          v[0] = {{pair(a[0], a[1]), pair(a[2], a[3]), pair(b[0], b[1]), pair(b[2], b[3])}};
+          scale = old[i];
+        }
+      }
+      if (r < pg.row1) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          sum.x[e] = C == kCodeNone ? add_pair(sum.x[e], v[0].x[e])
+                                    : fma_pair(v[0].x[e], twice(scale), sum.x[e]);
+      }
     }
-    unpack<BF16>(wa, a);
-    unpack<BF16>(wb, b);
-  } else {
-    const float scale = q8_scale<C>(row_max<D / V / 2>(magnitude(a, b)));
-    if (!on) return;
-    uint8_t* row = static_cast<uint8_t*>(pool) + at * D;
-    store_codes<C>(row + l.ca * V, a, scale);
-    store_codes<C>(row + l.cb * V, b, scale);
-    if (threadIdx.x % (D / V / 2) == 0) scales[at] = scale;
+    src += R::kLoad * src_step;
+    pool += R::kLoad * R::kGroups * D * kCached;
+    scales += R::kLoad * R::kGroups;
+    angles += static_cast<int64_t>(R::kLoad) * R::kGroups * p.rope_dim;
   }
+  const float2 s0 = halves(sum.x[0]), s1 = halves(sum.x[1]), s2 = halves(sum.x[2]), s3 = halves(sum.x[3]);
+  *reinterpret_cast<float4*>(part + group * D + l.a) = make_float4(s0.x, s0.y, s1.x, s1.y);
+  *reinterpret_cast<float4*>(part + group * D + l.b) = make_float4(s2.x, s2.y, s3.x, s3.y);
 }
 
-// The values of V codes in the first words of `w`.
-template <int C, int V>
-__device__ __forceinline__ void stored_codes(const uint4& w, float scale, float (&x)[V]) {
-  const uint32_t word[2] = {w.x, w.y};
-#pragma unroll
-  for (int i = 0; i < V / 4; ++i) {
-    float y[4];
-    q8_decode<C>(word[i], y);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[4 * i + e] = y[e] * scale;
-  }
-}
-template <int V>
-__device__ __forceinline__ void load_codes(const uint8_t* at, uint4& w) {
-  if constexpr (V == 8) {
-    const uint2 c = *reinterpret_cast<const uint2*>(at);
-    w.x = c.x;
-    w.y = c.y;
-  } else {
-    w.x = *reinterpret_cast<const uint32_t*>(at);
-  }
-}
-
+// Values: a lane has two 16-byte pieces of a row, half a row apart (nothing else is held in registers).
 template <bool BF16, int C, int D>
-__device__ void norm_page_item(const AppendNormParams& p, int64_t slot, int h, float* part) {
-  constexpr int V = Piece<BF16>::kVec;
-  constexpr int kCols = D / V;                       // pieces per row
-  constexpr int kPairs = kCols / 2;                  // lanes per row
-  constexpr int kGroups = 256 / kCols;               // row groups of the mean (as in reps.cu)
-  constexpr int kBatch = 4;                          // rows whose loads go out together
-  static_assert(kPairs * kGroups == kAppendThreads / 2, "half of the block covers the split");
+__device__ __forceinline__ void value_rows(const AppendNormParams& p, const Page& pg, int h, int thread) {
+  constexpr int V = Piece<BF16>::kVec, kLanes = D / V / 2, kRows = Rows<BF16, D>::kTeam / kLanes;
+  constexpr int kElement = BF16 ? 2 : 4, kCached = C == kCodeNone ? kElement : 1;   // bytes
+  constexpr int kLoad = 4;
+  const int group = thread / kLanes, col = thread % kLanes * V;
+  const char* src = static_cast<const char*>(p.v_new) +
+                    ((pg.tok0 + pg.row0 + group) * p.v_stride + h * D + col) * kElement;
+  const int64_t src_step = kRows * p.v_stride * kElement;
+  char* pool = static_cast<char*>(p.v_pool) + ((pg.at + pg.row0 + group) * D + col) * kCached;
+  float* scales = p.v_scale + pg.at + pg.row0 + group;
+  for (int base = pg.row0 + group; base - group < pg.row1; base += kLoad * kRows) {
+    uint4 xa[kLoad] = {}, xb[kLoad] = {};
+#pragma unroll
+    for (int i = 0; i < kLoad; ++i)
+      if (base + i * kRows < pg.row1) {
+        xa[i] = *reinterpret_cast<const uint4*>(src + i * src_step);
+        xb[i] = *reinterpret_cast<const uint4*>(src + i * src_step + D / 2 * kElement);
+      }
+#pragma unroll
+    for (int i = 0; i < kLoad; ++i) {
+      const int r = base + i * kRows;
+      if (r - group >= pg.row1) break;
+      char* row = pool + i * kRows * D * kCached;
+      if constexpr (C == kCodeNone) {
+        if (r < pg.row1) {
+          *reinterpret_cast<uint4*>(row) = xa[i];
+          *reinterpret_cast<uint4*>(row + D / 2 * kElement) = xb[i];
+        }
+      } else {
+        float a[V], b[V], amax[1];
+        unpack<BF16>(xa[i], a);
+        unpack<BF16>(xb[i], b);
+        if constexpr (BF16) {
+          const uint32_t m = max_abs_bf16x2(
+              max_abs_bf16x2(max_abs_bf16x2(xa[i].x, xa[i].y), max_abs_bf16x2(xa[i].z, xa[i].w)),
+              max_abs_bf16x2(max_abs_bf16x2(xb[i].x, xb[i].y), max_abs_bf16x2(xb[i].z, xb[i].w)));
+          amax[0] = max_abs(bf16_lo(m), bf16_hi(m), bf16_hi(m));
+        } else {
+          amax[0] = max_abs(max_abs(max_abs(a[0], a[1], a[2]), a[3], b[0]),
+                            max_abs(b[1], b[2], b[3]), 0.f);
+        }
+        row_max<kLanes>(amax);
+        if (r < pg.row1) {
+          const Scale s = q8_scale<C>(amax[0]);
+#pragma unroll
+          for (int piece = 0; piece < 2; ++piece) {
+            uint32_t codes[V / 4];
+#pragma unroll
+            for (int q = 0; q < V / 4; ++q) {
+              const float* x = (piece ? b : a) + 4 * q;
+              uint64_t y[2] = {pair(x[0], x[1]), pair(x[2], x[3])};
+              codes[q] = q8_encode<C>(y, s);
+            }
+            char* to = row + piece * (D / 2);
+            if constexpr (BF16)
+              *reinterpret_cast<uint2*>(to) = make_uint2(codes[0], codes[V / 4 - 1]);
+            else
+              *reinterpret_cast<uint32_t*>(to) = codes[0];
+          }
+          if (col == 0) scales[i * kRows] = s.s;
+        }
+      }
+    }
+    src += kLoad * src_step;
+    pool += kLoad * kRows * D * kCached;
+    scales += kLoad * kRows;
+  }
+}
+
+template <bool BF16, int C, int D, bool NORM>
+__device__ __forceinline__ void norm_page_item(const AppendNormParams& p, int64_t slot, int h,
+                                               bool values, float* part) {
+  using R = Rows<BF16, D>;
   const int T = p.team_size;
   const int b = find_sequence(p.cu_q, p.batch, p.num_tokens, T, 2, slot);
   Chunk c;
@@ -202,7 +413,7 @@ __device__ void norm_page_item(const AppendNormParams& p, int64_t slot, int h, f
     return;
   }
   const int64_t j = slot - (c.first / T + 2 * static_cast<int64_t>(b));
-  if (j == 0 && h == 0 && threadIdx.x == 0 && p.seq_lens_next)
+  if (j == 0 && h == 0 && !values && threadIdx.x == 0 && p.seq_lens_next)
     p.seq_lens_next[b] = static_cast<int32_t>(c.len + c.n);
   const int64_t team = c.len / T + j;                // the touched page, by position
   if (c.n == 0 || j < 0 || team * T >= c.len + c.n) return;
@@ -211,202 +422,129 @@ __device__ void norm_page_item(const AppendNormParams& p, int64_t slot, int h, f
     if (threadIdx.x == 0) set_status(p.status, SANTA_DEV_BAD_PAGE);
     return;
   }
-  const int row0 = static_cast<int>(max(c.len - team * T, static_cast<int64_t>(0)));
-  const int row1 = static_cast<int>(min(c.len + c.n - team * T, static_cast<int64_t>(T)));
-  const int64_t tok0 = c.first + team * T - c.len;   // token row of page row 0 (may be < first)
-  const int64_t blk = (page * p.num_kv_heads + h) * static_cast<int64_t>(T);
-  const int group = threadIdx.x % (kAppendThreads / 2) / kPairs;
-
-  if (threadIdx.x < kAppendThreads / 2) {
-    const Lane l = lane_of<BF16>(p, threadIdx.x % kPairs);
-    const uint4* src = static_cast<const uint4*>(p.k_new) + h * kCols;
-    const int64_t stride = p.k_stride / V;
-    float wa[V], wb[V], sa[V], sb[V];
-    load_weights<V>(p.k_norm, l, wa, wb);
-#pragma unroll
-    for (int e = 0; e < V; ++e) sa[e] = sb[e] = 0.f;
-    for (int base = 0; base < row1; base += kBatch * kGroups) {
-      uint4 xa[kBatch] = {}, xb[kBatch] = {};
-      float old[kBatch] = {};                        // scales of earlier rows
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int r = base + group + i * kGroups;
-        if (r >= row0 && r < row1) {
-          xa[i] = src[(tok0 + r) * stride + l.ca];
-          xb[i] = src[(tok0 + r) * stride + l.cb];
-        } else if (r < row1) {
-          if constexpr (C == kCodeNone) {
-            const uint4* row = static_cast<const uint4*>(p.k_pool) + (blk + r) * kCols;
-            xa[i] = row[l.ca];
-            xb[i] = row[l.cb];
-          } else {
-            const uint8_t* row = static_cast<const uint8_t*>(p.k_pool) + (blk + r) * D;
-            load_codes<V>(row + l.ca * V, xa[i]);
-            load_codes<V>(row + l.cb * V, xb[i]);
-            old[i] = p.k_scale[blk + r];
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        if (base + i * kGroups >= row1) break;       // no lane of the block has such a row
-        const int r = base + group + i * kGroups;
-        const bool on = r >= row0 && r < row1;
-        float a[V], y[V];
-        unpack<BF16>(xa[i], a);
-        unpack<BF16>(xb[i], y);
-        if (base + (i + 1) * kGroups > row0) {       // new rows among the block's
-          float na[V], nb[V];
-#pragma unroll
-          for (int e = 0; e < V; ++e) na[e] = a[e], nb[e] = y[e];
-          if (p.k_norm) norm_row<V, kPairs>(na, nb, wa, wb, D, p.eps);
-          if (on && l.turned)
-            turn_row<V>(na, nb, p.rope + (team * T + r) * p.rope_dim, p.rope_dim / 2, l.first,
-                        p.interleaved);
-          store_row<BF16, C, D>(p.k_pool, p.k_scale, blk + r, l, on, na, nb);
-          if (on) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) a[e] = na[e], y[e] = nb[e];
-          }
-        }
-        if constexpr (C != kCodeNone) {
-          if (r < row0) {
-            stored_codes<C, V>(xa[i], old[i], a);
-            stored_codes<C, V>(xb[i], old[i], y);
-          }
-        }
-        if (r < row1) {
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            sa[e] += a[e];
-            sb[e] += y[e];
-          }
-        }
-      }
+  Page pg;
+  pg.row0 = static_cast<int>(max(c.len - team * T, static_cast<int64_t>(0)));
+  pg.row1 = static_cast<int>(min(c.len + c.n - team * T, static_cast<int64_t>(T)));
+  pg.tok0 = c.first + team * T - c.len;
+  pg.at = (page * p.num_kv_heads + h) * static_cast<int64_t>(T);
+  pg.pos = team * T;
+  if constexpr (R::kApart) {
+    if (values) {
+      value_rows<BF16, C, D>(p, pg, h, threadIdx.x);
+      return;
     }
-#pragma unroll
-    for (int e = 0; e < V; e += 4) {
-      *reinterpret_cast<float4*>(part + group * D + l.ca * V + e) =
-          make_float4(sa[e], sa[e + 1], sa[e + 2], sa[e + 3]);
-      *reinterpret_cast<float4*>(part + group * D + l.cb * V + e) =
-          make_float4(sb[e], sb[e + 1], sb[e + 2], sb[e + 3]);
-    }
+    key_rows<BF16, C, D, NORM>(p, pg, h, threadIdx.x, part);
+  } else if (threadIdx.x < R::kTeam) {
+    key_rows<BF16, C, D, NORM>(p, pg, h, threadIdx.x, part);
   } else {
-    const int pr = threadIdx.x % kPairs;
-    const Lane l = {pr, pr + kPairs, 0, false};
-    const uint4* src = static_cast<const uint4*>(p.v_new) + h * kCols;
-    const int64_t stride = p.v_stride / V;
-    for (int base = row0; base < row1; base += kBatch * kGroups) {
-      uint4 xa[kBatch] = {}, xb[kBatch] = {};
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int r = base + group + i * kGroups;
-        if (r < row1) {
-          xa[i] = src[(tok0 + r) * stride + l.ca];
-          xb[i] = src[(tok0 + r) * stride + l.cb];
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        if (base + i * kGroups >= row1) break;
-        const int r = base + group + i * kGroups;
-        float a[V], y[V];
-        unpack<BF16>(xa[i], a);
-        unpack<BF16>(xb[i], y);
-        store_row<BF16, C, D>(p.v_pool, p.v_scale, blk + r, l, r < row1, a, y);
-      }
-    }
+    value_rows<BF16, C, D>(p, pg, h, threadIdx.x - R::kTeam);
   }
   __syncthreads();
   for (int e = threadIdx.x; e < D; e += kAppendThreads) {
     float s = part[e];
 #pragma unroll
-    for (int g = 1; g < kGroups; ++g) s += part[g * D + e];
-    p.reps[(page * p.num_kv_heads + h) * D + e] = s / row1;
+    for (int g = 1; g < R::kGroups; ++g) s += part[g * D + e];
+    p.reps[(page * p.num_kv_heads + h) * D + e] = s / pg.row1;
   }
 }
 
+// Units of a query item: (token, kHeads heads), one for every kLanes lanes.
 template <bool BF16, int D>
-__device__ void norm_query_item(const AppendNormParams& p, int64_t item) {
-  constexpr int V = Piece<BF16>::kVec;
-  constexpr int kCols = D / V;
-  constexpr int kPairs = kCols / 2;
-  constexpr int kUnits = kAppendThreads / kPairs;    // (token, head group) units per block
-  constexpr int kUnitsPerWarp = 32 / kPairs;
-  const int chunks = (p.num_q_heads + kHeadsPerUnit - 1) / kHeadsPerUnit;
-  const int64_t units = p.num_tokens * chunks;
-  const int64_t u0 = item * kUnits + (threadIdx.x / 32) * kUnitsPerWarp;   // of this warp
-  if (u0 >= units) return;
-  const int64_t u = u0 + (threadIdx.x % 32) / kPairs;
-  const int64_t tok = u / chunks;
+__host__ __device__ constexpr int query_units() {
+  return kAppendThreads / Rows<BF16, D>::kLanes;
+}
+
+template <bool BF16, int D, bool NORM>
+__device__ __forceinline__ void norm_query_item(const AppendNormParams& p, unsigned item) {
+  using R = Rows<BF16, D>;
+  constexpr int kStep = 2;                           // heads that are worked on together
+  constexpr int kElement = BF16 ? 2 : 4;             // bytes
+  constexpr int kUnits = query_units<BF16, D>();
+  constexpr int kUnitsPerWarp = 32 / R::kLanes;
+  // unit number = token * chunks + head group, by 32-bit divisions (chunks < 2^14, items < 2^31)
+  const unsigned chunks = (p.num_q_heads + R::kHeads - 1) / R::kHeads;
+  const unsigned whole = item / chunks, rest = item % chunks;
+  const unsigned at = rest * kUnits + (threadIdx.x / 32) * kUnitsPerWarp;       // of this warp
+  const unsigned mine = at + (threadIdx.x % 32) / R::kLanes;
+  const int64_t t0 = static_cast<int64_t>(whole) * kUnits + at / chunks;
+  if (t0 >= p.num_tokens) return;
+  const int64_t tok = static_cast<int64_t>(whole) * kUnits + mine / chunks;
+  const int h0 = static_cast<int>(mine % chunks) * R::kHeads;
+  const Lane l = lane_of(p, threadIdx.x % R::kLanes);
+  // the rows before the search, which they do not wait for
+  const int heads = tok < p.num_tokens ? min(p.num_q_heads - h0, R::kHeads) : 0;
+  const char* src = static_cast<const char*>(p.q) + (tok * p.q_stride + h0 * D) * kElement;
+  char* dst = static_cast<char*>(p.q_out) + (tok * p.num_q_heads + h0) * D * kElement;
+  Raw<BF16> xa[R::kHeads] = {}, xb[R::kHeads] = {};
+#pragma unroll
+  for (int i = 0; i < R::kHeads; ++i)
+    if (i < heads) {
+      xa[i] = load_raw<BF16>(src + i * D * kElement, l.a);
+      xb[i] = load_raw<BF16>(src + i * D * kElement, l.b);
+    }
+  const Part w = load_weights(NORM ? p.q_norm : nullptr, l);
   // the warp's units cover few tokens: one search for each
-  const int64_t last = min(u0 + kUnitsPerWarp, units) - 1;
+  const int64_t last = min(static_cast<int64_t>(whole) * kUnits + (at + kUnitsPerWarp - 1) / chunks,
+                           p.num_tokens - 1);
   int64_t pos = -1;
-  for (int64_t t = u0 / chunks; t <= last / chunks; ++t) {
+  for (int64_t t = t0; t <= last; ++t) {
     const int b = find_sequence(p.cu_q, p.batch, p.num_tokens, 1, 0, t);
     Chunk c;
     const bool ok = load_chunk(p, b, &c) && t >= c.first && t < c.first + c.n;
     if (ok && t == tok) pos = c.len + (t - c.first);
   }
-  const bool on = u < units && pos >= 0;             // not padding, not a skipped sequence
-  const int h0 = static_cast<int>(u % chunks) * kHeadsPerUnit;
-  const Lane l = lane_of<BF16>(p, threadIdx.x % kPairs);
-  const uint4* src = static_cast<const uint4*>(p.q) + tok * (p.q_stride / V);
-  uint4* dst = static_cast<uint4*>(p.q_out) + tok * p.num_q_heads * kCols;
-  uint4 xa[kHeadsPerUnit] = {}, xb[kHeadsPerUnit] = {};
+  const bool on = pos >= 0;                          // not padding, not a skipped sequence
+  Angles t = {};
+  if (on && l.turned) t = load_angles(p.rope + pos * p.rope_dim + l.first, p.rope_dim / 2);
 #pragma unroll
-  for (int i = 0; i < kHeadsPerUnit; ++i)
-    if (on && h0 + i < p.num_q_heads) {
-      xa[i] = src[(h0 + i) * kCols + l.ca];
-      xb[i] = src[(h0 + i) * kCols + l.cb];
-    }
-  float wa[V], wb[V];
-  load_weights<V>(p.q_norm, l, wa, wb);
+  for (int i0 = 0; i0 < R::kHeads; i0 += kStep) {
+    Part v[kStep];
 #pragma unroll
-  for (int i = 0; i < kHeadsPerUnit; ++i) {
-    float a[V], b[V];
-    unpack<BF16>(xa[i], a);
-    unpack<BF16>(xb[i], b);
-    if (p.q_norm) norm_row<V, kPairs>(a, b, wa, wb, D, p.eps);
-    if (on && h0 + i < p.num_q_heads) {
-      if (l.turned)
-        turn_row<V>(a, b, p.rope + pos * p.rope_dim, p.rope_dim / 2, l.first, p.interleaved);
-      dst[(h0 + i) * kCols + l.ca] = pack<BF16>(a);
-      dst[(h0 + i) * kCols + l.cb] = pack<BF16>(b);
+    for (int i = 0; i < kStep; ++i) v[i] = values_of<BF16>(xa[i0 + i], xb[i0 + i]);
+    if (NORM && p.q_norm) norm_rows<R::kLanes, D>(v, w, p.eps);
+#pragma unroll
+    for (int i = 0; i < kStep; ++i) {
+      if (!on || i0 + i >= heads) continue;
+      if (l.turned) turn_row<!NORM>(v[i], t, p.interleaved);
+      char* row = dst + (i0 + i) * D * kElement;
+      store_raw<BF16>(row, l.a, round_to<BF16>(v[i].x[0], v[i].x[1]));
+      store_raw<BF16>(row, l.b, round_to<BF16>(v[i].x[2], v[i].x[3]));
     }
   }
 }
 
-// Page items first (they are longer), then query items.
-template <bool BF16, int C, int D>
-__global__ void __launch_bounds__(kAppendThreads, 2) append_norm_kernel(AppendNormParams p) {
-  __shared__ __align__(16) float part[kAppendThreads / (D / Piece<BF16>::kVec) * D];
+// Every `period`-th block is a page item, so that these, whose chains of dependent reads leave the memory
+// idle, run beside query items, which only stream.
+template <bool BF16, int C, int D, bool NORM>
+__global__ void __launch_bounds__(kAppendThreads, 3) append_norm_kernel(AppendNormParams p) {
+  __shared__ __align__(16) float part[Rows<BF16, D>::kGroups * D];
   grid_dependency_wait();
-  if (blockIdx.x < p.page_items)
-    norm_page_item<BF16, C, D>(p, blockIdx.x / p.num_kv_heads, blockIdx.x % p.num_kv_heads, part);
-  else
-    norm_query_item<BF16, D>(p, blockIdx.x - p.page_items);
+  const unsigned round = blockIdx.x / p.period;
+  if (blockIdx.x % p.period == 0 && round < p.page_items) {
+    const unsigned item = Rows<BF16, D>::kApart ? round / 2 : round;
+    const bool values = Rows<BF16, D>::kApart && (round & 1);
+    norm_page_item<BF16, C, D, NORM>(p, item / p.num_kv_heads, item % p.num_kv_heads, values, part);
+  } else {
+    norm_query_item<BF16, D, NORM>(p, blockIdx.x - min(round + 1, p.page_items));
+  }
   if (blockIdx.x == 0) check_bounds(p.cu_q, p.batch, p.num_tokens, p.status);
 }
 
+// Blocks of query items of a launch.
 template <bool BF16, int D>
-cudaError_t launch_typed(const cudaLaunchConfig_t& cfg, const AppendNormParams& p, int code) {
-  switch (code) {
-    case kCodeI8: return cudaLaunchKernelEx(&cfg, append_norm_kernel<BF16, kCodeI8, D>, p);
-    case kCodeE4M3: return cudaLaunchKernelEx(&cfg, append_norm_kernel<BF16, kCodeE4M3, D>, p);
-    default: return cudaLaunchKernelEx(&cfg, append_norm_kernel<BF16, kCodeNone, D>, p);
-  }
+int64_t query_blocks(int64_t num_tokens, int num_q_heads) {
+  const int64_t chunks = (num_q_heads + Rows<BF16, D>::kHeads - 1) / Rows<BF16, D>::kHeads;
+  return (num_tokens * chunks + query_units<BF16, D>() - 1) / query_units<BF16, D>();
 }
 
-}  // namespace
-
-cudaError_t launch_append_norm(const AppendNormParams& params, int head_dim, bool bf16, int code,
-                               cudaStream_t stream) {
-  AppendNormParams p = params;
-  const int64_t items = append_chunk_blocks(p.num_tokens, p.batch, p.q ? p.num_q_heads : 0,
-                                            p.num_kv_heads, head_dim, p.team_size, bf16);
-  p.page_items =
-      static_cast<uint32_t>(append_page_blocks(p.num_tokens, p.batch, p.num_kv_heads, p.team_size));
+template <bool BF16, int D>
+cudaError_t launch_typed(AppendNormParams p, int code, cudaStream_t stream) {
+  p.page_items = static_cast<uint32_t>(
+      append_page_blocks(p.num_tokens, p.batch, p.num_kv_heads, p.team_size) *
+      (Rows<BF16, D>::kApart ? 2 : 1));
+  const int64_t queries = p.q ? query_blocks<BF16, D>(p.num_tokens, p.num_q_heads) : 0;
+  const int64_t items = p.page_items + queries;
+  p.period = 1 + static_cast<uint32_t>(queries / p.page_items);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -416,11 +554,38 @@ cudaError_t launch_append_norm(const AppendNormParams& params, int head_dim, boo
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  const bool norm = p.q_norm || p.k_norm;
+  switch (code) {
+    case kCodeI8:
+      return norm ? cudaLaunchKernelEx(&cfg, append_norm_kernel<BF16, kCodeI8, D, true>, p)
+                  : cudaLaunchKernelEx(&cfg, append_norm_kernel<BF16, kCodeI8, D, false>, p);
+    case kCodeE4M3:
+      return norm ? cudaLaunchKernelEx(&cfg, append_norm_kernel<BF16, kCodeE4M3, D, true>, p)
+                  : cudaLaunchKernelEx(&cfg, append_norm_kernel<BF16, kCodeE4M3, D, false>, p);
+    default:
+      return norm ? cudaLaunchKernelEx(&cfg, append_norm_kernel<BF16, kCodeNone, D, true>, p)
+                  : cudaLaunchKernelEx(&cfg, append_norm_kernel<BF16, kCodeNone, D, false>, p);
+  }
+}
+
+}  // namespace
+
+int64_t append_norm_blocks(int64_t num_tokens, int batch, int num_q_heads, int num_kv_heads,
+                           int head_dim, int team_size, bool bf16) {
+  const int64_t q = bf16 ? (head_dim == 128 ? query_blocks<true, 128>(num_tokens, num_q_heads)
+                                            : query_blocks<true, 64>(num_tokens, num_q_heads))
+                         : (head_dim == 128 ? query_blocks<false, 128>(num_tokens, num_q_heads)
+                                            : query_blocks<false, 64>(num_tokens, num_q_heads));
+  return append_page_blocks(num_tokens, batch, num_kv_heads, team_size) * 2 + q;
+}
+
+cudaError_t launch_append_norm(const AppendNormParams& p, int head_dim, bool bf16, int code,
+                               cudaStream_t stream) {
   if (bf16)
-    return head_dim == 128 ? launch_typed<true, 128>(cfg, p, code)
-                           : launch_typed<true, 64>(cfg, p, code);
-  return head_dim == 128 ? launch_typed<false, 128>(cfg, p, code)
-                         : launch_typed<false, 64>(cfg, p, code);
+    return head_dim == 128 ? launch_typed<true, 128>(p, code, stream)
+                           : launch_typed<true, 64>(p, code, stream);
+  return head_dim == 128 ? launch_typed<false, 128>(p, code, stream)
+                         : launch_typed<false, 64>(p, code, stream);
 }
 
 }  // namespace santa

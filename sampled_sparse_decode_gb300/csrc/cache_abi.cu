@@ -158,6 +158,9 @@ int santa_append_norm(const santa_append_norm_args* a, void* stream) {
       !aligned(a->k_norm, 16))
     return SANTA_ERR_INVALID_ARG;
   if (!(a->eps >= 0.f) || !std::isfinite(a->eps)) return SANTA_ERR_INVALID_ARG;
+  if (santa::append_norm_blocks(c->num_tokens, c->batch, c->q ? c->num_q_heads : 0, c->num_kv_heads,
+                                c->head_dim, c->team_size, c->dtype == SANTA_BF16) > 0x7fffffffll)
+    return SANTA_ERR_UNSUPPORTED;
   santa::AppendNormParams p = {};
   fill_append(c, &p);
   p.q_norm = a->q_norm;

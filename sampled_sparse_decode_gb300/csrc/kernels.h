@@ -111,7 +111,11 @@ struct AppendNormParams : AppendChunkParams {
   float eps;
   float* k_scale;             // [P][Hkv][T], 8-bit caches
   float* v_scale;
+  uint32_t period;            // every period-th block is a page item (set by the launcher)
 };
+// Blocks of the launch (no more than a grid dimension holds).
+int64_t append_norm_blocks(int64_t num_tokens, int batch, int num_q_heads, int num_kv_heads,
+                           int head_dim, int team_size, bool bf16);
 // code: CodeType of the cache
 cudaError_t launch_append_norm(const AppendNormParams& p, int head_dim, bool bf16, int code,
                                cudaStream_t stream);

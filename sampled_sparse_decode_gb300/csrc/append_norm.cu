@@ -513,19 +513,17 @@ __device__ __forceinline__ void norm_query_item(const AppendNormParams& p, unsig
   }
 }
 
-// Every `period`-th block is a page item, so that these, whose chains of dependent reads leave the memory
-// idle, run beside query items, which only stream.
+// Page items first (they are longer), then query items.
 template <bool BF16, int C, int D, bool NORM>
 __global__ void __launch_bounds__(kAppendThreads, 3) append_norm_kernel(AppendNormParams p) {
   __shared__ __align__(16) float part[Rows<BF16, D>::kGroups * D];
   grid_dependency_wait();
-  const unsigned round = blockIdx.x / p.period;
-  if (blockIdx.x % p.period == 0 && round < p.page_items) {
-    const unsigned item = Rows<BF16, D>::kApart ? round / 2 : round;
-    const bool values = Rows<BF16, D>::kApart && (round & 1);
+  if (blockIdx.x < p.page_items) {
+    const unsigned item = Rows<BF16, D>::kApart ? blockIdx.x / 2 : blockIdx.x;
+    const bool values = Rows<BF16, D>::kApart && (blockIdx.x & 1);
     norm_page_item<BF16, C, D, NORM>(p, item / p.num_kv_heads, item % p.num_kv_heads, values, part);
   } else {
-    norm_query_item<BF16, D, NORM>(p, blockIdx.x - min(round + 1, p.page_items));
+    norm_query_item<BF16, D, NORM>(p, blockIdx.x - p.page_items);
   }
   if (blockIdx.x == 0) check_bounds(p.cu_q, p.batch, p.num_tokens, p.status);
 }
@@ -542,9 +540,8 @@ cudaError_t launch_typed(AppendNormParams p, int code, cudaStream_t stream) {
   p.page_items = static_cast<uint32_t>(
       append_page_blocks(p.num_tokens, p.batch, p.num_kv_heads, p.team_size) *
       (Rows<BF16, D>::kApart ? 2 : 1));
-  const int64_t queries = p.q ? query_blocks<BF16, D>(p.num_tokens, p.num_q_heads) : 0;
-  const int64_t items = p.page_items + queries;
-  p.period = 1 + static_cast<uint32_t>(queries / p.page_items);
+  const int64_t items =
+      p.page_items + (p.q ? query_blocks<BF16, D>(p.num_tokens, p.num_q_heads) : 0);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

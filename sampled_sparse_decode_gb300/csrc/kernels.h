@@ -111,7 +111,6 @@ struct AppendNormParams : AppendChunkParams {
   float eps;
   float* k_scale;             // [P][Hkv][T], 8-bit caches
   float* v_scale;
-  uint32_t period;            // every period-th block is a page item (set by the launcher)
 };
 // Blocks of the launch (no more than a grid dimension holds).
 int64_t append_norm_blocks(int64_t num_tokens, int batch, int num_q_heads, int num_kv_heads,
@@ -136,7 +135,7 @@ struct Q8ReadParams {
   void* v_out;
   int32_t* status;
 };
-cudaError_t launch_q8_read(const Q8ReadParams& p, int head_dim, bool bf16, int code, int sms,
+cudaError_t launch_q8_read(const Q8ReadParams& p, int head_dim, bool bf16, int code,
                            cudaStream_t stream);
 
 // ---------------------------------------------------------------- 8-bit cache: attention

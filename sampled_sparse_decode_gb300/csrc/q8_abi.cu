@@ -209,8 +209,6 @@ int santa_q8_read(const santa_q8_read_args* a, void* stream) {
   const Span k = {a->k_out, bytes}, v = {a->v_out, bytes};
   if (meets_any(k, in) || meets_any(v, in) || meets(k.at, bytes, v.at, 1, bytes, bytes))
     return SANTA_ERR_INVALID_ARG;
-  const int sms = santa::device_sms();
-  if (sms <= 0) return SANTA_ERR_CUDA;
   santa::Q8ReadParams p = {};
   p.k = a->k;
   p.v = a->v;
@@ -229,7 +227,7 @@ int santa_q8_read(const santa_q8_read_args* a, void* stream) {
   p.k_out = a->k_out;
   p.v_out = a->v_out;
   p.status = a->device_status;
-  return map_cuda(santa::launch_q8_read(p, a->head_dim, a->out_dtype == SANTA_BF16, code, sms,
+  return map_cuda(santa::launch_q8_read(p, a->head_dim, a->out_dtype == SANTA_BF16, code,
                                         static_cast<cudaStream_t>(stream)));
 }
 

@@ -1,9 +1,12 @@
 // q8_read.cu — tokens of an 8-bit cache read back into a paged pool of bf16 or fp32 rows: a code
-// times its row's scale, rounded once (fp32 holds an int8 or e4m3 code times an fp32 scale to its last
-// bit or half of it).
+// times its row's scale, rounded to fp32 and, for bf16, once more.
 //
-// One block per (page, KV head): a thread takes 16 codes of a row (one 16-byte load) and stores 16
-// values.  Bound by HBM: d + 4 bytes read and d elements written for every row.
+// One block per (page, KV head).  A thread takes the codes of 16 bytes of output (8 or 4), so that a
+// warp's stores are whole lines; four pieces of keys and four of values are asked for before the first is
+// converted, and page ids are asked for beside the lengths that decide whether they count.  Bound by HBM:
+// d + 4 bytes read and d elements written for every row.
+#include <algorithm>
+
 #include "kernels.h"
 #include "q8.cuh"
 
@@ -12,60 +15,102 @@ namespace santa {
 namespace {
 
 constexpr int kReadThreads = 256;
+constexpr int kAhead = 4;                            // pieces of each of keys and values
+constexpr int kMostBlocks = 16384;
+
+template <bool BF16>
+struct Codes {
+  uint32_t w[BF16 ? 2 : 1];
+};
+template <bool BF16>
+__device__ __forceinline__ Codes<BF16> load_codes(const void* codes, int64_t at) {
+  const uint8_t* from = static_cast<const uint8_t*>(codes) + at;
+  Codes<BF16> c;
+  if constexpr (BF16) {
+    const uint2 v = *reinterpret_cast<const uint2*>(from);
+    c.w[0] = v.x, c.w[1] = v.y;
+  } else {
+    c.w[0] = *reinterpret_cast<const uint32_t*>(from);
+  }
+  return c;
+}
 
 template <bool BF16, int C>
-__device__ __forceinline__ void write_values(void* out, int64_t at, const uint4& w, float scale) {
-  const uint32_t word[4] = {w.x, w.y, w.z, w.w};
-  float x[16];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float y[4];
-    q8_decode<C>(word[i], y);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[4 * i + e] = y[e] * scale;
-  }
+__device__ __forceinline__ void write_values(void* out, int64_t at, const Codes<BF16>& c, float scale) {
+  float x[4];
+  q8_decode<C>(c.w[0], x);
   if constexpr (BF16) {
-    uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      to[i] = make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
-                         pack_bf16(x[8 * i + 4], x[8 * i + 5]),
-                         pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+    float y[4];
+    q8_decode<C>(c.w[1], y);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) =
+        make_uint4(pack_bf16(x[0] * scale, x[1] * scale), pack_bf16(x[2] * scale, x[3] * scale),
+                   pack_bf16(y[0] * scale, y[1] * scale), pack_bf16(y[2] * scale, y[3] * scale));
   } else {
-    float4* to = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      to[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    *reinterpret_cast<float4*>(static_cast<float*>(out) + at) =
+        make_float4(x[0] * scale, x[1] * scale, x[2] * scale, x[3] * scale);
   }
 }
 
 template <bool BF16, int C, int D>
-__global__ void __launch_bounds__(kReadThreads) q8_read_kernel(Q8ReadParams p) {
-  constexpr int kCols = D / 16;
-  grid_dependency_wait();
-  const int team = blockIdx.x, h = blockIdx.y, b = blockIdx.z, T = p.team_size;
-  const int64_t len = p.seq_lens[b], first = p.first ? p.first[b] : 0;
-  if (first < 0 || len < first || len > static_cast<int64_t>(p.max_teams) * T) {
-    if (team == 0 && h == 0 && threadIdx.x == 0) set_status(p.status, SANTA_DEV_BAD_SEQLEN);
-    return;
-  }
-  const int row0 = static_cast<int>(max(first - static_cast<int64_t>(team) * T, int64_t(0)));
-  const int row1 = static_cast<int>(min(len - static_cast<int64_t>(team) * T, int64_t(T)));
+__device__ __forceinline__ void read_page(const Q8ReadParams& p, int team, int h, int first, int len,
+                                          int64_t src, int64_t dst) {
+  constexpr int kPiece = BF16 ? 8 : 4, kCols = D / kPiece;
+  const int T = p.team_size;
+  const int row0 = max(first - team * T, 0), row1 = min(len - team * T, T);
   if (row0 >= row1) return;
-  const int64_t at = static_cast<int64_t>(b) * p.max_teams + team;
-  const int64_t src = p.page_table[at], dst = p.dst_table[at];
   if (src < 0 || src >= p.num_pages || dst < 0 || dst >= p.dst_pages) {
     if (h == 0 && threadIdx.x == 0) set_status(p.status, SANTA_DEV_BAD_PAGE);
     return;
   }
   const int64_t from = (src * p.num_kv_heads + h) * T, to = (dst * p.num_kv_heads + h) * T;
-  for (int i = row0 * kCols + threadIdx.x; i < row1 * kCols; i += kReadThreads) {
-    const int r = i / kCols, col = i % kCols;
-    const uint4 k = static_cast<const uint4*>(p.k)[(from + r) * kCols + col];
-    const uint4 v = static_cast<const uint4*>(p.v)[(from + r) * kCols + col];
-    write_values<BF16, C>(p.k_out, (to + r) * D + col * 16, k, p.k_scale[from + r]);
-    write_values<BF16, C>(p.v_out, (to + r) * D + col * 16, v, p.v_scale[from + r]);
+  for (int i0 = row0 * kCols + threadIdx.x; i0 < row1 * kCols; i0 += kAhead * kReadThreads) {
+    Codes<BF16> k[kAhead], v[kAhead];
+    float ks[kAhead], vs[kAhead];
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      const int i = i0 + e * kReadThreads;
+      if (i < row1 * kCols) {
+        k[e] = load_codes<BF16>(p.k, from * D + i * kPiece);
+        v[e] = load_codes<BF16>(p.v, from * D + i * kPiece);
+        ks[e] = p.k_scale[from + i / kCols];
+        vs[e] = p.v_scale[from + i / kCols];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      const int i = i0 + e * kReadThreads;
+      if (i < row1 * kCols) {
+        write_values<BF16, C>(p.k_out, to * D + i * kPiece, k[e], ks[e]);
+        write_values<BF16, C>(p.v_out, to * D + i * kPiece, v[e], vs[e]);
+      }
+    }
   }
+}
+
+template <bool BF16, int C, int D>
+__global__ void __launch_bounds__(kReadThreads) q8_read_kernel(Q8ReadParams p) {
+  grid_dependency_wait();
+  const int h = blockIdx.y, b = blockIdx.z, T = p.team_size;
+  const int32_t* src_ids = p.page_table + static_cast<int64_t>(b) * p.max_teams;
+  const int32_t* dst_ids = p.dst_table + static_cast<int64_t>(b) * p.max_teams;
+  const int len = p.seq_lens[b], first = p.first ? p.first[b] : 0;
+  // a grid as wide as the table: page ids beside the lengths; else every gridDim.x-th page from the first
+  const bool all = gridDim.x == p.max_teams;
+  int64_t src = 0, dst = 0;
+  if (all) {
+    src = src_ids[blockIdx.x];
+    dst = dst_ids[blockIdx.x];
+  }
+  if (first < 0 || len < first || len > p.max_teams * T) {
+    if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) set_status(p.status, SANTA_DEV_BAD_SEQLEN);
+    return;
+  }
+  if (all) {
+    read_page<BF16, C, D>(p, blockIdx.x, h, first, len, src, dst);
+    return;
+  }
+  for (int team = first / T + blockIdx.x; team * T < len; team += gridDim.x)
+    read_page<BF16, C, D>(p, team, h, first, len, src_ids[team], dst_ids[team]);
 }
 
 template <bool BF16, int C>
@@ -76,14 +121,16 @@ cudaError_t launch_typed(const cudaLaunchConfig_t& cfg, const Q8ReadParams& p, i
 
 }  // namespace
 
-cudaError_t launch_q8_read(const Q8ReadParams& p, int head_dim, bool bf16, int code, int sms,
+cudaError_t launch_q8_read(const Q8ReadParams& p, int head_dim, bool bf16, int code,
                            cudaStream_t stream) {
-  (void)sms;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.max_teams, p.num_kv_heads, p.batch);
+  // blocks of pages that are not asked for end at once, but still have to start: a bounded number of them
+  const int64_t units = static_cast<int64_t>(p.num_kv_heads) * p.batch;
+  const int64_t wide = std::max<int64_t>(1, std::min<int64_t>(p.max_teams, kMostBlocks / units));
+  cfg.gridDim = dim3(static_cast<unsigned>(wide), p.num_kv_heads, p.batch);
   cfg.blockDim = dim3(kReadThreads);
   cfg.stream = stream;
   cfg.attrs = attr;

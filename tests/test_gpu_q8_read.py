@@ -102,3 +102,19 @@ def test_far_pages():
     assert torch.equal(k[P - 1, :, :100].float(), cache.k[P - 1, :, :100].float() * 0.5)
     assert torch.equal(v[P - 1, :, :100].float(), cache.v[P - 1, :, :100].float() * 2.0)
     assert not k[P - 1, :, 100:].any() and not k[:P - 1].any()
+
+
+@pytest.mark.parametrize("first", [[0] * 40, [70, 0, 511] + [1] * 37])
+def test_wide_tables(first):
+    """More (page, head) pairs in the tables than the launch has blocks."""
+    lens = [900, 1, 512] + [65] * 37
+    c = Q8(lens, 8, 64, 64, I8, seed=3)
+    wide = torch.full((40, 300), 2**30, dtype=torch.int32, device="cuda")
+    wide[:, :c.table.shape[1]] = c.table
+    c.table = wide
+    k, v, table = destination(c, BF16)
+    f = torch.tensor(first, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    santa.santa_q8_read(c.cache, c.table, c.seq_lens, k, v, table, first=f, device_status=status)
+    assert int(status) == 0
+    check(c, lens, first, k, v, table)

@@ -155,12 +155,12 @@ struct Q8AttendParams {
   float scale;                // 1 / sqrt(d)
   float softcap;              // 0: none
   int window;                 // 0: none
-  bool short_line;            // few units and tiles (set by the launcher)
+  bool short_line;            // few sequences or units (set by the launcher)
   // per block (at most q8_attend_most_blocks()): the unit that goes on there from the block before and
   // the unit that begins there and goes on (-1: none), as far as it does not end there; their parts, sums
   // and (reference, sum of weights); per warp a piece
-  int64_t* goes_on;           // [blocks]
-  int64_t* begins;            // [blocks]
+  int32_t* goes_on;           // [blocks]
+  int32_t* begins;            // [blocks]
   float* part_acc;            // [blocks][2][kMaxGroup][d]
   float* part_ml;             // [blocks][2][kMaxGroup][2]
   float* piece;               // [blocks][q8_attend_warps()][kMaxGroup][d]
@@ -168,6 +168,8 @@ struct Q8AttendParams {
   int32_t* status;
 };
 int q8_attend_warps();
+// Whether the tiles of all units, `teams` pages each, can be counted in 32 bits.
+bool q8_attend_fits(int batch, int num_kv_heads, int team_size, int teams);
 int q8_attend_most_blocks();
 // `sms` blocks (one per multiprocessor); two launches.
 cudaError_t launch_q8_attend(const Q8AttendParams& p, int head_dim, bool bf16, int code, int sms,

@@ -48,7 +48,7 @@ int q8_layout(int d, Q8Layout* l) {
   l->sms = std::min(santa::device_sms(), santa::q8_attend_most_blocks());
   if (l->sms <= 0) return SANTA_ERR_CUDA;
   const size_t rows = static_cast<size_t>(l->sms) * santa::kMaxGroup;
-  l->split_bytes = round_up(2 * l->sms * sizeof(int64_t), kAlign);
+  l->split_bytes = round_up(2 * l->sms * sizeof(int32_t), kAlign);
   l->ml_bytes = round_up(2 * rows * 2 * sizeof(float), kAlign);
   l->acc_bytes = 2 * rows * d * sizeof(float);
   l->bytes = kAlign + l->split_bytes + l->ml_bytes + l->acc_bytes +
@@ -78,6 +78,9 @@ int check_q8_attend(const santa_decode_args* a, const santa_q8_args* c, bool lis
     if (!aligned(a->sel_ids, 4) || !aligned(a->sel_count, 4) || !aligned(a->pi, 4))
       return SANTA_ERR_INVALID_ARG;
   }
+  if (!santa::q8_attend_fits(a->batch, a->num_kv_heads, a->team_size,
+                             listed ? a->num_draws : a->max_teams))
+    return SANTA_ERR_UNSUPPORTED;
   if ((rc = q8_layout(a->head_dim, l))) return rc;
   if (!a->workspace || a->workspace_bytes < l->bytes) return SANTA_ERR_INVALID_ARG;
   const int64_t rows = a->num_pages * a->num_kv_heads * static_cast<int64_t>(a->team_size);
@@ -129,7 +132,7 @@ int launch_q8(const santa_decode_args* a, const santa_q8_args* c, bool listed, v
   p.window = c->window;
   unsigned char* base = reinterpret_cast<unsigned char*>(
       round_up(reinterpret_cast<uintptr_t>(a->workspace), kAlign));
-  p.goes_on = reinterpret_cast<int64_t*>(base);
+  p.goes_on = reinterpret_cast<int32_t*>(base);
   p.begins = p.goes_on + l.sms;
   p.part_ml = reinterpret_cast<float*>(base += l.split_bytes);
   p.part_acc = reinterpret_cast<float*>(base += l.ml_bytes);

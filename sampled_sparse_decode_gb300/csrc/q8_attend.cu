@@ -47,6 +47,8 @@ constexpr int kStages = 3;                 // tiles of a warp's ring
 constexpr int kOpen = 2;                   // what opening a unit counts, in tiles
 constexpr int kScanRounds = 8;             // 32 sequences or units each that a warp reads by itself
 constexpr int kJoinRounds = 8;             // 32 blocks each that a unit may reach over
+constexpr int kBeyond = INT32_MAX - 16;    // behind every place of a line
+constexpr int64_t kMostPlaces = INT32_MAX - (1 << 16);
 constexpr float kNoScore = -1e38f;         // a reference before the first score
 constexpr float kSlack = 8.f;              // how far a score may pass the reference (base 2)
 constexpr float kTopWeight = 256.f;        // the same for a weight
@@ -168,19 +170,19 @@ __device__ __forceinline__ Unit load_unit(const Q8AttendParams& p, int b, int h,
                     p.sel_ids ? p.sel_count[static_cast<int64_t>(b) * p.num_kv_heads + h] : 0, tell);
 }
 // A unit's length on the line: its tiles and its opening.
-__device__ __forceinline__ int64_t span(const Unit& u) { return u.tiles ? u.tiles + kOpen : 0; }
+__device__ __forceinline__ int span(const Unit& u) { return u.tiles ? u.tiles + kOpen : 0; }
 
 // A place on the line: unit (b, h), which begins at `base`; its tile k stands at base + kOpen + k.
 struct Walk {
   int b, h;
-  int64_t base;
+  int base;
   Unit u;
 };
 __device__ __forceinline__ void next_unit(const Q8AttendParams& p, Walk& w) {
   w.base += span(w.u);
   if (w.b == p.batch - 1 && w.h == p.num_kv_heads - 1) {
     // not reached while lengths and lists stay as they are; if not, the walk ends here
-    w.base = INT64_MAX / 2;
+    w.base = kBeyond;
     w.u = Unit{0, 0, 0, 0};
     return;
   }
@@ -192,21 +194,20 @@ __device__ __forceinline__ void next_unit(const Q8AttendParams& p, Walk& w) {
   if (wrap || p.sel_ids) w.u = load_unit(p, w.b, w.h, false);
 }
 // To the unit that owns place `at` (at < the line's length).
-__device__ __forceinline__ void walk_to(const Q8AttendParams& p, Walk& w, int64_t at) {
+__device__ __forceinline__ void walk_to(const Q8AttendParams& p, Walk& w, int at) {
   while (w.base + span(w.u) <= at) next_unit(p, w);
 }
 
-template <typename T>
-__device__ __forceinline__ T warp_scan(T v) {
+__device__ __forceinline__ int warp_scan(int v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const T up = __shfl_up_sync(0xffffffffu, v, o);
+    const int up = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += up;
   }
   return v;
 }
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums) {
+__device__ __forceinline__ int block_scan(int v, int* warp_sums) {
   const int warp = threadIdx.x >> 5;
   v = warp_scan(v);
   if ((threadIdx.x & 31) == 31) warp_sums[warp] = v;
@@ -602,22 +603,45 @@ __device__ __forceinline__ void add_part(float (&sum)[N], float& top, float& z, 
   for (int i = 0; i < N; ++i) sum[i] = sum[i] * keep + x[i] * f;
 }
 
-// A unit that a warp holds a piece of, or a block a part: where it stands on the line.
-struct Owner {
-  int64_t unit, base;   // unit -1: none
-  int tiles;
-  bool first;           // whether the piece has the unit's first tile
-};
+// Adds a chain of a unit's pieces, in the order of the line, by all threads of the block: a head's four
+// dimensions each.  `on_count` pieces lie `on_stride` floats apart from `on` on, `closing` (or null) follows
+// them; ml: their (reference, sum) by head.  `whole`: to rows of out; else to a part and its ml.  Short loops:
+// a launch runs this code once, and fetching it takes longer than running it.
+template <int D>
+__device__ __forceinline__ void add_chain(const float* on, int on_stride, int on_count, const float* closing,
+                                          const float* ml_on, const float* ml_closing, int G, bool whole,
+                                          float* rows, float* ml) {
+  const int count = on_count + (closing != nullptr);
+#pragma unroll 1
+  for (int e = threadIdx.x; e < G * (D / 4); e += kQ8Threads) {
+    const int head = e / (D / 4), dim = e % (D / 4) * 4;
+    float sum[4] = {}, top = kNoScore, z = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+      const float* row = i < on_count ? on + i * on_stride + head * Ring<D>::kPieceRow : closing + head * D;
+      const float* at = (i < on_count ? ml_on + i * kMaxGroup * 2 : ml_closing) + head * 2;
+      const float4 v = *reinterpret_cast<const float4*>(row + dim);
+      const float x[4] = {v.x, v.y, v.z, v.w};
+      add_part(sum, top, z, x, at[0], at[1]);
+    }
+    const float f = !whole ? 1.f : z == 0.f ? 0.f : 1.f / z;
+    *reinterpret_cast<float4*>(rows + head * D + dim) =
+        make_float4(sum[0] * f, sum[1] * f, sum[2] * f, sum[3] * f);
+    if (!whole && dim == 0) *reinterpret_cast<float2*>(ml + head * 2) = make_float2(top, z);
+  }
+}
 
 template <int NQ, int C, int D>
 __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t sums[2][kQ8Warps];
-  __shared__ int64_t start_s[2];                     // element of the block's start, its place
+  __shared__ int sums[2][kQ8Warps];
+  __shared__ int start_s[2];                         // element of the block's start, its place
   __shared__ int2 notes[kQ8Warps][kStages];
   // each warp's piece that closes a unit which another warp opened (0, in the workspace), and its
-  // piece that goes on beyond its stretch (1, in its ring), with their (reference, sum)
-  __shared__ Owner owner_s[2][kQ8Warps];
+  // piece that goes on beyond its stretch (1, in its ring): of which unit (-1: none), whether it has the
+  // unit's first tile, and its (reference, sum)
+  __shared__ int owner_s[2][kQ8Warps];
+  __shared__ bool first_s[kQ8Warps];
   __shared__ float ml_s[2][kQ8Warps][kMaxGroup][2];
   using R = Ring<D>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -625,11 +649,11 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
   grid_dependency_wait();
 
   // the line's length, and where this warp's stretch of it starts: by sequences (dense) or units
-  const int64_t elems = static_cast<int64_t>(p.batch) * (p.sel_ids ? p.num_kv_heads : 1);
+  const int elems = p.batch * (p.sel_ids ? p.num_kv_heads : 1);
   const int heads = p.sel_ids ? 1 : p.num_kv_heads;
   const bool tell = blockIdx.x == 0;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * kQ8Warps;
-  int64_t total, share, c0;
+  const unsigned warps = gridDim.x * kQ8Warps;
+  int total, share, c0;
   Walk use;
   use.h = 0;
   if (p.short_line) {
@@ -649,15 +673,13 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
     for (int i = 0; i < kScanRounds; ++i) {
       v[i] = upto[i] = 0;
       if (32 * i >= elems) continue;
-      v[i] = static_cast<int>(span(judge_unit(p, len[i], count[i], tell && warp == 0))) * heads;
+      v[i] = span(judge_unit(p, len[i], count[i], tell && warp == 0)) * heads;
       upto[i] = warp_scan(v[i]) + sum;
       sum = __shfl_sync(0xffffffffu, upto[i], 31);
     }
     total = sum;
-    const int each = static_cast<int>((static_cast<unsigned>(sum) + static_cast<unsigned>(warps) - 1) /
-                                      static_cast<unsigned>(warps));
-    share = each;
-    c0 = (static_cast<int64_t>(blockIdx.x) * kQ8Warps + warp) * share;
+    share = (static_cast<unsigned>(sum) + warps - 1) / warps;
+    c0 = (blockIdx.x * kQ8Warps + warp) * share;
     int elem = 0, base = 0;
 #pragma unroll
     for (int i = 0; i < kScanRounds; ++i) {
@@ -675,27 +697,25 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
     if (p.sel_ids) use.h = elem - use.b * p.num_kv_heads;
     use.base = base;
   } else {
-    auto tiles_of = [&](int64_t e, bool say) -> int64_t {
+    auto span_of = [&](int e, bool say) {
       if (e >= elems) return 0;
-      const int b = static_cast<int>(p.sel_ids ? e / p.num_kv_heads : e);
-      const int h = static_cast<int>(e - static_cast<int64_t>(b) * p.num_kv_heads);
-      return span(load_unit(p, b, p.sel_ids ? h : 0, say)) * heads;
+      const int b = p.sel_ids ? e / p.num_kv_heads : e;
+      return span(load_unit(p, b, p.sel_ids ? e - b * p.num_kv_heads : 0, say)) * heads;
     };
     total = 0;
-    for (int64_t e0 = 0; e0 < elems; e0 += kQ8Threads) {
-      const int64_t upto =
-          total + block_scan(tiles_of(e0 + threadIdx.x, tell), sums[(e0 / kQ8Threads) & 1]);
+    for (int e0 = 0; e0 < elems; e0 += kQ8Threads) {
+      const int upto = total + block_scan(span_of(e0 + threadIdx.x, tell), sums[(e0 / kQ8Threads) & 1]);
       if (threadIdx.x == kQ8Threads - 1) start_s[0] = upto;
       __syncthreads();
       total = start_s[0];
       __syncthreads();
     }
-    share = (total + warps - 1) / warps;
-    c0 = static_cast<int64_t>(blockIdx.x) * kQ8Warps * share;      // of the block, first
-    int64_t before = 0;
-    for (int64_t e0 = 0; e0 < elems && c0 < total; e0 += kQ8Threads) {
-      const int64_t mine = tiles_of(e0 + threadIdx.x, false);
-      const int64_t upto = before + block_scan(mine, sums[(e0 / kQ8Threads) & 1]);
+    share = (static_cast<unsigned>(total) + warps - 1) / warps;
+    c0 = blockIdx.x * kQ8Warps * share;              // of the block, first
+    int before = 0;
+    for (int e0 = 0; e0 < elems && c0 < total; e0 += kQ8Threads) {
+      const int mine = span_of(e0 + threadIdx.x, false);
+      const int upto = before + block_scan(mine, sums[(e0 / kQ8Threads) & 1]);
       if (upto > c0 && upto - mine <= c0) {
         start_s[0] = e0 + threadIdx.x;
         start_s[1] = upto - mine;
@@ -707,24 +727,22 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
       __syncthreads();
     }
     __syncthreads();
-    use.b = static_cast<int>(p.sel_ids ? start_s[0] / p.num_kv_heads : start_s[0]);
-    if (p.sel_ids) use.h = static_cast<int>(start_s[0] - static_cast<int64_t>(use.b) * p.num_kv_heads);
+    use.b = p.sel_ids ? start_s[0] / p.num_kv_heads : start_s[0];
+    if (p.sel_ids) use.h = start_s[0] - use.b * p.num_kv_heads;
     use.base = start_s[1];
     if (c0 < total) use.u = load_unit(p, use.b, use.h, false);
     c0 += warp * share;
   }
-  const int64_t block_share = share * kQ8Warps;
-  const int64_t c1 = min(c0 + share, total);
-  const int64_t block_c0 = static_cast<int64_t>(blockIdx.x) * block_share;
+  const int c1 = min(c0 + share, total);
 
-  if (threadIdx.x < 2 * kQ8Warps) owner_s[threadIdx.x & 1][threadIdx.x >> 1].unit = -1;
+  if (threadIdx.x < 2 * kQ8Warps) owner_s[threadIdx.x & 1][threadIdx.x >> 1] = -1;
   __syncthreads();
   uint8_t* ring = smem + warp * R::kWarp;
   float* closing = p.piece + (static_cast<int64_t>(blockIdx.x) * kQ8Warps + warp) * kMaxGroup * D;
   if (c0 < c1) {
     walk_to(p, use, c0);
     Walk ask = use;
-    int ask_k = static_cast<int>(max(c0 - use.base - kOpen, int64_t(0)));   // next tile of ask's unit
+    int ask_k = max(c0 - use.base - kOpen, 0);       // next tile of ask's unit
     PageCache pc;
     pc.b = -1;
     bool more = true;
@@ -752,8 +770,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
 
     Warp<NQ, C, D> w;
     for (;;) {
-      const int k0 = static_cast<int>(max(c0 - use.base - kOpen, int64_t(0)));
-      const int k1 = static_cast<int>(min(c1 - use.base - kOpen, static_cast<int64_t>(use.u.tiles)));
+      const int k0 = max(c0 - use.base - kOpen, 0), k1 = min(c1 - use.base - kOpen, use.u.tiles);
       if (k0 < k1) {
         open_unit(p, raw, w);
         for (int k = k0; k < k1; ++k) {
@@ -774,68 +791,49 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
         fetch_queries<NQ, D>(p, use.b, use.h, raw);
       }
       if (k0 < k1) {
-        const int64_t unit = static_cast<int64_t>(now.b) * p.num_kv_heads + now.h;
-        const Owner own = {unit, now.base, now.u.tiles, k0 == 0};
+        const int unit = now.b * p.num_kv_heads + now.h;
         if (k1 < now.u.tiles) {
-          if (lane == 0) owner_s[1][warp] = own;
+          if (lane == 0) {
+            owner_s[1][warp] = unit;
+            first_s[warp] = k0 == 0;
+          }
           store_piece(w, G, reinterpret_cast<float*>(ring), R::kPieceRow, ml_s[1][warp]);
         } else if (k0 > 0) {
-          if (lane == 0) owner_s[0][warp] = own;
+          if (lane == 0) owner_s[0][warp] = unit;
           store_piece(w, G, closing, D, ml_s[0][warp]);
         } else {
-          store_unit(w, G, p.out + unit * G * D);
+          store_unit(w, G, p.out + static_cast<int64_t>(unit) * G * D);
         }
       }
       if (last) break;
     }
   }
   __syncthreads();
-  int64_t part_of[2] = {-1, -1};                     // units of the block's parts
+  int part_of[2] = {-1, -1};                         // units of the block's parts
 
   // The block's chains: pieces that go on, up to one that closes the unit or to the block's end; before
   // them a piece at the block's start that only closes (w = -1).
   for (int w = -1; w < kQ8Warps;) {
     const bool lone = w < 0;
-    if (owner_s[!lone][max(w, 0)].unit < 0) {
+    const int begin = max(w, 0), unit = owner_s[!lone][begin];
+    if (unit < 0) {
       ++w;
       continue;
     }
-    const Owner own = owner_s[!lone][max(w, 0)];
-    int end = max(w, 0);                             // pieces w .. end - 1 go on
+    int end = begin;                                 // pieces begin .. end - 1 go on
     if (!lone)
       do ++end;
-      while (end < kQ8Warps && owner_s[1][end].unit >= 0 && owner_s[0][end].unit < 0);
-    const bool closed = end < kQ8Warps && owner_s[0][end].unit >= 0;
-    const int begin = max(w, 0), slot = !lone && own.first;
+      while (end < kQ8Warps && owner_s[1][end] >= 0 && owner_s[0][end] < 0);
+    const bool closed = end < kQ8Warps && owner_s[0][end] >= 0;
+    const int slot = !lone && first_s[begin];
     const bool whole = closed && slot;
-    const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * kMaxGroup;
-    const int count = end - begin + closed;
-    // a head's four dimensions per thread; a short loop, since the code is run once and must be fetched
-    for (int e = threadIdx.x; e < G * (D / 4); e += kQ8Threads) {
-      const int head = e / (D / 4), dim = e % (D / 4) * 4;
-      float sum[4] = {}, top = kNoScore, z = 0.f;
-#pragma unroll 1
-      for (int i = 0; i < count; ++i) {
-        const bool on = begin + i < end;
-        const float* row =
-            on ? reinterpret_cast<const float*>(smem + (begin + i) * R::kWarp) + head * R::kPieceRow
-               : p.piece + ((static_cast<int64_t>(blockIdx.x) * kQ8Warps + end) * kMaxGroup + head) * D;
-        const float4 v = *reinterpret_cast<const float4*>(row + dim);
-        const float x[4] = {v.x, v.y, v.z, v.w};
-        add_part(sum, top, z, x, ml_s[on][begin + i][head][0], ml_s[on][begin + i][head][1]);
-      }
-      if (whole) {
-        const float f = z == 0.f ? 0.f : 1.f / z;
-        *reinterpret_cast<float4*>(p.out + (own.unit * G + head) * D + dim) =
-            make_float4(sum[0] * f, sum[1] * f, sum[2] * f, sum[3] * f);
-      } else {
-        *reinterpret_cast<float4*>(p.part_acc + (part + head) * D + dim) =
-            make_float4(sum[0], sum[1], sum[2], sum[3]);
-        if (dim == 0)
-          *reinterpret_cast<float2*>(p.part_ml + (part + head) * 2) = make_float2(top, z);
-      }
-    }
-    if (!whole) part_of[slot] = own.unit;
+    const int64_t part = (blockIdx.x * 2 + slot) * kMaxGroup;
+    add_chain<D>(reinterpret_cast<const float*>(smem + begin * R::kWarp), R::kWarp / 4, end - begin,
+                 closed ? p.piece + static_cast<int64_t>(blockIdx.x * kQ8Warps + end) * kMaxGroup * D : nullptr,
+                 ml_s[1][begin][0], closed ? ml_s[0][end][0] : nullptr, G, whole,
+                 whole ? p.out + static_cast<int64_t>(unit) * G * D : p.part_acc + part * D,
+                 p.part_ml + part * 2);
+    if (!whole) part_of[slot] = unit;
     w = lone ? 0 : end;
   }
   if (threadIdx.x == 0) {
@@ -843,11 +841,10 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
     p.begins[blockIdx.x] = part_of[1];
   }
   // units that see nothing
-  for (int64_t e = blockIdx.x; e < elems; e += gridDim.x) {
-    const int b = static_cast<int>(p.sel_ids ? e / p.num_kv_heads : e);
-    if (load_unit(p, b, p.sel_ids ? static_cast<int>(e - static_cast<int64_t>(b) * p.num_kv_heads) : 0, false).tiles)
-      continue;
-    float* row = p.out + e * heads * G * D;
+  for (int e = blockIdx.x; e < elems; e += gridDim.x) {
+    const int b = p.sel_ids ? e / p.num_kv_heads : e;
+    if (load_unit(p, b, p.sel_ids ? e - b * p.num_kv_heads : 0, false).tiles) continue;
+    float* row = p.out + static_cast<int64_t>(e) * heads * G * D;
     for (int i = threadIdx.x; i < heads * G * D; i += kQ8Threads) row[i] = 0.f;
   }
 }
@@ -864,10 +861,10 @@ __global__ void __launch_bounds__(kQ8Threads) q8_join_kernel(Q8AttendParams p) {
   const int block = blockIdx.x / G, head = blockIdx.x % G;
   grid_dependency_wait();
   const int blocks = gridDim.x / G;
-  const int64_t unit = p.begins[block];
+  const int unit = p.begins[block];
   // the unit's parts: of this block and of those after it in which it goes on
   int count = 1;
-  int64_t after[kJoinRounds];
+  int after[kJoinRounds];
 #pragma unroll
   for (int i = 0; i < kJoinRounds; ++i) {
     const int k = block + 1 + 32 * i + lane;
@@ -920,7 +917,7 @@ __global__ void __launch_bounds__(kQ8Threads) q8_join_kernel(Q8AttendParams p) {
       const float x[1] = {acc_s[i][threadIdx.x]};
       add_part(all, best, l, x, ml_s[i][0], ml_s[i][1]);
     }
-    p.out[(unit * G + head) * D + threadIdx.x] = l == 0.f ? 0.f : all[0] / l;
+    p.out[(static_cast<int64_t>(unit) * G + head) * D + threadIdx.x] = l == 0.f ? 0.f : all[0] / l;
   }
 }
 
@@ -957,14 +954,15 @@ cudaError_t launch_code(const Q8AttendParams& p, int d, int blocks, cudaStream_t
 int q8_attend_warps() { return kQ8Warps; }
 int q8_attend_most_blocks() { return 32 * kJoinRounds; }
 
+bool q8_attend_fits(int batch, int num_kv_heads, int team_size, int teams) {
+  const int64_t unit = static_cast<int64_t>(teams) * (team_size / kTile) + kOpen;
+  return static_cast<int64_t>(batch) * num_kv_heads <= kMostPlaces / unit;
+}
+
 cudaError_t launch_q8_attend(const Q8AttendParams& params, int head_dim, bool bf16, int code, int sms,
                              cudaStream_t stream) {
   Q8AttendParams p = params;
-  const int64_t elems = static_cast<int64_t>(p.batch) * (p.sel_ids ? p.num_kv_heads : 1);
-  const int64_t teams = p.sel_ids ? p.num_draws : p.max_teams;
-  const int64_t places = static_cast<int64_t>(p.batch) * p.num_kv_heads *
-                         (teams * (p.team_size / kTile) + kOpen + 1);
-  p.short_line = elems <= 32 * kScanRounds && places < (1ll << 30);
+  p.short_line = static_cast<int64_t>(p.batch) * (p.sel_ids ? p.num_kv_heads : 1) <= 32 * kScanRounds;
   if (code == kCodeI8)
     return bf16 ? launch_code<1, kCodeI8>(p, head_dim, sms, stream)
                 : launch_code<2, kCodeI8>(p, head_dim, sms, stream);

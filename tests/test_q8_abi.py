@@ -94,6 +94,13 @@ def test_attend_refusals(lib, f, kw, cw, expect):
     assert getattr(lib, f)(ctypes.addressof(a), ctypes.addressof(c), None) == expect
 
 
+def test_more_tiles_than_32_bits_count(lib):
+    a, c = step_args(batch=65535, num_kv_heads=8, num_q_heads=8, max_teams=16384), cache_args()
+    assert lib.santa_q8_dense_decode(ctypes.addressof(a), ctypes.addressof(c), None) == UNSUPPORTED
+    a = step_args(batch=65535, num_kv_heads=64, num_q_heads=64, num_draws=4096)
+    assert lib.santa_q8_attend(ctypes.addressof(a), ctypes.addressof(c), None) == UNSUPPORTED
+
+
 @pytest.mark.parametrize("f", ATTEND[1:])
 @pytest.mark.parametrize("kw,expect", [
     (dict(num_draws=0), UNSUPPORTED), (dict(num_draws=4097), UNSUPPORTED), (dict(sel_ids=0), INVALID),

@@ -163,11 +163,11 @@ struct Q8AttendParams {
   int32_t* begins;            // [blocks]
   float* part_acc;            // [blocks][2][kMaxGroup][d]
   float* part_ml;             // [blocks][2][kMaxGroup][2]
-  float* piece;               // [blocks][q8_attend_warps()][kMaxGroup][d]
+  float* piece;               // [blocks][q8_attend_warps(d)][kMaxGroup][d]
   float* out;                 // [B][Hq][d]
   int32_t* status;
 };
-int q8_attend_warps();
+int q8_attend_warps(int head_dim);   // of a block
 // Whether the tiles of all units, `teams` pages each, can be counted in 32 bits.
 bool q8_attend_fits(int batch, int num_kv_heads, int team_size, int teams);
 int q8_attend_most_blocks();

@@ -52,7 +52,7 @@ int q8_layout(int d, Q8Layout* l) {
   l->ml_bytes = round_up(2 * rows * 2 * sizeof(float), kAlign);
   l->acc_bytes = 2 * rows * d * sizeof(float);
   l->bytes = kAlign + l->split_bytes + l->ml_bytes + l->acc_bytes +
-             santa::q8_attend_warps() * rows * d * sizeof(float);
+             santa::q8_attend_warps(d) * rows * d * sizeof(float);
   return SANTA_OK;
 }
 

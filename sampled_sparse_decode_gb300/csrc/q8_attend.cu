@@ -41,8 +41,8 @@ namespace santa {
 namespace {
 
 constexpr int kTile = 32;                  // tokens of a tile
-constexpr int kQ8Warps = 8;
-constexpr int kQ8Threads = kQ8Warps * 32;
+constexpr int kJoinWarps = 8;
+constexpr int kJoinThreads = kJoinWarps * 32;
 constexpr int kStages = 3;                 // tiles of a warp's ring
 constexpr int kOpen = 2;                   // what opening a unit counts, in tiles
 constexpr int kScanRounds = 8;             // 32 sequences or units each that a warp reads by itself
@@ -55,10 +55,12 @@ constexpr float kTopWeight = 256.f;        // the same for a weight
 
 template <int D>
 struct Ring {
+  static constexpr int kWarps = D == 128 ? 8 : 12;             // of a block
+  static constexpr int kThreads = kWarps * 32;
   static constexpr int kCodes = kTile * D;                     // bytes of a tile's keys or values
   static constexpr int kStage = 2 * kCodes + 2 * kTile * 4;    // keys, values, scales
   static constexpr int kWarp = kStages * kStage;
-  static constexpr int kBytes = kQ8Warps * kWarp;
+  static constexpr int kBytes = kWarps * kWarp;
   static constexpr int kPieceRow = D + 4;                      // floats of a head in a piece
   static_assert(kMaxGroup * kPieceRow * 4 <= kWarp, "a piece fits its warp's ring");
 };
@@ -207,13 +209,14 @@ __device__ __forceinline__ int warp_scan(int v) {
   }
   return v;
 }
+template <int W>
 __device__ __forceinline__ int block_scan(int v, int* warp_sums) {
   const int warp = threadIdx.x >> 5;
   v = warp_scan(v);
   if ((threadIdx.x & 31) == 31) warp_sums[warp] = v;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kQ8Warps; ++w)
+  for (int w = 0; w < W; ++w)
     if (w < warp) v += warp_sums[w];
   return v;
 }
@@ -613,7 +616,7 @@ __device__ __forceinline__ void add_chain(const float* on, int on_stride, int on
                                           float* rows, float* ml) {
   const int count = on_count + (closing != nullptr);
 #pragma unroll 1
-  for (int e = threadIdx.x; e < G * (D / 4); e += kQ8Threads) {
+  for (int e = threadIdx.x; e < G * (D / 4); e += Ring<D>::kThreads) {
     const int head = e / (D / 4), dim = e % (D / 4) * 4;
     float sum[4] = {}, top = kNoScore, z = 0.f;
 #pragma unroll 1
@@ -632,17 +635,17 @@ __device__ __forceinline__ void add_chain(const float* on, int on_stride, int on
 }
 
 template <int NQ, int C, int D>
-__global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams p) {
+__global__ void __launch_bounds__(Ring<D>::kThreads, 1) q8_attend_kernel(Q8AttendParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int sums[2][kQ8Warps];
+  __shared__ int sums[2][Ring<D>::kWarps];
   __shared__ int start_s[2];                         // element of the block's start, its place
-  __shared__ int2 notes[kQ8Warps][kStages];
+  __shared__ int2 notes[Ring<D>::kWarps][kStages];
   // each warp's piece that closes a unit which another warp opened (0, in the workspace), and its
   // piece that goes on beyond its stretch (1, in its ring): of which unit (-1: none), whether it has the
   // unit's first tile, and its (reference, sum)
-  __shared__ int owner_s[2][kQ8Warps];
-  __shared__ bool first_s[kQ8Warps];
-  __shared__ float ml_s[2][kQ8Warps][kMaxGroup][2];
+  __shared__ int owner_s[2][Ring<D>::kWarps];
+  __shared__ bool first_s[Ring<D>::kWarps];
+  __shared__ float ml_s[2][Ring<D>::kWarps][kMaxGroup][2];
   using R = Ring<D>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = p.num_q_heads / p.num_kv_heads;
@@ -652,7 +655,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
   const int elems = p.batch * (p.sel_ids ? p.num_kv_heads : 1);
   const int heads = p.sel_ids ? 1 : p.num_kv_heads;
   const bool tell = blockIdx.x == 0;
-  const unsigned warps = gridDim.x * kQ8Warps;
+  const unsigned warps = gridDim.x * Ring<D>::kWarps;
   int total, share, c0;
   Walk use;
   use.h = 0;
@@ -679,7 +682,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
     }
     total = sum;
     share = (static_cast<unsigned>(sum) + warps - 1) / warps;
-    c0 = (blockIdx.x * kQ8Warps + warp) * share;
+    c0 = (blockIdx.x * Ring<D>::kWarps + warp) * share;
     int elem = 0, base = 0;
 #pragma unroll
     for (int i = 0; i < kScanRounds; ++i) {
@@ -703,25 +706,25 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
       return span(load_unit(p, b, p.sel_ids ? e - b * p.num_kv_heads : 0, say)) * heads;
     };
     total = 0;
-    for (int e0 = 0; e0 < elems; e0 += kQ8Threads) {
-      const int upto = total + block_scan(span_of(e0 + threadIdx.x, tell), sums[(e0 / kQ8Threads) & 1]);
-      if (threadIdx.x == kQ8Threads - 1) start_s[0] = upto;
+    for (int e0 = 0; e0 < elems; e0 += Ring<D>::kThreads) {
+      const int upto = total + block_scan<Ring<D>::kWarps>(span_of(e0 + threadIdx.x, tell), sums[(e0 / Ring<D>::kThreads) & 1]);
+      if (threadIdx.x == Ring<D>::kThreads - 1) start_s[0] = upto;
       __syncthreads();
       total = start_s[0];
       __syncthreads();
     }
     share = (static_cast<unsigned>(total) + warps - 1) / warps;
-    c0 = blockIdx.x * kQ8Warps * share;              // of the block, first
+    c0 = blockIdx.x * Ring<D>::kWarps * share;              // of the block, first
     int before = 0;
-    for (int e0 = 0; e0 < elems && c0 < total; e0 += kQ8Threads) {
+    for (int e0 = 0; e0 < elems && c0 < total; e0 += Ring<D>::kThreads) {
       const int mine = span_of(e0 + threadIdx.x, false);
-      const int upto = before + block_scan(mine, sums[(e0 / kQ8Threads) & 1]);
+      const int upto = before + block_scan<Ring<D>::kWarps>(mine, sums[(e0 / Ring<D>::kThreads) & 1]);
       if (upto > c0 && upto - mine <= c0) {
         start_s[0] = e0 + threadIdx.x;
         start_s[1] = upto - mine;
       }
       if (__syncthreads_or(upto > c0)) break;
-      if (threadIdx.x == kQ8Threads - 1) sums[0][0] = upto;
+      if (threadIdx.x == Ring<D>::kThreads - 1) sums[0][0] = upto;
       __syncthreads();
       before = sums[0][0];
       __syncthreads();
@@ -735,10 +738,10 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
   }
   const int c1 = min(c0 + share, total);
 
-  if (threadIdx.x < 2 * kQ8Warps) owner_s[threadIdx.x & 1][threadIdx.x >> 1] = -1;
+  if (threadIdx.x < 2 * Ring<D>::kWarps) owner_s[threadIdx.x & 1][threadIdx.x >> 1] = -1;
   __syncthreads();
   uint8_t* ring = smem + warp * R::kWarp;
-  float* closing = p.piece + (static_cast<int64_t>(blockIdx.x) * kQ8Warps + warp) * kMaxGroup * D;
+  float* closing = p.piece + (static_cast<int64_t>(blockIdx.x) * Ring<D>::kWarps + warp) * kMaxGroup * D;
   if (c0 < c1) {
     walk_to(p, use, c0);
     Walk ask = use;
@@ -813,7 +816,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
 
   // The block's chains: pieces that go on, up to one that closes the unit or to the block's end; before
   // them a piece at the block's start that only closes (w = -1).
-  for (int w = -1; w < kQ8Warps;) {
+  for (int w = -1; w < Ring<D>::kWarps;) {
     const bool lone = w < 0;
     const int begin = max(w, 0), unit = owner_s[!lone][begin];
     if (unit < 0) {
@@ -823,13 +826,13 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
     int end = begin;                                 // pieces begin .. end - 1 go on
     if (!lone)
       do ++end;
-      while (end < kQ8Warps && owner_s[1][end] >= 0 && owner_s[0][end] < 0);
-    const bool closed = end < kQ8Warps && owner_s[0][end] >= 0;
+      while (end < Ring<D>::kWarps && owner_s[1][end] >= 0 && owner_s[0][end] < 0);
+    const bool closed = end < Ring<D>::kWarps && owner_s[0][end] >= 0;
     const int slot = !lone && first_s[begin];
     const bool whole = closed && slot;
     const int64_t part = (blockIdx.x * 2 + slot) * kMaxGroup;
     add_chain<D>(reinterpret_cast<const float*>(smem + begin * R::kWarp), R::kWarp / 4, end - begin,
-                 closed ? p.piece + static_cast<int64_t>(blockIdx.x * kQ8Warps + end) * kMaxGroup * D : nullptr,
+                 closed ? p.piece + static_cast<int64_t>(blockIdx.x * Ring<D>::kWarps + end) * kMaxGroup * D : nullptr,
                  ml_s[1][begin][0], closed ? ml_s[0][end][0] : nullptr, G, whole,
                  whole ? p.out + static_cast<int64_t>(unit) * G * D : p.part_acc + part * D,
                  p.part_ml + part * 2);
@@ -845,17 +848,17 @@ __global__ void __launch_bounds__(kQ8Threads, 1) q8_attend_kernel(Q8AttendParams
     const int b = p.sel_ids ? e / p.num_kv_heads : e;
     if (load_unit(p, b, p.sel_ids ? e - b * p.num_kv_heads : 0, false).tiles) continue;
     float* row = p.out + static_cast<int64_t>(e) * heads * G * D;
-    for (int i = threadIdx.x; i < heads * G * D; i += kQ8Threads) row[i] = 0.f;
+    for (int i = threadIdx.x; i < heads * G * D; i += Ring<D>::kThreads) row[i] = 0.f;
   }
 }
 
 // One block per (block of the first launch, query head of a group): joins the unit that begins there and
 // ends elsewhere, if there is one: a warp takes every eighth part, eight of them at a time.
 template <int D>
-__global__ void __launch_bounds__(kQ8Threads) q8_join_kernel(Q8AttendParams p) {
+__global__ void __launch_bounds__(kJoinThreads) q8_join_kernel(Q8AttendParams p) {
   constexpr int W = D / 32;                          // dimensions of a lane
-  __shared__ float acc_s[kQ8Warps][D];
-  __shared__ float ml_s[kQ8Warps][2];
+  __shared__ float acc_s[kJoinWarps][D];
+  __shared__ float ml_s[kJoinWarps][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = p.num_q_heads / p.num_kv_heads;
   const int block = blockIdx.x / G, head = blockIdx.x % G;
@@ -879,12 +882,12 @@ __global__ void __launch_bounds__(kQ8Threads) q8_join_kernel(Q8AttendParams p) {
   }
   float sum[W] = {}, top = kNoScore, z = 0.f;
   constexpr int kAhead = 8;
-  for (int k0 = warp; k0 < count; k0 += kAhead * kQ8Warps) {
+  for (int k0 = warp; k0 < count; k0 += kAhead * kJoinWarps) {
     float x[kAhead][W];
     float2 ml[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int k = k0 + i * kQ8Warps;
+      const int k = k0 + i * kJoinWarps;
       if (k < count) {
         // the first part is the second slot of its block, the others are the first slots of theirs
         const int64_t part = static_cast<int64_t>(2 * (block + k) + (k == 0)) * kMaxGroup + head;
@@ -901,7 +904,7 @@ __global__ void __launch_bounds__(kQ8Threads) q8_join_kernel(Q8AttendParams p) {
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
-      if (k0 + i * kQ8Warps < count) add_part(sum, top, z, x[i], ml[i].x, ml[i].y);
+      if (k0 + i * kJoinWarps < count) add_part(sum, top, z, x[i], ml[i].x, ml[i].y);
   }
 #pragma unroll
   for (int e = 0; e < W; ++e) acc_s[warp][lane * W + e] = sum[e];
@@ -913,7 +916,7 @@ __global__ void __launch_bounds__(kQ8Threads) q8_join_kernel(Q8AttendParams p) {
   if (threadIdx.x < D) {
     float all[1] = {0.f}, best = kNoScore, l = 0.f;
 #pragma unroll
-    for (int i = 0; i < kQ8Warps; ++i) {
+    for (int i = 0; i < kJoinWarps; ++i) {
       const float x[1] = {acc_s[i][threadIdx.x]};
       add_part(all, best, l, x, ml_s[i][0], ml_s[i][1]);
     }
@@ -932,13 +935,14 @@ cudaError_t launch_typed(const Q8AttendParams& p, int blocks, cudaStream_t strea
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(kQ8Threads);
+  cfg.blockDim = dim3(Ring<D>::kThreads);
   cfg.dynamicSmemBytes = Ring<D>::kBytes;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, kernel, p)) != cudaSuccess) return e;
   cfg.gridDim = dim3(blocks * (p.num_q_heads / p.num_kv_heads));
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, q8_join_kernel<D>, p);
 }
@@ -951,7 +955,7 @@ cudaError_t launch_code(const Q8AttendParams& p, int d, int blocks, cudaStream_t
 
 }  // namespace
 
-int q8_attend_warps() { return kQ8Warps; }
+int q8_attend_warps(int head_dim) { return head_dim == 128 ? Ring<128>::kWarps : Ring<64>::kWarps; }
 int q8_attend_most_blocks() { return 32 * kJoinRounds; }
 
 bool q8_attend_fits(int batch, int num_kv_heads, int team_size, int teams) {

@@ -581,7 +581,8 @@ typedef struct santa_q8_args {
   const float* v_scale;
   int type;                    /* SANTA_I8 or SANTA_E4M3 */
   int window;                  /* 0: none; else a token sees the last `window` cached tokens only */
-  float softcap;               /* 0: none; else scores s become softcap * tanh(s / softcap) */
+  float softcap;               /* 0: none; else (2^-20 .. 2^20) scores s become
+                                  softcap * tanh(s / softcap) */
 } santa_q8_args;
 
 /*

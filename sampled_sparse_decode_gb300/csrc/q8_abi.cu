@@ -11,6 +11,8 @@ using namespace santa::abi;
 namespace {
 
 constexpr int64_t kMaxPages = 0x7fffffff;   // page ids are int32
+// caps outside these would take the quotient of a score and its cap near the ends of fp32's range
+constexpr float kLeastCap = 0x1p-20f, kMostCap = 0x1p20f;
 
 // A buffer of a call, for the overlap checks.
 struct Span {
@@ -70,8 +72,9 @@ int check_q8_attend(const santa_decode_args* a, const santa_q8_args* c, bool lis
   if (!aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->page_table, 4) ||
       !aligned(a->seq_lens, 4) || !aligned(a->device_status, 4))
     return SANTA_ERR_INVALID_ARG;
-  if (!(c->softcap >= 0.f) || !std::isfinite(c->softcap) || c->window < 0)
+  if (c->softcap != 0.f && !(c->softcap >= kLeastCap && c->softcap <= kMostCap))
     return SANTA_ERR_INVALID_ARG;
+  if (c->window < 0) return SANTA_ERR_INVALID_ARG;
   if (listed) {
     if (a->num_draws < 1 || a->num_draws > kMaxDraws) return SANTA_ERR_UNSUPPORTED;
     if (!a->sel_ids || !a->sel_count || !a->pi) return SANTA_ERR_INVALID_ARG;

@@ -141,6 +141,51 @@ def test_all_teams_with_weight_one_is_dense():
     check_dense(c, q, out)
 
 
+def many(B, seed, T=64):
+    """Lengths of a large batch: empty runs, single tokens, a few long ones."""
+    g = torch.Generator().manual_seed(seed)
+    lens = torch.randint(0, 3 * T, (B,), generator=g)
+    lens[torch.rand(B, generator=g) < 0.3] = 0
+    lens[torch.rand(B, generator=g) < 0.2] = 1
+    lens[B // 3:B // 2] = 0
+    lens[B // 2], lens[-1] = 40 * T + 3, 7 * T
+    return lens.tolist()
+
+
+@pytest.mark.parametrize("B,hkv,hq,dtype,d,window", [
+    (256, 2, 4, BF16, 128, 0), (257, 1, 8, BF16, 128, 0), (300, 3, 3, F32, 64, 100), (1500, 1, 2, BF16, 64, 0),
+])
+def test_large_batches(B, hkv, hq, dtype, d, window):
+    """More sequences than a warp reads by itself, and than the grid has warps."""
+    c = Q8(many(B, B), hkv, d, 64, I8, seed=1)
+    q, status = queries(c, hq, dtype), status_word()
+    out = torch.full(q.shape, 9.0, device="cuda")
+    santa.santa_q8_dense_decode(q, c.cache, c.table, c.seq_lens, window=window, out=out, device_status=status)
+    assert int(status) == 0
+    check_dense(c, q, out, window=window)
+    c.seq_lens[5], c.seq_lens[B - 2] = -1, 10**6
+    c.lens[5], c.lens[B - 2] = 0, 0
+    santa.santa_q8_dense_decode(q, c.cache, c.table, c.seq_lens, window=window, out=out, device_status=status)
+    assert int(status) == DEV_BAD_SEQLEN
+    check_dense(c, q, out, window=window)
+
+
+@pytest.mark.parametrize("B,hkv", [(64, 4), (70, 4), (130, 3)])
+def test_large_batches_of_lists(B, hkv):
+    c = Q8(many(B, B), hkv, 128, 64, E4M3, seed=1)
+    q, status = queries(c, 2 * hkv, BF16), status_word()
+    ids, count, pi = listed(c, 6, seed=3)
+    out = santa.santa_q8_attend(q, c.cache, c.table, c.seq_lens, ids, count, pi, device_status=status)
+    assert int(status) == 0
+    check_listed(c, q, out, ids, count, pi)
+
+
+def test_one_long_sequence_behind_many_empty_ones():
+    c = Q8([0] * 1000 + [9000] + [0] * 500, 2, 64, 64, I8, seed=1)
+    q = queries(c, 4, BF16)
+    check_dense(c, q, santa.santa_q8_dense_decode(q, c.cache, c.table, c.seq_lens))
+
+
 def test_bad_lists_leave_teams_out():
     c = Q8([300, 300, 300, 300], 1, 64, 64, I8, seed=4)
     q = queries(c, 2, BF16)

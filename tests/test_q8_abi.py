@@ -88,6 +88,7 @@ ATTEND = ["santa_q8_dense_decode", "santa_q8_attend", "santa_q8_topk_decode", "s
     ({}, dict(v=0x2000008), INVALID), ({}, dict(k_scale=0), INVALID), ({}, dict(v_scale=0x3100004), INVALID),
     ({}, dict(softcap=-1.0), INVALID), ({}, dict(softcap=math.nan), INVALID),
     ({}, dict(softcap=math.inf), INVALID), ({}, dict(window=-1), INVALID),
+    ({}, dict(softcap=9e-7), INVALID), ({}, dict(softcap=1.1e6), INVALID),
 ])
 def test_attend_refusals(lib, f, kw, cw, expect):
     a, c = step_args(**kw), cache_args(**cw)

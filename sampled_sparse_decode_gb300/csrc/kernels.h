@@ -155,7 +155,6 @@ struct Q8AttendParams {
   float scale;                // 1 / sqrt(d)
   float softcap;              // 0: none
   int window;                 // 0: none
-  bool short_line;            // few sequences or units (set by the launcher)
   // per block (at most q8_attend_most_blocks()): the unit that goes on there from the block before and
   // the unit that begins there and goes on (-1: none), as far as it does not end there; their parts, sums
   // and (reference, sum of weights); per warp a piece

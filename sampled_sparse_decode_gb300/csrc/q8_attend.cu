@@ -32,6 +32,7 @@
 //   - The matrix units cut what they add; each tile's products start from zero and are added to the
 //     running sums in fp32 with rounding.
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.h"
 #include "q8.cuh"
@@ -659,13 +660,14 @@ __global__ void __launch_bounds__(Ring<D>::kThreads, 1) q8_attend_kernel(Q8Atten
   int total, share, c0;
   Walk use;
   use.h = 0;
-  if (p.short_line) {
-    // every warp for itself, without a barrier; all loads first
-    int len[kScanRounds], count[kScanRounds], v[kScanRounds], upto[kScanRounds], sum = 0;
+  // Every warp for itself, without a barrier, 32 elements to a round; all loads first.
+  auto scan = [&](auto rounds) {
+    constexpr int N = decltype(rounds)::value;
+    int len[N], count[N], v[N], upto[N], sum = 0;
 #pragma unroll
-    for (int i = 0; i < kScanRounds; ++i) {
+    for (int i = 0; i < N; ++i) {
       len[i] = count[i] = 0;
-      if (32 * i >= elems) continue;
+      if (N > 1 && 32 * i >= elems) continue;
       const unsigned e = 32 * i + lane;
       if (e < elems) {
         len[i] = p.seq_lens[p.sel_ids ? e / static_cast<unsigned>(p.num_kv_heads) : e];
@@ -673,9 +675,9 @@ __global__ void __launch_bounds__(Ring<D>::kThreads, 1) q8_attend_kernel(Q8Atten
       }
     }
 #pragma unroll
-    for (int i = 0; i < kScanRounds; ++i) {
+    for (int i = 0; i < N; ++i) {
       v[i] = upto[i] = 0;
-      if (32 * i >= elems) continue;
+      if (N > 1 && 32 * i >= elems) continue;
       v[i] = span(judge_unit(p, len[i], count[i], tell && warp == 0)) * heads;
       upto[i] = warp_scan(v[i]) + sum;
       sum = __shfl_sync(0xffffffffu, upto[i], 31);
@@ -685,8 +687,8 @@ __global__ void __launch_bounds__(Ring<D>::kThreads, 1) q8_attend_kernel(Q8Atten
     c0 = (blockIdx.x * Ring<D>::kWarps + warp) * share;
     int elem = 0, base = 0;
 #pragma unroll
-    for (int i = 0; i < kScanRounds; ++i) {
-      if (32 * i >= elems) continue;
+    for (int i = 0; i < N; ++i) {
+      if (N > 1 && 32 * i >= elems) continue;
       const unsigned hit = __ballot_sync(0xffffffffu, upto[i] > c0 && upto[i] - v[i] <= c0);
       if (hit) {
         const int from = __ffs(hit) - 1;
@@ -699,6 +701,11 @@ __global__ void __launch_bounds__(Ring<D>::kThreads, 1) q8_attend_kernel(Q8Atten
     use.b = p.sel_ids ? elem / p.num_kv_heads : elem;
     if (p.sel_ids) use.h = elem - use.b * p.num_kv_heads;
     use.base = base;
+  };
+  if (elems <= 32) {
+    scan(std::integral_constant<int, 1>());          // short code: a launch fetches what it runs
+  } else if (elems <= 32 * kScanRounds) {
+    scan(std::integral_constant<int, kScanRounds>());
   } else {
     auto span_of = [&](int e, bool say) {
       if (e >= elems) return 0;
@@ -963,10 +970,8 @@ bool q8_attend_fits(int batch, int num_kv_heads, int team_size, int teams) {
   return static_cast<int64_t>(batch) * num_kv_heads <= kMostPlaces / unit;
 }
 
-cudaError_t launch_q8_attend(const Q8AttendParams& params, int head_dim, bool bf16, int code, int sms,
+cudaError_t launch_q8_attend(const Q8AttendParams& p, int head_dim, bool bf16, int code, int sms,
                              cudaStream_t stream) {
-  Q8AttendParams p = params;
-  p.short_line = static_cast<int64_t>(p.batch) * (p.sel_ids ? p.num_kv_heads : 1) <= 32 * kScanRounds;
   if (code == kCodeI8)
     return bf16 ? launch_code<1, kCodeI8>(p, head_dim, sms, stream)
                 : launch_code<2, kCodeI8>(p, head_dim, sms, stream);

@@ -609,18 +609,15 @@ __device__ __forceinline__ void add_part(float (&sum)[N], float& top, float& z, 
 
 // Adds a chain of a unit's pieces, in the order of the line, by all threads of the block: a head's four
 // dimensions each.  `on_count` pieces lie `on_stride` floats apart from `on` on, `closing` (or null) follows
-// them; ml: their (reference, sum) by head.  `whole`: to rows of out; else to a part and its ml.  Short loops:
-// a launch runs this code once, and fetching it takes longer than running it.
+// them; ml: their (reference, sum) by head.  `whole`: to rows of out; else to a part and its ml.
 template <int D>
 __device__ __forceinline__ void add_chain(const float* on, int on_stride, int on_count, const float* closing,
                                           const float* ml_on, const float* ml_closing, int G, bool whole,
                                           float* rows, float* ml) {
   const int count = on_count + (closing != nullptr);
-#pragma unroll 1
   for (int e = threadIdx.x; e < G * (D / 4); e += Ring<D>::kThreads) {
     const int head = e / (D / 4), dim = e % (D / 4) * 4;
     float sum[4] = {}, top = kNoScore, z = 0.f;
-#pragma unroll 1
     for (int i = 0; i < count; ++i) {
       const float* row = i < on_count ? on + i * on_stride + head * Ring<D>::kPieceRow : closing + head * D;
       const float* at = (i < on_count ? ml_on + i * kMaxGroup * 2 : ml_closing) + head * 2;
@@ -704,6 +701,8 @@ __global__ void __launch_bounds__(Ring<D>::kThreads, 1) q8_attend_kernel(Q8Atten
   };
   if (elems <= 32) {
     scan(std::integral_constant<int, 1>());          // short code: a launch fetches what it runs
+  } else if (elems <= 128) {
+    scan(std::integral_constant<int, 4>());
   } else if (elems <= 32 * kScanRounds) {
     scan(std::integral_constant<int, kScanRounds>());
   } else {

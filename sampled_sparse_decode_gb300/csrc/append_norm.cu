@@ -12,12 +12,20 @@
 // two quads of elements each: the two that a rotation by halves pairs up, or neighbours.  The norm's sum
 // and the row's largest magnitude are shuffles among them; every element is read once and written once.
 // Quads rather than 16-byte pieces keep a thread's row, sums and weights in 8 registers each, so that
-// three blocks stay on a multiprocessor.
+// three blocks stay on a multiprocessor; values, which need no sums, are taken in 16-byte pieces.
 //
 // With a cache of the activations' type the mean is summed in the order of reps.cu (its bits are
 // santa_build_reps's): rows group, group + kGroups, ... of a quad in row order, then the groups.  bf16 rows
 // fill a block with the groups of reps.cu, and the values are blocks of their own; fp32 rows fill half of
 // one, and the other half takes the values.
+//
+// Bound by latency for single tokens, by issue and HBM together for prompts.  Measured on GB300: 8
+// sequences of 4096 tokens (32 query and 8 KV heads of 128, bf16, norms, e4m3) 140 us, 5.4 TB/s of what
+// must move; one token for each of 8 sequences into an int8 cache 4.2 us.  Both sides: 16-byte pieces, two
+// blocks per SM 200 us, quads and three 178 (two 220, four 174 with spills); true divisions 239 against
+// 200; register pairs 155 -> 144, kernels with and without norms 144 -> 139; four query heads per search
+// 205 against 178 (eight), 16 in two turns 158 against 141; page items spread among the query items 139
+// against 141.5, but 2148 tokens 18.5 against 16.8.
 #include "append.cuh"
 #include "q8.cuh"
 

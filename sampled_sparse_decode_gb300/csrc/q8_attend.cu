@@ -24,9 +24,11 @@
 // values' tokens, stand in a register, and which dimension stands at which k is free.
 //   - q enters as fp16 pieces (one for bf16, two for fp32) of q 2^-e, e the exponent of the head's
 //     largest element: fp16's range holds everything down to 2^-24 of it.
-//   - The weights enter the second product as two fp16 pieces (22 bits; one would leave 2^-12 of
-//     error in an fp32 result) of p_j vs_j over a power of two near the largest p vs so far: the scales of
-//     values may lie any powers of two apart.
+//   - The weights enter the second product as two fp16 pieces (one would leave 2^-12 of error in an fp32
+//     result) of p_j vs_j over a power of two, by which the largest p vs so far becomes 2^7 .. 2^15: the
+//     scales of values may lie any powers of two apart.  The second piece is what the first leaves, 2^11 up,
+//     with products of its own: fp16 rounds at 2^-25 below 2^-14, and its sums come down again with 2^-11.
+//     A weight so keeps 2^-22 of itself down to 2^-21 of the largest, and 2^-43 of the largest below.
 //   - The reference of the exponentials is raised only when a score passes it by 8 (powers of two),
 //     which is seldom after a few tiles, so a tile has no reduction among lanes.
 //   - The matrix units cut what they add; each tile's products start from zero and are added to the
@@ -64,7 +66,9 @@ constexpr int kBeyond = INT32_MAX - 16;    // behind every place of a line
 constexpr int64_t kMostPlaces = INT32_MAX - (1 << 16);
 constexpr float kNoScore = -1e38f;         // a reference before the first score
 constexpr float kSlack = 8.f;              // how far a score may pass the reference (base 2)
-constexpr float kTopWeight = 256.f;        // the same for a weight
+constexpr int kWeightBits = 7;             // the largest weight starts out at 2^7 .. 2^8
+constexpr float kTopWeight = 0x1p15f;      // and may grow to this (fp16 ends at 65504)
+constexpr float kUp = 0x1p11f;             // of second pieces
 
 template <int D>
 struct Ring {
@@ -123,9 +127,14 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// The leading 11 bits of x (fp16 holds them from 2^-14 on; below, it rounds at 2^-25).
-__device__ __forceinline__ float cut_f16(float x) {
-  return __uint_as_float(__float_as_uint(x) & 0xffffe000u);
+// Adds the products of first and second pieces.
+__device__ __forceinline__ void add_pieces(float (&sum)[4], const float (&c)[4], const float (&c2)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    const uint64_t both = fma_pair(pair(c2[i], c2[i + 1]), twice(1.f / kUp), pair(c[i], c[i + 1]));
+    const float2 r = halves(add_pair(pair(sum[i], sum[i + 1]), both));
+    sum[i] = r.x, sum[i + 1] = r.y;
+  }
 }
 
 // The two code pairs of a word, bytes (0, 1) and (2, 3), as fp16.  int8: with its sign bit turned
@@ -435,7 +444,10 @@ __device__ __forceinline__ void raise(Warp<NQ, C, D>& w, const float (&x)[8], co
     big = fmaxf(big, w.big[i] * keep);
     w.big[i] = big;
     float inv = w.inv[i];
-    if (big > 0.f) inv = __uint_as_float((254u - min(max(__float_as_uint(big) >> 23, 1u), 253u)) << 23);
+    if (big > 0.f) {
+      const uint32_t e = min(max(__float_as_uint(big) >> 23, 1u + kWeightBits), 253u);
+      inv = __uint_as_float((254u + kWeightBits - e) << 23);
+    }
     // inv / w.inv as a power of two inside fp32's range
     const int d = static_cast<int>(__float_as_uint(inv) >> 23) - static_cast<int>(__float_as_uint(w.inv[i]) >> 23);
     const float f = keep * __uint_as_float(static_cast<uint32_t>(min(max(d, -126), 127) + 127) << 23);
@@ -531,10 +543,9 @@ __device__ __forceinline__ void attend_tile(const Q8AttendParams& p, Warp<NQ, C,
   for (int k = 0; k < 4; ++k) {
     w.sum[0] += e[2 * k];
     w.sum[1] += e[2 * k + 1];
-    // the first piece is cut, not rounded: what it leaves out is then exact in fp32 at once
-    const float a = cut_f16(pw[2 * k]), b = cut_f16(pw[2 * k + 1]);
-    hi[k] = pack_f16(a, b);
-    lo[k] = pack_f16(pw[2 * k] - a, pw[2 * k + 1] - b);
+    hi[k] = pack_f16(pw[2 * k], pw[2 * k + 1]);
+    const float2 got = f16x2_to_f32(hi[k]);          // what it leaves is exact in fp32
+    lo[k] = pack_f16((pw[2 * k] - got.x) * kUp, (pw[2 * k + 1] - got.y) * kUp);
     hi[k] = movmatrix_trans(hi[k]);
     lo[k] = movmatrix_trans(lo[k]);
   }
@@ -543,17 +554,16 @@ __device__ __forceinline__ void attend_tile(const Q8AttendParams& p, Warp<NQ, C,
   for (int j = 0; j < D / 16; ++j) {
     uint32_t a[4];
     ldmatrix_x4_trans(a, at + kTile * D + piece_at<D>(lane, j));
-    float c[4] = {0.f, 0.f, 0.f, 0.f};
+    float c[4] = {0.f, 0.f, 0.f, 0.f}, c2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       uint32_t f[4];
       tokens_to_f16<C>(a[2 * m], f[0], f[1]);
       tokens_to_f16<C>(a[2 * m + 1], f[2], f[3]);
       mma_f16_16816(c, f, hi[2 * m], hi[2 * m + 1]);
-      mma_f16_16816(c, f, lo[2 * m], lo[2 * m + 1]);
+      mma_f16_16816(c2, f, lo[2 * m], lo[2 * m + 1]);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w.acc[j][i] += c[i];
+    add_pieces(w.acc[j], c, c2);
   }
 }
 

@@ -1,0 +1,46 @@
+"""How many bits of small weights reach the result over 8-bit caches: what lies beside them in the same
+tile may be far larger."""
+import pytest
+import torch
+
+import sampled_sparse_decode_gb300 as santa
+from q8_cases import E4M3, I8, Q8
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("kind", [I8, E4M3])
+@pytest.mark.parametrize("d,hq,hkv", [(64, 2, 1), (128, 12, 2)])
+@pytest.mark.parametrize("down,tol", [(10, 2.0**-18), (18, 2.0**-18), (24, 2.0**-17)])
+@pytest.mark.parametrize("first", [True, False])
+def test_small_weights_beside_a_large_one(kind, d, hq, hkv, down, tol, first):
+    """Queries of zeros, so that every weight is its value's scale.  One token's scale is 2^down times the
+    others', with a value in dimension 0 alone; the other dimensions hold the small weights' sums only, of
+    one sign.
+
+    Weights whose largest is scaled to 2^7 .. 2^8 are 2^(7 - down) here.  As two fp16 pieces, the second 2^11
+    up, they carry 2^-22 of themselves down to 2^-14, and 2^-36 below (down = 24: 2^-19 of 2^-17).  Two
+    products of 16 tokens cut 17 terms each at 2^-24 (2^-18.9); sums of tiles and pieces, a division and the
+    64-bit result's fp32 take 2^-21."""
+    lens = [32, 33, 96, 64, 500, 2, 31, 128] * 3
+    c = Q8(lens, hkv, d, 64, kind, seed=down)
+    g = torch.Generator().manual_seed(down)
+    for b, L in enumerate(lens):
+        pages = c.table[b, :-(-L // 64)].long()
+        v = c.cache.v.view(torch.uint8)
+        v[pages] = v[pages] & 0x7f                  # no signs; an e4m3 0x7f is a NaN and cut below
+        if kind == E4M3:
+            v[pages] = v[pages].clamp(max=0x7e)
+        v[pages, :, :, 0] = 0
+        c.cache.v_scale[pages] = (1 + torch.rand(len(pages), hkv, 64, generator=g)).cuda()
+        at = 0 if first else L - 1
+        strong = torch.zeros(d, dtype=torch.uint8, device="cuda")
+        strong[0] = 127 if kind == I8 else 0x7e
+        v[pages[at // 64], :, at % 64] = strong
+        c.cache.v_scale[pages[at // 64], :, at % 64] *= 2.0**down
+    q = torch.zeros(len(lens), hq, d, device="cuda")
+    out = santa.santa_q8_dense_decode(q, c.cache, c.table, c.seq_lens)
+    for b, L in enumerate(lens):
+        want = c.tokens("v", b, L).mean(1).repeat_interleave(hq // hkv, 0)
+        over = float(((out[b].double() - want).abs() - tol * want).max())
+        assert over <= 0, (b, L)

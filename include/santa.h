@@ -591,9 +591,9 @@ typedef struct santa_q8_args {
  * (santa_dense_decode and santa_attend over the values that the rows stand for).  With the score
  * s_j = q . k_j / sqrt(d), capped if asked, over the tokens j < seq_len that the window leaves,
  *   out = sum_j w_j e^{s_j} v_j / sum_j w_j e^{s_j}     (w_j = 1, or 1 / pi of j's team).
- * Sums are held in fp32.  q enters the products as fp16 pieces that carry it to 2^-22 of its head's
- * largest element, weights as fp16 pieces that carry each to 2^-22 of itself, or to 2^-43 of the
- * largest where that is more.
+ * Sums are held in fp32.  q and the weights enter the products as fp16 pieces: elements of bf16
+ * queries exact down to 2^-31 of their head's largest, of fp32 ones to 2^-22 of themselves (or 2^-50 of
+ * the largest where that is more), weights to 2^-22 of themselves (or 2^-43 of the largest).
  *   a    q, page_table, seq_lens, dtype (of q), shapes, num_pages, out, workspace, device_status;
  *        santa_q8_attend also sel_ids, sel_count, pi and num_draws (1 .. 4096).  k_pool, v_pool, reps
  *        and the other fields are not read.

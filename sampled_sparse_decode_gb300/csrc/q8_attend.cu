@@ -22,8 +22,10 @@
 // tokens for the output, so that the group's up to 8 query heads are the n = 8 columns.  Both are read
 // by ldmatrix as pairs of bytes: four dimensions of a key, or (transposed) two dimensions of two
 // values' tokens, stand in a register, and which dimension stands at which k is free.
-//   - q enters as fp16 pieces (one for bf16, two for fp32) of q 2^-e, e the exponent of the head's
-//     largest element: fp16's range holds everything down to 2^-24 of it.
+//   - q enters as fp16 pieces (one for bf16, two for fp32) over a power of two, by which the head's largest
+//     element becomes 2^14 .. 2^15: bf16 elements are exact down to 2^-31 of it.  The second piece is what
+//     the first leaves, 2^11 up, with products of its own, so that an fp32 element keeps 2^-22 of itself
+//     down to 2^-28 of the largest, and 2^-50 of the largest below.
 //   - The weights enter the second product as two fp16 pieces (one would leave 2^-12 of error in an fp32
 //     result) of p_j vs_j over a power of two, by which the largest p vs so far becomes 2^7 .. 2^15: the
 //     scales of values may lie any powers of two apart.  The second piece is what the first leaves, 2^11 up,
@@ -66,6 +68,7 @@ constexpr int kBeyond = INT32_MAX - 16;    // behind every place of a line
 constexpr int64_t kMostPlaces = INT32_MAX - (1 << 16);
 constexpr float kNoScore = -1e38f;         // a reference before the first score
 constexpr float kSlack = 8.f;              // how far a score may pass the reference (base 2)
+constexpr int kQueryBits = 14;             // a head's largest element stands at 2^14 .. 2^15
 constexpr int kWeightBits = 7;             // the largest weight starts out at 2^7 .. 2^8
 constexpr float kTopWeight = 0x1p15f;      // and may grow to this (fp16 ends at 65504)
 constexpr float kUp = 0x1p11f;             // of second pieces
@@ -394,8 +397,9 @@ __device__ __forceinline__ void open_unit(const Q8AttendParams& p, const Queries
   for (int i = 0; i < D / 4; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  // 2^-e and 2^e as exponent fields; zeros and queries near fp32's ends keep a factor inside its range
-  const uint32_t e = min(max(top >> 23, 16u), 253u);
+  // the power of two and its reciprocal as exponent fields; zeros and tiny queries keep a factor inside
+  // fp32's range
+  const uint32_t e = min(max(top >> 23, 16u), 254u) - kQueryBits;
   const float down = __uint_as_float((254u - e) << 23), up = __uint_as_float(e << 23);
 #pragma unroll
   for (int s = 0; s < D / 16; ++s) {
@@ -405,7 +409,7 @@ __device__ __forceinline__ void open_unit(const Q8AttendParams& p, const Queries
       w.q[0][s][i] = pack_f16(a, c);
       if constexpr (NQ == 2) {
         const float2 got = f16x2_to_f32(w.q[0][s][i]);
-        w.q[NQ - 1][s][i] = pack_f16(a - got.x, c - got.y);
+        w.q[NQ - 1][s][i] = pack_f16((a - got.x) * kUp, (c - got.y) * kUp);
       }
     }
   }
@@ -472,7 +476,7 @@ __device__ __forceinline__ void attend_tile(const Q8AttendParams& p, Warp<NQ, C,
   float x[8], ks[4], vs[4];                          // token 8 k + g; score 2 k + i: head 2 t + i
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
-    float c[4] = {0.f, 0.f, 0.f, 0.f};
+    float c[NQ][4] = {};
 #pragma unroll
     for (int s = 0; s < D / 16; s += 2) {
       // rows 16 m + 0 .. 7 and 8 .. 15, pieces s and s + 1: matrix lane / 8's row is given by the lane
@@ -484,16 +488,17 @@ __device__ __forceinline__ void attend_tile(const Q8AttendParams& p, Warp<NQ, C,
         pairs_to_f16<C>(a[2 * k], f[0], f[2]);
         pairs_to_f16<C>(a[2 * k + 1], f[1], f[3]);
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) mma_f16_16816(c, f, w.q[n][s + k][0], w.q[n][s + k][1]);
+        for (int n = 0; n < NQ; ++n) mma_f16_16816(c[n], f, w.q[n][s + k][0], w.q[n][s + k][1]);
       }
     }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       ks[2 * m + r] = scales[16 * m + 8 * r + g];
       vs[2 * m + r] = scales[kTile + 16 * m + 8 * r + g];
-      x[4 * m + 2 * r] = c[2 * r];
-      x[4 * m + 2 * r + 1] = c[2 * r + 1];
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      x[4 * m + i] = NQ == 1 ? c[0][i] : fmaf(c[NQ - 1][i], 1.f / kUp, c[0][i]);
   }
   const bool part = n0 > 0 || n1 < kTile;
   if (__builtin_expect(part, 0)) {

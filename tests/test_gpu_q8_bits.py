@@ -1,12 +1,16 @@
-"""How many bits of small weights reach the result over 8-bit caches: what lies beside them in the same
-tile may be far larger."""
+"""How many bits of small weights and of small elements of a query reach the result over 8-bit caches:
+what lies beside them in the same row or tile may be far larger."""
+import math
+
 import pytest
 import torch
 
 import sampled_sparse_decode_gb300 as santa
-from q8_cases import E4M3, I8, Q8
+from q8_cases import E4M3, I8, Q8, attend64
 
 pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
 
 
 @pytest.mark.parametrize("kind", [I8, E4M3])
@@ -44,3 +48,34 @@ def test_small_weights_beside_a_large_one(kind, d, hq, hkv, down, tol, first):
         want = c.tokens("v", b, L).mean(1).repeat_interleave(hq // hkv, 0)
         over = float(((out[b].double() - want).abs() - tol * want).max())
         assert over <= 0, (b, L)
+
+
+@pytest.mark.parametrize("kind", [I8, E4M3])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("up", [2.0**12, -2.0**20])
+@pytest.mark.parametrize("d,hq,hkv", [(64, 4, 1), (128, 12, 2)])
+def test_small_elements_beside_a_large_one(kind, dtype, up, d, hq, hkv):
+    """A query with one element far above the others, in a dimension where the keys are zeros.
+
+    bf16 elements are fp16 numbers down to 2^-17 with the largest at 2^14 .. 2^15; of fp32 ones two pieces,
+    the second 2^11 up, carry 2^-22 down to 2^-14: both hold at 2^-20 of the largest.  A score then has the
+    cuts of d / 16 chained products (17 terms at 2^-24 each; one more for the sum of two chains) and 2^-22 of
+    its products' magnitudes, and the rest is as in q8_cases.bound."""
+    lens = [33, 100, 500, 2]
+    c = Q8(lens, hkv, d, 64, kind, seed=3)
+    c.cache.k.view(torch.uint8)[..., 5] = 0
+    g = torch.Generator().manual_seed(1)
+    q = torch.randn(len(lens), hq, d, generator=g).to(dtype).cuda()
+    q[..., 5] = up
+    out = santa.santa_q8_dense_decode(q, c.cache, c.table, c.seq_lens)
+    for b, L in enumerate(lens):
+        K, V = c.tokens("k", b, L), c.tokens("v", b, L)
+        want, _ = attend64(q[b], K, V)
+        qi = q[b].double().view(hkv, hq // hkv, d)
+        qk = (qi.abs() @ K.abs().transpose(1, 2)).amax(-1) / math.sqrt(d)
+        ds = (17 * (d / 16 + 1) * 2.0**-24 + 2.0**-22 + 8 * 2.0**-24) * qk
+        rel = (2 * (ds + 2.0**-21) + 2.0**-18).reshape(-1, 1)
+        mag, _ = attend64(q[b], K, V.abs())
+        tol = rel * mag + 2.0**-21 * mag.amax(-1, keepdim=True)
+        worst = float(((out[b].double() - want).abs() / tol).max())
+        assert worst <= 1, (b, L)

@@ -33,8 +33,9 @@
 //     A weight so keeps 2^-22 of itself down to 2^-21 of the largest, and 2^-43 of the largest below.
 //   - The reference of the exponentials is raised only when a score passes it by 8 (powers of two),
 //     which is seldom after a few tiles, so a tile has no reduction among lanes.
-//   - The matrix units cut what they add; each tile's products start from zero and are added to the
-//     running sums in fp32 with rounding.
+//   - The matrix units cut what they add.  A score's products start from zero for every 32 dimensions,
+//     those of the output for every tile, and are added to the running sums in fp32 with rounding (a score
+//     summed in the unit: fp32 queries 1.1e-7 from 64-bit results instead of 0.4e-7, at the same time).
 //
 // Bound by HBM where there is much to read (2 d + 8 bytes for every token and head), by latency
 // where there is little: a launch's chain is lengths -> page ids -> tiles -> pieces -> parts, and its code
@@ -130,6 +131,13 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+__device__ __forceinline__ void add_sums(float (&sum)[4], const float (&c)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    const float2 r = halves(add_pair(pair(sum[i], sum[i + 1]), pair(c[i], c[i + 1])));
+    sum[i] = r.x, sum[i + 1] = r.y;
+  }
+}
 // Adds the products of first and second pieces.
 __device__ __forceinline__ void add_pieces(float (&sum)[4], const float (&c)[4], const float (&c2)[4]) {
 #pragma unroll
@@ -476,9 +484,10 @@ __device__ __forceinline__ void attend_tile(const Q8AttendParams& p, Warp<NQ, C,
   float x[8], ks[4], vs[4];                          // token 8 k + g; score 2 k + i: head 2 t + i
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
-    float c[NQ][4] = {};
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int s = 0; s < D / 16; s += 2) {
+      float c[NQ][4] = {};
       // rows 16 m + 0 .. 7 and 8 .. 15, pieces s and s + 1: matrix lane / 8's row is given by the lane
       uint32_t a[4];
       ldmatrix_x4(a, at + piece_at<D>(16 * m + (lane & 15), s + (lane >> 4)));
@@ -490,6 +499,10 @@ __device__ __forceinline__ void attend_tile(const Q8AttendParams& p, Warp<NQ, C,
 #pragma unroll
         for (int n = 0; n < NQ; ++n) mma_f16_16816(c[n], f, w.q[n][s + k][0], w.q[n][s + k][1]);
       }
+      if constexpr (NQ == 1)
+        add_sums(sum, c[0]);
+      else
+        add_pieces(sum, c[0], c[NQ - 1]);
     }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -497,8 +510,7 @@ __device__ __forceinline__ void attend_tile(const Q8AttendParams& p, Warp<NQ, C,
       vs[2 * m + r] = scales[kTile + 16 * m + 8 * r + g];
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      x[4 * m + i] = NQ == 1 ? c[0][i] : fmaf(c[NQ - 1][i], 1.f / kUp, c[0][i]);
+    for (int i = 0; i < 4; ++i) x[4 * m + i] = sum[i];
   }
   const bool part = n0 > 0 || n1 < kTile;
   if (__builtin_expect(part, 0)) {

@@ -79,3 +79,25 @@ def test_small_elements_beside_a_large_one(kind, dtype, up, d, hq, hkv):
         tol = rel * mag + 2.0**-21 * mag.amax(-1, keepdim=True)
         worst = float(((out[b].double() - want).abs() / tol).max())
         assert worst <= 1, (b, L)
+
+
+@pytest.mark.parametrize("kind", [I8, E4M3])
+@pytest.mark.parametrize("d,hq,hkv", [(64, 4, 1), (128, 8, 2)])
+def test_no_further_from_64_bits_than_fp32(kind, d, hq, hkv):
+    """fp32 queries, scores of all sizes: a plain fp32 evaluation sums its d products in some order and
+    rounds each sum; the kernel's distance from the 64-bit result (root mean square) is not more."""
+    lens = [4000, 900, 77]
+    c = Q8(lens, hkv, d, 64, kind, seed=4)
+    g = torch.Generator().manual_seed(2)
+    q = torch.randn(len(lens), hq, d, generator=g).cuda()
+    out = santa.santa_q8_dense_decode(q, c.cache, c.table, c.seq_lens)
+    here, plain = [], []
+    for b, L in enumerate(lens):
+        K, V = c.tokens("k", b, L), c.tokens("v", b, L)
+        want, _ = attend64(q[b], K, V)
+        s = (q[b].view(hkv, -1, 1, d) * K.float()[:, None]).cumsum(-1)[..., -1] / math.sqrt(d)
+        p = torch.exp(s - s.amax(-1, keepdim=True))
+        flat = (p[..., None] * V.float()[:, None]).cumsum(-2)[..., -1, :] / p.sum(-1, keepdim=True)
+        here.append((out[b].double() - want).flatten())
+        plain.append((flat.reshape(hq, d).double() - want).flatten())
+    assert float(torch.cat(here).norm()) <= float(torch.cat(plain).norm())

@@ -606,8 +606,10 @@ typedef struct santa_q8_args {
  *   - batch * num_kv_heads * teams * T / 32 (teams = max_teams, or num_draws of santa_q8_attend) must
  *     stay below about 2^31; more is SANTA_ERR_UNSUPPORTED.
  *   - out does not overlap what the call reads or the workspace.  The workspace
- *     (santa_q8_workspace_bytes) needs no initialisation and serves one call at a time.  Equal calls
- *     give equal bits.
+ *     (santa_q8_workspace_bytes) needs no initialisation and serves one call at a time.  The arrival
+ *     counters that santa_decode and santa_dense_decode keep in a workspace for the same batch and KV
+ *     heads, or fewer, are left as they are: one workspace, large enough for both and with its counters
+ *     zeroed once, serves layers of either kind in turn.  Equal calls give equal bits.
  */
 size_t santa_q8_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int head_dim,
                                 int team_size, int max_teams);

@@ -1281,7 +1281,10 @@ def _q8_sparse(name, q, cache, reps, page_table, seq_lens, num_teams, softcap, w
         _same_device(q=q)
         with _allocating(stream):
             views, _ = _output_views(B, Hq, Hkv, d, num_teams, q.device, False)
-            bufs = DecodeBuffers(*views[:5], None, _q8_workspace(a, q.device), views[5])
+            ws = _q8_workspace(a, q.device)
+            # the arrival counters of the calls over 16- and 32-bit caches, which may get these buffers
+            ws[:512 + 4 * B * Hkv].zero_()
+            bufs = DecodeBuffers(*views[:5], None, ws, views[5])
         made = tuple(t for t in vars(bufs).values() if t is not None)
     fields = [("out", (B, Hq, d), torch.float32), ("sel_ids", (B, Hkv, num_teams), torch.int32),
               ("sel_count", (B, Hkv), torch.int32), ("pi", (B, Hkv, num_teams), torch.float32)]

@@ -304,10 +304,12 @@ cudaError_t decode_launch_bf16_wide_full(const DecodeParams& p, int head_dim, in
                                          dim3 grid, int cluster, cudaStream_t stream);
 int decode_resident_bf16_wide_fast_var(int head_dim, int group);
 
-// Helpers of the host side that both ABI files use (defined in santa_abi.cu): streaming
-// multiprocessors of the current device (0 on failure), the driver's tensor-map encoder
-// (nullptr if it is not there), and the tensor map of a bf16 pool.
+// Helpers of the host side that the ABI files use (defined in santa_abi.cu): streaming
+// multiprocessors of the current device (0 on failure), the bytes of the arrival counters at the
+// start of a workspace, the driver's tensor-map encoder (nullptr if it is not there), and the
+// tensor map of a bf16 pool.
 int device_sms();
+size_t arrival_counter_bytes(int64_t units);
 typedef CUresult (*TensorMapEncode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                     const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                     const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,

@@ -41,19 +41,21 @@ int check_q8_shape(int batch, int hq, int hkv, int d, int T, int max_teams) {
   return rc ? rc : check_heads(hq, hkv);
 }
 
-// Workspace of an attention (see Q8AttendParams): split units, parts, pieces.
+// Workspace of an attention (see Q8AttendParams): split units, parts, pieces, behind room for the
+// arrival counters that santa_decode keeps at the start of a workspace (zero between calls).
 struct Q8Layout {
   int sms;
-  size_t split_bytes, ml_bytes, acc_bytes, bytes;
+  size_t counter_bytes, split_bytes, ml_bytes, acc_bytes, bytes;
 };
-int q8_layout(int d, Q8Layout* l) {
+int q8_layout(int batch, int hkv, int d, Q8Layout* l) {
   l->sms = std::min(santa::device_sms(), santa::q8_attend_most_blocks());
   if (l->sms <= 0) return SANTA_ERR_CUDA;
   const size_t rows = static_cast<size_t>(l->sms) * santa::kMaxGroup;
+  l->counter_bytes = santa::arrival_counter_bytes(static_cast<int64_t>(batch) * hkv);
   l->split_bytes = round_up(2 * l->sms * sizeof(int32_t), kAlign);
   l->ml_bytes = round_up(2 * rows * 2 * sizeof(float), kAlign);
   l->acc_bytes = 2 * rows * d * sizeof(float);
-  l->bytes = kAlign + l->split_bytes + l->ml_bytes + l->acc_bytes +
+  l->bytes = kAlign + l->counter_bytes + l->split_bytes + l->ml_bytes + l->acc_bytes +
              santa::q8_attend_warps(d) * rows * d * sizeof(float);
   return SANTA_OK;
 }
@@ -84,7 +86,7 @@ int check_q8_attend(const santa_decode_args* a, const santa_q8_args* c, bool lis
   if (!santa::q8_attend_fits(a->batch, a->num_kv_heads, a->team_size,
                              listed ? a->num_draws : a->max_teams))
     return SANTA_ERR_UNSUPPORTED;
-  if ((rc = q8_layout(a->head_dim, l))) return rc;
+  if ((rc = q8_layout(a->batch, a->num_kv_heads, a->head_dim, l))) return rc;
   if (!a->workspace || a->workspace_bytes < l->bytes) return SANTA_ERR_INVALID_ARG;
   const int64_t rows = a->num_pages * a->num_kv_heads * static_cast<int64_t>(a->team_size);
   const int64_t units = static_cast<int64_t>(a->batch) * a->num_kv_heads;
@@ -134,7 +136,7 @@ int launch_q8(const santa_decode_args* a, const santa_q8_args* c, bool listed, v
   p.softcap = c->softcap;
   p.window = c->window;
   unsigned char* base = reinterpret_cast<unsigned char*>(
-      round_up(reinterpret_cast<uintptr_t>(a->workspace), kAlign));
+      round_up(reinterpret_cast<uintptr_t>(a->workspace), kAlign) + l.counter_bytes);
   p.goes_on = reinterpret_cast<int32_t*>(base);
   p.begins = p.goes_on + l.sms;
   p.part_ml = reinterpret_cast<float*>(base += l.split_bytes);
@@ -155,7 +157,7 @@ size_t santa_q8_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, in
                                 int team_size, int max_teams) {
   Q8Layout l;
   if (check_q8_shape(batch, num_q_heads, num_kv_heads, head_dim, team_size, max_teams) ||
-      q8_layout(head_dim, &l))
+      q8_layout(batch, num_kv_heads, head_dim, &l))
     return 0;
   return l.bytes;
 }

@@ -547,6 +547,7 @@ int do_reps(const void* k_pool, int dtype, int64_t num_pages, int hkv, int T, in
 
 namespace santa {
 int device_sms() { return current_sms(); }
+size_t arrival_counter_bytes(int64_t units) { return counters_bytes(units); }
 TensorMapEncode tensor_map_encode() { return tensor_map_encoder(); }
 int pool_tensor_map(CUtensorMap* map, const void* pool, int64_t rows, int d) {
   return encode_pool_map(map, pool, rows, d);

@@ -12,6 +12,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
+import operator
 import os
 from dataclasses import dataclass
 
@@ -1077,6 +1079,29 @@ class Q8Cache:
                     cache_v_scale=self.v_scale)
 
 
+def _c_int(value, name) -> int:
+    """A whole number that a C int holds (ctypes would keep its low 32 bits)."""
+    try:
+        x = operator.index(int(value) if isinstance(value, float) and value.is_integer() else value)
+    except TypeError:
+        raise SantaError(f"{name} must be a whole number, got {value!r}") from None
+    if not -2**31 <= x < 2**31:
+        raise SantaError(f"{name} = {x} does not fit 32 bits")
+    return x
+
+
+def _c_float(value, name) -> float:
+    """A number that fp32 does not turn into zero or an infinity."""
+    try:
+        x = float(value)
+    except (TypeError, ValueError, OverflowError):
+        raise SantaError(f"{name} must be a number, got {value!r}") from None
+    y = ctypes.c_float(x).value
+    if (y == 0) != (x == 0) or math.isinf(y) != math.isinf(x):
+        raise SantaError(f"{name} = {x} is out of fp32's range")
+    return x
+
+
 def _norm_weight(w, name, d):
     if w is not None:
         _req(w, name, torch.float32, 1)
@@ -1103,6 +1128,7 @@ def _append_norm(q, k_new, v_new, cu_q, cache, reps, page_table, seq_lens, rope,
         dt = pools[0].dtype
         _pools(*pools, dt)
         a.cache_type = _DTYPES[dt]
+    a.eps = _c_float(eps, "eps")
     d = pools[0].shape[3]
     _norm_weight(q_norm, "q_norm", d)
     _norm_weight(k_norm, "k_norm", d)
@@ -1112,7 +1138,7 @@ def _append_norm(q, k_new, v_new, cu_q, cache, reps, page_table, seq_lens, rope,
         q, k_new, v_new, cu_q, pools, dt, reps, page_table, seq_lens, rope, seq_lens_next, q_out,
         interleaved, device_status, stream, q_norm=q_norm, k_norm=k_norm, k_scale=scales[0],
         v_scale=scales[1])
-    a.eps, a.q_norm, a.k_norm = float(eps), _ptr(q_norm), _ptr(k_norm)
+    a.q_norm, a.k_norm = _ptr(q_norm), _ptr(k_norm)
     a.k_scale, a.v_scale = _ptr(scales[0]), _ptr(scales[1])
     return _Prepared("santa_append_norm", a, keep, q_out, made, stream)
 
@@ -1170,7 +1196,8 @@ def _q8_step(q, cache, page_table, seq_lens, softcap, window):
     a.head_dim, a.team_size, a.max_teams, a.num_pages = d, T, page_table.shape[1], P
     c.k, c.v, c.k_scale, c.v_scale = (_ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale),
                                       _ptr(cache.v_scale))
-    c.type, c.window, c.softcap = _CODE_TYPES[cache.k.dtype], int(window), float(softcap)
+    c.type, c.window, c.softcap = (_CODE_TYPES[cache.k.dtype], _c_int(window, "window"),
+                                   _c_float(softcap, "softcap"))
     return a, c
 
 

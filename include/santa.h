@@ -567,6 +567,8 @@ typedef struct santa_append_norm_args {
  * santa_append_chunk's, bit for bit.
  *   - The representative of a touched page is the mean of its keys as stored; it does not depend on
  *     how the tokens were divided among calls.
+ *   - What the call writes (q_out, pools, scales, reps, seq_lens_next) overlaps nothing else that it
+ *     writes or reads, but for q_out = q.
  *   - Everything else (ragged chunks, lengths, refusals, device status, skipped sequences and pages)
  *     is as for santa_append_chunk.  Scales and weights are 16-byte aligned.
  */

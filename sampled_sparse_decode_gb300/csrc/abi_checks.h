@@ -1,6 +1,7 @@
 // abi_checks.h — argument checks that the ABI files share (internal to libsanta).
 #pragma once
 
+#include <algorithm>
 #include <cstdint>
 
 #include "kernels.h"
@@ -12,6 +13,7 @@ namespace abi {
 constexpr int kMaxTeams = 16384;
 constexpr int kMaxDraws = 4096;
 constexpr int kMaxRopeDim = 128;
+constexpr int64_t kMaxPages = 0x7fffffff;           // page ids are int32
 constexpr int64_t kMaxTokens = int64_t(1) << 24;    // tokens of one chunk call
 constexpr size_t kAlign = 256;
 
@@ -44,6 +46,18 @@ inline bool meets(const void* a, int64_t bytes, const void* b, int64_t rows, int
   // the first row that ends behind lo
   const __int128 r = at + row_bytes > lo ? 0 : (lo - at - row_bytes) / stride_bytes + 1;
   return r < rows && at + r * stride_bytes < lo + bytes;
+}
+
+// A buffer of a call, for the overlap checks.
+struct Span {
+  const void* at;
+  int64_t bytes;
+};
+template <int N>
+bool meets_any(const Span& out, const Span (&in)[N]) {
+  return std::any_of(in, in + N, [&](const Span& s) {
+    return meets(out.at, out.bytes, s.at, 1, s.bytes, s.bytes);
+  });
 }
 
 // CodeType of an 8-bit santa_dtype.

@@ -92,6 +92,34 @@ int check_append(const santa_append_chunk_args* a) {
   return SANTA_OK;
 }
 
+// Whether what santa_append_norm writes overlaps anything else that it writes or reads (queries rotated in
+// place aside).
+bool norm_overlaps(const santa_append_norm_args& a, int code) {
+  const santa_append_chunk_args& c = a.chunk;
+  const int64_t es = c.dtype == SANTA_BF16 ? 2 : 4, n = c.num_tokens, batch = c.batch, d = c.head_dim;
+  const int64_t q_row = (c.q ? c.num_q_heads : 0) * d * es, kv_row = c.num_kv_heads * d * es;
+  const int64_t teams = c.max_teams, pages = std::min(c.num_pages, kMaxPages);
+  const int64_t rows = pages * c.num_kv_heads * c.team_size;
+  const int64_t pool = rows * d * (code == santa::kCodeNone ? es : 1);
+  const int64_t positions = std::min(c.rope_positions, teams * c.team_size);
+  const Span out[] = {{c.q_out, n * q_row}, {c.k_pool, pool}, {c.v_pool, pool}, {a.k_scale, rows * 4},
+                      {a.v_scale, rows * 4}, {c.reps, pages * c.num_kv_heads * d * 4},
+                      {c.seq_lens_next, batch * 4}};
+  const Span in[] = {{c.cu_q, (batch + 1) * 4},  {c.page_table, batch * teams * 4},
+                     {c.seq_lens, batch * 4},    {c.rope, positions * c.rope_dim * 4},
+                     {a.q_norm, d * 4},          {a.k_norm, d * 4}};
+  for (const Span& o : out) {
+    if (meets_any(o, in) || meets(o.at, o.bytes, c.k_new, n, kv_row, c.k_stride * es) ||
+        meets(o.at, o.bytes, c.v_new, n, kv_row, c.v_stride * es))
+      return true;
+    if (!(&o == out && c.q_out == c.q) && meets(o.at, o.bytes, c.q, n, q_row, c.q_stride * es))
+      return true;
+    for (const Span* other = out; other != &o; ++other)
+      if (meets(o.at, o.bytes, other->at, 1, other->bytes, other->bytes)) return true;
+  }
+  return false;
+}
+
 void fill_append(const santa_append_chunk_args* a, santa::AppendChunkParams* p) {
   p->q = a->q;
   p->k_new = a->k_new;
@@ -161,6 +189,7 @@ int santa_append_norm(const santa_append_norm_args* a, void* stream) {
   if (santa::append_norm_blocks(c->num_tokens, c->batch, c->q ? c->num_q_heads : 0, c->num_kv_heads,
                                 c->head_dim, c->team_size, c->dtype == SANTA_BF16) > 0x7fffffffll)
     return SANTA_ERR_UNSUPPORTED;
+  if (norm_overlaps(*a, code)) return SANTA_ERR_INVALID_ARG;
   santa::AppendNormParams p = {};
   fill_append(c, &p);
   p.q_norm = a->q_norm;

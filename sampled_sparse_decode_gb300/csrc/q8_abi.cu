@@ -10,21 +10,8 @@ using namespace santa::abi;
 
 namespace {
 
-constexpr int64_t kMaxPages = 0x7fffffff;   // page ids are int32
 // caps outside these would take the quotient of a score and its cap near the ends of fp32's range
 constexpr float kLeastCap = 0x1p-20f, kMostCap = 0x1p20f;
-
-// A buffer of a call, for the overlap checks.
-struct Span {
-  const void* at;
-  int64_t bytes;
-};
-template <int N>
-bool meets_any(const Span& out, const Span (&in)[N]) {
-  return std::any_of(in, in + N, [&](const Span& s) {
-    return meets(out.at, out.bytes, s.at, 1, s.bytes, s.bytes);
-  });
-}
 
 int check_q8_cache(const void* k, const void* v, const float* k_scale, const float* v_scale,
                    int type, int* code) {

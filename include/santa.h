@@ -622,8 +622,8 @@ int santa_q8_attend(const santa_decode_args* a, const santa_q8_args* c, void* st
  * santa_q8_topk_decode / santa_q8_decode — santa_select_topk or santa_sample followed by
  * santa_q8_attend on `stream`: the sparse steps over an 8-bit cache.  a as for santa_topk_decode and
  * santa_decode but for k_pool and v_pool, which are not read, and the workspace, which is
- * santa_q8_attend's.  The selection takes every team of the sequence and plain scores; softcap and
- * window act in the attention.
+ * santa_q8_attend's.  The selection takes every team of the sequence and plain scores; softcap acts in
+ * the attention.  A window is SANTA_ERR_UNSUPPORTED: the chosen teams might all lie before it.
  */
 int santa_q8_topk_decode(const santa_decode_args* a, const santa_q8_args* c, void* stream);
 int santa_q8_decode(const santa_decode_args* a, const santa_q8_args* c, void* stream);

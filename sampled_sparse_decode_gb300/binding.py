@@ -1296,6 +1296,8 @@ def santa_q8_attend_prepared(q, cache: Q8Cache, page_table, seq_lens, sel_ids, s
 def _q8_sparse(name, q, cache, reps, page_table, seq_lens, num_teams, softcap, window, bufs,
                stream, seed=0, sampler="iid_ht", mix_alpha=0.0):
     a, c = _q8_step(q, cache, page_table, seq_lens, softcap, window)
+    if c.window:
+        raise SantaError("the steps over best and sampled teams take no window (window must be 0)")
     P, Hkv, T, d = cache.k.shape
     B, Hq, _ = q.shape
     _req(reps, "reps", torch.float32, 3)
@@ -1341,7 +1343,8 @@ def _q8_sparse(name, q, cache, reps, page_table, seq_lens, num_teams, softcap, w
 def santa_q8_topk_decode(q, cache: Q8Cache, reps, page_table, seq_lens, num_teams: int,
                          softcap: float = 0.0, window: int = 0,
                          bufs: DecodeBuffers | None = None, stream=None) -> DecodeBuffers:
-    """santa_topk_decode over an 8-bit cache: santa_select_topk, then santa_q8_attend."""
+    """santa_topk_decode over an 8-bit cache: santa_select_topk, then santa_q8_attend.  window must
+    be 0: teams are chosen from the whole sequence."""
     return _q8_sparse("santa_q8_topk_decode", q, cache, reps, page_table, seq_lens, num_teams,
                       softcap, window, bufs, stream).run(stream)
 
@@ -1358,7 +1361,8 @@ def santa_q8_topk_decode_prepared(q, cache: Q8Cache, reps, page_table, seq_lens,
 def santa_q8_decode(q, cache: Q8Cache, reps, page_table, seq_lens, num_draws: int, seed: int,
                     softcap: float = 0.0, window: int = 0, bufs: DecodeBuffers | None = None,
                     stream=None, sampler: str = "iid_ht", mix_alpha: float = 0.0) -> DecodeBuffers:
-    """santa_decode over an 8-bit cache: santa_sample, then santa_q8_attend."""
+    """santa_decode over an 8-bit cache: santa_sample, then santa_q8_attend.  window must be 0: teams
+    are drawn from the whole sequence."""
     return _q8_sparse("santa_q8_decode", q, cache, reps, page_table, seq_lens, num_draws, softcap,
                       window, bufs, stream, seed, sampler, mix_alpha).run(stream)
 

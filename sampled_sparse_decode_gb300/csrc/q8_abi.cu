@@ -96,6 +96,15 @@ int check_q8_attend(const santa_decode_args* a, const santa_q8_args* c, bool lis
   return SANTA_OK;
 }
 
+// Every check of the attention behind a choice of teams.  The choice is among all teams of a sequence: those
+// of a window may not be among them, so a window is refused.
+int check_q8_chosen(const santa_decode_args* a, const santa_q8_args* c) {
+  if (c && c->window > 0) return SANTA_ERR_UNSUPPORTED;
+  int code = 0;
+  Q8Layout l;
+  return check_q8_attend(a, c, true, &code, &l);
+}
+
 int launch_q8(const santa_decode_args* a, const santa_q8_args* c, bool listed, void* stream) {
   int code = 0;
   Q8Layout l;
@@ -159,17 +168,13 @@ int santa_q8_attend(const santa_decode_args* a, const santa_q8_args* c, void* st
 
 int santa_q8_topk_decode(const santa_decode_args* a, const santa_q8_args* c, void* stream) {
   // everything the attention refuses is refused before the selection is launched
-  int code = 0;
-  Q8Layout l;
-  int rc = check_q8_attend(a, c, true, &code, &l);
+  int rc = check_q8_chosen(a, c);
   if (rc || (rc = santa_select_topk(a, stream))) return rc;
   return launch_q8(a, c, true, stream);
 }
 
 int santa_q8_decode(const santa_decode_args* a, const santa_q8_args* c, void* stream) {
-  int code = 0;
-  Q8Layout l;
-  int rc = check_q8_attend(a, c, true, &code, &l);
+  int rc = check_q8_chosen(a, c);
   if (rc) return rc;
   // the sampling reads representatives only; its checks ask for pools all the same
   santa_decode_args b = *a;

@@ -562,8 +562,9 @@ typedef struct santa_append_norm_args {
  * of the activations' type or of 8 bits.  A query or key x of one head becomes
  *   y = x / sqrt(mean_j(x_j^2) + eps) * w
  * (q_norm for queries, k_norm for keys), then its pairs are turned as in santa_append_chunk, all in
- * fp32, and the result is rounded once: queries to their type, keys to the cache's.  Values are
- * neither normed nor turned.  With a cache of the activations' type and no norms the results are
+ * fp32, and the result is rounded once: queries to their type, keys to the cache's.  The squares'
+ * sum is held in fp32 too: where mean + eps lies outside 2^-120 .. 2^120, a row may become zeros,
+ * infinities or NaN.  Values are neither normed nor turned.  With a cache of the activations' type and no norms the results are
  * santa_append_chunk's, bit for bit.
  *   - The representative of a touched page is the mean of its keys as stored; it does not depend on
  *     how the tokens were divided among calls.

@@ -33,9 +33,8 @@
 //     A weight so keeps 2^-22 of itself down to 2^-21 of the largest, and 2^-43 of the largest below.
 //   - The reference of the exponentials is raised only when a score passes it by 8 (powers of two),
 //     which is seldom after a few tiles, so a tile has no reduction among lanes.
-//   - The matrix units cut what they add.  A score's products start from zero for every 32 dimensions,
-//     those of the output for every tile, and are added to the running sums in fp32 with rounding (a score
-//     summed in the unit: fp32 queries 1.1e-7 from 64-bit results instead of 0.4e-7, at the same time).
+//   - The matrix units cut what they add.  A score's products (of first pieces) start from zero for every 32
+//     dimensions, those of the output for every tile, and are added to the running sums in fp32 with rounding.
 //
 // Bound by HBM where there is much to read (2 d + 8 bytes for every token and head), by latency
 // where there is little: a launch's chain is lengths -> page ids -> tiles -> pieces -> parts, and its code
@@ -131,20 +130,20 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-__device__ __forceinline__ void add_sums(float (&sum)[4], const float (&c)[4]) {
+// Adds a matrix product to a running sum, in register pairs or one by one; which of them costs less depends
+// on the code around it (16 x 32K tokens, int8: scores of bf16 queries in pairs 166 us, one by one 172; of
+// fp32 queries 191 and 188; outputs 170 and 166).
+template <bool PAIRS>
+__device__ __forceinline__ void add_product(float (&sum)[4], const float (&c)[4]) {
+  if constexpr (PAIRS) {
 #pragma unroll
-  for (int i = 0; i < 4; i += 2) {
-    const float2 r = halves(add_pair(pair(sum[i], sum[i + 1]), pair(c[i], c[i + 1])));
-    sum[i] = r.x, sum[i + 1] = r.y;
-  }
-}
-// Adds the products of first and second pieces.
-__device__ __forceinline__ void add_pieces(float (&sum)[4], const float (&c)[4], const float (&c2)[4]) {
+    for (int i = 0; i < 4; i += 2) {
+      const float2 r = halves(add_pair(pair(sum[i], sum[i + 1]), pair(c[i], c[i + 1])));
+      sum[i] = r.x, sum[i + 1] = r.y;
+    }
+  } else {
 #pragma unroll
-  for (int i = 0; i < 4; i += 2) {
-    const uint64_t both = fma_pair(pair(c2[i], c2[i + 1]), twice(1.f / kUp), pair(c[i], c[i + 1]));
-    const float2 r = halves(add_pair(pair(sum[i], sum[i + 1]), both));
-    sum[i] = r.x, sum[i + 1] = r.y;
+    for (int i = 0; i < 4; ++i) sum[i] += c[i];
   }
 }
 
@@ -484,10 +483,10 @@ __device__ __forceinline__ void attend_tile(const Q8AttendParams& p, Warp<NQ, C,
   float x[8], ks[4], vs[4];                          // token 8 k + g; score 2 k + i: head 2 t + i
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    float sum[4] = {0.f, 0.f, 0.f, 0.f}, low[4] = {0.f, 0.f, 0.f, 0.f};   // low: of second pieces
 #pragma unroll
     for (int s = 0; s < D / 16; s += 2) {
-      float c[NQ][4] = {};
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
       // rows 16 m + 0 .. 7 and 8 .. 15, pieces s and s + 1: matrix lane / 8's row is given by the lane
       uint32_t a[4];
       ldmatrix_x4(a, at + piece_at<D>(16 * m + (lane & 15), s + (lane >> 4)));
@@ -497,12 +496,9 @@ __device__ __forceinline__ void attend_tile(const Q8AttendParams& p, Warp<NQ, C,
         pairs_to_f16<C>(a[2 * k], f[0], f[2]);
         pairs_to_f16<C>(a[2 * k + 1], f[1], f[3]);
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) mma_f16_16816(c[n], f, w.q[n][s + k][0], w.q[n][s + k][1]);
+        for (int n = 0; n < NQ; ++n) mma_f16_16816(n ? low : c, f, w.q[n][s + k][0], w.q[n][s + k][1]);
       }
-      if constexpr (NQ == 1)
-        add_sums(sum, c[0]);
-      else
-        add_pieces(sum, c[0], c[NQ - 1]);
+      add_product<NQ == 1>(sum, c);
     }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -510,7 +506,7 @@ __device__ __forceinline__ void attend_tile(const Q8AttendParams& p, Warp<NQ, C,
       vs[2 * m + r] = scales[kTile + 16 * m + 8 * r + g];
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[4 * m + i] = sum[i];
+    for (int i = 0; i < 4; ++i) x[4 * m + i] = NQ == 1 ? sum[i] : fmaf(low[i], 1.f / kUp, sum[i]);
   }
   const bool part = n0 > 0 || n1 < kTile;
   if (__builtin_expect(part, 0)) {
@@ -580,7 +576,9 @@ __device__ __forceinline__ void attend_tile(const Q8AttendParams& p, Warp<NQ, C,
       mma_f16_16816(c, f, hi[2 * m], hi[2 * m + 1]);
       mma_f16_16816(c2, f, lo[2 * m], lo[2 * m + 1]);
     }
-    add_pieces(w.acc[j], c, c2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = fmaf(c2[i], 1.f / kUp, c[i]);
+    add_product<false>(w.acc[j], c);
   }
 }
 

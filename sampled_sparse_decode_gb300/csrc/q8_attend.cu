@@ -41,10 +41,10 @@
 // is fetched as it is first run, so the code that short calls run is kept short.  The matrix units are a
 // fifth busy: with at most 8 columns mma.sync from registers feeds them well enough, and codes have to
 // pass through registers anyway.  Measured on GB300 (bf16 queries, 32 / 8 heads of 128, int8, against a
-// measured copy): 16 sequences at 32K and below 138 us, 95%; 16 at 32K with groups of 1 and 8 99 and 98%,
-// with fp32 queries 88% (twice the score products; e4m3 99%), heads of 64 83% (e4m3 91%); 4 x 128K e4m3 with
-// capped scores 86 us, 89%; one sequence of 32K 15 us; 523 tokens 8.8 us.
-// Both sides of the choices: one token at a time per warp 2445 us for the 16 sequences; stretches per
+// measured copy): 16 sequences at 32K and below 138 us, 95%; 16 at 32K with groups of 1 and 8 98 and 96%,
+// with fp32 queries 87% (twice the score products; e4m3 98%), capped scores 88%, heads of 64 83% (e4m3 89%);
+// 4 x 128K e4m3 with capped scores 86 us, 89%; one sequence of 32K 15.4 us; 523 tokens 8.7 us.
+// Both sides of the choices, each on the kernel as it was then: one token at a time per warp 2445 us for the 16 sequences; stretches per
 // block with a merge for each unit 164, per warp 149; an opening counted as 0, 1, 2 tiles 156, 149, 139;
 // twelve warps and two stages 144 against 149 (eight and three), but 523 tokens 12.3 against 10.3; the last
 // block to arrive joins the parts 11.7 and 30.5 us (523 tokens, one sequence of 32K) against 10.3 and 16.6

@@ -18,6 +18,8 @@ namespace {
 
 constexpr int kReadThreads = 256;
 constexpr int kAhead = 4;                            // pieces of each of keys and values
+// Of a grid that is otherwise as wide as the tables: 64 x 128 tokens with tables of 1024 pages take 21 us,
+// one block per entry 368, at most 2048 12; full tables 285, 283 and 298, 8 prompts 38.2, 38.3 and 40.9.
 constexpr int kMostBlocks = 16384;
 
 template <bool BF16>

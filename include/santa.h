@@ -605,7 +605,8 @@ typedef struct santa_q8_args {
  *     sets SANTA_DEV_BAD_PAGE and its tokens are left out; a listed team out of range, a weight that
  *     is not finite and positive or a count outside [0, num_draws] sets SANTA_DEV_BAD_SEL, and that
  *     team is left out (a count is clamped).  A team listed twice counts twice.
- *   - What is not seen has no influence, whatever its bytes and scales hold.
+ *   - What is not seen has no influence, whatever its bytes and scales hold; table entries of pages
+ *     that hold no seen token may be anything.
  *   - batch * num_kv_heads * teams * T / 32 (teams = max_teams, or num_draws of santa_q8_attend) must
  *     stay below about 2^31; more is SANTA_ERR_UNSUPPORTED.
  *   - out does not overlap what the call reads or the workspace.  The workspace

@@ -304,7 +304,8 @@ __device__ __forceinline__ void issue_tile(const Q8AttendParams& p, const Walk& 
       const int team = p.sel_ids[slot];
       const float pi = p.pi[slot];
       if (team >= 0 && team < p.max_teams && team * T < w.u.len && pi > 0.f && pi < INFINITY) {
-        pc.team = team;
+        // a team before the window: its page may have been given back, and is not looked at
+        if ((team + 1) * T > w.u.lo) pc.team = team;
         pc.bias = -log2f(pi);
       } else {
         set_status(p.status, SANTA_DEV_BAD_SEL);

@@ -607,6 +607,8 @@ typedef struct santa_q8_args {
  *     team is left out (a count is clamped).  A team listed twice counts twice.
  *   - What is not seen has no influence, whatever its bytes and scales hold; table entries of pages
  *     that hold no seen token may be anything.
+ *   - Scores may be as large as 2^25 in magnitude (before the cap: anything); rows with larger ones may
+ *     become NaN.
  *   - batch * num_kv_heads * teams * T / 32 (teams = max_teams, or num_draws of santa_q8_attend) must
  *     stay below about 2^31; more is SANTA_ERR_UNSUPPORTED.
  *   - out does not overlap what the call reads or the workspace.  The workspace

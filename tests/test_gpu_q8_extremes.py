@@ -128,10 +128,7 @@ def test_codes_of_any_byte(kind, dtype, d):
 @pytest.mark.parametrize("kind", [I8, E4M3])
 @pytest.mark.parametrize("dtype,d,hq,hkv", [(BF16, 128, 8, 2), (F32, 64, 3, 1)])
 def test_queries_of_every_size(kind, dtype, d, hq, hkv):
-    """Heads from 2^-120 to 2^107 over keys whose scales bring the scores back, the last to about 2^21: a
-    score's exponent is formed from the exact product less the rounded reference, which may differ by half a
-    step of the reference, and weights of 2^8 times two to that must stay below fp16's 65504: half a step is
-    4 at 2^26."""
+    """Heads from 2^-120 to 2^107 over keys whose scales bring the scores back, the last to about 2^21."""
     e = [-120, -100, -60, -20, 20, 60, 100, 105]
     c = Q8([200] * len(e), hkv, d, 64, kind, seed=2)
     q = queries(c, hq, F32, seed=1).clamp(-3.9, 3.9)
@@ -142,6 +139,34 @@ def test_queries_of_every_size(kind, dtype, d, hq, hkv):
         q = q.to(BF16)
     out = santa.santa_q8_dense_decode(q, c.cache, c.table, c.seq_lens, softcap=0.0)
     check_dense(c, q, out)
+
+
+@pytest.mark.parametrize("kind", [I8, E4M3])
+@pytest.mark.parametrize("dtype,d,hq,hkv", [(BF16, 128, 8, 2), (F32, 64, 3, 1)])
+@pytest.mark.parametrize("top", [2.0**15, 2.0**20, 2.0**25])
+def test_scores_of_the_largest_size(kind, dtype, d, hq, hkv, top):
+    """Largest scores up to the stated 2^25: the value of the largest where it stands out.  A score's exponent
+    is formed from the exact product less the rounded reference, and may lie half a step of the reference above
+    it (2 to the base of two at 2^25.5): weights of 2^8 times two to that stay below fp16's 65504."""
+    lens = [200, 3000]
+    c = Q8(lens, hkv, d, 64, kind, seed=2)
+    q = queries(c, hq, dtype, seed=1)
+    for b, L in enumerate(lens):
+        qk = (q[b].double().view(hkv, -1, d) @ c.tokens("k", b, L).transpose(1, 2)).abs().amax() / math.sqrt(d)
+        c.cache.k_scale[c.table[b, :-(-L // 64)].long()] *= float(0.99 * top / qk)
+    out = santa.santa_q8_dense_decode(q, c.cache, c.table, c.seq_lens)
+    assert bool(torch.isfinite(out).all())
+    for b, L in enumerate(lens):
+        K, V = c.tokens("k", b, L), c.tokens("v", b, L)
+        want, _ = attend64(q[b], K, V)
+        # heads whose largest score stands out by more than the sum's rounding (17 (d / 16 + 1) + 8 steps)
+        qi = q[b].double().view(hkv, -1, d)
+        s = (qi @ K.transpose(1, 2) / math.sqrt(d)).reshape(hq, L).topk(2, -1).values
+        slack = 2 * (17 * (d / 16 + 1) + 8) * 2.0**-24 * (qi.abs() @ K.abs().transpose(1, 2)).amax(-1) / math.sqrt(d)
+        clear = s[:, 0] - s[:, 1] > slack.reshape(hq) + 40
+        assert bool(clear.any())
+        err = (out[b].double() - want).abs() / want.abs().amax(-1, keepdim=True)
+        assert float(err[clear].amax()) <= 2.0**-18
 
 
 @pytest.mark.parametrize("bad", [math.nan, math.inf])

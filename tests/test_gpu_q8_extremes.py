@@ -147,7 +147,7 @@ def test_queries_of_every_size(kind, dtype, d, hq, hkv):
 def test_scores_of_the_largest_size(kind, dtype, d, hq, hkv, top):
     """Largest scores up to the stated 2^25: the value of the largest where it stands out.  A score's exponent
     is formed from the exact product less the rounded reference, and may lie half a step of the reference above
-    it (2 to the base of two at 2^25.5): weights of 2^8 times two to that stay below fp16's 65504."""
+    it, which is 2 for one of 2^25 log2(e): weights stay below 2^8 2^2, and fp16 ends at 65504."""
     lens = [200, 3000]
     c = Q8(lens, hkv, d, 64, kind, seed=2)
     q = queries(c, hq, dtype, seed=1)
